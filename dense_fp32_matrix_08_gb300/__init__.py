@@ -357,3 +357,10 @@ def sgemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     if rc != 0:
         raise SgemmError(rc)
     return C
+
+
+# The 8-bit block-scaled operators (they need torch, unlike the bindings above).
+from .f8 import (F8_EXPORTED, f8_gemm_status, f8_matmul, f8_quantize,  # noqa: E402
+                 f8_quantize_pair)
+
+__all__ += ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]

@@ -1,0 +1,599 @@
+// D = alpha * op(A) * op(B) + beta * D on 8-bit floating-point operands with one FP32 scale
+// for each block of 128 along k, on the 5th-generation tensor cores of sm_103a:
+//
+//   D[i][j] = alpha * sum_kb sA[i][kb] * sB[kb][j] * (sum_{k in block kb} qA[i][k] * qB[k][j])
+//             + beta * D[i][j]
+//
+// The inner sums (128 products of two 8-bit numbers) run in the tensor core with FP32
+// accumulation; the outer sum over the blocks runs in FP32 registers, because its terms carry
+// different scales. One accumulator tile in TMEM therefore holds one block of k only: while
+// the tensor core fills one TMEM buffer, the epilogue warps read the previous one, scale it
+// and add it to their registers.
+//
+// The kernel sees the product as P (128 rows per tile) times Q (TN columns per tile). P = op(A)
+// and Q = op(B) for products with many rows. With few rows (serving: a few tokens) the roles are
+// exchanged, P = op(B)^T and Q = op(A)^T, so that the 128-row side of the instruction holds rows
+// of the weight and none of it is wasted on absent tokens.
+//
+// Both operands may be stored with k contiguous or with the other index contiguous: TMA writes
+// either into the 128-byte-swizzled layout that the instruction's descriptors read (K-major or
+// MN-major), so no transposed copy is ever made.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/f8_gemm.h"
+#include "sgemm_internal.h"
+#include "sgemm_plan.h"
+#include "tc_common.cuh"
+
+namespace sgemm {
+namespace f8 {
+
+constexpr int BP = 128;                  // rows of P per tile
+constexpr int BK = 128;                  // k per block = per pipeline stage
+constexpr int P_BYTES = BP * BK;
+constexpr int MAX_CLUSTER = 8;
+
+template <int TN_>
+struct Cfg {
+  static constexpr int TN = TN_;
+  static constexpr int GROUPS = TN >= 128 ? 2 : 1;  // epilogue groups of four warps
+  static constexpr int COLS = TN / GROUPS;          // accumulator columns of a group
+  static constexpr int EPI_WARPS = 4 * GROUPS;
+  static constexpr int THREADS = 32 * (4 + EPI_WARPS);
+  static constexpr int Q_BYTES = TN * BK;
+  static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr int STAGES = TN == 256 ? 4 : TN == 128 ? 6 : 8;
+  static constexpr int NBUF = TN >= 128 ? 2 : 4;    // TMEM accumulators
+  static constexpr int ACC_COLS = TN < 32 ? 32 : TN;
+  static constexpr int TMEM_COLS = NBUF * ACC_COLS;
+  static constexpr int SQ_BYTES = 2 * TN * 4;       // Q scales of two k blocks
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * NBUF) + 16;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SQ_BYTES + BAR_BYTES;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(TMEM_COLS <= 512, "TMEM columns");
+  static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
+};
+
+struct Side {          // one operand as the kernel sees it
+  int extent;          // rows of P, columns of Q
+  int mn_major;        // stored with this extent contiguous
+  const float *scale;
+  int shift;           // 7: one scale for 128 of the extent, 0: one for each
+  long long s_mn, s_k; // scale strides along the extent and along the k blocks
+};
+
+struct Params {
+  Side p, q;
+  int KB;              // k blocks
+  int tiles_p, tiles_q, group_p;
+  int split;           // CTAs of a cluster, each with its range of k blocks
+  uint32_t idesc;
+  float alpha, beta;
+  void *D;
+  int d_type;
+  long long d_p, d_q;  // strides of D along P and Q; one of them is 1
+  int vec;             // 16-byte stores along the contiguous index are aligned
+};
+
+// Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the
+// epilogue gave up.
+__device__ int g_f8_status;
+
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ float load_d(const Params &p, long long at) {
+  if (p.d_type == F8_D_F32) return reinterpret_cast<const float *>(p.D)[at];
+  if (p.d_type == F8_D_BF16)
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.D)[at]);
+  return __half2float(reinterpret_cast<const __half *>(p.D)[at]);
+}
+
+__device__ __forceinline__ void store_d(const Params &p, long long at, float v) {
+  if (p.d_type == F8_D_F32)
+    reinterpret_cast<float *>(p.D)[at] = v;
+  else if (p.d_type == F8_D_BF16)
+    reinterpret_cast<__nv_bfloat16 *>(p.D)[at] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<__half *>(p.D)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ uint32_t pack16(const Params &p, float a, float b) {
+  if (p.d_type == F8_D_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Eight neighbouring accumulator columns of one row -> D. The one rounding to D's type is here.
+__device__ __forceinline__ void store8(const Params &p, int row, int col, float (&v)[8]) {
+  if (row >= p.p.extent || col >= p.q.extent) return;
+  const long long at = row * p.d_p + col * p.d_q;
+  const int n = min(8, p.q.extent - col);
+  if (p.beta != 0.0f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = j < n ? fmaf(p.alpha, v[j], p.beta * load_d(p, at + j * p.d_q)) : 0.0f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= p.alpha;
+  }
+  if (p.vec && n == 8 && p.d_q == 1) {
+    if (p.d_type == F8_D_F32) {
+      float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.D) + at);
+      d[0] = make_float4(v[0], v[1], v[2], v[3]);
+      d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.D) + at);
+      *d = make_uint4(pack16(p, v[0], v[1]), pack16(p, v[2], v[3]), pack16(p, v[4], v[5]),
+                      pack16(p, v[6], v[7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) store_d(p, at + j * p.d_q, v[j]);
+}
+
+// Warp 0 (one lane): TMA producer. Warp 1 (one lane): MMA issuer. Warps 4 ..: epilogue, group g
+// of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
+// rows) 32 (w % 4) .. + 31, one row per thread.
+// (Warps 2 and 3 only complete the first warpgroup: registers are granted to four warps at a time,
+// so they cost nothing.)
+// QVEC: Q has a scale for each column (else one for each 128, the same for a whole group).
+template <int TN, bool QVEC>
+__global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
+    f8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+              const Params p) {
+  using C = Cfg<TN>;
+  using namespace tcx;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = saddr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw);
+  float *sq_buf = reinterpret_cast<float *>(sbase + C::STAGES * C::STAGE_BYTES);
+  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SQ_BYTES;
+  const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
+  const uint32_t acc_empty = acc_full + 8 * C::NBUF;
+  const uint32_t tmem_slot = acc_empty + 8 * C::NBUF;
+  volatile uint32_t *tmem_slot_ptr =
+      reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.split;
+  const int rank = S > 1 ? (int)(blockIdx.x % (unsigned)S) : 0;
+  const int first = (int)(blockIdx.x / (unsigned)S), step = (int)(gridDim.x / (unsigned)S);
+  const int tiles = p.tiles_p * p.tiles_q;
+  const int kb0 = (int)((long long)p.KB * rank / S);
+  const int kb1 = (int)((long long)p.KB * (rank + 1) / S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bars + 8 * s, 1);
+      mbar_init(bars + 8 * (C::STAGES + s), 1);
+    }
+    for (int b = 0; b < C::NBUF; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, C::EPI_WARPS);
+    }
+    mbar_init_fence();
+    tma_prefetch_map(&map_p);
+    tma_prefetch_map(&map_q);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot_ptr;
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+
+  if (warp == 0 && lane == 0) {
+    // ---- TMA producer: stage g % STAGES holds k block g of this CTA's tiles, in order
+    long long g = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      int tp, tq;
+      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = (int)(g % C::STAGES);
+        if (g >= C::STAGES &&
+            !mbar_wait(bars + 8 * (C::STAGES + s), ((uint32_t)(g / C::STAGES) & 1u) ^ 1u)) {
+          atomicCAS(&g_f8_status, 0, 1);
+          ok = false;
+          break;
+        }
+        const uint32_t st = base + s * C::STAGE_BYTES, full = bars + 8 * s;
+        const int k = kb * BK;
+        mbar_expect_tx(full, C::STAGE_BYTES);
+        if (p.p.mn_major)
+          tma_load_2d(st, &map_p, tp * BP, k, full);
+        else
+          tma_load_2d(st, &map_p, k, tp * BP, full);
+        if (p.q.mn_major) {
+#pragma unroll
+          for (int c = 0; c < TN; c += 128)
+            tma_load_2d(st + P_BYTES + c * BK, &map_q, tq * TN + c, k, full);
+        } else {
+          tma_load_2d(st + P_BYTES, &map_q, k, tq * TN, full);
+        }
+      }
+    }
+    // the last loads issued must have landed before this thread leaves
+    for (long long k = g - 1; k >= 0 && k >= g - C::STAGES; --k)
+      mbar_wait(bars + 8 * (int)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
+  } else if (warp == 1 && lane == 0) {
+    // ---- MMA issuer: k block g goes to accumulator g % NBUF
+    const uint32_t lead_q = 128 * BK;
+    const uint32_t adv_p = p.p.mn_major ? 32 * 128 : 32, adv_q = p.q.mn_major ? 32 * 128 : 32;
+    long long g = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = (int)(g % C::STAGES), b = (int)(g % C::NBUF);
+        if ((g >= C::NBUF &&
+             !mbar_wait(acc_empty + 8 * b, ((uint32_t)(g / C::NBUF) & 1u) ^ 1u)) ||
+            !mbar_wait(bars + 8 * s, (uint32_t)(g / C::STAGES) & 1u)) {
+          atomicCAS(&g_f8_status, 0, 2);
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t st = base + s * C::STAGE_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk)
+          mma_f8(tmem + (uint32_t)b * C::ACC_COLS, sw128_desc(st + kk * adv_p, 16),
+                 sw128_desc(st + P_BYTES + kk * adv_q, lead_q), p.idesc, kk != 0 ? 1u : 0u);
+        mma_commit(bars + 8 * (C::STAGES + s));  // the stage is free once these complete
+        mma_commit(acc_full + 8 * b);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue
+    const int grp = (warp - 4) >> 2, quad = warp & 3;
+    const int gt = quad * 32 + lane;  // thread of the group
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
+    long long g = 0;
+    bool ok = true;
+    for (int t = first; t < tiles; t += step) {
+      int tp, tq;
+      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      const int row = tp * BP + quad * 32 + lane, col0 = tq * TN + grp * C::COLS;
+      unsigned long long acc[C::COLS / 2];
+#pragma unroll
+      for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
+      // scales of the next k block are fetched one block ahead; rows and columns out of range
+      // take 0 (their products are not stored)
+      const float *ps = row < p.p.extent ? p.p.scale + (row >> p.p.shift) * p.p.s_mn : nullptr;
+      const int qcol = QVEC ? col0 + gt : col0;
+      const float *qs = qcol < p.q.extent && (!QVEC || gt < C::COLS)
+                            ? p.q.scale + (qcol >> p.q.shift) * p.q.s_mn
+                            : nullptr;
+      float ps_next = ps && kb0 < kb1 ? __ldg(ps + kb0 * p.p.s_k) : 0.0f;
+      float qs_next = qs && kb0 < kb1 ? __ldg(qs + kb0 * p.q.s_k) : 0.0f;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int b = (int)(g % C::NBUF);
+        const float sp = ps_next, sq = qs_next;
+        if (kb + 1 < kb1) {
+          ps_next = ps ? __ldg(ps + (kb + 1) * p.p.s_k) : 0.0f;
+          qs_next = qs ? __ldg(qs + (kb + 1) * p.q.s_k) : 0.0f;
+        }
+        float *sqb = sq_buf + (int)(g & 1) * TN + grp * C::COLS;
+        if constexpr (QVEC) {
+          if (gt < C::COLS) sqb[gt] = sq;
+          named_barrier(1 + grp, 128);
+        }
+        // a warp whose wait gave up goes on without its sums, so that it still arrives at the
+        // barriers of its group
+        if (!ok) continue;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(acc_full + 8 * b, (uint32_t)(g / C::NBUF) & 1u));
+        if (!ok) {
+          if (lane == 0) atomicCAS(&g_f8_status, 0, 3);
+          continue;
+        }
+        fence_after();
+        constexpr int CH = TN == 256 || C::COLS < 32 ? 16 : 32;
+        const unsigned long long s2 = QVEC ? pack2(sp, sp) : pack2(sp * sq, sp * sq);
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += CH) {
+          uint32_t v[CH];
+          tmem_ld(lane_base + (uint32_t)(b * C::ACC_COLS + c), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            unsigned long long lo = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            unsigned long long hi = pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+            if constexpr (QVEC) {
+              const float4 w = *reinterpret_cast<const float4 *>(sqb + c + j);
+              lo = mul2(lo, pack2(w.x, w.y));
+              hi = mul2(hi, pack2(w.z, w.w));
+            }
+            ffma2(acc[(c + j) / 2], lo, s2);
+            ffma2(acc[(c + j) / 2 + 1], hi, s2);
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * b);
+      }
+      if (S == 1) {
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const float2 f = unpack2(acc[(c + j) / 2]);
+            v[j] = f.x;
+            v[j + 1] = f.y;
+          }
+          store8(p, row, col0 + c, v);
+        }
+      } else {
+        // partial tile -> the ring, which every MMA of this CTA has finished reading (the
+        // last accumulator is complete): [column][row]
+        float *part = reinterpret_cast<float *>(sbase);
+#pragma unroll
+        for (int j = 0; j < C::COLS; j += 2) {
+          const float2 f = unpack2(acc[j / 2]);
+          part[(grp * C::COLS + j) * BP + quad * 32 + lane] = f.x;
+          part[(grp * C::COLS + j + 1) * BP + quad * 32 + lane] = f.y;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  griddep_launch_dependents();
+  if (S > 1) {
+    // CTA `rank` finishes columns [rank * TN / S, (rank + 1) * TN / S): partials in rank order
+    cluster_sync_all();
+    if (warp >= 4) {
+      int tp, tq;
+      tile_coords(first, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      const int quad = warp & 3, grp = (warp - 4) >> 2;
+      const int r = quad * 32 + lane;
+      const int c0 = TN * rank / S, c1 = TN * (rank + 1) / S;
+      const uint32_t part = base + (uint32_t)r * 4;
+      for (int c = c0 + 8 * grp; c < c1; c += 8 * C::GROUPS) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        const int n = min(8, c1 - c);
+        for (int q = 0; q < S; ++q) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) v[j] += ld_cluster1(part + (uint32_t)((c + j) * BP * 4), (uint32_t)q);
+        }
+        const int row = tp * BP + r, col = tq * TN + c;
+        if (n == 8) {
+          store8(p, row, col, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n && row < p.p.extent && col + j < p.q.extent) {
+              const long long at = row * p.d_p + (col + j) * p.d_q;
+              const float y = p.alpha * v[j];
+              store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v[j], p.beta * load_d(p, at)) : y);
+            }
+        }
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another may still read its partial
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// D = beta * D (k == 0 or alpha == 0; 0 when beta == 0, without reading D).
+__global__ void f8_scale_kernel(Params p, int M, int N, long long ldd) {
+  griddep_wait();
+  const long long total = (long long)M * N;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
+       i += (long long)gridDim.x * blockDim.x) {
+    const long long at = i / N * ldd + i % N;
+    store_d(p, at, p.beta != 0.0f ? p.beta * load_d(p, at) : 0.0f);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Host side
+
+struct Plan {
+  bool swap;   // P = op(B)^T
+  int tn, split;
+};
+
+// Estimated time of a plan in units of 64 tensor-pipe cycles: the k blocks of the busiest SM
+// times a block's cost (the larger of the MMA and the copy of its operands), plus a fixed
+// cost for each tile and for a cluster's exchange.
+static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, int sms) {
+  Plan best{false, 128, 1};
+  double best_cost = 1e300;
+  const int tns[5] = {256, 128, 64, 32, 16};
+  for (int swap = 0; swap < 2; ++swap)
+    for (int tn : tns) {
+      const int P = swap ? N : M, Q = swap ? M : N;
+      if ((swap ? a_mn : b_mn) && tn < 128) continue;  // an MN-major Q comes in 128 columns
+      const long long tiles = (long long)ceil_div(P, BP) * ceil_div(Q, tn);
+      for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
+        if (S > 1 && (S > KB || tiles * S > sms)) break;
+        const long long per_sm = (tiles * S + sms - 1) / sms;
+        const double block = std::max(2.0 * tn / 64.0, 2.5);
+        const double cost = per_sm * (block * ((KB + S - 1) / S) + 6.0 + tn / 16.0) +
+                            (S > 1 ? 8.0 : 0.0) + tn / 256.0;
+        if (cost < best_cost) {
+          best_cost = cost;
+          best = Plan{swap != 0, tn, S};
+        }
+      }
+    }
+  return best;
+}
+
+template <int TN, bool QVEC>
+static cudaError_t launch(const CUtensorMap &mp, const CUtensorMap &mq, const Params &p, int grid,
+                          cudaStream_t stream) {
+  return launch_1d(f8_kernel<TN, QVEC>, grid, Cfg<TN>::THREADS, Cfg<TN>::SMEM_BYTES, p.split,
+                   stream, mp, mq, p);
+}
+
+template <int TN>
+static cudaError_t set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(f8_kernel<TN, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<TN>::SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(f8_kernel<TN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<TN>::SMEM_BYTES);
+  return e;
+}
+
+static std::once_flag g_once[64];
+static cudaError_t g_err[64];
+
+static cudaError_t kernel_setup() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(g_once[dev], [dev]() {
+    cudaError_t err = set_attributes<256>();
+    if (err == cudaSuccess) err = set_attributes<128>();
+    if (err == cudaSuccess) err = set_attributes<64>();
+    if (err == cudaSuccess) err = set_attributes<32>();
+    if (err == cudaSuccess) err = set_attributes<16>();
+    g_err[dev] = err;
+  });
+  return g_err[dev];
+}
+
+// Tensor map of one operand: `extent` rows (columns for Q) by K, k contiguous or not.
+static bool side_map(CUtensorMap *map, const void *ptr, int extent, int K, int ld, bool mn_major,
+                     int box_extent) {
+  return mn_major ? encode_map_2d_narrow(map, ptr, 1, K, extent, ld, BK)
+                  : encode_map_2d_narrow(map, ptr, 1, extent, K, ld, box_extent);
+}
+
+}  // namespace f8
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha, const void *A,
+                       int a_format, int lda, const float *a_scale, int a_rows,
+                       long long a_scale_mn, long long a_scale_k, const void *B, int b_format,
+                       int ldb, const float *b_scale, int b_cols, long long b_scale_mn,
+                       long long b_scale_k, float beta, void *D, int d_type, int ldd,
+                       cudaStream_t stream) {
+  const bool read = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+  const auto bad_ptr = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
+  if (transa != 0 && transa != 1) return -1;
+  if (transb != 0 && transb != 1) return -2;
+  if (M < 0) return -3;
+  if (N < 0) return -4;
+  if (K < 0) return -5;
+  if (read && (A == nullptr || bad_ptr(A))) return -7;
+  if (a_format != F8_E4M3 && a_format != F8_E5M2) return -8;
+  if (lda < std::max(1, transa ? M : K) || lda % 16 != 0) return -9;
+  if (read && a_scale == nullptr) return -10;
+  if (a_rows != 1 && a_rows != 128) return -11;
+  if (a_scale_mn < 0) return -12;
+  if (a_scale_k < 0) return -13;
+  if (read && (B == nullptr || bad_ptr(B))) return -14;
+  if (b_format != F8_E4M3 && b_format != F8_E5M2) return -15;
+  if (ldb < std::max(1, transb ? K : N) || ldb % 16 != 0) return -16;
+  if (read && b_scale == nullptr) return -17;
+  if (b_cols != 1 && b_cols != 128) return -18;
+  if (b_scale_mn < 0) return -19;
+  if (b_scale_k < 0) return -20;
+  if (M > 0 && N > 0 && D == nullptr) return -22;
+  if (d_type != F8_D_F32 && d_type != F8_D_BF16 && d_type != F8_D_F16) return -23;
+  if (ldd < std::max(1, N)) return -24;
+  if (D != nullptr && reinterpret_cast<uintptr_t>(D) % (d_type == F8_D_F32 ? 4 : 2) != 0)
+    return -22;
+  if (M == 0 || N == 0) return 0;
+
+  int sms = 0;
+  cudaError_t e = device_setup(&sms);
+  if (e == cudaSuccess) e = f8::kernel_setup();
+  if (e != cudaSuccess) return (int)e;
+
+  f8::Params p{};
+  p.alpha = alpha;
+  p.beta = beta;
+  p.D = D;
+  p.d_type = d_type;
+  if (!read) {
+    if (beta == 1.0f) return 0;
+    const long long blocks = std::min<long long>(((long long)M * N + 255) / 256, 8LL * sms);
+    return (int)launch_1d(f8::f8_scale_kernel, (int)blocks, 256, 0, 1, stream, p, M, N,
+                          (long long)ldd);
+  }
+  p.KB = ceil_div(K, f8::BK);
+  const f8::Plan pl = f8::make_plan(M, N, p.KB, transa == 1, transb == 0, sms);
+  const f8::Side sa{M, transa == 1, a_scale, a_rows == 128 ? 7 : 0, a_scale_mn, a_scale_k};
+  const f8::Side sb{N, transb == 0, b_scale, b_cols == 128 ? 7 : 0, b_scale_mn, b_scale_k};
+  p.p = pl.swap ? sb : sa;
+  p.q = pl.swap ? sa : sb;
+  p.d_p = pl.swap ? 1 : ldd;
+  p.d_q = pl.swap ? ldd : 1;
+  const int size = d_type == F8_D_F32 ? 4 : 2;
+  p.vec = !bad_ptr(D) && (long long)ldd * size % 16 == 0;
+  const long long tiles_p = ceil_div(p.p.extent, f8::BP), tiles_q = ceil_div(p.q.extent, pl.tn);
+  if (tiles_p * tiles_q > 0x7fffffffLL / f8::MAX_CLUSTER) return (int)cudaErrorInvalidConfiguration;
+  p.tiles_p = (int)tiles_p;
+  p.tiles_q = (int)tiles_q;
+  p.group_p = (int)std::min<long long>(16, tiles_p);
+  p.split = pl.split;
+  const uint32_t fp = pl.swap ? b_format : a_format, fq = pl.swap ? a_format : b_format;
+  // instruction descriptor: D in FP32 (bits 4-5 = 1), formats of P and Q (0 = e4m3, 1 = e5m2;
+  // bits 7-9, 10-12), MN-major P and Q (bits 15, 16), N / 8 (bits 17-22), M / 16 (24-28)
+  p.idesc = (1u << 4) | (fp << 7) | (fq << 10) | ((uint32_t)p.p.mn_major << 15) |
+            ((uint32_t)p.q.mn_major << 16) | ((uint32_t)(pl.tn >> 3) << 17) |
+            ((uint32_t)(f8::BP >> 4) << 24);
+
+  CUtensorMap mp, mq;
+  if (!f8::side_map(&mp, pl.swap ? B : A, p.p.extent, K, pl.swap ? ldb : lda, p.p.mn_major,
+                    f8::BP) ||
+      !f8::side_map(&mq, pl.swap ? A : B, p.q.extent, K, pl.swap ? lda : ldb, p.q.mn_major,
+                    pl.tn))
+    return (int)cudaErrorInvalidValue;
+  const int grid = (int)(p.split > 1 ? tiles_p * tiles_q * p.split
+                                     : std::min<long long>(tiles_p * tiles_q, sms));
+  const bool vec = p.q.shift == 0;
+  switch (pl.tn) {
+    case 256: return (int)(vec ? f8::launch<256, true>(mp, mq, p, grid, stream)
+                               : f8::launch<256, false>(mp, mq, p, grid, stream));
+    case 128: return (int)(vec ? f8::launch<128, true>(mp, mq, p, grid, stream)
+                               : f8::launch<128, false>(mp, mq, p, grid, stream));
+    case 64: return (int)(vec ? f8::launch<64, true>(mp, mq, p, grid, stream)
+                              : f8::launch<64, false>(mp, mq, p, grid, stream));
+    case 32: return (int)(vec ? f8::launch<32, true>(mp, mq, p, grid, stream)
+                              : f8::launch<32, false>(mp, mq, p, grid, stream));
+    default: return (int)(vec ? f8::launch<16, true>(mp, mq, p, grid, stream)
+                              : f8::launch<16, false>(mp, mq, p, grid, stream));
+  }
+}
+
+extern "C" int f8_gemm_status(int *status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, f8::g_f8_status, sizeof(int));
+  if (e != cudaSuccess) return (int)e;
+  const int zero = 0;
+  e = cudaMemcpyToSymbol(f8::g_f8_status, &zero, sizeof(int));
+  if (status) *status = v;
+  return (int)e;
+}

@@ -1,0 +1,147 @@
+// What the tensor-core operators (8-bit product, orthogonalisation) share: PTX wrappers of
+// the 5th-generation tensor cores (tcgen05, TMEM) and of thread-block clusters, and shared
+// memory descriptors of the operand layouts that TMA writes.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sgemm_ffma.cuh"
+#include "sgemm_ptx.cuh"
+
+namespace sgemm {
+namespace tcx {
+
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(slot),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// Arrive on `bar` once every tcgen05.mma this thread issued so far has completed.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= P[smem] * Q[smem]^T on 8-bit floating-point operands, K = 32.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t pdesc, uint64_t qdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= P[smem] * Q[smem]^T on fp16 operands, K = 16.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t pdesc, uint64_t qdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 (16) consecutive FP32 accumulator columns of this thread's TMEM lane; tmem_wait_ld()
+// makes them readable.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%32];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+        "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+
+// Shared-memory matrix descriptor of an operand that TMA wrote with the 128-byte swizzle
+// from 128-byte-wide boxes (descriptor version 1 in bits 46-47, swizzle mode 2 in 61-63).
+//  * K-major (a row of the box is 128 bytes of k for one row of the operand): 8-row groups
+//    are 1024 bytes apart (stride offset); the leading offset is not used. The next K step
+//    of 32 bytes adds 32 to the start address.
+//  * MN-major (a row of the box is 128 bytes along the operand's rows, for one k): 8-k groups
+//    are 1024 bytes apart (stride offset), and the next 128 bytes of rows are `lead` bytes
+//    further (leading offset). The next K step of n adds 128 n bytes to the start address.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lead) {
+  uint64_t d = (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Barrier among `threads` threads of the CTA (id 1 .. 15; 0 is __syncthreads).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster1(uint32_t local, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n"
+      ".reg .u32 a;\n"
+      "mapa.shared::cluster.u32 a, %1, %2;\n"
+      "ld.shared::cluster.f32 %0, [a];\n"
+      "}\n"
+      : "=f"(v)
+      : "r"(local), "r"(rank)
+      : "memory");
+  return v;
+}
+
+}  // namespace tcx
+
+// Tensor map of a rows x cols row-major matrix of 1- or 2-byte elements (row stride ld
+// elements, a multiple of 16 bytes; ptr 16-byte aligned) in boxes of 128 bytes x box_rows,
+// 128-byte swizzle; elements out of range read as zero. False if the driver rejects it.
+bool encode_map_2d_narrow(CUtensorMap *map, const void *ptr, int elem_bytes, long long rows,
+                          long long cols, long long ld, int box_rows);
+
+}  // namespace sgemm

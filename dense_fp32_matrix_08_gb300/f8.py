@@ -1,0 +1,175 @@
+"""8-bit block-scaled products and their quantiser (include/f8_gemm.h).
+
+A quantised matrix is a pair (q, scale): q in torch.float8_e4m3fn or torch.float8_e5m2 and FP32
+scales, one for each block of 1 x 128, 128 x 1 or 128 x 128 elements of q, so that element (i, j)
+stands for q[i, j] * scale[i // block_rows, j // block_cols]. `scale` has one entry for each
+block; its shape tells the block shape.
+
+For a linear layer y = x W^T:
+    forward          x (1, 128), W (128, 128):   f8_matmul(xq, xs, wq, ws, transb=True)
+    input gradient   dy (1, 128), W (128, 128):  f8_matmul(dyq, dys, wq, ws)
+    weight gradient  dy, x (128, 1):             f8_matmul(dyc, dycs, xc, xcs, transa=True)
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import SgemmError, _stream, lib
+
+__all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
+
+# Every symbol include/f8_gemm.h declares.
+F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_gemm_status")
+
+_FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_BLOCKS = ((1, 128), (128, 1), (128, 128))
+
+_i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
+lib.f8_quantize.argtypes = ([_i, _i, _vp, _i, _i, _i, _i, _i, _i] + [_vp, _i, _vp, _ll, _ll] * 2 +
+                            [_vp])
+lib.f8_gemm.argtypes = ([_i, _i, _i, _i, _i, _f] + [_vp, _i, _i, _vp, _i, _ll, _ll] * 2 +
+                        [_f, _vp, _i, _i, _vp])
+lib.f8_gemm_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
+for _name in F8_EXPORTED:
+    getattr(lib, _name).restype = ctypes.c_int
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) >> 7
+
+
+def _rows(name, t):
+    """Row stride of a 2-D CUDA tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must live on a CUDA device")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return max(ld, cols, 1) if rows > 1 else max(cols, 1)
+
+
+def _new_q(rows, cols, dtype, device):
+    # rows of a multiple of 16 bytes, as the product's copies need them
+    return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=dtype,
+                               device=device)
+
+
+def _quantize(x, block, both, dtype, pow2, stream):
+    if dtype not in _FORMAT:
+        raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+    if x.dtype not in _TYPE:
+        raise TypeError("x must be float32, bfloat16 or float16")
+    ldx = _rows("x", x)
+    rows, cols = x.shape
+    device = x.device
+    br, bc = block
+    q = _new_q(rows, cols, dtype, device)
+    if br == 1:
+        # neighbouring rows' scales of one block are neighbours, as the product reads them
+        s = torch.empty_strided((rows, _blocks(cols)), (1, max(rows, 1)), dtype=torch.float32,
+                                device=device)
+    else:
+        s = torch.empty((_blocks(rows), cols if bc == 1 else _blocks(cols)),
+                        dtype=torch.float32, device=device)
+    ss = s.stride()
+    qc = sc = None
+    second = (None, 0, None, 0, 0)
+    if both:
+        qc = _new_q(rows, cols, dtype, device)
+        sc = torch.empty((_blocks(rows), cols), dtype=torch.float32, device=device)
+        second = (qc.data_ptr() or None, max(qc.stride(0), 1), sc.data_ptr() or None,
+                  sc.stride(0), 1)
+    rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, _TYPE[x.dtype], ldx, br, bc,
+                         _FORMAT[dtype], int(pow2), q.data_ptr() or None, max(q.stride(0), 1),
+                         s.data_ptr() or None, ss[0], ss[1], *second, _stream(stream))
+    if rc != 0:
+        raise SgemmError(rc, "f8_quantize")
+    return (q, s, qc, sc) if both else (q, s)
+
+
+def f8_quantize(x, block=(1, 128), *, dtype=torch.float8_e4m3fn, pow2=False, stream=None):
+    """Quantise a 2-D CUDA tensor (float32, bfloat16, float16) by blocks of (1, 128), (128, 1) or
+    (128, 128): returns (q, scale). scale = max(amax / largest, 2^-126) of each block, with pow2
+    the least power of two not below it; q = x / scale rounded to dtype."""
+    if tuple(block) not in _BLOCKS:
+        raise ValueError(f"block must be one of {_BLOCKS}")
+    return _quantize(x, tuple(block), False, dtype, pow2, stream)
+
+
+def f8_quantize_pair(x, *, dtype=torch.float8_e4m3fn, pow2=False, stream=None):
+    """f8_quantize by (1, 128) and by (128, 1) blocks from one read of x: returns
+    (q_rows, scale_rows, q_columns, scale_columns)."""
+    return _quantize(x, (1, 128), True, dtype, pow2, stream)
+
+
+def _operand(name, q, scale, k_dim):
+    """(format, ld, group, stride along the other dimension, stride along k) of an operand."""
+    fmt = _FORMAT.get(q.dtype)
+    if fmt is None:
+        raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.float8_e5m2")
+    ld = _rows(name, q)
+    if q.shape[0] <= 1:
+        ld = (ld + 15) // 16 * 16
+    if scale.dtype != torch.float32 or scale.dim() != 2 or scale.device != q.device:
+        raise TypeError(f"{name}'s scale must be a 2-D float32 tensor on its device")
+    have, shape, st = scale.shape, q.shape, scale.stride()
+    k, mn = shape[k_dim], shape[1 - k_dim]
+    if have[k_dim] != (k + 127) >> 7:
+        raise ValueError(f"{name}'s scale needs one entry for each 128 along the contraction")
+    if have[1 - k_dim] == mn:
+        return fmt, ld, 1, st[1 - k_dim], st[k_dim]
+    if have[1 - k_dim] == (mn + 127) >> 7:
+        return fmt, ld, 128, st[1 - k_dim], st[k_dim]
+    raise ValueError(f"{name}'s scale does not fit its shape")
+
+
+def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, beta=0.0,
+              out=None, out_dtype=None, stream=None):
+    """out = alpha * op(a) @ op(b) + beta * out on quantised operands (op: transposed if the
+    flag is set). `out` is float32, bfloat16 or float16 with unit column stride; without one a
+    new tensor of out_dtype (bfloat16 unless given) is returned. Each operand's scales run along
+    the contraction in blocks of 128. Raises SgemmError on a nonzero status."""
+    fa, lda, ga, amn, ak = _operand("a", a, a_scale, 0 if transa else 1)
+    fb, ldb, gb, bmn, bk = _operand("b", b, b_scale, 1 if transb else 0)
+    M, K = a.shape
+    if transa:
+        M, K = K, M
+    K2, N = b.shape
+    if transb:
+        K2, N = N, K2
+    if K2 != K:
+        raise ValueError("shape mismatch")
+    if a.device != b.device:
+        raise ValueError("operands on different devices")
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta needs an out to scale")
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out has another type than out_dtype")
+    if out.dtype not in _TYPE:
+        raise TypeError("out must be float32, bfloat16 or float16")
+    if out.device != a.device:
+        raise ValueError("out is on another device")
+    if tuple(out.shape) != (M, N):
+        raise ValueError("shape mismatch")
+    rc = lib.f8_gemm(transa, transb, M, N, K, alpha, a.data_ptr() or None, fa, lda,
+                     a_scale.data_ptr() or None, ga, amn, ak, b.data_ptr() or None, fb, ldb,
+                     b_scale.data_ptr() or None, gb, bmn, bk, beta, out.data_ptr() or None,
+                     _TYPE[out.dtype], _rows("out", out), _stream(stream))
+    if rc != 0:
+        raise SgemmError(rc, "f8_gemm")
+    return out
+
+
+def f8_gemm_status() -> tuple[int, int]:
+    """(call status, device status word of f8_gemm); reading clears the word."""
+    v = ctypes.c_int(0)
+    rc = lib.f8_gemm_status(ctypes.byref(v))
+    return rc, v.value
