@@ -359,8 +359,13 @@ def sgemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     return C
 
 
-# The 8-bit block-scaled operators (they need torch, unlike the bindings above).
+# The tensor-core operators of a linear layer's training step and of its serving: 8-bit
+# block-scaled products and the orthogonalised update (they need torch, unlike the bindings above).
 from .f8 import (F8_EXPORTED, f8_gemm_status, f8_matmul, f8_quantize,  # noqa: E402
                  f8_quantize_pair)
+from .newton_schulz import (NS_EXPORTED, ns_orthogonalize_status,  # noqa: E402
+                            ns_orthogonalize_workspace_size, orthogonalize)
 
-__all__ += ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
+__all__ += ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED",
+            "orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
+            "NS_EXPORTED"]

@@ -1,0 +1,83 @@
+"""Orthogonalising updates by Newton-Schulz products (include/orthogonalize.h)."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import SgemmError, _stream, lib
+
+__all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
+           "NS_EXPORTED"]
+
+# Every symbol include/orthogonalize.h declares.
+NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status")
+
+_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+_i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
+lib.ns_orthogonalize.argtypes = [_i, _i, _i, _vp, _i, _i, _ll, _i, ctypes.POINTER(_f), _f, _f, _f,
+                                 _vp, _i, _i, _ll, _vp]
+lib.ns_orthogonalize_workspace_size.argtypes = [_i, _i, _i, ctypes.POINTER(ctypes.c_size_t)]
+lib.ns_orthogonalize_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
+for _name in NS_EXPORTED:
+    getattr(lib, _name).restype = ctypes.c_int
+
+
+def _matrices(name, t):
+    """(type, row stride, matrix stride) of a 2-D or 3-D CUDA tensor with unit column stride."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be 2-D or 3-D")
+    if t.dtype not in _TYPE:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must live on a CUDA device")
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = max(t.stride(-2), cols, 1) if rows > 1 else max(cols, 1)
+    return _TYPE[t.dtype], ld, t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else rows * ld
+
+
+def orthogonalize(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, alpha=1.0,
+                  beta=0.0, out=None, out_dtype=None, stream=None):
+    """out = alpha * X + beta * out, X the result of `steps` Newton-Schulz steps
+    X <- a X + (b S + c S^2) X, S = X X^T, from X = g / (|g|_F + eps); coefficients = (a, b, c).
+    g is a matrix or a batch of them (float32, bfloat16, float16). Without `out` a new tensor of
+    out_dtype (g's type unless given) is returned. With out = the weight, alpha = -rate and
+    beta = 1 - rate * decay it is the whole update. Raises SgemmError on a nonzero status."""
+    gt, ldg, gs = _matrices("g", g)
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta needs an out to scale")
+        out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out has another type than out_dtype")
+    ot, ldo, os_ = _matrices("out", out)
+    if out.shape != g.shape:
+        raise ValueError("shape mismatch")
+    if out.device != g.device:
+        raise ValueError("out is on another device")
+    batch = g.shape[0] if g.dim() == 3 else 1
+    rows, cols = g.shape[-2:]
+    a, b, c = coefficients
+    rc = lib.ns_orthogonalize(batch, rows, cols, g.data_ptr() or None, gt, ldg, gs, steps,
+                              (_f * 3)(a, b, c), eps, alpha, beta, out.data_ptr() or None, ot, ldo,
+                              os_, _stream(stream))
+    if rc != 0:
+        raise SgemmError(rc, "ns_orthogonalize")
+    return out
+
+
+def ns_orthogonalize_workspace_size(batch, rows, cols) -> tuple[int, int]:
+    """(status, bytes)."""
+    n = ctypes.c_size_t(0)
+    rc = lib.ns_orthogonalize_workspace_size(batch, rows, cols, ctypes.byref(n))
+    return rc, n.value
+
+
+def ns_orthogonalize_status() -> tuple[int, int]:
+    """(call status, device status word of ns_orthogonalize); reading clears the word."""
+    v = ctypes.c_int(0)
+    rc = lib.ns_orthogonalize_status(ctypes.byref(v))
+    return rc, v.value
