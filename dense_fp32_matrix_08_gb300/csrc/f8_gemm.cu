@@ -37,6 +37,9 @@ constexpr int BP = 128;                  // rows of P per tile
 constexpr int BK = 128;                  // k per block = per pipeline stage
 constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
+constexpr int TURN = 16;                 // columns that a warp turns at a time for its stores
+constexpr int TURN_PITCH = TURN + 1;
+constexpr int PART_PITCH = BP + 1;       // column pitch of a cluster's partial tiles (floats)
 
 template <int TN_>
 struct Cfg {
@@ -52,11 +55,13 @@ struct Cfg {
   static constexpr int ACC_COLS = TN < 32 ? 32 : TN;
   static constexpr int TMEM_COLS = NBUF * ACC_COLS;
   static constexpr int SQ_BYTES = 2 * TN * 4;       // Q scales of two k blocks
+  static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH * 4;
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * NBUF) + 16;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SQ_BYTES + BAR_BYTES;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * STAGE_BYTES + SQ_BYTES + TURN_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
-  static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
+  static_assert(PART_PITCH * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
 };
 
 struct Side {          // one operand as the kernel sees it
@@ -145,6 +150,12 @@ __device__ __forceinline__ void store8(const Params &p, int row, int col, float 
     if (j < n) store_d(p, at + j * p.d_q, v[j]);
 }
 
+__device__ __forceinline__ void store1(const Params &p, int row, int col, float v) {
+  if (row >= p.p.extent || col >= p.q.extent) return;
+  const long long at = row * p.d_p + col * p.d_q;
+  store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v, p.beta * load_d(p, at)) : p.alpha * v);
+}
+
 // Warp 0 (one lane): TMA producer. Warp 1 (one lane): MMA issuer. Warps 4 ..: epilogue, group g
 // of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
 // rows) 32 (w % 4) .. + 31, one row per thread.
@@ -162,7 +173,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);
   float *sq_buf = reinterpret_cast<float *>(sbase + C::STAGES * C::STAGE_BYTES);
-  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SQ_BYTES;
+  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SQ_BYTES + C::TURN_BYTES;
   const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
   const uint32_t acc_empty = acc_full + 8 * C::NBUF;
   const uint32_t tmem_slot = acc_empty + 8 * C::NBUF;
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + 8 * b);
       }
-      if (S == 1) {
+      if (S == 1 && (p.vec || p.d_q != 1)) {
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 8) {
           float v[8];
@@ -341,6 +352,25 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
           }
           store8(p, row, col0 + c, v);
         }
+      } else if (S == 1) {
+        // rows of D that allow no wide stores: turned in shared memory, so that neighbouring
+        // lanes store neighbouring elements
+        float *turn = sq_buf + 2 * TN + (warp - 4) * 32 * TURN_PITCH;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += TURN) {
+#pragma unroll
+          for (int j = 0; j < TURN; j += 2) {
+            const float2 f = unpack2(acc[(c + j) / 2]);
+            turn[lane * TURN_PITCH + j] = f.x;
+            turn[lane * TURN_PITCH + j + 1] = f.y;
+          }
+          __syncwarp();
+#pragma unroll 8
+          for (int r = lane / TURN; r < 32; r += 32 / TURN)
+            store1(p, tp * BP + quad * 32 + r, col0 + c + lane % TURN,
+                   turn[r * TURN_PITCH + lane % TURN]);
+          __syncwarp();
+        }
       } else {
         // partial tile -> the ring, which every MMA of this CTA has finished reading (the
         // last accumulator is complete): [column][row]
@@ -348,8 +378,8 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < C::COLS; j += 2) {
           const float2 f = unpack2(acc[j / 2]);
-          part[(grp * C::COLS + j) * BP + quad * 32 + lane] = f.x;
-          part[(grp * C::COLS + j + 1) * BP + quad * 32 + lane] = f.y;
+          part[(grp * C::COLS + j) * PART_PITCH + quad * 32 + lane] = f.x;
+          part[(grp * C::COLS + j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
         }
       }
     }
@@ -363,30 +393,26 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
       int tp, tq;
       tile_coords(first, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
       const int quad = warp & 3, grp = (warp - 4) >> 2;
-      const int r = quad * 32 + lane;
       const int c0 = TN * rank / S, c1 = TN * (rank + 1) / S;
-      const uint32_t part = base + (uint32_t)r * 4;
-      for (int c = c0 + 8 * grp; c < c1; c += 8 * C::GROUPS) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        const int n = min(8, c1 - c);
-        for (int q = 0; q < S; ++q) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n) v[j] += ld_cluster1(part + (uint32_t)((c + j) * BP * 4), (uint32_t)q);
+      if (p.d_q == 1) {
+        // neighbouring lanes take neighbouring columns, as D stores them
+        for (int c = c0 + lane; c < c1; c += 32) {
+          const uint32_t part = base + (uint32_t)(c * PART_PITCH) * 4;
+#pragma unroll 4
+          for (int r = warp - 4; r < BP; r += C::EPI_WARPS) {
+            float v = 0.0f;
+            for (int q = 0; q < S; ++q) v += ld_cluster1(part + (uint32_t)r * 4, (uint32_t)q);
+            store1(p, tp * BP + r, tq * TN + c, v);
+          }
         }
-        const int row = tp * BP + r, col = tq * TN + c;
-        if (n == 8) {
-          store8(p, row, col, v);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n && row < p.p.extent && col + j < p.q.extent) {
-              const long long at = row * p.d_p + (col + j) * p.d_q;
-              const float y = p.alpha * v[j];
-              store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v[j], p.beta * load_d(p, at)) : y);
-            }
+      } else {
+        const int r = quad * 32 + lane;
+#pragma unroll 4
+        for (int c = c0 + grp; c < c1; c += C::GROUPS) {
+          const uint32_t part = base + (uint32_t)(c * PART_PITCH + r) * 4;
+          float v = 0.0f;
+          for (int q = 0; q < S; ++q) v += ld_cluster1(part, (uint32_t)q);
+          store1(p, tp * BP + r, tq * TN + c, v);
         }
       }
     }

@@ -2,14 +2,21 @@
 //   s_b = max(max |x| / F, 2^-126), q = round(x / s_b)
 // with blocks of 1 x 128, 128 x 1, 128 x 128, or the first two at once from one read.
 //
-// Bound by HBM: sizeof(x) bytes in and one byte (two for the pair) out for each element.
-//  * rows_kernel (1 x 128): 16 lanes hold one block, 8 neighbouring elements each, so a block's
-//    maximum is four shuffles; a warp holds U blocks per half, all reads issued first.
-//  * tile_kernel (the other layouts): a CTA of 256 threads holds a 128 x 128 tile in registers,
-//    64 elements per thread (8 rows of 8 neighbouring columns); row maxima are shuffles, column
-//    maxima and the tile's maximum meet in shared memory.
-// Maxima are taken on the bits of |x| as integers, whose order is that of the numbers with
-// infinity and then NaN on top, so that neither is lost.
+// Bound by HBM: sizeof(x) bytes in and one byte (two for the pair) out for each element. What
+// stands in the way is arithmetic, so there is little of it per element:
+//  * x stays packed in registers as it was loaded, 16 neighbouring elements per thread, which
+//    spreads the work on a scale over many of them. Maxima of magnitudes are one instruction for
+//    two 16-bit numbers; NaN wins over everything, so that it is not lost.
+//  * No division per element. With r = 1 / s to 2^-23 the product y = x r is within 2^-22 of
+//    x / s. Let m be y rounded to 5 significant bits: every tie of the 8-bit formats is such a
+//    number. The remainder x - m s is exact in one FMA, and m + (x - m s) r is x / s corrected by
+//    one step of Markstein's remainder iteration: exact next to a tie, where m is the tie and the
+//    remainder tiny, and within an FP32 rounding elsewhere, where nothing depends on it. So q is
+//    what the correctly rounded FP32 quotient gives, for three packed FP32 instructions per two
+//    elements and no branch.
+//  * rows_kernel (1 x 128): 8 lanes hold one block, so a block's maximum is three shuffles.
+//  * tile_kernel (the other layouts): a CTA holds a 128 x 128 tile in registers, 32 of them per
+//    thread; row maxima are shuffles, column maxima and the tile's maximum meet in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,7 +37,7 @@ struct Result {
   long long ldq;
   float *s;
   long long s_row, s_col;
-  int vec;             // 8-byte stores to q are aligned
+  int vec;             // 16-byte stores to q are aligned
 };
 
 struct QuantParams {
@@ -42,132 +49,199 @@ struct QuantParams {
   Result a, c;         // a: rows or the only result; c: columns
 };
 
-// Eight neighbouring elements of row r from column c, as FP32 (0 out of range).
+// Types of x: 16 neighbouring elements are W words. larger(): the larger magnitudes of two words
+// (with either sign; NaN over all); top(): the largest magnitude in a word, and value(): number n
+// of a word, as FP32.
+struct F32 {
+  static constexpr int W = 16;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+  }
+  static __device__ __forceinline__ float top(uint32_t w) { return fabsf(__uint_as_float(w)); }
+  static __device__ __forceinline__ float value(uint32_t w, int) { return __uint_as_float(w); }
+};
+struct BF16 {
+  static constexpr int W = 8;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+  }
+  static __device__ __forceinline__ float top(uint32_t w) {
+    w &= 0x7fff7fffu;
+    return __uint_as_float(max(w & 0xffff0000u, w << 16));
+  }
+  static __device__ __forceinline__ float value(uint32_t w, int n) {
+    return __uint_as_float(n ? w & 0xffff0000u : w << 16);
+  }
+};
+struct F16 {
+  static constexpr int W = 8;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+  }
+  static __device__ __forceinline__ float top(uint32_t w) {
+    w &= 0x7fff7fffu;
+    return __half2float(__ushort_as_half((unsigned short)max(w >> 16, w & 0xffffu)));
+  }
+  static __device__ __forceinline__ float value(uint32_t w, int n) {
+    return __half2float(__ushort_as_half((unsigned short)(n ? w >> 16 : w & 0xffffu)));
+  }
+};
+
 template <class T>
-__device__ __forceinline__ void load8(const QuantParams &p, int r, int c, float (&v)[8]) {
-  const T *src = reinterpret_cast<const T *>(p.x) + r * p.ldx + c;
-  if (r < p.rows && p.vec && c + 8 <= p.cols) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = __ldcs(reinterpret_cast<const float4 *>(src));
-      const float4 b = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(src));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Sixteen {
+  uint32_t w[T::W];
+};
+
+// Element j (0 .. 15).
+template <class T>
+__device__ __forceinline__ float at(const Sixteen<T> &v, int j) {
+  return T::W == 16 ? T::value(v.w[j], 0) : T::value(v.w[j / 2], j & 1);
+}
+
+// n of 16 neighbouring elements from src (0 for the others).
+template <class T>
+__device__ __forceinline__ void load16(const char *src, bool vec, int n, Sixteen<T> &v) {
+  if (vec && n >= 16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 f;
-        if constexpr (sizeof(T) == 2 && T::is_bf16)
-          f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-        else
-          f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
+    for (int i = 0; i < T::W; i += 4) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(src) + i / 4);
+      v.w[i] = u.x, v.w[i + 1] = u.y, v.w[i + 2] = u.z, v.w[i + 3] = u.w;
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = 0.0f;
-    if (r < p.rows && c + j < p.cols) v[j] = src[j].value();
-  }
+  for (int i = 0; i < T::W; ++i) v.w[i] = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < n) {
+      if (T::W == 16)
+        v.w[j % T::W] = reinterpret_cast<const uint32_t *>(src)[j];
+      else
+        v.w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(src)[j] << (16 * (j & 1));
+    }
 }
 
-struct F32 {
-  float f;
-  static constexpr bool is_bf16 = false;
-  __device__ float value() const { return f; }
-};
-struct BF16 {
-  __nv_bfloat16 f;
-  static constexpr bool is_bf16 = true;
-  __device__ float value() const { return __bfloat162float(f); }
-};
-struct F16 {
-  __half f;
-  static constexpr bool is_bf16 = false;
-  __device__ float value() const { return __half2float(f); }
-};
-
-__device__ __forceinline__ uint32_t bits_abs(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
-  uint32_t m = 0;
+template <class T>
+__device__ __forceinline__ uint32_t max16(const Sixteen<T> &v) {
+  uint32_t m = v.w[0];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, bits_abs(v[j]));
+  for (int i = 1; i < T::W; ++i) m = T::larger(m, v.w[i]);
   return m;
 }
 
-__device__ __forceinline__ float scale_of(uint32_t amax, int format, int pow2) {
-  const uint32_t least = 0x00800000u;  // 2^-126
-  uint32_t s = __float_as_uint(__fdiv_rn(__uint_as_float(amax), format ? 57344.0f : 448.0f));
-  s = max(s, least);                   // (positive, infinite or NaN: ordered as integers)
-  if (pow2 && s < 0x7f800000u) s = (s + 0x007fffffu) & 0xff800000u;
-  return __uint_as_float(s);
+// A block's scale, and what its elements are multiplied with: r = 1 / s and -s.
+struct Scale {
+  float s, r, minus;
+};
+
+__device__ __forceinline__ Scale scale_of(float amax, int format, int pow2) {
+  const uint32_t least = 0x00800000u, inf = 0x7f800000u;  // 2^-126
+  uint32_t b = __float_as_uint(__fdiv_rn(amax, format ? 57344.0f : 448.0f));
+  b = max(b, least);                   // (positive, infinite or NaN: ordered as integers)
+  if (pow2 && b < inf) b = (b + 0x007fffffu) & 0xff800000u;
+  Scale o;
+  o.s = __uint_as_float(b);
+  if (pow2 && b < inf)
+    o.r = __uint_as_float(0x7f000000u - b);  // (an amax is under 2^128: b < 2^120)
+  else
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(o.r) : "f"(o.s));
+  // an infinite or NaN scale takes no part in the remainder: r = 0 or NaN decides alone
+  o.minus = b < inf ? -o.s : 0.0f;
+  return o;
 }
 
 // Two numbers to two bytes, nearest with ties to even, limited to the largest finite number;
 // NaN stays NaN. The first number goes to the low byte.
-__device__ __forceinline__ uint32_t round2(float lo, float hi, int format) {
+template <int FORMAT>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
   uint16_t r;
-  if (format)
+  if (FORMAT)
     asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
   else
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-__device__ __forceinline__ void store8(const Result &o, const QuantParams &p, int r, int c,
-                                       const float (&y)[8]) {
-  if (r >= p.rows || c >= p.cols) return;
-  uint2 w;
-  w.x = round2(y[0], y[1], p.format) | round2(y[2], y[3], p.format) << 16;
-  w.y = round2(y[4], y[5], p.format) | round2(y[6], y[7], p.format) << 16;
-  uint8_t *dst = o.q + r * o.ldq + c;
-  if (o.vec && c + 8 <= p.cols) {
-    *reinterpret_cast<uint2 *>(dst) = w;
+// q of two elements; r, minus: both elements' factors.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t quantize2(float x0, float x1, unsigned long long r,
+                                              unsigned long long minus) {
+  const unsigned long long x = pack2(x0, x1);
+  unsigned long long y, rest;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(y) : "l"(x), "l"(r));
+  const float2 v = unpack2(y);
+  const unsigned long long m =
+      pack2(__uint_as_float((__float_as_uint(v.x) + 0x40000u) & 0xfff80000u),
+            __uint_as_float((__float_as_uint(v.y) + 0x40000u) & 0xfff80000u));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(rest) : "l"(m), "l"(minus), "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(y) : "l"(rest), "l"(r), "l"(m));
+  const float2 t = unpack2(y);
+  return round2<FORMAT>(t.x, t.y);
+}
+
+template <class T, int FORMAT>
+__device__ __forceinline__ uint4 quantize16(const Sixteen<T> &v, const Scale &s) {
+  uint32_t w[4];
+  const unsigned long long r = pack2(s.r, s.r), minus = pack2(s.minus, s.minus);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = quantize2<FORMAT>(at<T>(v, 4 * i), at<T>(v, 4 * i + 1), r, minus) |
+           quantize2<FORMAT>(at<T>(v, 4 * i + 2), at<T>(v, 4 * i + 3), r, minus) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The first n of 16 bytes.
+__device__ __forceinline__ void store16(uint8_t *dst, bool vec, int n, const uint4 &w) {
+  if (vec && n >= 16) {
+    *reinterpret_cast<uint4 *>(dst) = w;
     return;
   }
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < p.cols) dst[j] = (uint8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * j - 32)) & 0xff);
+  for (int j = 0; j < 16; ++j)
+    if (j < n) dst[j] = (uint8_t)(u[j / 4] >> (8 * (j & 3)));
 }
 
-// Maximum over the 16 lanes of a half-warp.
-__device__ __forceinline__ uint32_t half_max(uint32_t m) {
+// Scale of the block that 8 neighbouring lanes hold, from each lane's magnitudes.
+template <class T>
+__device__ __forceinline__ Scale lanes_scale(uint32_t m, int format, int pow2) {
 #pragma unroll
-  for (int d = 1; d < 16; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m;
+  for (int d = 1; d < 8; d *= 2) m = T::larger(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return scale_of(T::top(m), format, pow2);
 }
 
-// 1 x 128 blocks: unit u = row * blocks + block, 2 U units per warp.
-template <class T, int U>
+// 1 x 128 blocks: unit u = row * blocks + block; a warp takes 4 neighbouring units at a time.
+template <class T, int FORMAT>
 __global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
-  const int lane = threadIdx.x & 31, sub = lane & 15, half = lane >> 4;
+  constexpr int size = T::W == 16 ? 4 : 2;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
   const int blocks = (p.cols + 127) / 128;
   const long long units = (long long)p.rows * blocks;
-  const long long warps = (long long)gridDim.x * 8;
-  const long long w0 = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  for (long long u0 = w0 * 2 * U; u0 < units; u0 += warps * 2 * U) {
-    float v[U][8];
-    int r[U], c[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const long long u = u0 + 2 * i + half;
-      r[i] = u < units ? (int)(u / blocks) : p.rows;
-      c[i] = (int)(u % blocks) * 128 + sub * 8;
-      load8<T>(p, r[i], c[i], v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const float s = scale_of(half_max(max8(v[i])), p.format, p.pow2);
-      if (sub == 0 && r[i] < p.rows) p.a.s[r[i] * p.a.s_row + (c[i] >> 7) * p.a.s_col] = s;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
-      store8(p.a, p, r[i], c[i], v[i]);
+  const long long step = (long long)gridDim.x * 8 * 4;
+  const int step_r = (int)(step / blocks), step_b = (int)(step % blocks);
+  long long u = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
+  const long long mine = u + (lane >> 3);
+  int r = (int)(mine / blocks), b = (int)(mine % blocks);
+  for (; u < units; u += step) {
+    const int c = b * 128 + sub * 16;
+    const int n = r < p.rows ? p.cols - c : 0;
+    Sixteen<T> v;
+    load16<T>(reinterpret_cast<const char *>(p.x) + (r * p.ldx + c) * size, p.vec, n, v);
+    const Scale s = lanes_scale<T>(max16<T>(v), FORMAT, p.pow2);
+    if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + b * p.a.s_col] = s.s;
+    store16(p.a.q + r * p.a.ldq + c, p.a.vec, n, quantize16<T, FORMAT>(v, s));
+    r += step_r;
+    b += step_b;
+    if (b >= blocks) {
+      b -= blocks;
+      ++r;
     }
   }
   griddep_launch_dependents();
@@ -175,103 +249,124 @@ __global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
 
 enum { COLS = 0, SQUARE = 1, PAIR = 2 };
 
-// One 128 x 128 tile per CTA: thread (g = tid / 16, sub = tid % 16) holds columns 8 sub .. + 7 of
-// rows g, g + 16, ..., g + 112.
-template <class T, int WHICH>
-__global__ void __launch_bounds__(256) tile_kernel(const QuantParams p, int tiles_c) {
+// One 128 x 128 tile per CTA of 8 G threads: thread (g = tid / 8, sub = tid % 8) holds columns
+// 16 sub .. + 15 of rows g, g + G, ...: 32 registers of x.
+template <class T>
+constexpr int kRowGroups = T::W == 16 ? 64 : 32;
+
+template <class T, int FORMAT, int WHICH>
+__global__ void __launch_bounds__(8 * kRowGroups<T>, T::W == 16 ? 2 : WHICH == PAIR ? 3 : 4)
+    tile_kernel(const QuantParams p, int tiles_c) {
   griddep_wait();
-  __shared__ uint32_t top[8][128];
-  __shared__ float scale[128];
-  const int tid = threadIdx.x, sub = tid & 15, g = tid >> 4, warp = tid >> 5;
+  constexpr int size = T::W == 16 ? 4 : 2;
+  constexpr int G = kRowGroups<T>, WARPS = G / 4, ROWS = 128 / G;
+  __shared__ uint32_t top[WARPS][8 * T::W];
+  __shared__ __align__(16) float col_r[128], col_minus[128];
+  const int tid = threadIdx.x, sub = tid & 7, g = tid >> 3, warp = tid >> 5;
   const int br = blockIdx.x / tiles_c, bc = blockIdx.x % tiles_c;
-  const int r0 = br * 128 + g, c0 = bc * 128 + sub * 8;
-  float v[8][8];
+  const int r0 = br * 128 + g, c0 = bc * 128 + sub * 16;
+  const int n = p.cols - c0;
+  Sixteen<T> v[ROWS];
+  const char *src = reinterpret_cast<const char *>(p.x) + (r0 * p.ldx + c0) * size;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8<T>(p, r0 + 16 * i, c0, v[i]);
+  for (int i = 0; i < ROWS; ++i)
+    load16<T>(src + i * (G * p.ldx * size), p.vec, r0 + G * i < p.rows ? n : 0, v[i]);
 
   if constexpr (WHICH == SQUARE) {
-    uint32_t m = 0;
+    uint32_t m = max16<T>(v[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, max8(v[i]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((tid & 31) == 0) top[0][warp] = m;
+    for (int i = 1; i < ROWS; ++i) m = T::larger(m, max16<T>(v[i]));
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) m = T::larger(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((tid & 31) == 0) top[warp][0] = m;
     __syncthreads();
-    m = top[0][0];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) m = max(m, top[0][w]);
-    const float s = scale_of(m, p.format, p.pow2);
-    if (tid == 0) p.a.s[br * p.a.s_row + bc * p.a.s_col] = s;
+    for (int w = 0; w < WARPS; ++w) m = T::larger(m, top[w][0]);
+    const Scale s = scale_of(T::top(m), FORMAT, p.pow2);
+    if (tid == 0) p.a.s[br * p.a.s_row + bc * p.a.s_col] = s.s;
+    uint8_t *dst = p.a.q + r0 * p.a.ldq + c0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
-      store8(p.a, p, r0 + 16 * i, c0, v[i]);
-    }
+    for (int i = 0; i < ROWS; ++i)
+      store16(dst + i * (G * p.a.ldq), p.a.vec, r0 + G * i < p.rows ? n : 0,
+              quantize16<T, FORMAT>(v[i], s));
   } else {
     const Result &o = WHICH == PAIR ? p.c : p.a;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t m = 0;
+    for (int k = 0; k < T::W; ++k) {
+      uint32_t m = v[0].w[k];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, bits_abs(v[i][j]));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if ((tid & 16) == 0) top[warp][sub * 8 + j] = m;
+      for (int i = 1; i < ROWS; ++i) m = T::larger(m, v[i].w[k]);
+      m = T::larger(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = T::larger(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if ((tid & 31) < 8) top[warp][sub * T::W + k] = m;
     }
     __syncthreads();
-    if (tid < 128) {
-      uint32_t m = top[0][tid];
+    if (tid < 128) {  // column tid of the tile
+      const int word = T::W == 16 ? tid : tid / 2;
+      uint32_t m = top[0][word];
 #pragma unroll
-      for (int w = 1; w < 8; ++w) m = max(m, top[w][tid]);
-      const float s = scale_of(m, p.format, p.pow2);
-      scale[tid] = s;
-      const int c = bc * 128 + tid;
-      if (c < p.cols) o.s[br * o.s_row + c * o.s_col] = s;
-    }
-    __syncthreads();
-    float sc[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = scale[sub * 8 + j];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(v[i][j], sc[j]);
-      store8(o, p, r0 + 16 * i, c0, y);
+      for (int w = 1; w < WARPS; ++w) m = T::larger(m, top[w][word]);
+      const Scale s = scale_of(fabsf(T::value(m, tid & 1)), FORMAT, p.pow2);
+      col_r[tid] = s.r;
+      col_minus[tid] = s.minus;
+      if (bc * 128 + tid < p.cols) o.s[br * o.s_row + (bc * 128 + tid) * o.s_col] = s.s;
     }
     if constexpr (WHICH == PAIR) {
+      uint8_t *dst = p.a.q + r0 * p.a.ldq + c0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        const float s = scale_of(half_max(max8(v[i])), p.format, p.pow2);
-        if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + bc * p.a.s_col] = s;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
-        store8(p.a, p, r, c0, v[i]);
+      for (int i = 0; i < ROWS; ++i) {
+        const int r = r0 + G * i;
+        const Scale s = lanes_scale<T>(max16<T>(v[i]), FORMAT, p.pow2);
+        if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + bc * p.a.s_col] = s.s;
+        store16(dst + i * (G * p.a.ldq), p.a.vec, r < p.rows ? n : 0,
+                quantize16<T, FORMAT>(v[i], s));
       }
+    }
+    __syncthreads();
+    uint8_t *dst = o.q + r0 * o.ldq + c0;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int c = sub * 16 + 4 * h;
+        const float4 f = *reinterpret_cast<const float4 *>(col_r + c);
+        const float4 d = *reinterpret_cast<const float4 *>(col_minus + c);
+        w[h] = quantize2<FORMAT>(at<T>(v[i], 4 * h), at<T>(v[i], 4 * h + 1), pack2(f.x, f.y),
+                                 pack2(d.x, d.y)) |
+               quantize2<FORMAT>(at<T>(v[i], 4 * h + 2), at<T>(v[i], 4 * h + 3), pack2(f.z, f.w),
+                                 pack2(d.z, d.w))
+                   << 16;
+      }
+      store16(dst + i * (G * o.ldq), o.vec, r0 + G * i < p.rows ? n : 0,
+              make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
   griddep_launch_dependents();
 }
 
-template <class T>
+template <class T, int FORMAT>
 static cudaError_t launch_quantize(const QuantParams &p, int which, int sms, cudaStream_t stream) {
   if (which < 0) {
     const long long units = (long long)p.rows * ceil_div(p.cols, 128);
-    // two blocks in flight per half-warp once every SM has several warps of work
-    if (units >= 4LL * 8 * 8 * sms) {
-      const long long grid = std::min<long long>(ceil_div(units, 8 * 4), 8LL * sms);
-      return launch_1d(rows_kernel<T, 2>, (int)grid, 256, 0, 1, stream, p);
-    }
-    return launch_1d(rows_kernel<T, 1>, (int)ceil_div(units, 8 * 2), 256, 0, 1, stream, p);
+    const long long grid = std::min<long long>(ceil_div(units, 8 * 4), 8LL * sms);
+    return launch_1d(rows_kernel<T, FORMAT>, (int)grid, 256, 0, 1, stream, p);
   }
   const int tiles_c = (int)ceil_div(p.cols, 128);
   const long long tiles = (long long)tiles_c * ceil_div(p.rows, 128);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  constexpr int threads = 8 * kRowGroups<T>;
   if (which == SQUARE)
-    return launch_1d(tile_kernel<T, SQUARE>, (int)tiles, 256, 0, 1, stream, p, tiles_c);
+    return launch_1d(tile_kernel<T, FORMAT, SQUARE>, (int)tiles, threads, 0, 1, stream, p, tiles_c);
   if (which == COLS)
-    return launch_1d(tile_kernel<T, COLS>, (int)tiles, 256, 0, 1, stream, p, tiles_c);
-  return launch_1d(tile_kernel<T, PAIR>, (int)tiles, 256, 0, 1, stream, p, tiles_c);
+    return launch_1d(tile_kernel<T, FORMAT, COLS>, (int)tiles, threads, 0, 1, stream, p, tiles_c);
+  return launch_1d(tile_kernel<T, FORMAT, PAIR>, (int)tiles, threads, 0, 1, stream, p, tiles_c);
+}
+
+template <class T>
+static cudaError_t launch_quantize(const QuantParams &p, int which, int sms, cudaStream_t stream) {
+  return p.format ? launch_quantize<T, F8_E5M2>(p, which, sms, stream)
+                  : launch_quantize<T, F8_E4M3>(p, which, sms, stream);
 }
 
 }  // namespace f8
@@ -321,8 +416,8 @@ extern "C" int f8_quantize(int rows, int cols, const void *x, int x_type, int ld
   p.vec = aligned(x, (long long)ldx * size, 16);
   p.format = format;
   p.pow2 = pow2 != 0;
-  p.a = f8::Result{static_cast<uint8_t *>(q), ldq, s, s_row, s_col, aligned(q, ldq, 8)};
-  p.c = f8::Result{static_cast<uint8_t *>(qc), ldqc, sc, sc_row, sc_col, aligned(qc, ldqc, 8)};
+  p.a = f8::Result{static_cast<uint8_t *>(q), ldq, s, s_row, s_col, aligned(q, ldq, 16)};
+  p.c = f8::Result{static_cast<uint8_t *>(qc), ldqc, sc, sc_row, sc_col, aligned(qc, ldqc, 16)};
   const int which = qc != nullptr ? f8::PAIR
                     : block_rows == 1 ? -1
                     : block_cols == 1 ? f8::COLS
