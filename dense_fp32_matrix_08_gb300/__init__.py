@@ -118,7 +118,10 @@ def _ptr(x) -> int | None:
 def _stream(s) -> int | None:
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        try:  # the handle alone: a Stream object costs more than a small kernel
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream or None
     if isinstance(s, int):
         return s or None
     return int(s.cuda_stream) or None

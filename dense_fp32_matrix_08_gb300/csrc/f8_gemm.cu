@@ -39,7 +39,7 @@ constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
 constexpr int TURN = 16;                 // columns that a warp turns at a time for its stores
 constexpr int TURN_PITCH = TURN + 1;
-constexpr int PART_PITCH = BP + 1;       // column pitch of a cluster's partial tiles (floats)
+constexpr int PART_PITCH = BP + 4;       // column pitch of a cluster's partial tiles (floats)
 
 template <int TN_>
 struct Cfg {
@@ -50,17 +50,22 @@ struct Cfg {
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
   static constexpr int Q_BYTES = TN * BK;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = TN == 256 ? 4 : TN == 128 ? 6 : 8;
+  // narrow tiles: about 100 KB, so that the next call's CTA fits beside this one's and is past its
+  // setup when this one ends
+  static constexpr int STAGES = TN == 256 ? 4 : TN == 128 ? 6 : TN == 64 ? 4 : 5;
   static constexpr int NBUF = TN >= 128 ? 2 : 4;    // TMEM accumulators
   static constexpr int ACC_COLS = TN < 32 ? 32 : TN;
   static constexpr int TMEM_COLS = NBUF * ACC_COLS;
-  static constexpr int SQ_BYTES = 2 * TN * 4;       // Q scales of two k blocks
+  // scales of a k block: 128 of P (one if its rows share it), then TN of Q (one for each 128)
+  static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
+  static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
   static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH * 4;
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * NBUF) + 16;
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
-      1024 + STAGES * STAGE_BYTES + SQ_BYTES + TURN_BYTES + BAR_BYTES;
+      1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
+  static_assert(TN > 64 || 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
   static_assert(PART_PITCH * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
 };
 
@@ -85,8 +90,8 @@ struct Params {
   int vec;             // 16-byte stores along the contiguous index are aligned
 };
 
-// Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the
-// epilogue gave up.
+// Device status word: 0 = fine; 1, 2, 3, 4 = a wait of the producer, the MMA issuer, the epilogue
+// or the scale loader gave up.
 __device__ int g_f8_status;
 
 __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
@@ -156,11 +161,11 @@ __device__ __forceinline__ void store1(const Params &p, int row, int col, float 
   store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v, p.beta * load_d(p, at)) : p.alpha * v);
 }
 
-// Warp 0 (one lane): TMA producer. Warp 1 (one lane): MMA issuer. Warps 4 ..: epilogue, group g
+// Warp 0: TMA producer. Warp 1: MMA issuer (one elected lane of either). Warps 4 ..: epilogue, group g
 // of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
 // rows) 32 (w % 4) .. + 31, one row per thread.
-// (Warps 2 and 3 only complete the first warpgroup: registers are granted to four warps at a time,
-// so they cost nothing.)
+// Warp 2: scale loader. (Warp 3 only completes the first warpgroup: registers are granted to four
+// warps at a time, so it costs nothing.)
 // QVEC: Q has a scale for each column (else one for each 128, the same for a whole group).
 template <int TN, bool QVEC>
 __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
@@ -172,15 +177,16 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
   const uint32_t raw = saddr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);
-  float *sq_buf = reinterpret_cast<float *>(sbase + C::STAGES * C::STAGE_BYTES);
-  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SQ_BYTES + C::TURN_BYTES;
+  float *scales = reinterpret_cast<float *>(sbase + C::STAGES * C::STAGE_BYTES);
+  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SC_BYTES + C::TURN_BYTES;
   const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
   const uint32_t acc_empty = acc_full + 8 * C::NBUF;
-  const uint32_t tmem_slot = acc_empty + 8 * C::NBUF;
+  const uint32_t sc_full = acc_empty + 8 * C::NBUF, sc_empty = sc_full + 8 * C::SC_DEPTH;
+  const uint32_t tmem_slot = sc_empty + 8 * C::SC_DEPTH;
   volatile uint32_t *tmem_slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.split;
   const int rank = S > 1 ? (int)(blockIdx.x % (unsigned)S) : 0;
   const int first = (int)(blockIdx.x / (unsigned)S), step = (int)(gridDim.x / (unsigned)S);
@@ -197,6 +203,10 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
       mbar_init(acc_full + 8 * b, 1);
       mbar_init(acc_empty + 8 * b, C::EPI_WARPS);
     }
+    for (int d = 0; d < C::SC_DEPTH; ++d) {
+      mbar_init(sc_full + 8 * d, 32);
+      mbar_init(sc_empty + 8 * d, C::EPI_WARPS);
+    }
     mbar_init_fence();
     tma_prefetch_map(&map_p);
     tma_prefetch_map(&map_q);
@@ -210,118 +220,151 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_slot_ptr;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  // (every CTA of the grid is resident, so the next launch may take what room is left)
+  griddep_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
-    // ---- TMA producer: stage g % STAGES holds k block g of this CTA's tiles, in order
-    long long g = 0;
+  if (warp == 0) {
+    // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
+    Ring<C::STAGES> st;
+    int issued = 0;  // (up to STAGES)
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int s = (int)(g % C::STAGES);
-        if (g >= C::STAGES &&
-            !mbar_wait(bars + 8 * (C::STAGES + s), ((uint32_t)(g / C::STAGES) & 1u) ^ 1u)) {
-          atomicCAS(&g_f8_status, 0, 1);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u)) {
+          if (lane == 0) atomicCAS(&g_f8_status, 0, 1);
           ok = false;
           break;
         }
-        const uint32_t st = base + s * C::STAGE_BYTES, full = bars + 8 * s;
-        const int k = kb * BK;
-        mbar_expect_tx(full, C::STAGE_BYTES);
-        if (p.p.mn_major)
-          tma_load_2d(st, &map_p, tp * BP, k, full);
-        else
-          tma_load_2d(st, &map_p, k, tp * BP, full);
-        if (p.q.mn_major) {
+        if (elect_one()) {
+          const uint32_t dst = base + st.slot * C::STAGE_BYTES, full = bars + 8 * st.slot;
+          const int k = kb * BK;
+          mbar_expect_tx(full, C::STAGE_BYTES);
+          if (p.p.mn_major)
+            tma_load_2d(dst, &map_p, tp * BP, k, full);
+          else
+            tma_load_2d(dst, &map_p, k, tp * BP, full);
+          if (p.q.mn_major) {
 #pragma unroll
-          for (int c = 0; c < TN; c += 128)
-            tma_load_2d(st + P_BYTES + c * BK, &map_q, tq * TN + c, k, full);
-        } else {
-          tma_load_2d(st + P_BYTES, &map_q, k, tq * TN, full);
+            for (int c = 0; c < TN; c += 128)
+              tma_load_2d(dst + P_BYTES + c * BK, &map_q, tq * TN + c, k, full);
+          } else {
+            tma_load_2d(dst + P_BYTES, &map_q, k, tq * TN, full);
+          }
         }
+        __syncwarp();
+        issued = min(issued + 1, C::STAGES);
+        st.next();
       }
     }
-    // the last loads issued must have landed before this thread leaves
-    for (long long k = g - 1; k >= 0 && k >= g - C::STAGES; --k)
-      mbar_wait(bars + 8 * (int)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
-  } else if (warp == 1 && lane == 0) {
-    // ---- MMA issuer: k block g goes to accumulator g % NBUF
+    // the last loads issued must have landed before this warp leaves
+    for (; issued > 0; --issued) {
+      st.parity ^= st.slot == 0 ? 1u : 0u;
+      st.slot = st.slot == 0 ? C::STAGES - 1 : st.slot - 1;
+      wait_short(bars + 8 * st.slot, st.parity);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer: one k block per TMEM accumulator
     const uint32_t lead_q = 128 * BK;
     const uint32_t adv_p = p.p.mn_major ? 32 * 128 : 32, adv_q = p.q.mn_major ? 32 * 128 : 32;
-    long long g = 0;
+    Ring<C::STAGES> st;
+    Ring<C::NBUF> buf;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int s = (int)(g % C::STAGES), b = (int)(g % C::NBUF);
-        if ((g >= C::NBUF &&
-             !mbar_wait(acc_empty + 8 * b, ((uint32_t)(g / C::NBUF) & 1u) ^ 1u)) ||
-            !mbar_wait(bars + 8 * s, (uint32_t)(g / C::STAGES) & 1u)) {
-          atomicCAS(&g_f8_status, 0, 2);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) ||
+            !wait_short(bars + 8 * st.slot, st.parity)) {
+          if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
           ok = false;
           break;
         }
         fence_after();
-        const uint32_t st = base + s * C::STAGE_BYTES;
+        if (elect_one()) {
+          const uint32_t src = base + st.slot * C::STAGE_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk)
-          mma_f8(tmem + (uint32_t)b * C::ACC_COLS, sw128_desc(st + kk * adv_p, 16),
-                 sw128_desc(st + P_BYTES + kk * adv_q, lead_q), p.idesc, kk != 0 ? 1u : 0u);
-        mma_commit(bars + 8 * (C::STAGES + s));  // the stage is free once these complete
-        mma_commit(acc_full + 8 * b);
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_f8(tmem + buf.slot * C::ACC_COLS, sw128_desc(src + kk * adv_p, 16),
+                   sw128_desc(src + P_BYTES + kk * adv_q, lead_q), p.idesc, kk != 0 ? 1u : 0u);
+          mma_commit(bars + 8 * (C::STAGES + st.slot));  // the stage is free once these complete
+          mma_commit(acc_full + 8 * buf.slot);
+        }
+        __syncwarp();
+        st.next();
+        buf.next();
       }
     }
+  } else if (warp == 2) {
+    // ---- scale loader: the scales of each k block, several blocks ahead of the epilogue, which
+    // would otherwise wait for memory once per block; 0 out of range
+    Ring<C::SC_DEPTH> sl;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      int tp, tq;
+      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_short(sc_empty + 8 * sl.slot, sl.parity ^ 1u));
+        if (!ok) {
+          if (lane == 0) atomicCAS(&g_f8_status, 0, 4);
+          break;
+        }
+        const uint32_t dst = saddr(scales + sl.slot * (BP + TN));
+        const float *ps = p.p.scale + kb * p.p.s_k, *qs = p.q.scale + kb * p.q.s_k;
+        if (p.p.shift) {
+          if (lane == 0) cp_async_4(dst, ps + tp * p.p.s_mn, 4);
+        } else {
+#pragma unroll
+          for (int i = lane; i < BP; i += 32) {
+            const int row = tp * BP + i;
+            const bool in = row < p.p.extent;
+            cp_async_4(dst + 4 * i, in ? ps + row * p.p.s_mn : ps, in ? 4 : 0);
+          }
+        }
+#pragma unroll
+        for (int i = lane; i < (QVEC ? TN : (TN + 127) / 128); i += 32) {
+          const int col = tq * TN + (QVEC ? i : 128 * i);
+          const bool in = col < p.q.extent;
+          cp_async_4(dst + 4 * (BP + i), in ? qs + (QVEC ? col : col >> 7) * p.q.s_mn : qs,
+                     in ? 4 : 0);
+        }
+        cp_async_arrive(sc_full + 8 * sl.slot);
+        sl.next();
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
   } else if (warp >= 4) {
     // ---- epilogue
     const int grp = (warp - 4) >> 2, quad = warp & 3;
-    const int gt = quad * 32 + lane;  // thread of the group
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
-    long long g = 0;
+    const int p_at = p.p.shift ? 0 : quad * 32 + lane;
+    Ring<C::NBUF> buf;
+    Ring<C::SC_DEPTH> sl;
     bool ok = true;
-    for (int t = first; t < tiles; t += step) {
+    for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
       const int row = tp * BP + quad * 32 + lane, col0 = tq * TN + grp * C::COLS;
       unsigned long long acc[C::COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
-      // scales of the next k block are fetched one block ahead; rows and columns out of range
-      // take 0 (their products are not stored)
-      const float *ps = row < p.p.extent ? p.p.scale + (row >> p.p.shift) * p.p.s_mn : nullptr;
-      const int qcol = QVEC ? col0 + gt : col0;
-      const float *qs = qcol < p.q.extent && (!QVEC || gt < C::COLS)
-                            ? p.q.scale + (qcol >> p.q.shift) * p.q.s_mn
-                            : nullptr;
-      float ps_next = ps && kb0 < kb1 ? __ldg(ps + kb0 * p.p.s_k) : 0.0f;
-      float qs_next = qs && kb0 < kb1 ? __ldg(qs + kb0 * p.q.s_k) : 0.0f;
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int b = (int)(g % C::NBUF);
-        const float sp = ps_next, sq = qs_next;
-        if (kb + 1 < kb1) {
-          ps_next = ps ? __ldg(ps + (kb + 1) * p.p.s_k) : 0.0f;
-          qs_next = qs ? __ldg(qs + (kb + 1) * p.q.s_k) : 0.0f;
-        }
-        float *sqb = sq_buf + (int)(g & 1) * TN + grp * C::COLS;
-        if constexpr (QVEC) {
-          if (gt < C::COLS) sqb[gt] = sq;
-          named_barrier(1 + grp, 128);
-        }
-        // a warp whose wait gave up goes on without its sums, so that it still arrives at the
-        // barriers of its group
-        if (!ok) continue;
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(acc_full + 8 * b, (uint32_t)(g / C::NBUF) & 1u));
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_short(sc_full + 8 * sl.slot, sl.parity) &&
+                                         wait_short(acc_full + 8 * buf.slot, buf.parity));
         if (!ok) {
           if (lane == 0) atomicCAS(&g_f8_status, 0, 3);
-          continue;
+          break;
         }
         fence_after();
+        const float *sc = scales + sl.slot * (BP + TN);
+        const float *sqb = sc + BP + (QVEC ? grp * C::COLS : grp * C::COLS / 128);
         constexpr int CH = TN == 256 || C::COLS < 32 ? 16 : 32;
-        const unsigned long long s2 = QVEC ? pack2(sp, sp) : pack2(sp * sq, sp * sq);
+        const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
+        const unsigned long long s2 = pack2(s, s);
 #pragma unroll
         for (int c = 0; c < C::COLS; c += CH) {
           uint32_t v[CH];
-          tmem_ld(lane_base + (uint32_t)(b * C::ACC_COLS + c), v);
+          tmem_ld(lane_base + buf.slot * C::ACC_COLS + (uint32_t)c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < CH; j += 4) {
@@ -338,8 +381,14 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty + 8 * b);
+        if (lane == 0) {
+          mbar_arrive(acc_empty + 8 * buf.slot);
+          mbar_arrive(sc_empty + 8 * sl.slot);
+        }
+        buf.next();
+        sl.next();
       }
+      if (!ok) break;
       if (S == 1 && (p.vec || p.d_q != 1)) {
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 8) {
@@ -355,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
       } else if (S == 1) {
         // rows of D that allow no wide stores: turned in shared memory, so that neighbouring
         // lanes store neighbouring elements
-        float *turn = sq_buf + 2 * TN + (warp - 4) * 32 * TURN_PITCH;
+        float *turn = scales + C::SC_DEPTH * (BP + TN) + (warp - 4) * 32 * TURN_PITCH;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += TURN) {
 #pragma unroll
@@ -385,35 +434,38 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
     }
   }
   __syncwarp();
-  griddep_launch_dependents();
   if (S > 1) {
-    // CTA `rank` finishes columns [rank * TN / S, (rank + 1) * TN / S): partials in rank order
+    // CTA `rank` finishes columns [rank * TN / S, (rank + 1) * TN / S): partials in rank order,
+    // four rows at a time. Neighbouring lanes take what D stores side by side.
     cluster_sync_all();
     if (warp >= 4) {
       int tp, tq;
       tile_coords(first, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
-      const int quad = warp & 3, grp = (warp - 4) >> 2;
-      const int c0 = TN * rank / S, c1 = TN * (rank + 1) / S;
-      if (p.d_q == 1) {
-        // neighbouring lanes take neighbouring columns, as D stores them
-        for (int c = c0 + lane; c < c1; c += 32) {
-          const uint32_t part = base + (uint32_t)(c * PART_PITCH) * 4;
-#pragma unroll 4
-          for (int r = warp - 4; r < BP; r += C::EPI_WARPS) {
-            float v = 0.0f;
-            for (int q = 0; q < S; ++q) v += ld_cluster1(part + (uint32_t)r * 4, (uint32_t)q);
-            store1(p, tp * BP + r, tq * TN + c, v);
+      const int c0 = TN * rank / S;
+      const int cols = min(TN * (rank + 1) / S, p.q.extent - tq * TN) - c0;
+      const int quads = (min(BP, p.p.extent - tp * BP) + 3) / 4;
+#pragma unroll 2
+      for (int u = threadIdx.x - 128; u < cols * quads; u += 32 * C::EPI_WARPS) {
+        const int c = c0 + (p.d_q == 1 ? u % cols : u / quads);
+        const int r = 4 * (p.d_q == 1 ? u / cols : u % quads);
+        const uint32_t part = base + (uint32_t)(c * PART_PITCH + r) * 4;
+        float4 v[MAX_CLUSTER];
+#pragma unroll
+        for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
+          if (q < S) v[q] = ld_cluster4(part, (uint32_t)q);
+        float4 a = v[0];
+#pragma unroll
+        for (int q = 1; q < MAX_CLUSTER; ++q)
+          if (q < S) {
+            a.x += v[q].x;
+            a.y += v[q].y;
+            a.z += v[q].z;
+            a.w += v[q].w;
           }
-        }
-      } else {
-        const int r = quad * 32 + lane;
-#pragma unroll 4
-        for (int c = c0 + grp; c < c1; c += C::GROUPS) {
-          const uint32_t part = base + (uint32_t)(c * PART_PITCH + r) * 4;
-          float v = 0.0f;
-          for (int q = 0; q < S; ++q) v += ld_cluster1(part, (uint32_t)q);
-          store1(p, tp * BP + r, tq * TN + c, v);
-        }
+        store1(p, tp * BP + r, tq * TN + c, a.x);
+        store1(p, tp * BP + r + 1, tq * TN + c, a.y);
+        store1(p, tp * BP + r + 2, tq * TN + c, a.z);
+        store1(p, tp * BP + r + 3, tq * TN + c, a.w);
       }
     }
     cluster_sync_all();  // no CTA leaves while another may still read its partial

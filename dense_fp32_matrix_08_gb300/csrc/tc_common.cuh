@@ -16,6 +16,60 @@
 namespace sgemm {
 namespace tcx {
 
+// Wait for the phase of parity `parity`, with the limit of mbar_wait (sgemm_ptx.cuh). Each try
+// suspends the thread for up to 20 us, so that waiting warps leave the issue slots and the shared
+// memory port to the others; the global timer is read between tries only.
+__device__ __forceinline__ bool try_wait_suspended(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(20000)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) {
+  if (try_wait_suspended(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 0; i < (1u << 27); ++i) {
+    if (try_wait_suspended(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return false;
+}
+
+// Position in a ring of N slots: the slot and the parity of its use (0 for the first, 1 for the
+// second, ...). A consumer waits for the slot's "full" phase of this parity, a producer for the
+// "empty" phase of the opposite one (which a fresh mbarrier counts as complete).
+template <int N>
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
 }
@@ -117,23 +171,9 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lead
   return d;
 }
 
-// Barrier among `threads` threads of the CTA (id 1 .. 15; 0 is __syncthreads).
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ float ld_cluster1(uint32_t local, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n"
-      ".reg .u32 a;\n"
-      "mapa.shared::cluster.u32 a, %1, %2;\n"
-      "ld.shared::cluster.f32 %0, [a];\n"
-      "}\n"
-      : "=f"(v)
-      : "r"(local), "r"(rank)
-      : "memory");
-  return v;
+// This thread's arrival at `bar` once its cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
 }  // namespace tcx

@@ -37,10 +37,6 @@ for _name in F8_EXPORTED:
     getattr(lib, _name).restype = ctypes.c_int
 
 
-def _blocks(n: int) -> int:
-    return (n + 127) >> 7
-
-
 def _rows(name, t):
     """Row stride of a 2-D CUDA tensor with unit column stride."""
     if t.dim() != 2:
@@ -54,40 +50,41 @@ def _rows(name, t):
     return max(ld, cols, 1) if rows > 1 else max(cols, 1)
 
 
-def _new_q(rows, cols, dtype, device):
-    # rows of a multiple of 16 bytes, as the product's copies need them
-    return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=dtype,
-                               device=device)
-
-
 def _quantize(x, block, both, dtype, pow2, stream):
-    if dtype not in _FORMAT:
+    fmt = _FORMAT.get(dtype)
+    if fmt is None:
         raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
-    if x.dtype not in _TYPE:
+    xt = _TYPE.get(x.dtype)
+    if xt is None:
         raise TypeError("x must be float32, bfloat16 or float16")
     ldx = _rows("x", x)
     rows, cols = x.shape
     device = x.device
     br, bc = block
-    q = _new_q(rows, cols, dtype, device)
+    ldq = (cols + 15) // 16 * 16 or 1
+    nb = (cols + 127) >> 7
+    # rows of a multiple of 16 bytes, as the product's copies need them
+    q = torch.empty_strided((rows, cols), (ldq, 1), dtype=dtype, device=device)
     if br == 1:
         # neighbouring rows' scales of one block are neighbours, as the product reads them
-        s = torch.empty_strided((rows, _blocks(cols)), (1, max(rows, 1)), dtype=torch.float32,
-                                device=device)
+        s_row, s_col = 1, rows or 1
+        s = torch.empty_strided((rows, nb), (1, s_col), dtype=torch.float32, device=device)
     else:
-        s = torch.empty((_blocks(rows), cols if bc == 1 else _blocks(cols)),
-                        dtype=torch.float32, device=device)
-    ss = s.stride()
-    qc = sc = None
-    second = (None, 0, None, 0, 0)
+        s_row, s_col = (cols if bc == 1 else nb) or 1, 1
+        s = torch.empty_strided(((rows + 127) >> 7, cols if bc == 1 else nb), (s_row, 1),
+                                dtype=torch.float32, device=device)
     if both:
-        qc = _new_q(rows, cols, dtype, device)
-        sc = torch.empty((_blocks(rows), cols), dtype=torch.float32, device=device)
-        second = (qc.data_ptr() or None, max(qc.stride(0), 1), sc.data_ptr() or None,
-                  sc.stride(0), 1)
-    rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, _TYPE[x.dtype], ldx, br, bc,
-                         _FORMAT[dtype], int(pow2), q.data_ptr() or None, max(q.stride(0), 1),
-                         s.data_ptr() or None, ss[0], ss[1], *second, _stream(stream))
+        qc = torch.empty_strided((rows, cols), (ldq, 1), dtype=dtype, device=device)
+        sc = torch.empty_strided(((rows + 127) >> 7, cols), (cols or 1, 1), dtype=torch.float32,
+                                 device=device)
+        rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, xt, ldx, br, bc, fmt, pow2,
+                             q.data_ptr() or None, ldq, s.data_ptr() or None, s_row, s_col,
+                             qc.data_ptr() or None, ldq, sc.data_ptr() or None, cols, 1,
+                             _stream(stream))
+    else:
+        rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, xt, ldx, br, bc, fmt, pow2,
+                             q.data_ptr() or None, ldq, s.data_ptr() or None, s_row, s_col,
+                             None, 0, None, 0, 0, _stream(stream))
     if rc != 0:
         raise SgemmError(rc, "f8_quantize")
     return (q, s, qc, sc) if both else (q, s)
@@ -97,35 +94,42 @@ def f8_quantize(x, block=(1, 128), *, dtype=torch.float8_e4m3fn, pow2=False, str
     """Quantise a 2-D CUDA tensor (float32, bfloat16, float16) by blocks of (1, 128), (128, 1) or
     (128, 128): returns (q, scale). scale = max(amax / largest, 2^-126) of each block, with pow2
     the least power of two not below it; q = x / scale rounded to dtype."""
-    if tuple(block) not in _BLOCKS:
+    if block not in _BLOCKS:
         raise ValueError(f"block must be one of {_BLOCKS}")
-    return _quantize(x, tuple(block), False, dtype, pow2, stream)
+    return _quantize(x, block, False, dtype, bool(pow2), stream)
 
 
 def f8_quantize_pair(x, *, dtype=torch.float8_e4m3fn, pow2=False, stream=None):
     """f8_quantize by (1, 128) and by (128, 1) blocks from one read of x: returns
     (q_rows, scale_rows, q_columns, scale_columns)."""
-    return _quantize(x, (1, 128), True, dtype, pow2, stream)
+    return _quantize(x, (1, 128), True, dtype, bool(pow2), stream)
 
 
 def _operand(name, q, scale, k_dim):
-    """(format, ld, group, stride along the other dimension, stride along k) of an operand."""
+    """(format, ld, group, stride along the other dimension, stride along k, k, other size) of an
+    operand."""
     fmt = _FORMAT.get(q.dtype)
     if fmt is None:
         raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.float8_e5m2")
     ld = _rows(name, q)
     if q.shape[0] <= 1:
         ld = (ld + 15) // 16 * 16
-    if scale.dtype != torch.float32 or scale.dim() != 2 or scale.device != q.device:
-        raise TypeError(f"{name}'s scale must be a 2-D float32 tensor on its device")
-    have, shape, st = scale.shape, q.shape, scale.stride()
-    k, mn = shape[k_dim], shape[1 - k_dim]
-    if have[k_dim] != (k + 127) >> 7:
+    if scale.dtype is not torch.float32 or scale.dim() != 2 or not scale.is_cuda:
+        raise TypeError(f"{name}'s scale must be a 2-D float32 CUDA tensor")
+    if k_dim:
+        mn, k = q.shape
+        have, blocks = scale.shape
+        s_mn, s_k = scale.stride()
+    else:
+        k, mn = q.shape
+        blocks, have = scale.shape
+        s_k, s_mn = scale.stride()
+    if blocks != (k + 127) >> 7:
         raise ValueError(f"{name}'s scale needs one entry for each 128 along the contraction")
-    if have[1 - k_dim] == mn:
-        return fmt, ld, 1, st[1 - k_dim], st[k_dim]
-    if have[1 - k_dim] == (mn + 127) >> 7:
-        return fmt, ld, 128, st[1 - k_dim], st[k_dim]
+    if have == mn:
+        return fmt, ld, 1, s_mn, s_k, k, mn
+    if have == (mn + 127) >> 7:
+        return fmt, ld, 128, s_mn, s_k, k, mn
     raise ValueError(f"{name}'s scale does not fit its shape")
 
 
@@ -135,34 +139,31 @@ def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, 
     flag is set). `out` is float32, bfloat16 or float16 with unit column stride; without one a
     new tensor of out_dtype (bfloat16 unless given) is returned. Each operand's scales run along
     the contraction in blocks of 128. Raises SgemmError on a nonzero status."""
-    fa, lda, ga, amn, ak = _operand("a", a, a_scale, 0 if transa else 1)
-    fb, ldb, gb, bmn, bk = _operand("b", b, b_scale, 1 if transb else 0)
-    M, K = a.shape
-    if transa:
-        M, K = K, M
-    K2, N = b.shape
-    if transb:
-        K2, N = N, K2
+    fa, lda, ga, amn, ak, K, M = _operand("a", a, a_scale, 0 if transa else 1)
+    fb, ldb, gb, bmn, bk, K2, N = _operand("b", b, b_scale, 1 if transb else 0)
     if K2 != K:
         raise ValueError("shape mismatch")
-    if a.device != b.device:
-        raise ValueError("operands on different devices")
+    device = a.device
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs an out to scale")
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out has another type than out_dtype")
-    if out.dtype not in _TYPE:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=device)
+        ldd = N or 1
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out has another type than out_dtype")
+        ldd = _rows("out", out)
+        if out.shape != (M, N):
+            raise ValueError("shape mismatch")
+    dt = _TYPE.get(out.dtype)
+    if dt is None:
         raise TypeError("out must be float32, bfloat16 or float16")
-    if out.device != a.device:
-        raise ValueError("out is on another device")
-    if tuple(out.shape) != (M, N):
-        raise ValueError("shape mismatch")
+    if not (device == b.device == out.device == a_scale.device == b_scale.device):
+        raise ValueError("operands, scales and out must be on one device")
     rc = lib.f8_gemm(transa, transb, M, N, K, alpha, a.data_ptr() or None, fa, lda,
                      a_scale.data_ptr() or None, ga, amn, ak, b.data_ptr() or None, fb, ldb,
-                     b_scale.data_ptr() or None, gb, bmn, bk, beta, out.data_ptr() or None,
-                     _TYPE[out.dtype], _rows("out", out), _stream(stream))
+                     b_scale.data_ptr() or None, gb, bmn, bk, beta, out.data_ptr() or None, dt,
+                     ldd, _stream(stream))
     if rc != 0:
         raise SgemmError(rc, "f8_gemm")
     return out

@@ -70,7 +70,7 @@ int f8_gemm(int transa, int transb, int M, int N, int K, float alpha, const void
             int b_cols, long long b_scale_mn, long long b_scale_k, float beta, void *D,
             int d_type, int ldd, cudaStream_t stream);
 
-/* Reads and clears the device status word of f8_gemm (synchronising): 0 = fine, 1 - 3 = a wait
+/* Reads and clears the device status word of f8_gemm (synchronising): 0 = fine, 1 - 4 = a wait
  * gave up after about a second and the call's result is not to be used. Returns 0 or a
  * cudaError_t. */
 int f8_gemm_status(int *status);
