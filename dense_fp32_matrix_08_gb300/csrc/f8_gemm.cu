@@ -41,26 +41,37 @@ constexpr int TURN = 16;                 // columns that a warp turns at a time 
 constexpr int TURN_PITCH = TURN + 1;
 constexpr int PART_PITCH = BP + 4;       // column pitch of a cluster's partial tiles (floats)
 
-template <int TN_>
+// PAIR: two CTAs share a tile of 256 rows and TN columns (tcgen05 cta_group::2), each with its 128
+// rows of P and half of Q.
+template <int TN_, bool PAIR_ = false>
 struct Cfg {
   static constexpr int TN = TN_;
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int QN = PAIR ? TN / 2 : TN;     // columns of Q that this CTA holds
   static constexpr int GROUPS = TN >= 128 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;          // accumulator columns of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
-  static constexpr int Q_BYTES = TN * BK;
+  static constexpr int Q_BYTES = QN * BK;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   // narrow tiles: about 100 KB, so that the next call's CTA fits beside this one's and is past its
   // setup when this one ends
-  static constexpr int STAGES = TN == 256 ? 4 : TN == 128 ? 6 : TN == 64 ? 4 : 5;
-  static constexpr int NBUF = TN >= 128 ? 2 : 4;    // TMEM accumulators
-  static constexpr int ACC_COLS = TN < 32 ? 32 : TN;
-  static constexpr int TMEM_COLS = NBUF * ACC_COLS;
+  static constexpr int STAGES = TN == 256 && !PAIR ? 4 : TN >= 128 ? 6 : TN == 64 ? 4 : 5;
+  // A pair's tile is computed in two parts of 128 columns, one for each epilogue group, with
+  // accumulators of their own: a group hands its accumulator back without waiting for the other,
+  // and the tensor core always has one to fill. (With one accumulator of 256 columns for both,
+  // two in all, a block of k took 970 cycles instead of PAIR_CYCLES.)
+  static constexpr int PARTS = PAIR ? 2 : 1;
+  static constexpr int PART = TN / PARTS;           // columns of one accumulator
+  static constexpr int NBUF = PAIR ? 2 : 4;         // accumulators per part
+  static constexpr int ACC_COLS = PART < 32 ? 32 : PART;
+  static constexpr int TMEM_COLS = PARTS * NBUF * ACC_COLS;
+  static constexpr int ACC_WARPS = EPI_WARPS / PARTS * (PAIR ? 2 : 1);  // readers of one
   // scales of a k block: 128 of P (one if its rows share it), then TN of Q (one for each 128)
   static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
   static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
   static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH * 4;
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * NBUF + 2 * SC_DEPTH) + 16;
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
@@ -161,17 +172,15 @@ __device__ __forceinline__ void store1(const Params &p, int row, int col, float 
   store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v, p.beta * load_d(p, at)) : p.alpha * v);
 }
 
-// Warp 0: TMA producer. Warp 1: MMA issuer (one elected lane of either). Warps 4 ..: epilogue, group g
-// of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
+// Warp 0: TMA producer, warps 1 and 3: MMA issuers (one elected lane of each), warp 2: scale loader.
+// Warps 4 ..: epilogue, group g of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
 // rows) 32 (w % 4) .. + 31, one row per thread.
-// Warp 2: scale loader. (Warp 3 only completes the first warpgroup: registers are granted to four
-// warps at a time, so it costs nothing.)
 // QVEC: Q has a scale for each column (else one for each 128, the same for a whole group).
-template <int TN, bool QVEC>
-__global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
+template <int TN, bool QVEC, bool PAIR>
+__global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     f8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
               const Params p) {
-  using C = Cfg<TN>;
+  using C = Cfg<TN, PAIR>;
   using namespace tcx;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = saddr(smem_raw);
@@ -180,28 +189,31 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
   float *scales = reinterpret_cast<float *>(sbase + C::STAGES * C::STAGE_BYTES);
   const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::SC_BYTES + C::TURN_BYTES;
   const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
-  const uint32_t acc_empty = acc_full + 8 * C::NBUF;
-  const uint32_t sc_full = acc_empty + 8 * C::NBUF, sc_empty = sc_full + 8 * C::SC_DEPTH;
+  const uint32_t acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
+  const uint32_t sc_full = acc_empty + 8 * C::PARTS * C::NBUF, sc_empty = sc_full + 8 * C::SC_DEPTH;
   const uint32_t tmem_slot = sc_empty + 8 * C::SC_DEPTH;
   volatile uint32_t *tmem_slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int S = p.split;
-  const int rank = S > 1 ? (int)(blockIdx.x % (unsigned)S) : 0;
-  const int first = (int)(blockIdx.x / (unsigned)S), step = (int)(gridDim.x / (unsigned)S);
-  const int tiles = p.tiles_p * p.tiles_q;
+  // a cluster is S CTAs with a range of k blocks each, or a pair on one tile of 256 rows
+  const int S = PAIR ? 1 : p.split, CS = PAIR ? 2 : S;
+  const int cta = CS > 1 ? (int)(blockIdx.x % (unsigned)CS) : 0;  // rank in the cluster
+  const int rank = PAIR ? 0 : cta;
+  const int first = (int)(blockIdx.x / (unsigned)CS), step = (int)(gridDim.x / (unsigned)CS);
+  const int units = PAIR ? (p.tiles_p + 1) / 2 : p.tiles_p;       // rows of tiles
+  const int tiles = units * p.tiles_q;
   const int kb0 = (int)((long long)p.KB * rank / S);
   const int kb1 = (int)((long long)p.KB * (rank + 1) / S);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bars + 8 * s, 1);
-      mbar_init(bars + 8 * (C::STAGES + s), 1);
+      mbar_init(bars + 8 * (C::STAGES + s), C::PARTS);
     }
-    for (int b = 0; b < C::NBUF; ++b) {
+    for (int b = 0; b < C::PARTS * C::NBUF; ++b) {
       mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, C::EPI_WARPS);
+      mbar_init(acc_empty + 8 * b, C::ACC_WARPS);
     }
     for (int d = 0; d < C::SC_DEPTH; ++d) {
       mbar_init(sc_full + 8 * d, 32);
@@ -212,17 +224,32 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
     tma_prefetch_map(&map_q);
   }
   if (warp == 0) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are initialised
   fence_after();
   const uint32_t tmem = *tmem_slot_ptr;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   // (every CTA of the grid is resident, so the next launch may take what room is left)
   griddep_launch_dependents();
 
+  const auto tile_at = [&](int t, int &tp, int &tq) {
+    tile_coords(t, units, p.tiles_q, p.group_p, tp, tq);
+    if (PAIR) tp = 2 * tp + cta;
+  };
+
+  if (warp < 4) {
+  // 384 threads x 168 registers at launch = 128 x 56 + 256 x 224: the sums of a 256-column tile
+  // take 128 of a thread's registers
+  if constexpr (TN == 256) reg_dealloc<56>();
   if (warp == 0) {
     // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
     Ring<C::STAGES> st;
@@ -230,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
-      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      tile_at(t, tp, tq);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u)) {
           if (lane == 0) atomicCAS(&g_f8_status, 0, 1);
@@ -239,18 +266,23 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
         }
         if (elect_one()) {
           const uint32_t dst = base + st.slot * C::STAGE_BYTES, full = bars + 8 * st.slot;
-          const int k = kb * BK;
-          mbar_expect_tx(full, C::STAGE_BYTES);
-          if (p.p.mn_major)
-            tma_load_2d(dst, &map_p, tp * BP, k, full);
-          else
-            tma_load_2d(dst, &map_p, k, tp * BP, full);
-          if (p.q.mn_major) {
-#pragma unroll
-            for (int c = 0; c < TN; c += 128)
-              tma_load_2d(dst + P_BYTES + c * BK, &map_q, tq * TN + c, k, full);
+          const int k = kb * BK, p0 = tp * BP, q0 = tq * TN + cta * (PAIR ? C::QN : 0);
+          if constexpr (PAIR) {  // both CTAs' copies complete the leader's barrier
+            const uint32_t lead = in_cta(full, 0);
+            if (cta == 0) mbar_expect_tx(full, 2 * C::STAGE_BYTES);
+            tma_load_2d_pair(dst, &map_p, p.p.mn_major ? p0 : k, p.p.mn_major ? k : p0, lead);
+            tma_load_2d_pair(dst + P_BYTES, &map_q, p.q.mn_major ? q0 : k, p.q.mn_major ? k : q0,
+                             lead);
           } else {
-            tma_load_2d(dst + P_BYTES, &map_q, k, tq * TN, full);
+            mbar_expect_tx(full, C::STAGE_BYTES);
+            tma_load_2d(dst, &map_p, p.p.mn_major ? p0 : k, p.p.mn_major ? k : p0, full);
+            if (p.q.mn_major) {
+#pragma unroll
+              for (int c = 0; c < TN; c += 128)
+                tma_load_2d(dst + P_BYTES + c * BK, &map_q, q0 + c, k, full);
+            } else {
+              tma_load_2d(dst + P_BYTES, &map_q, k, q0, full);
+            }
           }
         }
         __syncwarp();
@@ -258,38 +290,63 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
         st.next();
       }
     }
-    // the last loads issued must have landed before this warp leaves
-    for (; issued > 0; --issued) {
+    // the last loads issued must have landed before this warp leaves (a pair's: the leader waits for
+    // both, and the CTAs leave together)
+    for (; issued > 0 && (!PAIR || cta == 0); --issued) {
       st.parity ^= st.slot == 0 ? 1u : 0u;
       st.slot = st.slot == 0 ? C::STAGES - 1 : st.slot - 1;
       wait_short(bars + 8 * st.slot, st.parity);
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer: one k block per TMEM accumulator
-    const uint32_t lead_q = 128 * BK;
-    const uint32_t adv_p = p.p.mn_major ? 32 * 128 : 32, adv_q = p.q.mn_major ? 32 * 128 : 32;
+  } else if (warp == 1 || warp == 3) {
+    // ---- MMA issuers. What a warp does for one accumulator (two waits, four instructions, the
+    // commits) takes longer than the tensor core takes for 128 columns, so two warps share it:
+    // each issues one part of every k block of a pair, else every other k block.
+    const int me = warp >> 1;
+    const uint64_t lead_q = 128 * BK;
+    const uint32_t adv_p = (p.p.mn_major ? 32 * 128 : 32) >> 4;
+    const uint32_t adv_q = (p.q.mn_major ? 32 * 128 : 32) >> 4;
+    const uint64_t pd0 = sw128_desc(base, 16);
+    // a part's 64 rows of this CTA's Q: 8 KB further, or 64 bytes into the rows of k
+    const uint64_t qd0 =
+        sw128_desc(base + P_BYTES + (PAIR ? me * (p.q.mn_major ? 64 : 64 * 128) : 0), lead_q);
+    const uint32_t acc0 = PAIR ? me * C::NBUF : 0;
     Ring<C::STAGES> st;
     Ring<C::NBUF> buf;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    int mine = me;  // (not a pair) k blocks until the next one of this warp
+    for (int t = first; t < tiles && ok && (!PAIR || cta == 0); t += step) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) ||
-            !wait_short(bars + 8 * st.slot, st.parity)) {
-          if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
-          ok = false;
-          break;
-        }
-        fence_after();
-        if (elect_one()) {
-          const uint32_t src = base + st.slot * C::STAGE_BYTES;
+        if (PAIR || mine == 0) {
+          const uint32_t a = acc0 + buf.slot;
+          ok = wait_short(bars + 8 * st.slot, st.parity) &&
+               wait_short(acc_empty + 8 * a, buf.parity ^ 1u);
+          if (!ok) {
+            if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
+            break;
+          }
+          fence_after();
+          if (elect_one()) {
+            const uint32_t at = st.slot * (uint32_t)(C::STAGE_BYTES >> 4);
+            const uint32_t d = tmem + a * C::ACC_COLS;
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_f8(tmem + buf.slot * C::ACC_COLS, sw128_desc(src + kk * adv_p, 16),
-                   sw128_desc(src + P_BYTES + kk * adv_q, lead_q), p.idesc, kk != 0 ? 1u : 0u);
-          mma_commit(bars + 8 * (C::STAGES + st.slot));  // the stage is free once these complete
-          mma_commit(acc_full + 8 * buf.slot);
+            for (uint32_t kk = 0; kk < BK / 32; ++kk) {
+              if constexpr (PAIR)
+                mma_f8_pair(d, pd0 + at + kk * adv_p, qd0 + at + kk * adv_q, p.idesc, kk != 0);
+              else
+                mma_f8(d, pd0 + at + kk * adv_p, qd0 + at + kk * adv_q, p.idesc, kk != 0);
+            }
+            // once these have completed the accumulator is, and the stage is free of this warp
+            if constexpr (PAIR) {
+              mma_commit_pair(acc_full + 8 * a);
+              mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
+            } else {
+              mma_commit(acc_full + 8 * a);
+              mma_commit(bars + 8 * (C::STAGES + st.slot));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        mine ^= 1;
         st.next();
         buf.next();
       }
@@ -301,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
-      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
+      tile_at(t, tp, tq);
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_short(sc_empty + 8 * sl.slot, sl.parity ^ 1u));
         if (!ok) {
@@ -311,7 +368,8 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
         const uint32_t dst = saddr(scales + sl.slot * (BP + TN));
         const float *ps = p.p.scale + kb * p.p.s_k, *qs = p.q.scale + kb * p.q.s_k;
         if (p.p.shift) {
-          if (lane == 0) cp_async_4(dst, ps + tp * p.p.s_mn, 4);
+          const bool in = tp * BP < p.p.extent;  // (a pair's second CTA may have no rows)
+          if (lane == 0) cp_async_4(dst, in ? ps + tp * p.p.s_mn : ps, in ? 4 : 0);
         } else {
 #pragma unroll
           for (int i = lane; i < BP; i += 32) {
@@ -333,56 +391,74 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
     }
     cp_async_commit();
     cp_async_wait<0>();
-  } else if (warp >= 4) {
+  }
+  } else {
     // ---- epilogue
+    if constexpr (TN == 256) reg_alloc<224>();
     const int grp = (warp - 4) >> 2, quad = warp & 3;
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
+    const uint32_t acc0 = PAIR ? grp * C::NBUF : 0;  // the first accumulator that this warp reads
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + acc0 * C::ACC_COLS +
+                               (uint32_t)(PAIR ? 0 : grp * C::COLS);
+    // column c of this group in the tile; a pair's part holds 64 columns of either CTA's half
+    const auto column = [&](int c) {
+      return PAIR ? 64 * grp + c + (c < 64 ? 0 : 64) : grp * C::COLS + c;
+    };
     const int p_at = p.p.shift ? 0 : quad * 32 + lane;
     Ring<C::NBUF> buf;
     Ring<C::SC_DEPTH> sl;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
-      tile_coords(t, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
-      const int row = tp * BP + quad * 32 + lane, col0 = tq * TN + grp * C::COLS;
+      tile_at(t, tp, tq);
+      const int row = tp * BP + quad * 32 + lane, col0 = tq * TN;
       unsigned long long acc[C::COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_short(sc_full + 8 * sl.slot, sl.parity) &&
-                                         wait_short(acc_full + 8 * buf.slot, buf.parity));
+                                         wait_short(acc_full + 8 * (acc0 + buf.slot), buf.parity));
         if (!ok) {
           if (lane == 0) atomicCAS(&g_f8_status, 0, 3);
           break;
         }
         fence_after();
         const float *sc = scales + sl.slot * (BP + TN);
-        const float *sqb = sc + BP + (QVEC ? grp * C::COLS : grp * C::COLS / 128);
-        constexpr int CH = TN == 256 || C::COLS < 32 ? 16 : 32;
-        const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
-        const unsigned long long s2 = pack2(s, s);
+        const float *sqb = sc + BP;
+        const float sp = sc[p_at];
+        // (one scale of Q for each 128 columns: a pair's part has columns of two)
+        const float sa = QVEC ? sp : sp * sqb[PAIR ? 0 : grp * C::COLS / 128];
+        const float sb = QVEC || !PAIR ? sa : sp * sqb[1];
+        const unsigned long long s2[2] = {pack2(sa, sa), pack2(sb, sb)};
+        // the next columns are on their way from TMEM while these are scaled and added
+        constexpr int CH = C::COLS < 32 ? 16 : 32;
+        uint32_t v[2][CH];
+        const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
+        tmem_ld(src, v[0]);
 #pragma unroll
         for (int c = 0; c < C::COLS; c += CH) {
-          uint32_t v[CH];
-          tmem_ld(lane_base + buf.slot * C::ACC_COLS + (uint32_t)c, v);
-          tmem_wait_ld();
+          uint32_t(&w)[CH] = v[c / CH % 2];
+          tmem_wait_ld(w);
+          if (c + CH < C::COLS) tmem_ld(src + (uint32_t)(c + CH), v[(c / CH + 1) % 2]);
 #pragma unroll
           for (int j = 0; j < CH; j += 4) {
-            unsigned long long lo = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-            unsigned long long hi = pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+            unsigned long long lo = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+            unsigned long long hi = pack2(__uint_as_float(w[j + 2]), __uint_as_float(w[j + 3]));
             if constexpr (QVEC) {
-              const float4 w = *reinterpret_cast<const float4 *>(sqb + c + j);
-              lo = mul2(lo, pack2(w.x, w.y));
-              hi = mul2(hi, pack2(w.z, w.w));
+              const float4 f = *reinterpret_cast<const float4 *>(sqb + column(c + j));
+              lo = mul2(lo, pack2(f.x, f.y));
+              hi = mul2(hi, pack2(f.z, f.w));
             }
-            ffma2(acc[(c + j) / 2], lo, s2);
-            ffma2(acc[(c + j) / 2 + 1], hi, s2);
+            ffma2(acc[(c + j) / 2], lo, s2[PAIR && c >= 64]);
+            ffma2(acc[(c + j) / 2 + 1], hi, s2[PAIR && c >= 64]);
           }
         }
         fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(acc_empty + 8 * buf.slot);
+          if constexpr (PAIR)
+            arrive_in(in_cta(acc_empty + 8 * (acc0 + buf.slot), 0));  // the leader's
+          else
+            mbar_arrive(acc_empty + 8 * buf.slot);
           mbar_arrive(sc_empty + 8 * sl.slot);
         }
         buf.next();
@@ -399,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
             v[j] = f.x;
             v[j + 1] = f.y;
           }
-          store8(p, row, col0 + c, v);
+          store8(p, row, col0 + column(c), v);
         }
       } else if (S == 1) {
         // rows of D that allow no wide stores: turned in shared memory, so that neighbouring
@@ -416,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
           __syncwarp();
 #pragma unroll 8
           for (int r = lane / TURN; r < 32; r += 32 / TURN)
-            store1(p, tp * BP + quad * 32 + r, col0 + c + lane % TURN,
+            store1(p, tp * BP + quad * 32 + r, col0 + column(c) + lane % TURN,
                    turn[r * TURN_PITCH + lane % TURN]);
           __syncwarp();
         }
@@ -427,8 +503,8 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < C::COLS; j += 2) {
           const float2 f = unpack2(acc[j / 2]);
-          part[(grp * C::COLS + j) * PART_PITCH + quad * 32 + lane] = f.x;
-          part[(grp * C::COLS + j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
+          part[column(j) * PART_PITCH + quad * 32 + lane] = f.x;
+          part[column(j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
         }
       }
     }
@@ -472,7 +548,12 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, 1)
   }
   fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+  if constexpr (PAIR) {
+    cluster_sync_all();  // no instruction, copy or arrival of the other CTA is under way
+    if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  } else {
+    if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+  }
 }
 
 // D = beta * D (k == 0 or alpha == 0; 0 when beta == 0, without reading D).
@@ -491,6 +572,7 @@ __global__ void f8_scale_kernel(Params p, int M, int N, long long ldd) {
 
 struct Plan {
   bool swap;   // P = op(B)^T
+  bool pair;   // two CTAs per tile of 256 rows
   int tn, split;
 };
 
@@ -498,44 +580,50 @@ struct Plan {
 // times a block's cost (the larger of the MMA and the copy of its operands), plus a fixed
 // cost for each tile and for a cluster's exchange.
 static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, int sms) {
-  Plan best{false, 128, 1};
+  Plan best{false, false, 128, 1};
   double best_cost = 1e300;
   const int tns[5] = {256, 128, 64, 32, 16};
   for (int swap = 0; swap < 2; ++swap)
     for (int tn : tns) {
       const int P = swap ? N : M, Q = swap ? M : N;
+      const bool pair = tn == 256;
       if ((swap ? a_mn : b_mn) && tn < 128) continue;  // an MN-major Q comes in 128 columns
-      const long long tiles = (long long)ceil_div(P, BP) * ceil_div(Q, tn);
+      const long long tiles = (long long)ceil_div(P, pair ? 2 * BP : BP) * ceil_div(Q, tn);
       for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
-        if (S > 1 && (S > KB || tiles * S > sms)) break;
-        const long long per_sm = (tiles * S + sms - 1) / sms;
-        const double block = std::max(2.0 * tn / 64.0, 2.5);
+        if (S > 1 && (pair || S > KB || tiles * S > sms)) break;
+        const int at_once = pair ? sms / 2 : sms;
+        const long long per_sm = (tiles * S + at_once - 1) / at_once;
+        const double block = pair ? 11.0 : std::max(4.0 * tn / 64.0, 2.5);
         const double cost = per_sm * (block * ((KB + S - 1) / S) + 6.0 + tn / 16.0) +
                             (S > 1 ? 8.0 : 0.0) + tn / 256.0;
         if (cost < best_cost) {
           best_cost = cost;
-          best = Plan{swap != 0, tn, S};
+          best = Plan{swap != 0, pair, tn, S};
         }
       }
     }
   return best;
 }
 
-template <int TN, bool QVEC>
-static cudaError_t launch(const CUtensorMap &mp, const CUtensorMap &mq, const Params &p, int grid,
-                          cudaStream_t stream) {
-  return launch_1d(f8_kernel<TN, QVEC>, grid, Cfg<TN>::THREADS, Cfg<TN>::SMEM_BYTES, p.split,
-                   stream, mp, mq, p);
+template <int TN, bool PAIR = false>
+static cudaError_t launch(bool vec, const CUtensorMap &mp, const CUtensorMap &mq, const Params &p,
+                          int grid, cudaStream_t stream) {
+  using C = Cfg<TN, PAIR>;
+  const int cluster = PAIR ? 2 : p.split;
+  return vec ? launch_1d(f8_kernel<TN, true, PAIR>, grid, C::THREADS, C::SMEM_BYTES, cluster,
+                         stream, mp, mq, p)
+             : launch_1d(f8_kernel<TN, false, PAIR>, grid, C::THREADS, C::SMEM_BYTES, cluster,
+                         stream, mp, mq, p);
 }
 
-template <int TN>
+template <int TN, bool PAIR = false>
 static cudaError_t set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(f8_kernel<TN, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<TN>::SMEM_BYTES);
+  const int bytes = Cfg<TN, PAIR>::SMEM_BYTES;
+  cudaError_t e = cudaFuncSetAttribute(f8_kernel<TN, false, PAIR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(f8_kernel<TN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<TN>::SMEM_BYTES);
+    e = cudaFuncSetAttribute(f8_kernel<TN, true, PAIR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e;
 }
 
@@ -548,7 +636,7 @@ static cudaError_t kernel_setup() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(g_once[dev], [dev]() {
-    cudaError_t err = set_attributes<256>();
+    cudaError_t err = set_attributes<256, true>();
     if (err == cudaSuccess) err = set_attributes<128>();
     if (err == cudaSuccess) err = set_attributes<64>();
     if (err == cudaSuccess) err = set_attributes<32>();
@@ -634,35 +722,33 @@ extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha,
   if (tiles_p * tiles_q > 0x7fffffffLL / f8::MAX_CLUSTER) return (int)cudaErrorInvalidConfiguration;
   p.tiles_p = (int)tiles_p;
   p.tiles_q = (int)tiles_q;
-  p.group_p = (int)std::min<long long>(16, tiles_p);
+  p.group_p = (int)std::min<long long>(pl.pair ? 8 : 16, tiles_p);
   p.split = pl.split;
   const uint32_t fp = pl.swap ? b_format : a_format, fq = pl.swap ? a_format : b_format;
   // instruction descriptor: D in FP32 (bits 4-5 = 1), formats of P and Q (0 = e4m3, 1 = e5m2;
   // bits 7-9, 10-12), MN-major P and Q (bits 15, 16), N / 8 (bits 17-22), M / 16 (24-28)
   p.idesc = (1u << 4) | (fp << 7) | (fq << 10) | ((uint32_t)p.p.mn_major << 15) |
-            ((uint32_t)p.q.mn_major << 16) | ((uint32_t)(pl.tn >> 3) << 17) |
-            ((uint32_t)(f8::BP >> 4) << 24);
+            ((uint32_t)p.q.mn_major << 16) |
+            ((uint32_t)((pl.pair ? pl.tn / 2 : pl.tn) >> 3) << 17) |
+            ((uint32_t)((pl.pair ? 2 * f8::BP : f8::BP) >> 4) << 24);
 
   CUtensorMap mp, mq;
   if (!f8::side_map(&mp, pl.swap ? B : A, p.p.extent, K, pl.swap ? ldb : lda, p.p.mn_major,
                     f8::BP) ||
       !f8::side_map(&mq, pl.swap ? A : B, p.q.extent, K, pl.swap ? lda : ldb, p.q.mn_major,
-                    pl.tn))
+                    pl.pair ? pl.tn / 2 : pl.tn))
     return (int)cudaErrorInvalidValue;
-  const int grid = (int)(p.split > 1 ? tiles_p * tiles_q * p.split
-                                     : std::min<long long>(tiles_p * tiles_q, sms));
+  const int grid =
+      (int)(pl.pair ? 2 * std::min<long long>(ceil_div(tiles_p, 2) * tiles_q, sms / 2)
+            : p.split > 1 ? tiles_p * tiles_q * p.split
+                          : std::min<long long>(tiles_p * tiles_q, sms));
   const bool vec = p.q.shift == 0;
   switch (pl.tn) {
-    case 256: return (int)(vec ? f8::launch<256, true>(mp, mq, p, grid, stream)
-                               : f8::launch<256, false>(mp, mq, p, grid, stream));
-    case 128: return (int)(vec ? f8::launch<128, true>(mp, mq, p, grid, stream)
-                               : f8::launch<128, false>(mp, mq, p, grid, stream));
-    case 64: return (int)(vec ? f8::launch<64, true>(mp, mq, p, grid, stream)
-                              : f8::launch<64, false>(mp, mq, p, grid, stream));
-    case 32: return (int)(vec ? f8::launch<32, true>(mp, mq, p, grid, stream)
-                              : f8::launch<32, false>(mp, mq, p, grid, stream));
-    default: return (int)(vec ? f8::launch<16, true>(mp, mq, p, grid, stream)
-                              : f8::launch<16, false>(mp, mq, p, grid, stream));
+    case 256: return (int)f8::launch<256, true>(vec, mp, mq, p, grid, stream);
+    case 128: return (int)f8::launch<128>(vec, mp, mq, p, grid, stream);
+    case 64: return (int)f8::launch<64>(vec, mp, mq, p, grid, stream);
+    case 32: return (int)f8::launch<32>(vec, mp, mq, p, grid, stream);
+    default: return (int)f8::launch<16>(vec, mp, mq, p, grid, stream);
   }
 }
 

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j0 = 0; j0 < COLS; j0 += 32) {
           uint32_t v[32];
           tmem_ld(lane_base + buf.slot * BT + (uint32_t)j0, v);
-          tmem_wait_ld();
+          tmem_wait_ld(v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[j0 + j] += __uint_as_float(v[j]);
         }

@@ -224,6 +224,28 @@ def test_product_many_tiles_per_cta():
     assert (err <= (256 + 16) * 2.0 ** -23 * (a.abs() @ b.abs().t())).all()
 
 
+@pytest.mark.parametrize("transa", [False, True])
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("ga,gb", [(1, 128), (128, 128), (1, 1)])
+@pytest.mark.parametrize("shape", [(2305, 4400, 260), (2433, 4353, 129)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_large_tiles(shape, transa, transb, ga, gb):
+    """Enough tiles for the largest tile width, an odd number of 128-row blocks among them."""
+    M, N, K = shape
+    ablk = (ga, 128) if not transa else (128, ga)
+    bblk = (128, gb) if not transb else (gb, 128)
+    qa, sa = operand(*((K, M) if transa else (M, K)), ablk, E4, 1)
+    qb, sb = operand(*((N, K) if transb else (K, N)), bblk, E5, 2)
+    d0 = torch.randn(M, N, device="cuda")
+    got = sg.f8_matmul(on_gpu(qa), sa.cuda(), on_gpu(qb), sb.cuda(), transa=transa, transb=transb,
+                       beta=1.0, out=d0.clone())
+    a, b = plain.values(qa, sa).cuda(), plain.values(qb, sb).cuda()
+    a, b = (a.t() if transa else a), (b.t() if transb else b)
+    R = a @ b + d0.double()
+    tol = (K + 8) * 2.0 ** -23 * (a.abs() @ b.abs()) + 2.0 ** -23 * (d0.double().abs() + R.abs())
+    assert ((got.double() - R).abs() <= tol).all()
+
+
 def test_product_scales_in_any_layout():
     M, N, K = 70, 200, 500
     qa, sa = operand(M, K, (1, 128), E4, 1)
