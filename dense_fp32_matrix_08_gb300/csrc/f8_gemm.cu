@@ -37,8 +37,9 @@ constexpr int BP = 128;                  // rows of P per tile
 constexpr int BK = 128;                  // k per block = per pipeline stage
 constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
-constexpr int TURN = 16;                 // columns that a warp turns at a time for its stores
-constexpr int TURN_PITCH = TURN + 1;
+// Stores go through a buffer of each warp: 32 rows of 64 bytes, 80 bytes apart, so that a row's
+// segment is stored by neighbouring lanes.
+constexpr int TURN_PITCH = 80;
 constexpr int PART_PITCH = BP + 4;       // column pitch of a cluster's partial tiles (floats)
 
 // PAIR: two CTAs share a tile of 256 rows and TN columns (tcgen05 cta_group::2), each with its 128
@@ -48,7 +49,7 @@ struct Cfg {
   static constexpr int TN = TN_;
   static constexpr bool PAIR = PAIR_;
   static constexpr int QN = PAIR ? TN / 2 : TN;     // columns of Q that this CTA holds
-  static constexpr int GROUPS = TN >= 128 ? 2 : 1;  // epilogue groups of four warps
+  static constexpr int GROUPS = PAIR ? 4 : TN >= 128 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;          // accumulator columns of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
@@ -56,11 +57,10 @@ struct Cfg {
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   // narrow tiles: about 100 KB, so that the next call's CTA fits beside this one's and is past its
   // setup when this one ends
-  static constexpr int STAGES = TN == 256 && !PAIR ? 4 : TN >= 128 ? 6 : TN == 64 ? 4 : 5;
-  // A pair's tile is computed in two parts of 128 columns, one for each epilogue group, with
-  // accumulators of their own: a group hands its accumulator back without waiting for the other,
-  // and the tensor core always has one to fill. (With one accumulator of 256 columns for both,
-  // two in all, a block of k took 970 cycles instead of PAIR_CYCLES.)
+  static constexpr int STAGES = PAIR || TN == 16 ? 5 : TN == 128 ? 6 : 4;
+  // A pair's tile is computed in two parts of 128 columns with accumulators of their own, each read
+  // by two of the epilogue groups: the tensor core fills one while the other is read and handed
+  // back.
   static constexpr int PARTS = PAIR ? 2 : 1;
   static constexpr int PART = TN / PARTS;           // columns of one accumulator
   static constexpr int NBUF = PAIR ? 2 : 4;         // accumulators per part
@@ -70,7 +70,7 @@ struct Cfg {
   // scales of a k block: 128 of P (one if its rows share it), then TN of Q (one for each 128)
   static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
   static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
-  static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH * 4;
+  static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH;
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
@@ -136,45 +136,109 @@ __device__ __forceinline__ uint32_t pack16(const Params &p, float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Eight neighbouring accumulator columns of one row -> D. The one rounding to D's type is here.
-__device__ __forceinline__ void store8(const Params &p, int row, int col, float (&v)[8]) {
+// Eight neighbouring accumulator columns of one row -> D (P of D's columns: neighbouring lanes store
+// neighbouring elements).
+__device__ __forceinline__ void store8(const Params &p, int row, int col, const float (&v)[8]) {
   if (row >= p.p.extent || col >= p.q.extent) return;
   const long long at = row * p.d_p + col * p.d_q;
   const int n = min(8, p.q.extent - col);
-  if (p.beta != 0.0f) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = j < n ? fmaf(p.alpha, v[j], p.beta * load_d(p, at + j * p.d_q)) : 0.0f;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= p.alpha;
-  }
-  if (p.vec && n == 8 && p.d_q == 1) {
-    if (p.d_type == F8_D_F32) {
-      float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.D) + at);
-      d[0] = make_float4(v[0], v[1], v[2], v[3]);
-      d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.D) + at);
-      *d = make_uint4(pack16(p, v[0], v[1]), pack16(p, v[2], v[3]), pack16(p, v[4], v[5]),
-                      pack16(p, v[6], v[7]));
-    }
-    return;
-  }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < n) store_d(p, at + j * p.d_q, v[j]);
+    if (j < n) {
+      const float y = p.alpha * v[j];
+      store_d(p, at + j * p.d_q, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at + j * p.d_q), y) : y);
+    }
 }
 
 __device__ __forceinline__ void store1(const Params &p, int row, int col, float v) {
   if (row >= p.p.extent || col >= p.q.extent) return;
   const long long at = row * p.d_p + col * p.d_q;
-  store_d(p, at, p.beta != 0.0f ? fmaf(p.alpha, v, p.beta * load_d(p, at)) : p.alpha * v);
+  const float y = p.alpha * v;
+  store_d(p, at, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at), y) : y);
+}
+
+// CN neighbouring accumulator columns from `col` of 32 rows (one per lane, the first is `row0`) -> D
+// with its rows along the lanes' columns. buf: the warp's buffer. The one rounding to D's type is
+// here.
+template <int CN>
+__device__ __forceinline__ void store_rows(const Params &p, uint8_t *buf, int lane, int row0, int col,
+                                           const float (&v)[CN]) {
+  const int rows = min(32, p.p.extent - row0), cols = min(CN, p.q.extent - col);
+  if (p.vec && p.beta == 0.0f && p.d_type != F8_D_F32) {
+    // packed: 2 CN bytes of a row
+#pragma unroll
+    for (int j = 0; j < CN; j += 8)
+      *reinterpret_cast<uint4 *>(buf + lane * TURN_PITCH + 2 * j) =
+          make_uint4(pack16(p, p.alpha * v[j], p.alpha * v[j + 1]),
+                     pack16(p, p.alpha * v[j + 2], p.alpha * v[j + 3]),
+                     pack16(p, p.alpha * v[j + 4], p.alpha * v[j + 5]),
+                     pack16(p, p.alpha * v[j + 6], p.alpha * v[j + 7]));
+    __syncwarp();
+    constexpr int LANES = CN / 8;  // per row
+    const int c = 8 * (lane % LANES);
+#pragma unroll
+    for (int r = lane / LANES; r < 32; r += 32 / LANES) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(buf + r * TURN_PITCH + 2 * c);
+      if (r >= rows) continue;
+      uint16_t *d = reinterpret_cast<uint16_t *>(p.D) + (row0 + r) * p.d_p + col + c;
+      if (c + 8 <= cols) {
+        *reinterpret_cast<uint4 *>(d) = w;
+      } else {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < cols) d[j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
+      }
+    }
+    __syncwarp();
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < CN; h += 16) {  // 16 columns at a time in FP32
+#pragma unroll
+    for (int j = 0; j < 16; j += 4)
+      *reinterpret_cast<float4 *>(buf + lane * TURN_PITCH + 4 * j) =
+          make_float4(p.alpha * v[h + j], p.alpha * v[h + j + 1], p.alpha * v[h + j + 2],
+                      p.alpha * v[h + j + 3]);
+    __syncwarp();
+    if (p.vec && p.d_type == F8_D_F32) {
+      const int c = 4 * (lane & 3);
+#pragma unroll
+      for (int r = lane >> 2; r < 32; r += 8) {
+        float4 w = *reinterpret_cast<const float4 *>(buf + r * TURN_PITCH + 4 * c);
+        if (r >= rows || h + c >= cols) continue;
+        float *d = reinterpret_cast<float *>(p.D) + (row0 + r) * p.d_p + col + h + c;
+        if (h + c + 4 <= cols) {
+          if (p.beta != 0.0f) {
+            const float4 o = *reinterpret_cast<const float4 *>(d);
+            w = make_float4(fmaf(p.beta, o.x, w.x), fmaf(p.beta, o.y, w.y), fmaf(p.beta, o.z, w.z),
+                            fmaf(p.beta, o.w, w.w));
+          }
+          *reinterpret_cast<float4 *>(d) = w;
+        } else {
+          const float y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (h + c + j < cols) d[j] = p.beta != 0.0f ? fmaf(p.beta, d[j], y[j]) : y[j];
+        }
+      }
+    } else {
+      const int c = lane & 15;
+#pragma unroll 4
+      for (int r = lane >> 4; r < 32; r += 2) {
+        const float y = *reinterpret_cast<const float *>(buf + r * TURN_PITCH + 4 * c);
+        if (r >= rows || h + c >= cols) continue;
+        const long long at = (row0 + r) * p.d_p + col + h + c;
+        store_d(p, at, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at), y) : y);
+      }
+    }
+    __syncwarp();
+  }
 }
 
 // Warp 0: TMA producer, warps 1 and 3: MMA issuers (one elected lane of each), warp 2: scale loader.
-// Warps 4 ..: epilogue, group g of four warps owns accumulator columns g * COLS .. + COLS - 1, warp w of it TMEM lanes (tile
-// rows) 32 (w % 4) .. + 31, one row per thread.
+// Warps 4 ..: epilogue; a group of four warps owns COLS columns of the tile, warp w of it TMEM lanes
+// (tile rows) 32 (w % 4) .. + 31, one row per thread.
 // QVEC: Q has a scale for each column (else one for each 128, the same for a whole group).
 template <int TN, bool QVEC, bool PAIR>
 __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
@@ -247,9 +311,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   };
 
   if (warp < 4) {
-  // 384 threads x 168 registers at launch = 128 x 56 + 256 x 224: the sums of a 256-column tile
-  // take 128 of a thread's registers
-  if constexpr (TN == 256) reg_dealloc<56>();
+  // a pair's 640 threads x 96 registers at launch = 128 x 64 + 512 x 104
+  if constexpr (PAIR) reg_dealloc<64>();
   if (warp == 0) {
     // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
     Ring<C::STAGES> st;
@@ -394,15 +457,14 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   }
   } else {
     // ---- epilogue
-    if constexpr (TN == 256) reg_alloc<224>();
+    if constexpr (PAIR) reg_alloc<104>();
     const int grp = (warp - 4) >> 2, quad = warp & 3;
-    const uint32_t acc0 = PAIR ? grp * C::NBUF : 0;  // the first accumulator that this warp reads
+    // accumulators and columns of this group: a quarter of a pair's tile is 64 columns of the half
+    // of Q that CTA grp % 2 holds, in the accumulators of part grp / 2
+    const uint32_t acc0 = PAIR ? (grp >> 1) * C::NBUF : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + acc0 * C::ACC_COLS +
-                               (uint32_t)(PAIR ? 0 : grp * C::COLS);
-    // column c of this group in the tile; a pair's part holds 64 columns of either CTA's half
-    const auto column = [&](int c) {
-      return PAIR ? 64 * grp + c + (c < 64 ? 0 : 64) : grp * C::COLS + c;
-    };
+                               (uint32_t)((PAIR ? grp & 1 : grp) * C::COLS);
+    const int tile_col = PAIR ? 128 * (grp & 1) + 64 * (grp >> 1) : grp * C::COLS;
     const int p_at = p.p.shift ? 0 : quad * 32 + lane;
     Ring<C::NBUF> buf;
     Ring<C::SC_DEPTH> sl;
@@ -410,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_at(t, tp, tq);
-      const int row = tp * BP + quad * 32 + lane, col0 = tq * TN;
+      const int row0 = tp * BP + quad * 32, col0 = tq * TN + tile_col;
       unsigned long long acc[C::COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
@@ -423,14 +485,11 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         }
         fence_after();
         const float *sc = scales + sl.slot * (BP + TN);
-        const float *sqb = sc + BP;
-        const float sp = sc[p_at];
-        // (one scale of Q for each 128 columns: a pair's part has columns of two)
-        const float sa = QVEC ? sp : sp * sqb[PAIR ? 0 : grp * C::COLS / 128];
-        const float sb = QVEC || !PAIR ? sa : sp * sqb[1];
-        const unsigned long long s2[2] = {pack2(sa, sa), pack2(sb, sb)};
+        const float *sqb = sc + BP + (QVEC ? tile_col : tile_col / 128);
+        const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
+        const unsigned long long s2 = pack2(s, s);
         // the next columns are on their way from TMEM while these are scaled and added
-        constexpr int CH = C::COLS < 32 ? 16 : 32;
+        constexpr int CH = PAIR || C::COLS < 32 ? 16 : 32;
         uint32_t v[2][CH];
         const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
         tmem_ld(src, v[0]);
@@ -444,12 +503,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             unsigned long long lo = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
             unsigned long long hi = pack2(__uint_as_float(w[j + 2]), __uint_as_float(w[j + 3]));
             if constexpr (QVEC) {
-              const float4 f = *reinterpret_cast<const float4 *>(sqb + column(c + j));
+              const float4 f = *reinterpret_cast<const float4 *>(sqb + c + j);
               lo = mul2(lo, pack2(f.x, f.y));
               hi = mul2(hi, pack2(f.z, f.w));
             }
-            ffma2(acc[(c + j) / 2], lo, s2[PAIR && c >= 64]);
-            ffma2(acc[(c + j) / 2 + 1], hi, s2[PAIR && c >= 64]);
+            ffma2(acc[(c + j) / 2], lo, s2);
+            ffma2(acc[(c + j) / 2 + 1], hi, s2);
           }
         }
         fence_before();
@@ -465,7 +524,23 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         sl.next();
       }
       if (!ok) break;
-      if (S == 1 && (p.vec || p.d_q != 1)) {
+      if (S == 1 && p.d_q == 1) {
+        uint8_t *turn = reinterpret_cast<uint8_t *>(scales + C::SC_DEPTH * (BP + TN)) +
+                        (warp - 4) * 32 * TURN_PITCH;
+        constexpr int CN = C::COLS < 32 ? 16 : 32;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += CN) {
+          float v[CN];
+#pragma unroll
+          for (int j = 0; j < CN; j += 2) {
+            const float2 f = unpack2(acc[(c + j) / 2]);
+            v[j] = f.x;
+            v[j + 1] = f.y;
+          }
+          if (row0 < p.p.extent && col0 + c < p.q.extent)
+            store_rows<CN>(p, turn, lane, row0, col0 + c, v);
+        }
+      } else if (S == 1) {
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 8) {
           float v[8];
@@ -475,26 +550,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             v[j] = f.x;
             v[j + 1] = f.y;
           }
-          store8(p, row, col0 + column(c), v);
-        }
-      } else if (S == 1) {
-        // rows of D that allow no wide stores: turned in shared memory, so that neighbouring
-        // lanes store neighbouring elements
-        float *turn = scales + C::SC_DEPTH * (BP + TN) + (warp - 4) * 32 * TURN_PITCH;
-#pragma unroll
-        for (int c = 0; c < C::COLS; c += TURN) {
-#pragma unroll
-          for (int j = 0; j < TURN; j += 2) {
-            const float2 f = unpack2(acc[(c + j) / 2]);
-            turn[lane * TURN_PITCH + j] = f.x;
-            turn[lane * TURN_PITCH + j + 1] = f.y;
-          }
-          __syncwarp();
-#pragma unroll 8
-          for (int r = lane / TURN; r < 32; r += 32 / TURN)
-            store1(p, tp * BP + quad * 32 + r, col0 + column(c) + lane % TURN,
-                   turn[r * TURN_PITCH + lane % TURN]);
-          __syncwarp();
+          store8(p, row0 + lane, col0 + c, v);
         }
       } else {
         // partial tile -> the ring, which every MMA of this CTA has finished reading (the
@@ -503,8 +559,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < C::COLS; j += 2) {
           const float2 f = unpack2(acc[j / 2]);
-          part[column(j) * PART_PITCH + quad * 32 + lane] = f.x;
-          part[column(j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
+          part[(tile_col + j) * PART_PITCH + quad * 32 + lane] = f.x;
+          part[(tile_col + j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
         }
       }
     }
