@@ -37,9 +37,6 @@ constexpr int BP = 128;                  // rows of P per tile
 constexpr int BK = 128;                  // k per block = per pipeline stage
 constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
-// Stores go through a buffer of each warp: 32 rows of 64 bytes, 80 bytes apart, so that a row's
-// segment is stored by neighbouring lanes.
-constexpr int TURN_PITCH = 80;
 constexpr int PART_PITCH = BP + 4;       // column pitch of a cluster's partial tiles (floats)
 
 // PAIR: two CTAs share a tile of 256 rows and TN columns (tcgen05 cta_group::2), each with its 128
@@ -70,10 +67,12 @@ struct Cfg {
   // scales of a k block: 128 of P (one if its rows share it), then TN of Q (one for each 128)
   static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
   static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
-  static constexpr int TURN_BYTES = EPI_WARPS * 32 * TURN_PITCH;
+  static constexpr int TURN_BYTES = EPI_WARPS * tcx::TURN_BYTES;
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
+  static_assert((int)F8_D_F32 == tcx::OUT_F32 && (int)F8_D_BF16 == tcx::OUT_BF16 &&
+                (int)F8_D_F16 == tcx::OUT_F16, "types of D");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
   static_assert(TN > 64 || 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -111,129 +110,9 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
   return d;
 }
 
-__device__ __forceinline__ float load_d(const Params &p, long long at) {
-  if (p.d_type == F8_D_F32) return reinterpret_cast<const float *>(p.D)[at];
-  if (p.d_type == F8_D_BF16)
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.D)[at]);
-  return __half2float(reinterpret_cast<const __half *>(p.D)[at]);
-}
-
-__device__ __forceinline__ void store_d(const Params &p, long long at, float v) {
-  if (p.d_type == F8_D_F32)
-    reinterpret_cast<float *>(p.D)[at] = v;
-  else if (p.d_type == F8_D_BF16)
-    reinterpret_cast<__nv_bfloat16 *>(p.D)[at] = __float2bfloat16_rn(v);
-  else
-    reinterpret_cast<__half *>(p.D)[at] = __float2half_rn(v);
-}
-
-__device__ __forceinline__ uint32_t pack16(const Params &p, float a, float b) {
-  if (p.d_type == F8_D_BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Eight neighbouring accumulator columns of one row -> D (P of D's columns: neighbouring lanes store
-// neighbouring elements).
-__device__ __forceinline__ void store8(const Params &p, int row, int col, const float (&v)[8]) {
-  if (row >= p.p.extent || col >= p.q.extent) return;
-  const long long at = row * p.d_p + col * p.d_q;
-  const int n = min(8, p.q.extent - col);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) {
-      const float y = p.alpha * v[j];
-      store_d(p, at + j * p.d_q, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at + j * p.d_q), y) : y);
-    }
-}
-
 __device__ __forceinline__ void store1(const Params &p, int row, int col, float v) {
-  if (row >= p.p.extent || col >= p.q.extent) return;
-  const long long at = row * p.d_p + col * p.d_q;
-  const float y = p.alpha * v;
-  store_d(p, at, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at), y) : y);
-}
-
-// CN neighbouring accumulator columns from `col` of 32 rows (one per lane, the first is `row0`) -> D
-// with its rows along the lanes' columns. buf: the warp's buffer. The one rounding to D's type is
-// here.
-template <int CN>
-__device__ __forceinline__ void store_rows(const Params &p, uint8_t *buf, int lane, int row0, int col,
-                                           const float (&v)[CN]) {
-  const int rows = min(32, p.p.extent - row0), cols = min(CN, p.q.extent - col);
-  if (p.vec && p.beta == 0.0f && p.d_type != F8_D_F32) {
-    // packed: 2 CN bytes of a row
-#pragma unroll
-    for (int j = 0; j < CN; j += 8)
-      *reinterpret_cast<uint4 *>(buf + lane * TURN_PITCH + 2 * j) =
-          make_uint4(pack16(p, p.alpha * v[j], p.alpha * v[j + 1]),
-                     pack16(p, p.alpha * v[j + 2], p.alpha * v[j + 3]),
-                     pack16(p, p.alpha * v[j + 4], p.alpha * v[j + 5]),
-                     pack16(p, p.alpha * v[j + 6], p.alpha * v[j + 7]));
-    __syncwarp();
-    constexpr int LANES = CN / 8;  // per row
-    const int c = 8 * (lane % LANES);
-#pragma unroll
-    for (int r = lane / LANES; r < 32; r += 32 / LANES) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(buf + r * TURN_PITCH + 2 * c);
-      if (r >= rows) continue;
-      uint16_t *d = reinterpret_cast<uint16_t *>(p.D) + (row0 + r) * p.d_p + col + c;
-      if (c + 8 <= cols) {
-        *reinterpret_cast<uint4 *>(d) = w;
-      } else {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j < cols) d[j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
-      }
-    }
-    __syncwarp();
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < CN; h += 16) {  // 16 columns at a time in FP32
-#pragma unroll
-    for (int j = 0; j < 16; j += 4)
-      *reinterpret_cast<float4 *>(buf + lane * TURN_PITCH + 4 * j) =
-          make_float4(p.alpha * v[h + j], p.alpha * v[h + j + 1], p.alpha * v[h + j + 2],
-                      p.alpha * v[h + j + 3]);
-    __syncwarp();
-    if (p.vec && p.d_type == F8_D_F32) {
-      const int c = 4 * (lane & 3);
-#pragma unroll
-      for (int r = lane >> 2; r < 32; r += 8) {
-        float4 w = *reinterpret_cast<const float4 *>(buf + r * TURN_PITCH + 4 * c);
-        if (r >= rows || h + c >= cols) continue;
-        float *d = reinterpret_cast<float *>(p.D) + (row0 + r) * p.d_p + col + h + c;
-        if (h + c + 4 <= cols) {
-          if (p.beta != 0.0f) {
-            const float4 o = *reinterpret_cast<const float4 *>(d);
-            w = make_float4(fmaf(p.beta, o.x, w.x), fmaf(p.beta, o.y, w.y), fmaf(p.beta, o.z, w.z),
-                            fmaf(p.beta, o.w, w.w));
-          }
-          *reinterpret_cast<float4 *>(d) = w;
-        } else {
-          const float y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (h + c + j < cols) d[j] = p.beta != 0.0f ? fmaf(p.beta, d[j], y[j]) : y[j];
-        }
-      }
-    } else {
-      const int c = lane & 15;
-#pragma unroll 4
-      for (int r = lane >> 4; r < 32; r += 2) {
-        const float y = *reinterpret_cast<const float *>(buf + r * TURN_PITCH + 4 * c);
-        if (r >= rows || h + c >= cols) continue;
-        const long long at = (row0 + r) * p.d_p + col + h + c;
-        store_d(p, at, p.beta != 0.0f ? fmaf(p.beta, load_d(p, at), y) : y);
-      }
-    }
-    __syncwarp();
-  }
+  if (row < p.p.extent && col < p.q.extent)
+    tcx::finish_out(p.D, p.d_type, row * p.d_p + col * p.d_q, p.alpha * v, p.beta);
 }
 
 // Warp 0: TMA producer, warps 1 and 3: MMA issuers (one elected lane of each), warp 2: scale loader.
@@ -526,7 +405,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       if (!ok) break;
       if (S == 1 && p.d_q == 1) {
         uint8_t *turn = reinterpret_cast<uint8_t *>(scales + C::SC_DEPTH * (BP + TN)) +
-                        (warp - 4) * 32 * TURN_PITCH;
+                        (warp - 4) * TURN_BYTES;
+        const Out out{p.D, p.d_type, p.d_p, p.p.extent, p.q.extent, p.alpha, p.beta, p.vec};
         constexpr int CN = C::COLS < 32 ? 16 : 32;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += CN) {
@@ -538,19 +418,14 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             v[j + 1] = f.y;
           }
           if (row0 < p.p.extent && col0 + c < p.q.extent)
-            store_rows<CN>(p, turn, lane, row0, col0 + c, v);
+            store_rows<CN>(out, turn, lane, row0, col0 + c, v);
         }
-      } else if (S == 1) {
+      } else if (S == 1) {  // P of D's columns: the lanes hold neighbouring elements
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 8) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float2 f = unpack2(acc[(c + j) / 2]);
-            v[j] = f.x;
-            v[j + 1] = f.y;
-          }
-          store8(p, row0 + lane, col0 + c, v);
+        for (int c = 0; c < C::COLS; c += 2) {
+          const float2 f = unpack2(acc[c / 2]);
+          store1(p, row0 + lane, col0 + c, f.x);
+          store1(p, row0 + lane, col0 + c + 1, f.y);
         }
       } else {
         // partial tile -> the ring, which every MMA of this CTA has finished reading (the
@@ -619,7 +494,7 @@ __global__ void f8_scale_kernel(Params p, int M, int N, long long ldd) {
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
     const long long at = i / N * ldd + i % N;
-    store_d(p, at, p.beta != 0.0f ? p.beta * load_d(p, at) : 0.0f);
+    tcx::finish_out(p.D, p.d_type, at, 0.0f, p.beta);
   }
 }
 

@@ -11,15 +11,23 @@
 // scale. The host derives it from the coefficients: |X_0| <= 1 in the spectral norm, the
 // polynomial bounds every later norm, and no element exceeds the norm.
 //
-// Three products per step, each one launch of ns_kernel over 128 x 128 tiles:
+// Three products per step:
 //   GRAM   S = X X^T              both operands K-major; S is symmetric: tiles on or below the
-//                                 diagonal, each written twice
+//                                 diagonal, those below written twice
 //   POLY   R = a I + b S + c S^2  S symmetric, so K-major twice; R symmetric too
 //   APPLY  X' = R X               X read MN-major: no transposed copy of it is ever made
-// The identity in R makes X' one product with no addend. The tensor core's
-// accumulator is read out after every 64 k and added up in FP32 registers: its own additions
-// truncate (with 512 k per accumulator the result at 8 x 1024 x 1024 is 1.5e-5 off, with 64 1.4e-6,
-// and 32-bit products give 2.7e-6).
+// The identity in R makes X' one product with no addend. The tensor core's accumulator is read out
+// after every 64 k and added up in FP32 registers: its own additions truncate (with 512 k per
+// accumulator the result at 8 x 1024 x 1024 is 1.5e-5 off, with 64 1.4e-6, and 32-bit products
+// give 2.7e-6).
+//
+// A call is two launches: norm_kernel (sums of squares) and ns_kernel, which stays resident and
+// runs all products with a grid-wide barrier between them. With a launch for each product the
+// chain of 15 small products of a 256 x 256 matrix took 175 us, most of it launches.
+//
+// Tiles of ns_kernel, chosen by choose(): 256 x 256 by a CTA pair, 128 x 128 or 128 x 64 by one
+// CTA. Where a product has fewer tiles than SMs its sum is split along k: the parts go to the
+// workspace in FP32 and are added in order after another barrier.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -36,45 +44,71 @@
 namespace sgemm {
 namespace ns {
 
-constexpr int BT = 128;                   // tile rows and columns
-constexpr int BK = 64;                    // k per stage: 128 bytes of FP16
-constexpr int TILE_BYTES = BT * BK * 2;   // one operand tile, hi or lo
-constexpr int STAGE_BYTES = 4 * TILE_BYTES;
-constexpr int STAGES = 3;
-constexpr int GROUPS = 2, COLS = BT / GROUPS;
-constexpr int EPI_WARPS = 4 * GROUPS, THREADS = 32 * (4 + EPI_WARPS);
-constexpr int TMEM_COLS = 2 * BT;
-constexpr int BAR_BYTES = 8 * (2 * STAGES + 4) + 16;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+using namespace tcx;
 
-// kind::f16: D in FP32 (bits 4-5 = 1), FP16 operands (bits 7-9, 10-12 = 0), MN-major Q (bit 16)
-// where asked, N / 8 (bits 17-22), M / 16 (bits 24-28).
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BT >> 3) << 17) | ((uint32_t)(BT >> 4) << 24);
+constexpr int BK = 64;                    // k per stage: 128 bytes of FP16
+constexpr int BOX = 64;                   // rows of a TMA box
+constexpr int BOX_BYTES = BOX * 128;
+constexpr int MAX_STEPS = 64;
+
+template <int TN_, bool PAIR_>
+struct Cfg {
+  static constexpr int TN = TN_;                        // tile columns
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int BS = PAIR ? 256 : 128;           // tile rows; sizes are padded to it
+  static constexpr int QN = PAIR ? TN / 2 : TN;         // columns of Q that a CTA holds
+  static constexpr int P_TILE = 128 * 128, Q_TILE = QN * 128;  // bytes of hi or lo
+  static constexpr int STAGE_BYTES = 2 * (P_TILE + Q_TILE);
+  static constexpr int STAGES = TN == 64 ? 4 : 3;
+  static constexpr int GROUPS = TN == 64 ? 2 : 4;       // epilogue groups of four warps
+  static constexpr int COLS = TN / GROUPS;
+  static constexpr int EPI_WARPS = 4 * GROUPS, THREADS = 32 * (4 + EPI_WARPS);
+  static constexpr int TMEM_COLS = 2 * TN;
+  static constexpr int SLOTS = BS / 32 * (TN / 32);     // 32 x 32 blocks of a tile
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 4) + 16;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + BAR_BYTES;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(COLS % 32 == 0 && 64 * 65 * 4 <= STAGES * STAGE_BYTES, "epilogue blocks");
+  // kind::f16: D in FP32 (bits 4-5 = 1), FP16 operands (bits 7-9, 10-12 = 0), MN-major Q (bit 16)
+  // where asked, N / 8 (bits 17-22), M / 16 (bits 24-28).
+  static constexpr uint32_t IDESC =
+      (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(BS >> 4) << 24);
+};
 
 enum { GRAM = 0, POLY = 1, APPLY = 2 };
 
+struct Input {
+  const void *g;
+  int type, rows, cols;
+  long long ld, stride;
+  int vec;                 // matrices without gaps, 16-byte aligned
+};
+
 struct Params {
-  int batch, mp, np;       // padded sizes of the short and the long side
-  int K;                   // contraction: np for GRAM, mp else
-  int tiles;               // per matrix
-  int tiles_q;             // APPLY: tiles along n
-  long long lo_p, lo_q;    // rows between the hi and the lo part of an operand
-  float f;                 // factor of the sum
-  __half *out;             // hi; lo is lo_out elements further
-  long long lo_out;
-  const __half *s;         // POLY: S (hi), lo is lo_s elements further
-  long long lo_s;
-  float fs, diag;          // POLY: factor of S, value added on the diagonal
-  // last APPLY: the result in the caller's orientation and type
+  int batch, steps;
+  int mp, np;              // padded sizes of the short and the long side
+  int tiles[3], split[3];  // per product: tiles of a matrix, parts of a sum
+  long long half;          // rows between the hi and the lo part of a matrix: batch * mp
+  __half *x[2], *s, *r;
+  float *partial;
+  unsigned *counter;       // arrivals at the grid-wide barrier
+  Input in;
+  const double *part;      // pieces of the sums of squares
+  int parts;
+  double eps;
+  float x_scale;
+  // per step: factors of the sums of the three products, of S in R, and R's diagonal
+  float f[MAX_STEPS][3], fs[MAX_STEPS], diag[MAX_STEPS];
+  // the result
   void *user;
-  int user_type, tall, m, n;
+  int user_type, tall, m, n, vec;
   long long ldu, user_stride;
   float alpha, beta;
 };
 
-// Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the
-// epilogue gave up.
+// Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the epilogue
+// gave up, 4 = a wait at the grid-wide barrier did.
 __device__ int g_ns_status;
 
 __device__ __forceinline__ uint32_t pack_half(__half a, __half b) {
@@ -82,299 +116,230 @@ __device__ __forceinline__ uint32_t pack_half(__half a, __half b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void split(float v, __half &hi, __half &lo) {
-  hi = __float2half_rn(v);
-  lo = __float2half_rn(v - __half2float(hi));
+// ---- Grid-wide barrier: every CTA arrives once per use, and not before the use before is complete;
+// the count only grows. Work that a CTA
+// does before its arrival is visible to whoever has seen the count, TMA copies included.
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;\n" ::: "memory"); }
+
+__device__ __forceinline__ void grid_arrive(unsigned *counter) {  // one thread, after a CTA barrier
+  proxy_fence();
+  __threadfence();
+  atomicAdd(counter, 1u);
 }
 
-// Tile `t` of a matrix: on and below the diagonal for the symmetric results, else all.
-template <int MODE>
-__device__ __forceinline__ void tile_of(const Params &p, int t, int &tp, int &tq) {
-  if constexpr (MODE == APPLY) {
-    tile_coords(t, p.mp / BT, p.tiles_q, 8, tp, tq);
-  } else {
-    int i = (int)((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    while (i * (i + 1) / 2 > t) --i;
-    tp = i;
-    tq = t - i * (i + 1) / 2;
-  }
-}
-
-template <int MODE, bool LAST>
-__global__ void __launch_bounds__(THREADS, 1)
-    ns_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-              const Params p) {
-  using namespace tcx;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = saddr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t bars = base + STAGES * STAGE_BYTES;
-  const uint32_t acc_full = bars + 8 * (2 * STAGES), acc_empty = acc_full + 16;
-  const uint32_t tmem_slot = acc_empty + 16;
-  volatile uint32_t *tmem_slot_ptr =
-      reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int total = p.tiles * p.batch;
-  const int KT = p.K / BK;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bars + 8 * s, 1);
-      mbar_init(bars + 8 * (STAGES + s), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, EPI_WARPS);
-    }
-    mbar_init_fence();
-    tma_prefetch_map(&map_p);
-    tma_prefetch_map(&map_q);
-  }
-  if (warp == 0) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = *tmem_slot_ptr;
-  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
-
-  if (warp == 0) {
-    // ---- TMA producer: P hi, P lo, Q hi, Q lo of each k step, 64-row boxes of 8 KB
-    Ring<STAGES> st;
-    int issued = 0;  // (up to STAGES)
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      int tp, tq;
-      tile_of<MODE>(p, t % p.tiles, tp, tq);
-      const int y0 = t / p.tiles * p.mp;  // first row of the matrix in its buffer
-      for (int kt = 0; kt < KT; ++kt) {
-        if (!wait_short(bars + 8 * (STAGES + st.slot), st.parity ^ 1u)) {
-          if (lane == 0) atomicCAS(&g_ns_status, 0, 1);
+// One warp; false if the count has not been reached after 8 s.
+__device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned target) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    unsigned v;
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(counter) : "memory");
+      if (v >= target) break;
+      if ((i & 255u) == 255u) {
+        const unsigned long long t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 8 * kWaitLimitNs || i >= (1u << 31)) {
           ok = false;
           break;
         }
-        if (elect_one()) {
-          const uint32_t dst = base + st.slot * STAGE_BYTES, full = bars + 8 * st.slot;
-          const int k = kt * BK;
-          mbar_expect_tx(full, STAGE_BYTES);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int yp = y0 + (h ? (int)p.lo_p : 0), yq = y0 + (h ? (int)p.lo_q : 0);
-            const uint32_t dp = dst + h * TILE_BYTES, dq = dp + 2 * TILE_BYTES;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tma_load_2d(dp + c * 8192, &map_p, k, yp + tp * BT + 64 * c, full);
-              if (MODE == APPLY)
-                tma_load_2d(dq + c * 8192, &map_q, tq * BT + 64 * c, yq + k, full);
-              else
-                tma_load_2d(dq + c * 8192, &map_q, k, yq + tq * BT + 64 * c, full);
-            }
-          }
-        }
-        __syncwarp();
-        issued = min(issued + 1, STAGES);
-        st.next();
       }
     }
-    // the last loads issued must have landed before this warp leaves
-    for (; issued > 0; --issued) {
-      st.parity ^= st.slot == 0 ? 1u : 0u;
-      st.slot = st.slot == 0 ? STAGES - 1 : st.slot - 1;
-      wait_short(bars + 8 * st.slot, st.parity);
-    }
-  } else if (warp == 1) {
-    // ---- MMA issuer: one k step per TMEM accumulator, the corrections first, so that only four
-    // additions meet a sum of full size
-    constexpr uint32_t idesc = IDESC | (MODE == APPLY ? 1u << 16 : 0u);
-    constexpr uint32_t adv_q = MODE == APPLY ? 16 * 128 : 32;
-    Ring<STAGES> st;
-    Ring<2> buf;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      for (int kt = 0; kt < KT; ++kt) {
-        if (!wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) ||
-            !wait_short(bars + 8 * st.slot, st.parity)) {
-          if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
-          ok = false;
-          break;
-        }
-        fence_after();
-        if (elect_one()) {
-          const uint32_t src = base + st.slot * STAGE_BYTES, acc = tmem + buf.slot * BT;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ph = sw128_desc(src + kk * 32, 16);
-            const uint64_t pl = sw128_desc(src + TILE_BYTES + kk * 32, 16);
-            const uint64_t qh = sw128_desc(src + 2 * TILE_BYTES + kk * adv_q, 8192);
-            const uint64_t ql = sw128_desc(src + 3 * TILE_BYTES + kk * adv_q, 8192);
-            mma_f16(acc, pl, qh, idesc, kk != 0 ? 1u : 0u);
-            mma_f16(acc, ph, ql, idesc, 1u);
-          }
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_f16(acc, sw128_desc(src + kk * 32, 16),
-                    sw128_desc(src + 2 * TILE_BYTES + kk * adv_q, 8192), idesc, 1u);
-          mma_commit(bars + 8 * (STAGES + st.slot));
-          mma_commit(acc_full + 8 * buf.slot);
-        }
-        __syncwarp();
-        st.next();
-        buf.next();
-      }
-    }
-  } else if (warp >= 4) {
-    // ---- epilogue: group grp of four warps owns 64 columns, one row per thread
-    const int grp = (warp - 4) >> 2, quad = warp & 3;
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * COLS);
-    Ring<2> buf;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      int tp, tq;
-      tile_of<MODE>(p, t % p.tiles, tp, tq);
-      const int mat = t / p.tiles;
-      const int row = tp * BT + quad * 32 + lane, col0 = tq * BT + grp * COLS;
-      float acc[COLS];
-#pragma unroll
-      for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
-      for (int kt = 0; kt < KT; ++kt) {
-        ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
-        if (!ok) {
-          if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
-          break;
-        }
-        fence_after();
-#pragma unroll
-        for (int j0 = 0; j0 < COLS; j0 += 32) {
-          uint32_t v[32];
-          tmem_ld(lane_base + buf.slot * BT + (uint32_t)j0, v);
-          tmem_wait_ld(v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[j0 + j] += __uint_as_float(v[j]);
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty + 8 * buf.slot);
-        buf.next();
-      }
-      if (!ok) break;
-
-      if constexpr (LAST) {
-        if (row < p.m) {
-#pragma unroll
-          for (int j = 0; j < COLS; ++j) {
-            const int col = col0 + j;
-            if (col < p.n) {
-              const long long at = mat * p.user_stride +
-                                   (p.tall ? col * p.ldu + row : row * p.ldu + col);
-              float v = p.alpha * (acc[j] * p.f);
-              if (p.user_type == NS_F32) {
-                float *d = reinterpret_cast<float *>(p.user) + at;
-                *d = p.beta != 0.0f ? fmaf(p.beta, *d, v) : v;
-              } else if (p.user_type == NS_BF16) {
-                __nv_bfloat16 *d = reinterpret_cast<__nv_bfloat16 *>(p.user) + at;
-                if (p.beta != 0.0f) v = fmaf(p.beta, __bfloat162float(*d), v);
-                *d = __float2bfloat16_rn(v);
-              } else {
-                __half *d = reinterpret_cast<__half *>(p.user) + at;
-                if (p.beta != 0.0f) v = fmaf(p.beta, __half2float(*d), v);
-                *d = __float2half_rn(v);
-              }
-            }
-          }
-        }
-      } else {
-        const long long ld = MODE == APPLY ? p.np : p.mp;
-        __half *o = p.out + ((long long)mat * p.mp + row) * ld + col0;
-        const __half *sh = MODE == POLY ? p.s + ((long long)mat * p.mp + row) * ld + col0 : nullptr;
-#pragma unroll
-        for (int j0 = 0; j0 < COLS; j0 += 8) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = acc[j0 + j] * p.f;
-          if constexpr (MODE == POLY) {
-            const uint4 uh = *reinterpret_cast<const uint4 *>(sh + j0);
-            const uint4 ul = *reinterpret_cast<const uint4 *>(sh + p.lo_s + j0);
-            const uint32_t wh[4] = {uh.x, uh.y, uh.z, uh.w}, wl[4] = {ul.x, ul.y, ul.z, ul.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&wh[j]));
-              const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&wl[j]));
-              v[2 * j] = fmaf(p.fs, a.x + b.x, v[2 * j]);
-              v[2 * j + 1] = fmaf(p.fs, a.y + b.y, v[2 * j + 1]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (row == col0 + j0 + j) v[j] += p.diag;
-          }
-          __half hi[8], lo[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) split(v[j], hi[j], lo[j]);
-          *reinterpret_cast<uint4 *>(o + j0) =
-              make_uint4(pack_half(hi[0], hi[1]), pack_half(hi[2], hi[3]),
-                         pack_half(hi[4], hi[5]), pack_half(hi[6], hi[7]));
-          *reinterpret_cast<uint4 *>(o + p.lo_out + j0) =
-              make_uint4(pack_half(lo[0], lo[1]), pack_half(lo[2], lo[3]),
-                         pack_half(lo[4], lo[5]), pack_half(lo[6], lo[7]));
-          if (MODE != APPLY && tp != tq) {
-            __half *mir = p.out + ((long long)mat * p.mp + col0 + j0) * ld + row;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              mir[j * ld] = hi[j];
-              mir[j * ld + p.lo_out] = lo[j];
-            }
-          }
-        }
-      }
-    }
+    proxy_fence();
+    if (!ok) atomicCAS(&g_ns_status, 0, 4);
   }
-  __syncwarp();
-  griddep_launch_dependents();
-  fence_before();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Unit u of a product: part `sp` of the sum of tile (tp, tq) of matrix `mat`. Tiles of the symmetric
+// products are those on or below the diagonal, row by row (BS / TN of them in a diagonal block).
+template <class C>
+__device__ __forceinline__ void unit_at(const Params &p, int mode, int u, int &mat, int &tp, int &tq,
+                                        int &sp) {
+  sp = u % p.split[mode];
+  u /= p.split[mode];
+  mat = u / p.tiles[mode];
+  const int t = u % p.tiles[mode];
+  if (mode == APPLY) {
+    tile_coords(t, p.mp / C::BS, p.np / C::TN, 4, tp, tq);
+    return;
+  }
+  constexpr int Q = C::BS / C::TN;
+  int i = (int)((sqrtf(8.0f * (t / Q) + 1.0f) - 1.0f) * 0.5f);
+  while (Q * (i + 1) * (i + 2) / 2 <= t) ++i;
+  while (Q * i * (i + 1) / 2 > t) --i;
+  tp = i;
+  tq = t - Q * i * (i + 1) / 2;
+}
+
+// 32 columns from col0 of 32 rows (one per lane, from row0) -> hi and lo of a matrix; mirror: its
+// transposed elements too.
+__device__ __forceinline__ void store_split(__half *o, long long lo, long long ld, uint8_t *buf,
+                                            int lane, long long row0, int col0, bool mirror,
+                                            long long mrow0, int mcol0, const float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      __half a = __float2half_rn(v[j]), b = __float2half_rn(v[j + 1]);
+      if (h) {
+        a = __float2half_rn(v[j] - __half2float(a));
+        b = __float2half_rn(v[j + 1] - __half2float(b));
+      }
+      w[j / 2] = pack_half(a, b);
+      if (mirror) {
+        __half *m = o + h * lo + (mrow0 + j) * ld + mcol0 + lane;
+        m[0] = a;
+        m[ld] = b;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *turn_at(buf, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), j = lane & 3;
+      *reinterpret_cast<uint4 *>(o + h * lo + (row0 + r) * ld + col0 + 8 * j) = *turn_at(buf, r, j);
+    }
+    __syncwarp();
+  }
+}
+
+// What becomes of 32 x 32 sums of a product at (row0, col0) of matrix `mat`.
+__device__ __forceinline__ void finish(const Params &p, int mode, int step, int mat, int row0,
+                                       int col0, bool mirror, uint8_t *buf, int lane,
+                                       float (&v)[32]) {
+  const float f = p.f[step][mode];
+  if (mode == APPLY && step == p.steps - 1) {
+    const int size = p.user_type == NS_F32 ? 4 : 2;
+    void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= f;
+    if (row0 >= p.m || col0 >= p.n) return;
+    if (!p.tall) {
+      store_rows<32>(Out{out, p.user_type, p.ldu, p.m, p.n, p.alpha, p.beta, p.vec}, buf, lane, row0,
+                     col0, v);
+    } else if (row0 + lane < p.m) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j < p.n)
+          finish_out(out, p.user_type, (col0 + j) * p.ldu + row0 + lane, p.alpha * v[j], p.beta);
+    }
+    return;
+  }
+  const long long first = (long long)mat * p.mp;  // row of the matrix in its buffer
+  const long long lds = p.mp, lo_s = p.half * p.mp;
+  if (mode == POLY) {
+    const float fs = p.fs[step];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), j = lane & 3;
+        *turn_at(buf, r, j) = __ldcg(reinterpret_cast<const uint4 *>(
+            p.s + h * lo_s + (first + row0 + r) * lds + col0 + 8 * j));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 u = *turn_at(buf, lane, j);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+          v[8 * j + 2 * e] = fmaf(fs, a.x, v[8 * j + 2 * e]);
+          v[8 * j + 2 * e + 1] = fmaf(fs, a.y, v[8 * j + 2 * e + 1]);
+        }
+      }
+      __syncwarp();
+    }
+    if (row0 == col0) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == lane) v[j] += p.diag[step];
+    }
+    store_split(p.r, lo_s, lds, buf, lane, first + row0, col0, mirror, first + col0, row0, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] *= f;
+  if (mode == GRAM)
+    store_split(p.s, lo_s, lds, buf, lane, first + row0, col0, mirror, first + col0, row0, v);
+  else
+    store_split(p.x[(step + 1) & 1], p.half * p.np, p.np, buf, lane, first + row0, col0, false, 0, 0,
+                v);
 }
 
 // ------------------------------------------------------------------------------------
 // Norm and start values.
 
-template <class T>
-__device__ __forceinline__ float load(const void *x, long long i) {
-  return (float)reinterpret_cast<const T *>(x)[i];
-}
 __device__ __forceinline__ float load(const void *x, int type, long long i) {
-  if (type == NS_F32) return load<float>(x, i);
-  if (type == NS_BF16) return load<__nv_bfloat16>(x, i);
-  return load<__half>(x, i);
+  return load_out(x, type, i);
 }
 
 // Squares of numbers over 2^64 overflow FP32 and those under 2^-64 vanish, so each thread sums
 // the squares of x, of x 2^-70 and of x 2^70; the last step takes the sum that did neither.
 constexpr float kDown = 0x1p-70f, kUp = 0x1p70f;
 
-struct Input {
-  const void *g;
-  int type, rows, cols;
-  long long ld, stride;
-};
+__device__ __forceinline__ void add_square(float (&s)[3], float x) {
+  s[0] = fmaf(x, x, s[0]);
+  s[1] = fmaf(x * kDown, x * kDown, s[1]);
+  s[2] = fmaf(x * kUp, x * kUp, s[2]);
+}
 
-__global__ void __launch_bounds__(256) norm_kernel(const Input in, double *part, int parts) {
+// Block b of matrix b / parts: its share of the matrix, in an order fixed by the shape. Block 0 also
+// resets the counter of the grid-wide barrier.
+__global__ void __launch_bounds__(256)
+    norm_kernel(const Input in, double *part, int parts, unsigned *counter) {
   griddep_wait();
   __shared__ double red[3][8];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
   const int mat = blockIdx.x / parts, piece = blockIdx.x % parts;
-  const long long total = (long long)in.rows * in.cols;
-  const long long first = total * piece / parts, last = total * (piece + 1) / parts;
+  const long long total = (long long)in.rows * in.cols, eights = (total + 7) / 8;
+  const long long first = eights * piece / parts * 8;
+  const long long last = min(total, eights * (piece + 1) / parts * 8);
   float s[3] = {0.0f, 0.0f, 0.0f};
-  long long i = first + threadIdx.x;
-  int r = (int)(i / in.cols), c = (int)(i % in.cols);
-  for (; i < last; i += 256) {
-    const float x = load(in.g, in.type, mat * in.stride + r * in.ld + c);
-    s[0] = fmaf(x, x, s[0]);
-    s[1] = fmaf(x * kDown, x * kDown, s[1]);
-    s[2] = fmaf(x * kUp, x * kUp, s[2]);
-    for (c += 256; c >= in.cols; c -= in.cols) ++r;
+  if (in.vec) {
+    const int size = in.type == NS_F32 ? 4 : 2, per = 16 / size;  // (last - first) % 8 == 0 but at the end
+    const char *g = reinterpret_cast<const char *>(in.g) + mat * in.stride * size;
+#pragma unroll 4
+    for (long long i = first + threadIdx.x * per; i + per <= last; i += 256 * per) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(g + i * size);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (in.type == NS_F32) {
+          add_square(s, __uint_as_float(w[e]));
+        } else if (in.type == NS_BF16) {
+          add_square(s, __uint_as_float(w[e] << 16));
+          add_square(s, __uint_as_float(w[e] & 0xffff0000u));
+        } else {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+          add_square(s, a.x);
+          add_square(s, a.y);
+        }
+      }
+    }
+    const long long tail = last - (last - first) % per + threadIdx.x;
+    if (tail < last) add_square(s, load(g, in.type, tail));
+  } else {
+    long long i = first + threadIdx.x;
+    int r = (int)(i / in.cols), c = (int)(i % in.cols);
+    const int step_r = 256 / in.cols, step_c = 256 % in.cols;
+#pragma unroll 4
+    for (; i < last; i += 256) {
+      add_square(s, load(in.g, in.type, mat * in.stride + r * in.ld + c));
+      r += step_r;
+      c += step_c;
+      if (c >= in.cols) {
+        c -= in.cols;
+        ++r;
+      }
+    }
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -389,117 +354,495 @@ __global__ void __launch_bounds__(256) norm_kernel(const Input in, double *part,
     for (int w = 0; w < 8; ++w) d += red[threadIdx.x][w];
     part[(long long)blockIdx.x * 3 + threadIdx.x] = d;
   }
-  griddep_launch_dependents();
 }
 
-// X_0 times its scale, split, in the short orientation, with zero padding. 64 x 64 tiles; a tall
-// G is turned in shared memory.
-__global__ void __launch_bounds__(256)
-    start_kernel(const Input in, const double *part, int parts, double eps, float scale, int tall,
-                 int mp, int np, __half *x, long long lo) {
-  griddep_wait();
-  __shared__ float t[64][65];
-  __shared__ float mul[2];
-  const int tiles_n = np / 64, per = tiles_n * (mp / 64);
-  const int mat = blockIdx.x / per, tile = blockIdx.x % per;
-  const int r0 = tile / tiles_n * 64, c0 = tile % tiles_n * 64;
-  if (threadIdx.x < 32) {
-    double s[3] = {0.0, 0.0, 0.0};
-    for (int i = threadIdx.x; i < parts; i += 32)
-      for (int q = 0; q < 3; ++q) s[q] += part[((long long)mat * parts + i) * 3 + q];
+// What X_0 of matrix `mat` is multiplied with, in two factors, by one warp.
+__device__ __forceinline__ void start_factors(const Params &p, int mat, float *mul) {
+  const int lane = threadIdx.x & 31;
+  double s[3] = {0.0, 0.0, 0.0};
+  for (int i = lane; i < p.parts; i += 32)
+    for (int q = 0; q < 3; ++q) s[q] += p.part[((long long)mat * p.parts + i) * 3 + q];
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
+  for (int q = 0; q < 3; ++q)
 #pragma unroll
-      for (int o = 16; o > 0; o /= 2) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
-    if (threadIdx.x == 0) {
-      // a sum of NaN fails every comparison and stays NaN
-      double pre = 1.0, sum = s[0];
-      if (s[0] > 1e35) {
-        pre = kDown;
-        sum = s[1];
-      } else if (s[0] < 1e-25) {
-        pre = kUp;
-        sum = s[2];
-      }
-      const double norm = sqrt(sum) / pre;
-      mul[0] = (float)pre;
-      mul[1] = norm + eps > 0.0 ? (float)(scale / (norm + eps) / pre) : (float)(norm * 0.0);
+    for (int o = 16; o > 0; o /= 2) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
+  if (lane == 0) {
+    // a sum of NaN fails every comparison and stays NaN
+    double pre = 1.0, sum = s[0];
+    if (s[0] > 1e35) {
+      pre = kDown;
+      sum = s[1];
+    } else if (s[0] < 1e-25) {
+      pre = kUp;
+      sum = s[2];
     }
+    const double norm = sqrt(sum) / pre;
+    mul[0] = (float)pre;
+    mul[1] = norm + p.eps > 0.0 ? (float)(p.x_scale / (norm + p.eps) / pre) : (float)(norm * 0.0);
   }
-  __syncthreads();
-  const float pre = mul[0], f = mul[1];
-  const int a = threadIdx.x & 63, b = threadIdx.x >> 6;
-  if (tall) {
+}
+
+// X_0 times its scale as hi and lo, in the short orientation, with zero padding. 64 x 64 tiles by
+// whole CTAs; a tall G is turned in t (64 x 65).
+__device__ __forceinline__ void start(const Params &p, float *t, float *mul) {
+  const int tiles_n = p.np / 64, per = tiles_n * (p.mp / 64), nt = blockDim.x;
+  const long long lo = p.half * p.np;
+  const Input &in = p.in;
+  int known = -1;
+  for (int u = blockIdx.x; u < per * p.batch; u += gridDim.x) {
+    const int mat = u / per, tile = u % per;
+    const int r0 = tile / tiles_n * 64, c0 = tile % tiles_n * 64;
+    if (mat != known) {
+      __syncthreads();
+      if (threadIdx.x < 32) start_factors(p, mat, mul);
+      __syncthreads();
+      known = mat;
+    }
+    const float pre = mul[0], f = mul[1];
+    if (p.tall) {
+      __syncthreads();  // the last tile has been read
 #pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const int n = c0 + b + 4 * i, m = r0 + a;  // G is n x m
-      t[a][b + 4 * i] = n < in.rows && m < in.cols
+      for (int e = threadIdx.x; e < 4096; e += nt) {
+        const int a = e & 63, b = e >> 6, n = c0 + b, m = r0 + a;  // G is n x m
+        t[a * 65 + b] = n < in.rows && m < in.cols
                             ? load(in.g, in.type, mat * in.stride + n * in.ld + m)
                             : 0.0f;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
 #pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int m = r0 + b + 4 * i, n = c0 + a;
-    float v;
-    if (tall)
-      v = t[b + 4 * i][a];
-    else
-      v = m < in.rows && n < in.cols ? load(in.g, in.type, mat * in.stride + m * in.ld + n) : 0.0f;
-    __half hi, lw;
-    split(v * pre * f, hi, lw);
-    __half *o = x + ((long long)mat * mp + m) * np + n;
-    o[0] = hi;
-    o[lo] = lw;
+    for (int e = threadIdx.x; e < 2048; e += nt) {
+      const int a = 2 * (e & 31), b = e >> 5, m = r0 + b, n = c0 + a;
+      float v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (p.tall)
+          v[j] = t[b * 65 + a + j];
+        else
+          v[j] = m < in.rows && n + j < in.cols
+                     ? load(in.g, in.type, mat * in.stride + m * in.ld + n + j)
+                     : 0.0f;
+        v[j] = v[j] * pre * f;
+      }
+      const __half h0 = __float2half_rn(v[0]), h1 = __float2half_rn(v[1]);
+      __half *o = p.x[0] + ((long long)mat * p.mp + m) * p.np + n;
+      *reinterpret_cast<uint32_t *>(o) = pack_half(h0, h1);
+      *reinterpret_cast<uint32_t *>(o + lo) = pack_half(__float2half_rn(v[0] - __half2float(h0)),
+                                                        __float2half_rn(v[1] - __half2float(h1)));
+    }
   }
-  griddep_launch_dependents();
 }
 
 // steps == 0: out = alpha X_0 + beta out.
-__global__ void __launch_bounds__(256)
-    copy_kernel(const __half *x, long long lo, float f, Params p) {
-  griddep_wait();
-  const long long total = (long long)p.batch * p.m * p.n;
+__global__ void __launch_bounds__(256) copy_kernel(const Params p) {
+  __shared__ float mul[2];
+  const long long total = (long long)p.in.rows * p.in.cols;
+  const int mat = blockIdx.y;
+  if (threadIdx.x < 32) start_factors(p, mat, mul);
+  __syncthreads();
+  const int size = p.user_type == NS_F32 ? 4 : 2;
+  void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const int mat = (int)(i / ((long long)p.m * p.n));
-    const long long e = i % ((long long)p.m * p.n);
-    const int row = (int)(e / p.n), col = (int)(e % p.n);
-    const __half *s = x + ((long long)mat * p.mp + row) * p.np + col;
-    const long long at =
-        mat * p.user_stride + (p.tall ? col * p.ldu + row : row * p.ldu + col);
-    float v = p.alpha * (f * (__half2float(s[0]) + __half2float(s[lo])));
-    if (p.beta != 0.0f) v = fmaf(p.beta, load(p.user, p.user_type, at), v);
-    if (p.user_type == NS_F32)
-      reinterpret_cast<float *>(p.user)[at] = v;
-    else if (p.user_type == NS_BF16)
-      reinterpret_cast<__nv_bfloat16 *>(p.user)[at] = __float2bfloat16_rn(v);
-    else
-      reinterpret_cast<__half *>(p.user)[at] = __float2half_rn(v);
+    const long long r = i / p.in.cols, c = i % p.in.cols;
+    const float x = load(p.in.g, p.in.type, mat * p.in.stride + r * p.in.ld + c) * mul[0] * mul[1];
+    finish_out(out, p.user_type, r * p.ldu + c, p.alpha * x, p.beta);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// All products. Warp 0: TMA producer, warp 1: MMA issuer (one elected lane of each); warps 4 ..:
+// epilogue, a group of four warps owns COLS columns of the tile, warp w of it TMEM lanes (rows)
+// 32 (w % 4) .. + 31. All warps together make the start values.
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    ns_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
+              const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_r,
+              const __grid_constant__ Params p) {
+  constexpr bool PAIR = C::PAIR;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = saddr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::STAGES * C::STAGE_BYTES + C::EPI_WARPS * TURN_BYTES;
+  const uint32_t acc_full = bars + 8 * (2 * C::STAGES), acc_empty = acc_full + 16;
+  const uint32_t tmem_slot = acc_empty + 16;
+  volatile uint32_t *tmem_slot_ptr =
+      reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int cta = PAIR ? (int)(blockIdx.x & 1u) : 0;
+  const int first = (int)(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+  const int stride = (int)(PAIR ? gridDim.x >> 1 : gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bars + 8 * s, 1);
+      mbar_init(bars + 8 * (C::STAGES + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, PAIR ? 2 * C::EPI_WARPS : C::EPI_WARPS);
+    }
+    mbar_init_fence();
+    tma_prefetch_map(&map_x0);
+    tma_prefetch_map(&map_x1);
+    tma_prefetch_map(&map_s);
+    tma_prefetch_map(&map_r);
+  }
+  if (warp == 0) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  {
+    __shared__ float mul[2];
+    start(p, reinterpret_cast<float *>(sbase), mul);
+  }
+  proxy_fence();
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) grid_arrive(p.counter);  // (orders this CTA's use of shared memory too)
+  if constexpr (PAIR) cluster_sync_all();        // the other CTA's barriers are initialised
+  fence_after();
+  const uint32_t tmem = *tmem_slot_ptr;
+  unsigned passed = gridDim.x;                   // count of the barrier uses so far
+
+  if (warp < 4) {
+    if constexpr (PAIR) reg_dealloc<64>();       // 640 x 96 = 128 x 64 + 512 x 104
+    if (warp == 0) {
+      // ---- TMA producer: P hi, P lo, Q hi, Q lo of each k step, in boxes of 64 rows
+      Ring<C::STAGES> st;
+      int issued = 0;  // (up to STAGES)
+      bool ok = true;
+      for (int ph = 0; ph < 3 * p.steps && ok; ++ph) {
+        const int mode = ph % 3, step = ph / 3;
+        ok = grid_wait(p.counter, passed);
+        if (!ok) break;
+        const CUtensorMap *mx = step & 1 ? &map_x1 : &map_x0;
+        const CUtensorMap *mp = mode == GRAM ? mx : mode == POLY ? &map_s : &map_r;
+        const CUtensorMap *mq = mode == POLY ? &map_s : mx;
+        const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
+        const int total = p.batch * p.tiles[mode] * S;
+        for (int u = first; u < total && ok; u += stride) {
+          int mat, tp, tq, sp;
+          unit_at<C>(p, mode, u, mat, tp, tq, sp);
+          const int y0 = mat * p.mp, yp = y0 + tp * C::BS + cta * 128;
+          const int q0 = tq * C::TN + cta * (PAIR ? C::QN : 0);
+          const int k1 = (int)((long long)KT * (sp + 1) / S);
+          for (int kt = (int)((long long)KT * sp / S); kt < k1; ++kt) {
+            ok = wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u);
+            if (!ok) {
+              if (lane == 0) atomicCAS(&g_ns_status, 0, 1);
+              break;
+            }
+            if (elect_one()) {
+              const uint32_t dst = base + st.slot * C::STAGE_BYTES;
+              const uint32_t full = PAIR ? in_cta(bars + 8 * st.slot, 0) : bars + 8 * st.slot;
+              const int k = kt * BK;
+              if (!PAIR || cta == 0)
+                mbar_expect_tx(bars + 8 * st.slot, (PAIR ? 2 : 1) * C::STAGE_BYTES);
+              const auto get = [&](uint32_t to, const CUtensorMap *m, int x, int y) {
+                if constexpr (PAIR)
+                  tma_load_2d_pair(to, m, x, y, full);
+                else
+                  tma_load_2d(to, m, x, y, full);
+              };
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int lo = h ? (int)p.half : 0;
+#pragma unroll
+                for (int c = 0; c < 128 / BOX; ++c)
+                  get(dst + h * C::P_TILE + c * BOX_BYTES, mp, k, lo + yp + BOX * c);
+                const uint32_t dq = dst + 2 * C::P_TILE + h * C::Q_TILE;
+#pragma unroll
+                for (int c = 0; c < C::QN / BOX; ++c) {
+                  if (mode == APPLY)
+                    get(dq + c * BOX_BYTES, mq, q0 + BOX * c, lo + y0 + k);
+                  else
+                    get(dq + c * BOX_BYTES, mq, k, lo + y0 + q0 + BOX * c);
+                }
+              }
+            }
+            __syncwarp();
+            issued = min(issued + 1, C::STAGES);
+            st.next();
+          }
+        }
+        passed += gridDim.x * (S > 1 ? 2u : 1u);
+      }
+      // the last loads issued must have landed before this warp leaves (a pair's: the leader waits
+      // for both, and the CTAs leave together)
+      for (; issued > 0 && (!PAIR || cta == 0); --issued) {
+        st.parity ^= st.slot == 0 ? 1u : 0u;
+        st.slot = st.slot == 0 ? C::STAGES - 1 : st.slot - 1;
+        wait_short(bars + 8 * st.slot, st.parity);
+      }
+    } else if (warp == 1 && (!PAIR || cta == 0)) {
+      // ---- MMA issuer: one k step per TMEM accumulator, the corrections first, so that only four
+      // additions meet a sum of full size
+      const uint64_t ph0 = sw128_desc(base, 16), pl0 = sw128_desc(base + C::P_TILE, 16);
+      const uint64_t qh0 = sw128_desc(base + 2 * C::P_TILE, BOX_BYTES);
+      const uint64_t ql0 = sw128_desc(base + 2 * C::P_TILE + C::Q_TILE, BOX_BYTES);
+      Ring<C::STAGES> st;
+      Ring<2> buf;
+      bool ok = true;
+      for (int ph = 0; ph < 3 * p.steps && ok; ++ph) {
+        const int mode = ph % 3;
+        const uint32_t idesc = C::IDESC | (mode == APPLY ? 1u << 16 : 0u);
+        const uint32_t adv_q = (mode == APPLY ? 16 * 128 : 32) >> 4;
+        const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
+        const int total = p.batch * p.tiles[mode] * S;
+        for (int u = first; u < total && ok; u += stride) {
+          const int sp = u % S;
+          const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
+          for (int kt = 0; kt < steps; ++kt) {
+            ok = wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
+                 wait_short(bars + 8 * st.slot, st.parity);
+            if (!ok) {
+              if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
+              break;
+            }
+            fence_after();
+            if (elect_one()) {
+              const uint32_t at = st.slot * (uint32_t)(C::STAGE_BYTES >> 4);
+              const uint32_t acc = tmem + buf.slot * C::TN;
+              const auto mma = [&](uint64_t a, uint64_t b, uint32_t more) {
+                if constexpr (PAIR)
+                  mma_f16_pair(acc, a, b, idesc, more);
+                else
+                  mma_f16(acc, a, b, idesc, more);
+              };
+#pragma unroll
+              for (uint32_t kk = 0; kk < BK / 16; ++kk) {
+                mma(pl0 + at + kk * 2, qh0 + at + kk * adv_q, kk != 0);
+                mma(ph0 + at + kk * 2, ql0 + at + kk * adv_q, 1u);
+              }
+#pragma unroll
+              for (uint32_t kk = 0; kk < BK / 16; ++kk)
+                mma(ph0 + at + kk * 2, qh0 + at + kk * adv_q, 1u);
+              if constexpr (PAIR) {
+                mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
+                mma_commit_pair(acc_full + 8 * buf.slot);
+              } else {
+                mma_commit(bars + 8 * (C::STAGES + st.slot));
+                mma_commit(acc_full + 8 * buf.slot);
+              }
+            }
+            __syncwarp();
+            st.next();
+            buf.next();
+          }
+        }
+      }
+    }
+  } else {
+    // ---- epilogue. After a wait that gave up a warp goes on without its sums, so that it still
+    // arrives at the barriers of its CTA.
+    if constexpr (PAIR) reg_alloc<104>();
+    const int grp = (warp - 4) >> 2, quad = warp & 3;
+    const uint32_t src0 = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
+    uint8_t *turn = sbase + C::STAGES * C::STAGE_BYTES + (warp - 4) * TURN_BYTES;
+    Ring<2> buf;
+    bool ok = true;
+    for (int ph = 0; ph < 3 * p.steps; ++ph) {
+      const int mode = ph % 3, step = ph / 3;
+      const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
+      const int total = p.batch * p.tiles[mode] * S;
+      for (int u = first; u < total; u += stride) {
+        int mat, tp, tq, sp;
+        unit_at<C>(p, mode, u, mat, tp, tq, sp);
+        const int row0 = tp * C::BS + cta * 128 + quad * 32, col0 = tq * C::TN + grp * C::COLS;
+        const bool mirror = mode != APPLY && tq * C::TN < tp * C::BS;
+        const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
+        float acc[C::COLS];
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+        for (int kt = 0; kt < steps && ok; ++kt) {
+          ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
+          if (!ok) {
+            if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
+            break;
+          }
+          fence_after();
+#pragma unroll
+          for (int j0 = 0; j0 < C::COLS; j0 += 16) {
+            uint32_t v[16];
+            tmem_ld(src0 + buf.slot * C::TN + (uint32_t)j0, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              arrive_in(in_cta(acc_empty + 8 * buf.slot, 0));
+            else
+              mbar_arrive(acc_empty + 8 * buf.slot);
+          }
+          buf.next();
+        }
+        // (S is read for R: this CTA's producer has seen it written before its first copy, and this
+        // makes it visible to this warp)
+        if (mode == POLY && S == 1) ok = grid_wait(p.counter, passed) && ok;
+#pragma unroll
+        for (int j0 = 0; j0 < C::COLS; j0 += 32) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = acc[j0 + j];
+          if (S == 1) {
+            finish(p, mode, step, mat, row0, col0 + j0, mirror, turn, lane, v);
+          } else {
+            const int slot = (cta * 4 + quad) * (C::TN / 32) + (grp * C::COLS + j0) / 32;
+            float *o = p.partial + ((long long)u * C::SLOTS + slot) * 1024 + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[32 * j] = v[j];
+          }
+        }
+      }
+      proxy_fence();
+      named_barrier(1, 32 * C::EPI_WARPS);
+      if (warp == 4) {
+        // (a CTA without work in this product must not arrive while others are still to arrive for
+        // the one before)
+        ok = grid_wait(p.counter, passed) && ok;
+        if (lane == 0) grid_arrive(p.counter);
+        __syncwarp();
+      }
+      if (S > 1) {
+        // the parts of each sum, in order; one 32 x 32 block per warp at a time
+        ok = grid_wait(p.counter, passed + gridDim.x) && ok;
+        const int blocks = p.batch * p.tiles[mode] * C::SLOTS;
+        for (int w = blockIdx.x * C::EPI_WARPS + warp - 4; w < blocks;
+             w += gridDim.x * C::EPI_WARPS) {
+          const int t = w / C::SLOTS, slot = w % C::SLOTS;
+          int mat, tp, tq, sp;
+          unit_at<C>(p, mode, t * S, mat, tp, tq, sp);
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+          for (int q = 0; q < S; ++q) {
+            const float *i = p.partial + (((long long)t * S + q) * C::SLOTS + slot) * 1024 + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += __ldcg(i + 32 * j);
+          }
+          finish(p, mode, step, mat, tp * C::BS + slot / (C::TN / 32) * 32,
+                 tq * C::TN + slot % (C::TN / 32) * 32, mode != APPLY && tq * C::TN < tp * C::BS,
+                 turn, lane, v);
+        }
+        proxy_fence();
+        named_barrier(1, 32 * C::EPI_WARPS);
+        if (threadIdx.x == 128) grid_arrive(p.counter);
+        __syncwarp();
+      }
+      passed += gridDim.x * (S > 1 ? 2u : 1u);
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {
+    cluster_sync_all();  // no instruction, copy or arrival of the other CTA is under way
+    if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  } else {
+    if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
 // ------------------------------------------------------------------------------------
 // Host side
 
-struct Layout {
-  long long m, n, mp, np;       // short and long side, padded to whole tiles
+using Pair = Cfg<256, true>;
+using Wide = Cfg<128, false>;
+using Narrow = Cfg<64, false>;
+
+// How a problem runs: tile shape and parts of the sums, with the sizes that follow.
+struct Plan {
+  int shape;                    // 0 Pair, 1 Wide, 2 Narrow
+  long long mp, np;             // short and long side, padded
+  long long tiles[3];
+  int split[3];
   int parts;                    // pieces of a matrix in the norm
-  size_t x, s, part, bytes;     // element counts (FP16) of one X, of one S; bytes of all
+  long long ctas;
+  size_t x, s, partial, bytes;  // elements of one X and one S (FP16) and of the partials (FP32)
 };
 
-static Layout layout(int batch, int rows, int cols) {
-  Layout l;
-  l.m = std::min(rows, cols);
-  l.n = std::max(rows, cols);
-  l.mp = ceil_div(l.m, BT) * BT;
-  l.np = ceil_div(l.n, BT) * BT;
-  l.parts = (int)std::min<long long>(128, ceil_div(l.m * l.n, 4096));
-  l.x = (size_t)2 * batch * l.mp * l.np;
-  l.s = (size_t)2 * batch * l.mp * l.mp;
-  l.part = (size_t)3 * batch * l.parts * sizeof(double);
-  l.bytes = 2 * (2 * l.x + 2 * l.s) + l.part;
-  return l;
+// Estimated time of a plan in cycles. A k step of 64 costs its MMAs (12 instructions of TN / 2
+// cycles) or the copy of its operands, whichever is longer (measured: about 50 bytes per cycle and
+// SM with every SM loading, 64 with few); a product also costs its barrier and the stores of a
+// CTA's tiles, and a split sum another barrier and pass.
+static double cost(const Plan &q, int shape, int batch, long long mp, long long np, long long slots,
+                   Plan *out) {
+  static const int rows[3] = {Pair::BS, Wide::BS, Narrow::BS}, tn[3] = {256, 128, 64};
+  static const double mma[3] = {1536, 768, 384};
+  static const double bytes[3] = {Pair::STAGE_BYTES, Wide::STAGE_BYTES, Narrow::STAGE_BYTES};
+  static const double tile[3] = {6000, 2500, 2000};
+  *out = q;
+  const long long tm = mp / rows[shape], per = rows[shape] / tn[shape];
+  out->tiles[GRAM] = out->tiles[POLY] = per * tm * (tm + 1) / 2;
+  out->tiles[APPLY] = tm * (np / tn[shape]);
+  double total = 0.0;
+  for (int mode = 0; mode < 3; ++mode) {
+    const long long t = out->tiles[mode] * batch, KT = (mode == GRAM ? np : mp) / BK;
+    double best = 1e300;
+    for (int S = 1; S <= 16 && S <= KT; ++S) {
+      if (S > 1 && t * S > slots) break;
+      const long long waves = (t * S + slots - 1) / slots;
+      const double busy = std::min<double>(1.0, (double)t * S / slots);
+      const double step = std::max(mma[shape], bytes[shape] / (64.0 - 14.0 * busy));
+      const double c = waves * (step * ((KT + S - 1) / S) + tile[shape]) + 2500.0 +
+                       (S > 1 ? 5000.0 : 0.0);
+      if (c < best) {
+        best = c;
+        out->split[mode] = S;
+      }
+    }
+    total += best;
+  }
+  return total;
+}
+
+static Plan choose(int batch, int rows, int cols, int sms, const int *pairs) {
+  Plan best{};
+  const long long m = std::min(rows, cols), n = std::max(rows, cols);
+  double least = 1e300;
+  for (int shape = 0; shape < 3; ++shape) {
+    const int unit = shape == 0 ? Pair::BS : 128;
+    const long long mp = ceil_div(m, unit) * unit, np = ceil_div(n, unit) * unit;
+    Plan q{};
+    q.shape = shape;
+    q.mp = mp;
+    q.np = np;
+    const long long slots = shape == 0 ? *pairs : sms;
+    if (slots < 1) continue;
+    Plan w;
+    const double c = cost(q, shape, batch, mp, np, slots, &w);
+    if (c < least) {
+      least = c;
+      best = w;
+    }
+  }
+  const long long slots = best.shape == 0 ? *pairs : sms;
+  long long units = 1;
+  size_t most = 0;
+  const int area = best.shape == 0 ? 256 * 256 : best.shape == 1 ? 128 * 128 : 128 * 64;
+  for (int mode = 0; mode < 3; ++mode) {
+    const long long u = best.tiles[mode] * batch * best.split[mode];
+    units = std::max(units, u);
+    if (best.split[mode] > 1) most = std::max(most, (size_t)u * area);
+  }
+  best.ctas = std::min(units, slots) * (best.shape == 0 ? 2 : 1);
+  best.parts = (int)std::min<long long>(592, ceil_div(m * n, 8192));
+  best.x = (size_t)2 * batch * best.mp * best.np;
+  best.s = (size_t)2 * batch * best.mp * best.mp;
+  best.partial = most;
+  best.bytes = 2 * (2 * best.x + 2 * best.s) + 4 * best.partial +
+               (size_t)3 * batch * best.parts * sizeof(double) + 256;
+  return best;
 }
 
 // Bounds of the spectral norms: of X_t in bx[0 .. steps], of a I + b S + c S^2 in br[t], each with
@@ -536,98 +879,107 @@ static bool bounds(const float *co, int steps, double *bx, double *br) {
 // Power of two that takes numbers up to `bound` below 2^14 (FP16 ends at 65504).
 static float scale_for(double bound) { return (float)std::exp2(14.0 - std::ceil(std::log2(bound))); }
 
-static std::once_flag g_once[64];
-static cudaError_t g_err[64];
+struct Device {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int pairs = 0;  // CTA pairs resident at once
+};
+static Device g_dev[64];
 
-static cudaError_t kernel_setup() {
+static cudaError_t kernel_setup(const int **pairs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(g_once[dev], [dev]() {
-    const auto set = [](auto k) {
-      return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  Device &d = g_dev[dev];
+  std::call_once(d.once, [&d]() {
+    const auto set = [](auto k, int bytes) {
+      return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     };
-    cudaError_t err = set(ns_kernel<GRAM, false>);
-    if (err == cudaSuccess) err = set(ns_kernel<POLY, false>);
-    if (err == cudaSuccess) err = set(ns_kernel<APPLY, false>);
-    if (err == cudaSuccess) err = set(ns_kernel<APPLY, true>);
-    g_err[dev] = err;
+    d.err = set(ns_kernel<Pair>, Pair::SMEM_BYTES);
+    if (d.err == cudaSuccess) d.err = set(ns_kernel<Wide>, Wide::SMEM_BYTES);
+    if (d.err == cudaSuccess) d.err = set(ns_kernel<Narrow>, Narrow::SMEM_BYTES);
+    if (d.err == cudaSuccess)
+      d.pairs = cluster_ctas_of(ns_kernel<Pair>, Pair::THREADS, Pair::SMEM_BYTES, 2) / 2;
   });
-  return g_err[dev];
+  *pairs = &d.pairs;
+  return d.err;
 }
 
-static cudaError_t run(const Layout &l, const Input &in, int batch, int steps, const float *co,
-                       const double *bx, const double *br, float eps, Params p, __half *ws,
-                       int sms, cudaStream_t stream) {
-  __half *x[2] = {ws, ws + l.x};
-  __half *s = x[1] + l.x, *r = s + l.s;
-  double *part = reinterpret_cast<double *>(r + l.s);
-  const long long rows = 2LL * batch * l.mp;   // hi, then lo
-  if (rows > 0x7fffffffLL || l.np > 0x7fffffffLL) return cudaErrorInvalidValue;
-  CUtensorMap mx[2], ms, mr;
-  if (!encode_map_2d_narrow(&mx[0], x[0], 2, rows, l.np, l.np, 64) ||
-      !encode_map_2d_narrow(&mx[1], x[1], 2, rows, l.np, l.np, 64) ||
-      !encode_map_2d_narrow(&ms, s, 2, rows, l.mp, l.mp, 64) ||
-      !encode_map_2d_narrow(&mr, r, 2, rows, l.mp, l.mp, 64))
-    return cudaErrorInvalidValue;
-  const long long starts = (l.mp / 64) * (l.np / 64) * batch;
-  const long long tm = l.mp / BT, tn = l.np / BT;
-  if (starts > 0x7fffffffLL || (long long)batch * l.parts > 0x7fffffffLL)
-    return cudaErrorInvalidConfiguration;
-  float sx = scale_for(bx[0]);
-  cudaError_t e = launch_1d(norm_kernel, batch * l.parts, 256, 0, 1, stream, in, part, l.parts);
-  if (e == cudaSuccess)
-    e = launch_1d(start_kernel, (int)starts, 256, 0, 1, stream, in, part, l.parts, (double)eps, sx,
-                  p.tall, (int)l.mp, (int)l.np, x[0], (long long)(l.x / 2));
-  if (e != cudaSuccess) return e;
+// All CTAs wait for one another, so the launch is cooperative: it starts when all fit.
+template <class C>
+static cudaError_t launch(const CUtensorMap (&m)[4], const Params &p, int ctas,
+                          cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C::PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ns_kernel<C>, m[0], m[1], m[2], m[3], p);
+}
+
+static cudaError_t run(const Plan &l, const float *co, const double *bx, const double *br,
+                       Params &p, char *ws, cudaStream_t stream) {
   p.mp = (int)l.mp;
   p.np = (int)l.np;
-  if (steps == 0) {
-    const long long blocks = std::min<long long>(8LL * sms, ceil_div(batch * l.m * l.n, 256));
-    return launch_1d(copy_kernel, (int)blocks, 256, 0, 1, stream, x[0], (long long)(l.x / 2),
-                     1.0f / sx, p);
+  p.half = p.batch * l.mp;
+  p.x[0] = reinterpret_cast<__half *>(ws);
+  p.x[1] = p.x[0] + l.x;
+  p.s = p.x[1] + l.x;
+  p.r = p.s + l.s;
+  p.partial = reinterpret_cast<float *>(p.r + l.s);
+  double *part = reinterpret_cast<double *>(p.partial + l.partial);
+  p.part = part;
+  p.parts = l.parts;
+  p.counter = reinterpret_cast<unsigned *>(part + (size_t)3 * p.batch * l.parts);
+  p.x_scale = p.steps > 0 ? scale_for(bx[0]) : 1.0f;
+  const long long rows = 2 * p.half;  // hi, then lo
+  long long units = (long long)p.batch * l.parts;
+  for (int mode = 0; mode < 3; ++mode) {
+    p.tiles[mode] = (int)l.tiles[mode];
+    p.split[mode] = l.split[mode];
+    units = std::max(units, p.batch * l.tiles[mode] * l.split[mode] * 64);
   }
-  const long long half_rows = (long long)batch * l.mp;
-  p.lo_p = p.lo_q = half_rows;
-  const auto grid = [&](long long tiles) { return (int)std::min<long long>(tiles * batch, sms); };
-  for (int t = 0; t < steps; ++t) {
+  units = std::max(units, l.mp / 64 * (l.np / 64) * p.batch);
+  if (rows > 0x7fffffffLL || l.np > 0x7fffffffLL || units > 0x7fffffffLL)
+    return cudaErrorInvalidConfiguration;
+  cudaError_t e = launch_1d(norm_kernel, p.batch * l.parts, 256, 0, 1, stream, p.in, part, l.parts,
+                            p.counter);
+  if (e != cudaSuccess) return e;
+  if (p.steps == 0) {
+    const long long blocks = std::min<long long>(1024, ceil_div((long long)p.m * p.n, 1024));
+    if (p.batch > 65535) return cudaErrorInvalidConfiguration;
+    copy_kernel<<<dim3((unsigned)blocks, (unsigned)p.batch), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  float sx = p.x_scale;
+  for (int t = 0; t < p.steps; ++t) {
     const float ss = scale_for(bx[t] * bx[t]), sr = scale_for(br[t]), sn = scale_for(bx[t + 1]);
-    Params q = p;
-    q.K = (int)l.np;
-    q.tiles = (int)(tm * (tm + 1) / 2);
-    q.f = ss / (sx * sx);
-    q.out = s;
-    q.lo_out = (long long)(l.s / 2);
-    e = launch_1d(ns_kernel<GRAM, false>, grid(q.tiles), THREADS, SMEM_BYTES, 1, stream, mx[t & 1],
-                  mx[t & 1], q);
-    if (e != cudaSuccess) return e;
-    q.K = (int)l.mp;
-    q.f = (float)((double)co[2] * sr / ((double)ss * ss));
-    q.fs = (float)((double)co[1] * sr / ss);
-    q.diag = co[0] * sr;
-    q.s = s;
-    q.lo_s = (long long)(l.s / 2);
-    q.out = r;
-    e = launch_1d(ns_kernel<POLY, false>, grid(q.tiles), THREADS, SMEM_BYTES, 1, stream, ms, ms, q);
-    if (e != cudaSuccess) return e;
-    q.tiles = (int)(tm * tn);
-    q.tiles_q = (int)tn;
-    q.lo_out = (long long)(l.x / 2);
-    q.out = x[(t + 1) & 1];
-    if (t + 1 < steps) {
-      q.f = sn / (sr * sx);
-      e = launch_1d(ns_kernel<APPLY, false>, grid(q.tiles), THREADS, SMEM_BYTES, 1, stream, mr,
-                    mx[t & 1], q);
-    } else {
-      q.f = 1.0f / (sr * sx);
-      e = launch_1d(ns_kernel<APPLY, true>, grid(q.tiles), THREADS, SMEM_BYTES, 1, stream, mr,
-                    mx[t & 1], q);
-    }
-    if (e != cudaSuccess) return e;
+    p.f[t][GRAM] = ss / (sx * sx);
+    p.f[t][POLY] = (float)((double)co[2] * sr / ((double)ss * ss));
+    p.fs[t] = (float)((double)co[1] * sr / ss);
+    p.diag[t] = co[0] * sr;
+    p.f[t][APPLY] = t + 1 < p.steps ? sn / (sr * sx) : 1.0f / (sr * sx);
     sx = sn;
   }
-  return cudaSuccess;
+  CUtensorMap m[4];
+  if (!encode_map_2d_narrow(&m[0], p.x[0], 2, rows, l.np, l.np, BOX) ||
+      !encode_map_2d_narrow(&m[1], p.x[1], 2, rows, l.np, l.np, BOX) ||
+      !encode_map_2d_narrow(&m[2], p.s, 2, rows, l.mp, l.mp, BOX) ||
+      !encode_map_2d_narrow(&m[3], p.r, 2, rows, l.mp, l.mp, BOX))
+    return cudaErrorInvalidValue;
+  if (l.shape == 0) return launch<Pair>(m, p, (int)l.ctas, stream);
+  if (l.shape == 1) return launch<Wide>(m, p, (int)l.ctas, stream);
+  return launch<Narrow>(m, p, (int)l.ctas, stream);
 }
 
 }  // namespace ns
@@ -639,7 +991,17 @@ extern "C" int ns_orthogonalize_workspace_size(int batch, int rows, int cols, si
   if (batch < 0) return -1;
   if (rows < 0) return -2;
   if (cols < 0) return -3;
-  if (bytes) *bytes = batch == 0 || rows == 0 || cols == 0 ? 0 : ns::layout(batch, rows, cols).bytes;
+  if (bytes == nullptr) return 0;
+  *bytes = 0;
+  if (batch == 0 || rows == 0 || cols == 0) return 0;
+  int sms = 0;
+  const int whole = 76, *pairs = nullptr;
+  if (device_setup(&sms) != cudaSuccess || ns::kernel_setup(&pairs) != cudaSuccess) {
+    (void)cudaGetLastError();
+    sms = 152;  // no device here: the answer for a whole GB300
+    pairs = &whole;
+  }
+  *bytes = ns::choose(batch, rows, cols, sms, pairs).bytes;
   return 0;
 }
 
@@ -674,26 +1036,35 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   if (!any) return 0;
 
   int sms = 0;
+  const int *pairs = nullptr;
   cudaError_t e = device_setup(&sms);
-  if (e == cudaSuccess) e = ns::kernel_setup();
+  if (e == cudaSuccess) e = ns::kernel_setup(&pairs);
   if (e != cudaSuccess) return (int)e;
-  const ns::Layout l = ns::layout(batch, rows, cols);
+  const ns::Plan l = ns::choose(batch, rows, cols, sms, pairs);
+  const auto aligned = [](const void *q, long long a, long long b, int t) {
+    const int size = t == NS_F32 ? 4 : 2;
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && a * size % 16 == 0 && b * size % 16 == 0;
+  };
   ns::Params p{};
   p.batch = batch;
+  p.steps = steps;
+  p.in = ns::Input{G, g_type, rows, cols, ldg, g_stride,
+                   (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type)};
+  p.eps = eps;
   p.user = out;
   p.user_type = out_type;
   p.tall = rows > cols;
-  p.m = (int)l.m;
-  p.n = (int)l.n;
+  p.m = std::min(rows, cols);
+  p.n = std::max(rows, cols);
+  p.vec = aligned(out, ldo, batch > 1 ? o_stride : 0, out_type);
   p.ldu = ldo;
   p.user_stride = o_stride;
   p.alpha = alpha;
   p.beta = beta;
-  __half *ws = nullptr;
+  char *ws = nullptr;
   e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), l.bytes, workspace_pool(), stream);
   if (e != cudaSuccess) return (int)e;
-  const ns::Input in{G, g_type, rows, cols, ldg, g_stride};
-  e = ns::run(l, in, batch, steps, coefficients, bx, br, eps, p, ws, sms, stream);
+  e = ns::run(l, coefficients, bx, br, p, ws, stream);
   const cudaError_t ef = cudaFreeAsync(ws, stream);
   return (int)(e == cudaSuccess ? ef : e);
 }

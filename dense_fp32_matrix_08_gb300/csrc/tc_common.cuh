@@ -272,9 +272,143 @@ __device__ __forceinline__ void reg_alloc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// Barrier among `threads` threads of the CTA (id 1 .. 15; 0 is __syncthreads), whole warps: a warp
+// of which some lanes are still elsewhere would be counted twice.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
 // This thread's arrival at `bar` once its cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// ---- Results on their way out. A warp's buffer of 2 KB holds 64 bytes of each of 32 rows as four
+// 16-byte pieces; piece j of row r lies at j ^ (r / 2 % 4), so that 8 neighbouring rows' pieces,
+// and the four pieces of 2 neighbouring rows, lie in different banks. Lanes put the rows that they
+// hold and take what neighbouring lanes then store side by side (or the other way round).
+constexpr int TURN_BYTES = 32 * 64;
+
+__device__ __forceinline__ uint4 *turn_at(uint8_t *buf, int row, int piece) {
+  return reinterpret_cast<uint4 *>(buf + row * 64 + ((piece ^ (row >> 1 & 3)) << 4));
+}
+
+enum { OUT_F32 = 0, OUT_BF16 = 1, OUT_F16 = 2 };
+
+// A row-major result out = alpha * v + beta * out; rows and cols: what exists of it.
+struct Out {
+  void *ptr;
+  int type;
+  long long ld;
+  int rows, cols;
+  float alpha, beta;
+  int vec;  // 16-byte accesses to rows are aligned
+};
+
+__device__ __forceinline__ float load_out(const void *ptr, int type, long long at) {
+  if (type == OUT_F32) return reinterpret_cast<const float *>(ptr)[at];
+  if (type == OUT_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(ptr)[at]);
+  return __half2float(reinterpret_cast<const __half *>(ptr)[at]);
+}
+
+__device__ __forceinline__ void store_out(void *ptr, int type, long long at, float v) {
+  if (type == OUT_F32)
+    reinterpret_cast<float *>(ptr)[at] = v;
+  else if (type == OUT_BF16)
+    reinterpret_cast<__nv_bfloat16 *>(ptr)[at] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<__half *>(ptr)[at] = __float2half_rn(v);
+}
+
+// out[at] = y + beta * out[at]
+__device__ __forceinline__ void finish_out(void *ptr, int type, long long at, float y, float beta) {
+  store_out(ptr, type, at, beta != 0.0f ? fmaf(beta, load_out(ptr, type, at), y) : y);
+}
+
+__device__ __forceinline__ uint32_t pack_out(int type, float a, float b) {
+  if (type == OUT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// CN (16 or 32) neighbouring columns from `col` of 32 rows, one per lane, the first is row0.
+template <int CN>
+__device__ __forceinline__ void store_rows(const Out &o, uint8_t *buf, int lane, int row0, int col,
+                                           const float (&v)[CN]) {
+  const int rows = min(32, o.rows - row0), cols = min(CN, o.cols - col);
+  if (o.vec && o.beta == 0.0f && o.type != OUT_F32) {
+    // packed: 2 CN bytes of a row
+#pragma unroll
+    for (int j = 0; j < CN; j += 8)
+      *turn_at(buf, lane, j / 8) =
+          make_uint4(pack_out(o.type, o.alpha * v[j], o.alpha * v[j + 1]),
+                     pack_out(o.type, o.alpha * v[j + 2], o.alpha * v[j + 3]),
+                     pack_out(o.type, o.alpha * v[j + 4], o.alpha * v[j + 5]),
+                     pack_out(o.type, o.alpha * v[j + 6], o.alpha * v[j + 7]));
+    __syncwarp();
+    constexpr int LANES = CN / 8;  // per row
+    const int c = 8 * (lane % LANES);
+#pragma unroll
+    for (int r = lane / LANES; r < 32; r += 32 / LANES) {
+      const uint4 w = *turn_at(buf, r, lane % LANES);
+      if (r >= rows) continue;
+      uint16_t *d = reinterpret_cast<uint16_t *>(o.ptr) + (row0 + r) * o.ld + col + c;
+      if (c + 8 <= cols) {
+        *reinterpret_cast<uint4 *>(d) = w;
+      } else {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < cols) d[j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
+      }
+    }
+    __syncwarp();
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < CN; h += 16) {  // 16 columns at a time in FP32
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4 *>(turn_at(buf, lane, j)) =
+          make_float4(o.alpha * v[h + 4 * j], o.alpha * v[h + 4 * j + 1],
+                      o.alpha * v[h + 4 * j + 2], o.alpha * v[h + 4 * j + 3]);
+    __syncwarp();
+    if (o.vec && o.type == OUT_F32) {
+      const int c = 4 * (lane & 3);
+#pragma unroll
+      for (int r = lane >> 2; r < 32; r += 8) {
+        float4 w = *reinterpret_cast<const float4 *>(turn_at(buf, r, lane & 3));
+        if (r >= rows || h + c >= cols) continue;
+        float *d = reinterpret_cast<float *>(o.ptr) + (row0 + r) * o.ld + col + h + c;
+        if (h + c + 4 <= cols) {
+          if (o.beta != 0.0f) {
+            const float4 q = *reinterpret_cast<const float4 *>(d);
+            w = make_float4(fmaf(o.beta, q.x, w.x), fmaf(o.beta, q.y, w.y), fmaf(o.beta, q.z, w.z),
+                            fmaf(o.beta, q.w, w.w));
+          }
+          *reinterpret_cast<float4 *>(d) = w;
+        } else {
+          const float y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (h + c + j < cols) d[j] = o.beta != 0.0f ? fmaf(o.beta, d[j], y[j]) : y[j];
+        }
+      }
+    } else {
+      const int c = lane & 15;
+#pragma unroll 4
+      for (int r = lane >> 4; r < 32; r += 2) {
+        const float y = reinterpret_cast<const float *>(turn_at(buf, r, c >> 2))[c & 3];
+        if (r < rows && h + c < cols)
+          finish_out(o.ptr, o.type, (row0 + r) * o.ld + col + h + c, y, o.beta);
+      }
+    }
+    __syncwarp();
+  }
 }
 
 }  // namespace tcx

@@ -46,11 +46,11 @@ int ns_orthogonalize(int batch, int rows, int cols, const void *G, int g_type, i
                      float alpha, float beta, void *out, int out_type, int ldo,
                      long long o_stride, cudaStream_t stream);
 
-/* Bytes of workspace that the call takes from the library's pool. Returns 0 or -1, -2, -3 for a
- * negative batch, rows or cols. */
+/* Bytes of workspace that the call takes from the library's pool on the current device (without
+ * one: on a whole GB300). Returns 0 or -1, -2, -3 for a negative batch, rows or cols. */
 int ns_orthogonalize_workspace_size(int batch, int rows, int cols, size_t *bytes);
 
-/* Reads and clears the device status word of ns_orthogonalize (synchronising): 0 = fine, 1 - 3 =
+/* Reads and clears the device status word of ns_orthogonalize (synchronising): 0 = fine, 1 - 4 =
  * a wait gave up after about a second and the call's result is not to be used. Returns 0 or a
  * cudaError_t. */
 int ns_orthogonalize_status(int *status);
