@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + EPI_WARPS * TURN_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-  static_assert(COLS % 32 == 0 && 64 * 65 * 4 <= STAGES * STAGE_BYTES, "epilogue blocks");
+  static_assert(COLS % 32 == 0 && 128 * 129 * 4 <= STAGES * STAGE_BYTES, "epilogue blocks");
   // kind::f16: D in FP32 (bits 4-5 = 1), FP16 operands (bits 7-9, 10-12 = 0), MN-major Q (bit 16)
   // where asked, N / 8 (bits 17-22), M / 16 (bits 24-28).
   static constexpr uint32_t IDESC =
@@ -83,6 +83,7 @@ struct Input {
   int type, rows, cols;
   long long ld, stride;
   int vec;                 // matrices without gaps, 16-byte aligned
+  int rows_vec;            // 16-byte loads of rows are aligned
 };
 
 struct Params {
@@ -122,9 +123,7 @@ __device__ __forceinline__ uint32_t pack_half(__half a, __half b) {
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;\n" ::: "memory"); }
 
 __device__ __forceinline__ void grid_arrive(unsigned *counter) {  // one thread, after a CTA barrier
-  proxy_fence();
-  __threadfence();
-  atomicAdd(counter, 1u);
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;\n" ::"l"(counter) : "memory");
 }
 
 // One warp; false if the count has not been reached after 8 s.
@@ -145,7 +144,7 @@ __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned targ
         }
       }
     }
-    proxy_fence();
+    proxy_fence();  // the copies that follow read what other CTAs' plain stores wrote
     if (!ok) atomicCAS(&g_ns_status, 0, 4);
   }
   return __all_sync(0xffffffffu, ok);
@@ -188,22 +187,33 @@ __device__ __forceinline__ void store_split(__half *o, long long lo, long long l
         b = __float2half_rn(v[j + 1] - __half2float(b));
       }
       w[j / 2] = pack_half(a, b);
-      if (mirror) {
-        __half *m = o + h * lo + (mrow0 + j) * ld + mcol0 + lane;
-        m[0] = a;
-        m[ld] = b;
-      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *turn_at(buf, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     __syncwarp();
+    const int piece = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), j = lane & 3;
-      *reinterpret_cast<uint4 *>(o + h * lo + (row0 + r) * ld + col0 + 8 * j) = *turn_at(buf, r, j);
+      const int r = 8 * i + (lane >> 2);
+      *reinterpret_cast<uint4 *>(o + h * lo + (row0 + r) * ld + col0 + 8 * piece) =
+          *turn_at(buf, r, piece);
     }
     __syncwarp();
+    if (mirror) {  // the block's columns as rows of the buffer
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        reinterpret_cast<uint16_t *>(turn_at(buf, j, lane >> 3))[lane & 7] =
+            (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        *reinterpret_cast<uint4 *>(o + h * lo + (mrow0 + r) * ld + mcol0 + 8 * piece) =
+            *turn_at(buf, r, piece);
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -235,14 +245,17 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
     const float fs = p.fs[step];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= f;
+    uint4 in[2][4];  // both halves are on their way before the first is used
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        in[h][i] = __ldcg(reinterpret_cast<const uint4 *>(
+            p.s + h * lo_s + (first + row0 + 8 * i + (lane >> 2)) * lds + col0 + 8 * (lane & 3)));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), j = lane & 3;
-        *turn_at(buf, r, j) = __ldcg(reinterpret_cast<const uint4 *>(
-            p.s + h * lo_s + (first + row0 + r) * lds + col0 + 8 * j));
-      }
+      for (int i = 0; i < 4; ++i) *turn_at(buf, 8 * i + (lane >> 2), lane & 3) = in[h][i];
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -382,16 +395,50 @@ __device__ __forceinline__ void start_factors(const Params &p, int mat, float *m
   }
 }
 
-// X_0 times its scale as hi and lo, in the short orientation, with zero padding. 64 x 64 tiles by
-// whole CTAs; a tall G is turned in t (64 x 65).
+// Eight neighbouring elements of row r from column c (0 out of range).
+__device__ __forceinline__ void load8(const Input &in, const char *g, int r, int c, float (&v)[8]) {
+  const int size = in.type == NS_F32 ? 4 : 2;
+  if (in.rows_vec && r < in.rows && c + 8 <= in.cols) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(g + (r * in.ld + c) * size);
+    const uint4 u = __ldg(q);
+    if (in.type == NS_F32) {
+      const uint4 u2 = __ldg(q + 1);
+      const uint32_t w[8] = {u.x, u.y, u.z, u.w, u2.x, u2.y, u2.z, u2.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (in.type == NS_BF16) {
+          v[2 * e] = __uint_as_float(w[e] << 16);
+          v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        } else {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+          v[2 * e] = a.x;
+          v[2 * e + 1] = a.y;
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = r < in.rows && c + e < in.cols ? load(g, in.type, r * in.ld + c + e) : 0.0f;
+}
+
+// X_0 times its scale as hi and lo, in the short orientation, with zero padding. 128 x 128 tiles by
+// whole CTAs; a tall G is turned in t (128 x 129).
 __device__ __forceinline__ void start(const Params &p, float *t, float *mul) {
-  const int tiles_n = p.np / 64, per = tiles_n * (p.mp / 64), nt = blockDim.x;
+  const int tiles_n = p.np / 128, per = tiles_n * (p.mp / 128), nt = blockDim.x;
   const long long lo = p.half * p.np;
   const Input &in = p.in;
+  const int size = in.type == NS_F32 ? 4 : 2;
   int known = -1;
   for (int u = blockIdx.x; u < per * p.batch; u += gridDim.x) {
     const int mat = u / per, tile = u % per;
-    const int r0 = tile / tiles_n * 64, c0 = tile % tiles_n * 64;
+    const int r0 = tile / tiles_n * 128, c0 = tile % tiles_n * 128;
+    const char *g = reinterpret_cast<const char *>(in.g) + mat * in.stride * size;
     if (mat != known) {
       __syncthreads();
       if (threadIdx.x < 32) start_factors(p, mat, mul);
@@ -401,34 +448,37 @@ __device__ __forceinline__ void start(const Params &p, float *t, float *mul) {
     const float pre = mul[0], f = mul[1];
     if (p.tall) {
       __syncthreads();  // the last tile has been read
-#pragma unroll 4
-      for (int e = threadIdx.x; e < 4096; e += nt) {
-        const int a = e & 63, b = e >> 6, n = c0 + b, m = r0 + a;  // G is n x m
-        t[a * 65 + b] = n < in.rows && m < in.cols
-                            ? load(in.g, in.type, mat * in.stride + n * in.ld + m)
-                            : 0.0f;
+#pragma unroll 2
+      for (int e = threadIdx.x; e < 2048; e += nt) {
+        const int m = 8 * (e & 15), n = e >> 4;  // G is n x m
+        float v[8];
+        load8(in, g, c0 + n, r0 + m, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[(m + j) * 129 + n] = v[j];
       }
       __syncthreads();
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int e = threadIdx.x; e < 2048; e += nt) {
-      const int a = 2 * (e & 31), b = e >> 5, m = r0 + b, n = c0 + a;
-      float v[2];
+      const int n = 8 * (e & 15), m = e >> 4;
+      float v[8];
+      if (p.tall) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (p.tall)
-          v[j] = t[b * 65 + a + j];
-        else
-          v[j] = m < in.rows && n + j < in.cols
-                     ? load(in.g, in.type, mat * in.stride + m * in.ld + n + j)
-                     : 0.0f;
-        v[j] = v[j] * pre * f;
+        for (int j = 0; j < 8; ++j) v[j] = t[m * 129 + n + j];
+      } else {
+        load8(in, g, r0 + m, c0 + n, v);
       }
-      const __half h0 = __float2half_rn(v[0]), h1 = __float2half_rn(v[1]);
-      __half *o = p.x[0] + ((long long)mat * p.mp + m) * p.np + n;
-      *reinterpret_cast<uint32_t *>(o) = pack_half(h0, h1);
-      *reinterpret_cast<uint32_t *>(o + lo) = pack_half(__float2half_rn(v[0] - __half2float(h0)),
-                                                        __float2half_rn(v[1] - __half2float(h1)));
+      uint32_t hi[4], lw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = v[2 * j] * pre * f, b = v[2 * j + 1] * pre * f;
+        const __half ha = __float2half_rn(a), hb = __float2half_rn(b);
+        hi[j] = pack_half(ha, hb);
+        lw[j] = pack_half(__float2half_rn(a - __half2float(ha)), __float2half_rn(b - __half2float(hb)));
+      }
+      __half *o = p.x[0] + ((long long)mat * p.mp + r0 + m) * p.np + c0 + n;
+      *reinterpret_cast<uint4 *>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4 *>(o + lo) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
   }
 }
@@ -704,12 +754,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       }
-      proxy_fence();
       named_barrier(1, 32 * C::EPI_WARPS);
       if (warp == 4) {
         // (a CTA without work in this product must not arrive while others are still to arrive for
         // the one before)
-        ok = grid_wait(p.counter, passed) && ok;
+        if (first >= total) ok = grid_wait(p.counter, passed) && ok;
         if (lane == 0) grid_arrive(p.counter);
         __syncwarp();
       }
@@ -734,7 +783,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                  tq * C::TN + slot % (C::TN / 32) * 32, mode != APPLY && tq * C::TN < tp * C::BS,
                  turn, lane, v);
         }
-        proxy_fence();
         named_barrier(1, 32 * C::EPI_WARPS);
         if (threadIdx.x == 128) grid_arrive(p.counter);
         __syncwarp();
@@ -949,7 +997,7 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
     p.split[mode] = l.split[mode];
     units = std::max(units, p.batch * l.tiles[mode] * l.split[mode] * 64);
   }
-  units = std::max(units, l.mp / 64 * (l.np / 64) * p.batch);
+  units = std::max(units, l.mp / 128 * (l.np / 128) * p.batch);
   if (rows > 0x7fffffffLL || l.np > 0x7fffffffLL || units > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
   cudaError_t e = launch_1d(norm_kernel, p.batch * l.parts, 256, 0, 1, stream, p.in, part, l.parts,
@@ -1049,7 +1097,8 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   p.batch = batch;
   p.steps = steps;
   p.in = ns::Input{G, g_type, rows, cols, ldg, g_stride,
-                   (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type)};
+                   (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type),
+                   aligned(G, ldg, batch > 1 ? g_stride : 0, g_type)};
   p.eps = eps;
   p.user = out;
   p.user_type = out_type;
