@@ -47,7 +47,7 @@ namespace ns {
 using namespace tcx;
 
 constexpr int BK = 64;                    // k per stage: 128 bytes of FP16
-constexpr int BOX = 64;                   // rows of a TMA box
+constexpr int BOX = 64;                   // rows of a small TMA box
 constexpr int BOX_BYTES = BOX * 128;
 constexpr int MAX_STEPS = 64;
 
@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr int P_TILE = 128 * 128, Q_TILE = QN * 128;  // bytes of hi or lo
   static constexpr int STAGE_BYTES = 2 * (P_TILE + Q_TILE);
   static constexpr int STAGES = TN == 64 ? 4 : 3;
-  static constexpr int GROUPS = TN == 64 ? 2 : 4;       // epilogue groups of four warps
+  static constexpr int GROUPS = 2;                      // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;
   static constexpr int EPI_WARPS = 4 * GROUPS, THREADS = 32 * (4 + EPI_WARPS);
   static constexpr int TMEM_COLS = 2 * TN;
@@ -106,6 +106,12 @@ struct Params {
   int user_type, tall, m, n, vec;
   long long ldu, user_stride;
   float alpha, beta;
+};
+
+// Tensor maps. p: X_0, X_1 (both X buffers), S, R in boxes of 128 rows; q: X_0, X_1, S in boxes of
+// 64 rows (K-major for 64 columns of Q; MN-major for a k step).
+struct Maps {
+  CUtensorMap p[4], q[3];
 };
 
 // Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the epilogue
@@ -171,62 +177,18 @@ __device__ __forceinline__ void unit_at(const Params &p, int mode, int u, int &m
   tq = t - Q * i * (i + 1) / 2;
 }
 
-// 32 columns from col0 of 32 rows (one per lane, from row0) -> hi and lo of a matrix; mirror: its
-// transposed elements too.
-__device__ __forceinline__ void store_split(__half *o, long long lo, long long ld, uint8_t *buf,
-                                            int lane, long long row0, int col0, bool mirror,
-                                            long long mrow0, int mcol0, const float (&v)[32]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      __half a = __float2half_rn(v[j]), b = __float2half_rn(v[j + 1]);
-      if (h) {
-        a = __float2half_rn(v[j] - __half2float(a));
-        b = __float2half_rn(v[j + 1] - __half2float(b));
-      }
-      w[j / 2] = pack_half(a, b);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *turn_at(buf, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    __syncwarp();
-    const int piece = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      *reinterpret_cast<uint4 *>(o + h * lo + (row0 + r) * ld + col0 + 8 * piece) =
-          *turn_at(buf, r, piece);
-    }
-    __syncwarp();
-    if (mirror) {  // the block's columns as rows of the buffer
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        reinterpret_cast<uint16_t *>(turn_at(buf, j, lane >> 3))[lane & 7] =
-            (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        *reinterpret_cast<uint4 *>(o + h * lo + (mrow0 + r) * ld + mcol0 + 8 * piece) =
-            *turn_at(buf, r, piece);
-      }
-      __syncwarp();
-    }
-  }
-}
-
-// What becomes of 32 x 32 sums of a product at (row0, col0) of matrix `mat`.
+// What becomes of 32 x 32 sums of a product at (row0, col0) of matrix `mat`: v holds 32 columns of
+// one row per lane. One copy of this code serves all products (ns_kernel): each CTA runs it once or
+// twice between two barriers, and what it costs then is mostly the fetching of its instructions.
 __device__ __forceinline__ void finish(const Params &p, int mode, int step, int mat, int row0,
                                        int col0, bool mirror, uint8_t *buf, int lane,
                                        float (&v)[32]) {
   const float f = p.f[step][mode];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] *= f;
   if (mode == APPLY && step == p.steps - 1) {
     const int size = p.user_type == NS_F32 ? 4 : 2;
     void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= f;
     if (row0 >= p.m || col0 >= p.n) return;
     if (!p.tall) {
       store_rows<32>(Out{out, p.user_type, p.ldu, p.m, p.n, p.alpha, p.beta, p.vec}, buf, lane, row0,
@@ -239,23 +201,22 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
     }
     return;
   }
-  const long long first = (long long)mat * p.mp;  // row of the matrix in its buffer
-  const long long lds = p.mp, lo_s = p.half * p.mp;
+  const int part = lane & 3, sub = lane >> 2;  // 16-byte piece and row of 8 of coalesced accesses
+  const long long ld = mode == APPLY ? p.np : p.mp, lo = p.half * ld;
+  const long long row = (long long)mat * p.mp + row0;  // in the buffer
   if (mode == POLY) {
     const float fs = p.fs[step];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= f;
+    const __half *s = p.s + (row + sub) * ld + col0 + 8 * part;
     uint4 in[2][4];  // both halves are on their way before the first is used
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        in[h][i] = __ldcg(reinterpret_cast<const uint4 *>(
-            p.s + h * lo_s + (first + row0 + 8 * i + (lane >> 2)) * lds + col0 + 8 * (lane & 3)));
+        in[h][i] = __ldcg(reinterpret_cast<const uint4 *>(s + h * lo + 8 * i * ld));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *turn_at(buf, 8 * i + (lane >> 2), lane & 3) = in[h][i];
+      for (int i = 0; i < 4; ++i) *turn_at(buf, 8 * i + sub, part) = in[h][i];
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -275,16 +236,42 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
       for (int j = 0; j < 32; ++j)
         if (j == lane) v[j] += p.diag[step];
     }
-    store_split(p.r, lo_s, lds, buf, lane, first + row0, col0, mirror, first + col0, row0, v);
-    return;
   }
+  // hi, then lo = what hi leaves; below the diagonal the transposed block too
+  __half *base = mode == GRAM ? p.s : mode == POLY ? p.r : p.x[(step + 1) & 1];
+  __half *o = base + (row + sub) * ld + col0 + 8 * part;
+  __half *m = base + ((long long)mat * p.mp + col0 + sub) * ld + row0 + 8 * part;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h, o += lo, m += lo) {
+    uint32_t w[16];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] *= f;
-  if (mode == GRAM)
-    store_split(p.s, lo_s, lds, buf, lane, first + row0, col0, mirror, first + col0, row0, v);
-  else
-    store_split(p.x[(step + 1) & 1], p.half * p.np, p.np, buf, lane, first + row0, col0, false, 0, 0,
-                v);
+    for (int j = 0; j < 32; j += 2) {
+      const __half2 a = __floats2half2_rn(v[j], v[j + 1]);
+      w[j / 2] = *reinterpret_cast<const uint32_t *>(&a);
+      const float2 b = __half22float2(a);
+      v[j] -= b.x;
+      v[j + 1] -= b.y;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *turn_at(buf, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4 *>(o + 8 * i * ld) = *turn_at(buf, 8 * i + sub, part);
+    __syncwarp();
+    if (mirror) {  // the block's columns as rows of the buffer
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        reinterpret_cast<uint16_t *>(turn_at(buf, j, lane >> 3))[lane & 7] =
+            (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(m + 8 * i * ld) = *turn_at(buf, 8 * i + sub, part);
+      __syncwarp();
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------
@@ -506,9 +493,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const Params p) {
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    ns_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
-              const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_r,
-              const __grid_constant__ Params p) {
+    ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   constexpr bool PAIR = C::PAIR;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = saddr(smem_raw);
@@ -534,10 +519,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(acc_empty + 8 * b, PAIR ? 2 * C::EPI_WARPS : C::EPI_WARPS);
     }
     mbar_init_fence();
-    tma_prefetch_map(&map_x0);
-    tma_prefetch_map(&map_x1);
-    tma_prefetch_map(&map_s);
-    tma_prefetch_map(&map_r);
+    for (int i = 0; i < 4; ++i) tma_prefetch_map(&maps.p[i]);
+    for (int i = 0; i < 3; ++i) tma_prefetch_map(&maps.q[i]);
   }
   if (warp == 0) {
     if constexpr (PAIR) {
@@ -562,9 +545,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   unsigned passed = gridDim.x;                   // count of the barrier uses so far
 
   if (warp < 4) {
-    if constexpr (PAIR) reg_dealloc<64>();       // 640 x 96 = 128 x 64 + 512 x 104
+    if constexpr (PAIR) reg_dealloc<56>();       // 384 x 168 = 128 x 56 + 256 x 224
     if (warp == 0) {
-      // ---- TMA producer: P hi, P lo, Q hi, Q lo of each k step, in boxes of 64 rows
+      // ---- TMA producer: P hi, P lo, Q hi, Q lo of each k step
       Ring<C::STAGES> st;
       int issued = 0;  // (up to STAGES)
       bool ok = true;
@@ -572,9 +555,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int mode = ph % 3, step = ph / 3;
         ok = grid_wait(p.counter, passed);
         if (!ok) break;
-        const CUtensorMap *mx = step & 1 ? &map_x1 : &map_x0;
-        const CUtensorMap *mp = mode == GRAM ? mx : mode == POLY ? &map_s : &map_r;
-        const CUtensorMap *mq = mode == POLY ? &map_s : mx;
+        const int x = step & 1;
+        const CUtensorMap *mp = &maps.p[mode == GRAM ? x : mode + 1];
+        const CUtensorMap *mq = &maps.q[mode == POLY ? 2 : x];
+        if (C::QN == 128 && mode != APPLY) mq = &maps.p[mode == POLY ? 2 : x];
         const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
         const int total = p.batch * p.tiles[mode] * S;
         for (int u = first; u < total && ok; u += stride) {
@@ -604,16 +588,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int lo = h ? (int)p.half : 0;
-#pragma unroll
-                for (int c = 0; c < 128 / BOX; ++c)
-                  get(dst + h * C::P_TILE + c * BOX_BYTES, mp, k, lo + yp + BOX * c);
+                get(dst + h * C::P_TILE, mp, k, lo + yp);
                 const uint32_t dq = dst + 2 * C::P_TILE + h * C::Q_TILE;
+                if (mode != APPLY) {
+                  get(dq, mq, k, lo + y0 + q0);
+                } else {
 #pragma unroll
-                for (int c = 0; c < C::QN / BOX; ++c) {
-                  if (mode == APPLY)
+                  for (int c = 0; c < C::QN / BOX; ++c)
                     get(dq + c * BOX_BYTES, mq, q0 + BOX * c, lo + y0 + k);
-                  else
-                    get(dq + c * BOX_BYTES, mq, k, lo + y0 + q0 + BOX * c);
                 }
               }
             }
@@ -692,7 +674,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ---- epilogue. After a wait that gave up a warp goes on without its sums, so that it still
     // arrives at the barriers of its CTA.
-    if constexpr (PAIR) reg_alloc<104>();
+    if constexpr (PAIR) reg_alloc<224>();
     const int grp = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t src0 = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
     uint8_t *turn = sbase + C::STAGES * C::STAGE_BYTES + (warp - 4) * TURN_BYTES;
@@ -702,90 +684,92 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int mode = ph % 3, step = ph / 3;
       const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
       const int total = p.batch * p.tiles[mode] * S;
-      for (int u = first; u < total; u += stride) {
-        int mat, tp, tq, sp;
-        unit_at<C>(p, mode, u, mat, tp, tq, sp);
-        const int row0 = tp * C::BS + cta * 128 + quad * 32, col0 = tq * C::TN + grp * C::COLS;
-        const bool mirror = mode != APPLY && tq * C::TN < tp * C::BS;
-        const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
-        float acc[C::COLS];
+      // pass 0: this CTA's units; pass 1, of split sums: their parts added in order, one 32 x 32
+      // block per warp at a time
+#pragma unroll 1
+      for (int pass = 0; pass < (S > 1 ? 2 : 1); ++pass) {
+        const int end = pass ? p.batch * p.tiles[mode] * C::SLOTS : total;
+        const int by = pass ? (int)gridDim.x * C::EPI_WARPS : stride;
+#pragma unroll 1
+        for (int i = pass ? (int)blockIdx.x * C::EPI_WARPS + warp - 4 : first; i < end; i += by) {
+          float acc[C::COLS];
 #pragma unroll
-        for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
-        for (int kt = 0; kt < steps && ok; ++kt) {
-          ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
-          if (!ok) {
-            if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
-            break;
-          }
-          fence_after();
+          for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+          int mat, tp, tq, sp, row0, col0;
+          unit_at<C>(p, mode, pass ? i / C::SLOTS * S : i, mat, tp, tq, sp);
+          if (pass == 0) {
+            row0 = tp * C::BS + cta * 128 + quad * 32;
+            col0 = tq * C::TN + grp * C::COLS;
+            const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
+            for (int kt = 0; kt < steps && ok; ++kt) {
+              ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
+              if (!ok) {
+                if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
+                break;
+              }
+              fence_after();
 #pragma unroll
-          for (int j0 = 0; j0 < C::COLS; j0 += 16) {
-            uint32_t v[16];
-            tmem_ld(src0 + buf.slot * C::TN + (uint32_t)j0, v);
-            tmem_wait_ld(v);
+              for (int j0 = 0; j0 < C::COLS; j0 += 16) {
+                uint32_t v[16];
+                tmem_ld(src0 + buf.slot * C::TN + (uint32_t)j0, v);
+                tmem_wait_ld(v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
-          }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              arrive_in(in_cta(acc_empty + 8 * buf.slot, 0));
-            else
-              mbar_arrive(acc_empty + 8 * buf.slot);
-          }
-          buf.next();
-        }
-        // (S is read for R: this CTA's producer has seen it written before its first copy, and this
-        // makes it visible to this warp)
-        if (mode == POLY && S == 1) ok = grid_wait(p.counter, passed) && ok;
-#pragma unroll
-        for (int j0 = 0; j0 < C::COLS; j0 += 32) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = acc[j0 + j];
-          if (S == 1) {
-            finish(p, mode, step, mat, row0, col0 + j0, mirror, turn, lane, v);
+                for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+              }
+              fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (PAIR)
+                  arrive_in(in_cta(acc_empty + 8 * buf.slot, 0));
+                else
+                  mbar_arrive(acc_empty + 8 * buf.slot);
+              }
+              buf.next();
+            }
+            // (S is read for R: this CTA's producer has seen it written before its first copy, and
+            // this makes it visible to this warp)
+            if (mode == POLY && S == 1) ok = grid_wait(p.counter, passed) && ok;
           } else {
-            const int slot = (cta * 4 + quad) * (C::TN / 32) + (grp * C::COLS + j0) / 32;
-            float *o = p.partial + ((long long)u * C::SLOTS + slot) * 1024 + lane;
+            const int t = i / C::SLOTS, slot = i % C::SLOTS;
+            row0 = tp * C::BS + slot / (C::TN / 32) * 32;
+            col0 = tq * C::TN + slot % (C::TN / 32) * 32;
+            for (int q = 0; q < S; ++q) {
+              const float *from =
+                  p.partial + (((long long)t * S + q) * C::SLOTS + slot) * 1024 + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[32 * j] = v[j];
+              for (int j = 0; j < 32; ++j) acc[j] += __ldcg(from + 32 * j);
+            }
           }
-        }
-      }
-      named_barrier(1, 32 * C::EPI_WARPS);
-      if (warp == 4) {
-        // (a CTA without work in this product must not arrive while others are still to arrive for
-        // the one before)
-        if (first >= total) ok = grid_wait(p.counter, passed) && ok;
-        if (lane == 0) grid_arrive(p.counter);
-        __syncwarp();
-      }
-      if (S > 1) {
-        // the parts of each sum, in order; one 32 x 32 block per warp at a time
-        ok = grid_wait(p.counter, passed + gridDim.x) && ok;
-        const int blocks = p.batch * p.tiles[mode] * C::SLOTS;
-        for (int w = blockIdx.x * C::EPI_WARPS + warp - 4; w < blocks;
-             w += gridDim.x * C::EPI_WARPS) {
-          const int t = w / C::SLOTS, slot = w % C::SLOTS;
-          int mat, tp, tq, sp;
-          unit_at<C>(p, mode, t * S, mat, tp, tq, sp);
-          float v[32];
+          const bool mirror = mode != APPLY && tq * C::TN < tp * C::BS;
+#pragma unroll 1
+          for (int j0 = 0; j0 < (pass ? 32 : C::COLS); j0 += 32) {
+            float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-          for (int q = 0; q < S; ++q) {
-            const float *i = p.partial + (((long long)t * S + q) * C::SLOTS + slot) * 1024 + lane;
+            for (int j = 0; j < 32; ++j) {  // (acc stays in registers: no index that varies)
+              v[j] = acc[j];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += __ldcg(i + 32 * j);
+              for (int c = 32; c < C::COLS; c += 32)
+                if (j0 == c) v[j] = acc[c + j];
+            }
+            if (pass == 1 || S == 1) {
+              finish(p, mode, step, mat, row0, col0 + j0, mirror, turn, lane, v);
+            } else {
+              const int slot = (cta * 4 + quad) * (C::TN / 32) + (grp * C::COLS + j0) / 32;
+              float *o = p.partial + ((long long)i * C::SLOTS + slot) * 1024 + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[32 * j] = v[j];
+            }
           }
-          finish(p, mode, step, mat, tp * C::BS + slot / (C::TN / 32) * 32,
-                 tq * C::TN + slot % (C::TN / 32) * 32, mode != APPLY && tq * C::TN < tp * C::BS,
-                 turn, lane, v);
         }
         named_barrier(1, 32 * C::EPI_WARPS);
-        if (threadIdx.x == 128) grid_arrive(p.counter);
-        __syncwarp();
+        if (warp == 4) {
+          // (a CTA without work in this product must not arrive while others are still to arrive
+          // for the one before)
+          if (pass == 0 && first >= total) ok = grid_wait(p.counter, passed) && ok;
+          if (lane == 0) grid_arrive(p.counter);
+          __syncwarp();
+        }
+        if (S > 1 && pass == 0) ok = grid_wait(p.counter, passed + gridDim.x) && ok;
       }
       passed += gridDim.x * (S > 1 ? 2u : 1u);
     }
@@ -956,8 +940,7 @@ static cudaError_t kernel_setup(const int **pairs) {
 
 // All CTAs wait for one another, so the launch is cooperative: it starts when all fit.
 template <class C>
-static cudaError_t launch(const CUtensorMap (&m)[4], const Params &p, int ctas,
-                          cudaStream_t stream) {
+static cudaError_t launch(const Maps &m, const Params &p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
   cfg.blockDim = dim3(C::THREADS, 1, 1);
@@ -972,7 +955,7 @@ static cudaError_t launch(const CUtensorMap (&m)[4], const Params &p, int ctas,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C::PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, ns_kernel<C>, m[0], m[1], m[2], m[3], p);
+  return cudaLaunchKernelEx(&cfg, ns_kernel<C>, m, p);
 }
 
 static cudaError_t run(const Plan &l, const float *co, const double *bx, const double *br,
@@ -1019,12 +1002,14 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
     p.f[t][APPLY] = t + 1 < p.steps ? sn / (sr * sx) : 1.0f / (sr * sx);
     sx = sn;
   }
-  CUtensorMap m[4];
-  if (!encode_map_2d_narrow(&m[0], p.x[0], 2, rows, l.np, l.np, BOX) ||
-      !encode_map_2d_narrow(&m[1], p.x[1], 2, rows, l.np, l.np, BOX) ||
-      !encode_map_2d_narrow(&m[2], p.s, 2, rows, l.mp, l.mp, BOX) ||
-      !encode_map_2d_narrow(&m[3], p.r, 2, rows, l.mp, l.mp, BOX))
-    return cudaErrorInvalidValue;
+  Maps m;
+  const __half *const at[4] = {p.x[0], p.x[1], p.s, p.r};
+  for (int i = 0; i < 4; ++i) {
+    const long long ld = i < 2 ? l.np : l.mp;
+    if (!encode_map_2d_narrow(&m.p[i], at[i], 2, rows, ld, ld, 128) ||
+        (i < 3 && !encode_map_2d_narrow(&m.q[i], at[i], 2, rows, ld, ld, BOX)))
+      return cudaErrorInvalidValue;
+  }
   if (l.shape == 0) return launch<Pair>(m, p, (int)l.ctas, stream);
   if (l.shape == 1) return launch<Wide>(m, p, (int)l.ctas, stream);
   return launch<Narrow>(m, p, (int)l.ctas, stream);
