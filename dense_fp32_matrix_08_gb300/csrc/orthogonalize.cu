@@ -12,11 +12,12 @@
 // polynomial bounds every later norm, and no element exceeds the norm.
 //
 // Three products per step:
-//   GRAM   S = X X^T              both operands K-major; S is symmetric: tiles on or below the
-//                                 diagonal, those below written twice
-//   POLY   R = a I + b S + c S^2  S symmetric, so K-major twice; R symmetric too
+//   GRAM   S = X X^T              both operands K-major
+//   POLY   R = a I + b S + c S^2
 //   APPLY  X' = R X               X read MN-major: no transposed copy of it is ever made
-// The identity in R makes X' one product with no addend. The tensor core's accumulator is read out
+// S and R are symmetric: only the tiles on or below the diagonal are computed and stored. A k step
+// to the right of the diagonal block reads the transposed tile below it, as an MN-major operand.
+// (Storing both halves made the stores of a tile 10000 of 24000 cycles longer.) The identity in R makes X' one product with no addend. The tensor core's accumulator is read out
 // after every 64 k and added up in FP32 registers: its own additions truncate (with 512 k per
 // accumulator the result at 8 x 1024 x 1024 is 1.5e-5 off, with 64 1.4e-6, and 32-bit products
 // give 2.7e-6).
@@ -26,7 +27,7 @@
 // chain of 15 small products of a 256 x 256 matrix took 175 us, most of it launches.
 //
 // Tiles of ns_kernel, chosen by choose(): 256 x 256 by a CTA pair, 128 x 128 or 128 x 64 by one
-// CTA. Where a product has fewer tiles than SMs its sum is split along k: the parts go to the
+// CTA. Tiles that do not fill the SMs once more are split along k: the parts of their sums go to the
 // workspace in FP32 and are added in order after another barrier.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -89,7 +90,8 @@ struct Input {
 struct Params {
   int batch, steps;
   int mp, np;              // padded sizes of the short and the long side
-  int tiles[3], split[3];  // per product: tiles of a matrix, parts of a sum
+  // per product: tiles of a matrix, tiles of the batch computed whole, parts of the others' sums
+  int tiles[3], whole[3], split[3];
   long long half;          // rows between the hi and the lo part of a matrix: batch * mp
   __half *x[2], *s, *r;
   float *partial;
@@ -108,10 +110,10 @@ struct Params {
   float alpha, beta;
 };
 
-// Tensor maps. p: X_0, X_1 (both X buffers), S, R in boxes of 128 rows; q: X_0, X_1, S in boxes of
-// 64 rows (K-major for 64 columns of Q; MN-major for a k step).
+// Tensor maps of both X buffers, S and R, in boxes of 128 rows (K-major tiles of 128 rows) and of 64
+// (K-major tiles of 64 rows; MN-major tiles, whose box rows are the k of a step).
 struct Maps {
-  CUtensorMap p[4], q[3];
+  CUtensorMap large[4], small[4];
 };
 
 // Device status word: 0 = fine; 1, 2, 3 = a wait of the producer, the MMA issuer or the epilogue
@@ -156,32 +158,67 @@ __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned targ
   return __all_sync(0xffffffffu, ok);
 }
 
-// Unit u of a product: part `sp` of the sum of tile (tp, tq) of matrix `mat`. Tiles of the symmetric
-// products are those on or below the diagonal, row by row (BS / TN of them in a diagonal block).
+// Units of a product: the tiles computed whole, then the parts of the others.
+__device__ __forceinline__ int units_of(const Params &p, int mode) {
+  return p.whole[mode] + (p.batch * p.tiles[mode] - p.whole[mode]) * p.split[mode];
+}
+
+struct Unit {
+  int mat, tp, tq;  // matrix, tile row and column
+  int part;         // index of the part among all parts, -1 for a whole tile
+  int k0, k1;       // steps of k
+};
+
+// Tile t of the batch. Tiles of the symmetric products are those on or below the diagonal, row by
+// row (BS / TN of them in a diagonal block).
 template <class C>
-__device__ __forceinline__ void unit_at(const Params &p, int mode, int u, int &mat, int &tp, int &tq,
-                                        int &sp) {
-  sp = u % p.split[mode];
-  u /= p.split[mode];
-  mat = u / p.tiles[mode];
-  const int t = u % p.tiles[mode];
+__device__ __forceinline__ void tile_at(const Params &p, int mode, int t, Unit &u) {
+  u.mat = t / p.tiles[mode];
+  t %= p.tiles[mode];
   if (mode == APPLY) {
-    tile_coords(t, p.mp / C::BS, p.np / C::TN, 4, tp, tq);
+    tile_coords(t, p.mp / C::BS, p.np / C::TN, 4, u.tp, u.tq);
     return;
   }
   constexpr int Q = C::BS / C::TN;
   int i = (int)((sqrtf(8.0f * (t / Q) + 1.0f) - 1.0f) * 0.5f);
   while (Q * (i + 1) * (i + 2) / 2 <= t) ++i;
   while (Q * i * (i + 1) / 2 > t) --i;
-  tp = i;
-  tq = t - Q * i * (i + 1) / 2;
+  u.tp = i;
+  u.tq = t - Q * i * (i + 1) / 2;
+}
+
+template <class C>
+__device__ __forceinline__ Unit unit_at(const Params &p, int mode, int i) {
+  Unit u;
+  const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
+  u.part = i - p.whole[mode];
+  u.k0 = 0;
+  u.k1 = KT;
+  int t = i;
+  if (u.part >= 0) {
+    const int sp = u.part % S;
+    t = p.whole[mode] + u.part / S;
+    u.k0 = (int)((long long)KT * sp / S);
+    u.k1 = (int)((long long)KT * (sp + 1) / S);
+  } else {
+    u.part = -1;
+  }
+  tile_at<C>(p, mode, t, u);
+  return u;
+}
+
+// Whether step k (elements) of a symmetric operand's rows from `row` lies to the right of their
+// diagonal block, where only the transposed tile is stored.
+template <class C>
+__device__ __forceinline__ bool beyond(int row, int k) {
+  return k >= (row / C::BS + 1) * C::BS;
 }
 
 // What becomes of 32 x 32 sums of a product at (row0, col0) of matrix `mat`: v holds 32 columns of
 // one row per lane. One copy of this code serves all products (ns_kernel): each CTA runs it once or
 // twice between two barriers, and what it costs then is mostly the fetching of its instructions.
 __device__ __forceinline__ void finish(const Params &p, int mode, int step, int mat, int row0,
-                                       int col0, bool mirror, uint8_t *buf, int lane,
+                                       int col0, uint8_t *buf, int lane,
                                        float (&v)[32]) {
   const float f = p.f[step][mode];
 #pragma unroll
@@ -237,12 +274,11 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
         if (j == lane) v[j] += p.diag[step];
     }
   }
-  // hi, then lo = what hi leaves; below the diagonal the transposed block too
+  // hi, then lo = what hi leaves
   __half *base = mode == GRAM ? p.s : mode == POLY ? p.r : p.x[(step + 1) & 1];
   __half *o = base + (row + sub) * ld + col0 + 8 * part;
-  __half *m = base + ((long long)mat * p.mp + col0 + sub) * ld + row0 + 8 * part;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h, o += lo, m += lo) {
+  for (int h = 0; h < 2; ++h, o += lo) {
     uint32_t w[16];
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -260,17 +296,6 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4 *>(o + 8 * i * ld) = *turn_at(buf, 8 * i + sub, part);
     __syncwarp();
-    if (mirror) {  // the block's columns as rows of the buffer
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        reinterpret_cast<uint16_t *>(turn_at(buf, j, lane >> 3))[lane & 7] =
-            (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(m + 8 * i * ld) = *turn_at(buf, 8 * i + sub, part);
-      __syncwarp();
-    }
   }
 }
 
@@ -519,8 +544,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(acc_empty + 8 * b, PAIR ? 2 * C::EPI_WARPS : C::EPI_WARPS);
     }
     mbar_init_fence();
-    for (int i = 0; i < 4; ++i) tma_prefetch_map(&maps.p[i]);
-    for (int i = 0; i < 3; ++i) tma_prefetch_map(&maps.q[i]);
+    for (int i = 0; i < 4; ++i) {
+      tma_prefetch_map(&maps.large[i]);
+      tma_prefetch_map(&maps.small[i]);
+    }
   }
   if (warp == 0) {
     if constexpr (PAIR) {
@@ -556,18 +583,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ok = grid_wait(p.counter, passed);
         if (!ok) break;
         const int x = step & 1;
-        const CUtensorMap *mp = &maps.p[mode == GRAM ? x : mode + 1];
-        const CUtensorMap *mq = &maps.q[mode == POLY ? 2 : x];
-        if (C::QN == 128 && mode != APPLY) mq = &maps.p[mode == POLY ? 2 : x];
-        const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
-        const int total = p.batch * p.tiles[mode] * S;
-        for (int u = first; u < total && ok; u += stride) {
-          int mat, tp, tq, sp;
-          unit_at<C>(p, mode, u, mat, tp, tq, sp);
-          const int y0 = mat * p.mp, yp = y0 + tp * C::BS + cta * 128;
-          const int q0 = tq * C::TN + cta * (PAIR ? C::QN : 0);
-          const int k1 = (int)((long long)KT * (sp + 1) / S);
-          for (int kt = (int)((long long)KT * sp / S); kt < k1; ++kt) {
+        const int ip = mode == GRAM ? x : mode + 1, iq = mode == POLY ? 2 : x;  // maps of P and Q
+        const int total = units_of(p, mode);
+        for (int i = first; i < total && ok; i += stride) {
+          const Unit u = unit_at<C>(p, mode, i);
+          const int y0 = u.mat * p.mp, p0 = u.tp * C::BS + cta * 128;
+          const int q0 = u.tq * C::TN + cta * (PAIR ? C::QN : 0);
+          for (int kt = u.k0; kt < u.k1; ++kt) {
             ok = wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u);
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 1);
@@ -585,17 +607,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 else
                   tma_load_2d(to, m, x, y, full);
               };
+              // rows [r0, + ROWS) of an operand at this step of k: K-major, or MN-major from rows
+              // [k, + 64) of the matrix
+              const bool pt = mode != GRAM && beyond<C>(p0, k);
+              const bool qt = mode == APPLY || (mode == POLY && beyond<C>(q0, k));
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int lo = h ? (int)p.half : 0;
-                get(dst + h * C::P_TILE, mp, k, lo + yp);
-                const uint32_t dq = dst + 2 * C::P_TILE + h * C::Q_TILE;
-                if (mode != APPLY) {
-                  get(dq, mq, k, lo + y0 + q0);
+                const int y = y0 + (h ? (int)p.half : 0);
+                const uint32_t dp = dst + h * C::P_TILE, dq = dst + 2 * C::P_TILE + h * C::Q_TILE;
+                if (pt) {
+                  get(dp, &maps.small[ip], p0, y + k);
+                  get(dp + BOX_BYTES, &maps.small[ip], p0 + BOX, y + k);
                 } else {
+                  get(dp, &maps.large[ip], k, y + p0);
+                }
+                if (qt) {
 #pragma unroll
                   for (int c = 0; c < C::QN / BOX; ++c)
-                    get(dq + c * BOX_BYTES, mq, q0 + BOX * c, lo + y0 + k);
+                    get(dq + c * BOX_BYTES, &maps.small[iq], q0 + BOX * c, y + k);
+                } else {
+                  get(dq, C::QN == 128 ? &maps.large[iq] : &maps.small[iq], k, y + q0);
                 }
               }
             }
@@ -604,7 +635,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             st.next();
           }
         }
-        passed += gridDim.x * (S > 1 ? 2u : 1u);
+        passed += gridDim.x * (p.split[mode] > 1 ? 2u : 1u);
       }
       // the last loads issued must have landed before this warp leaves (a pair's: the leader waits
       // for both, and the CTAs leave together)
@@ -616,22 +647,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (warp == 1 && (!PAIR || cta == 0)) {
       // ---- MMA issuer: one k step per TMEM accumulator, the corrections first, so that only four
       // additions meet a sum of full size
-      const uint64_t ph0 = sw128_desc(base, 16), pl0 = sw128_desc(base + C::P_TILE, 16);
-      const uint64_t qh0 = sw128_desc(base + 2 * C::P_TILE, BOX_BYTES);
-      const uint64_t ql0 = sw128_desc(base + 2 * C::P_TILE + C::Q_TILE, BOX_BYTES);
+      const uint64_t ph0 = sw128_desc(base, BOX_BYTES), pl0 = ph0 + (C::P_TILE >> 4);
+      const uint64_t qh0 = ph0 + (2 * C::P_TILE >> 4), ql0 = qh0 + (C::Q_TILE >> 4);
       Ring<C::STAGES> st;
       Ring<2> buf;
       bool ok = true;
       for (int ph = 0; ph < 3 * p.steps && ok; ++ph) {
         const int mode = ph % 3;
-        const uint32_t idesc = C::IDESC | (mode == APPLY ? 1u << 16 : 0u);
-        const uint32_t adv_q = (mode == APPLY ? 16 * 128 : 32) >> 4;
-        const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
-        const int total = p.batch * p.tiles[mode] * S;
-        for (int u = first; u < total && ok; u += stride) {
-          const int sp = u % S;
-          const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
-          for (int kt = 0; kt < steps; ++kt) {
+        const int total = units_of(p, mode);
+        for (int i = first; i < total && ok; i += stride) {
+          const Unit u = unit_at<C>(p, mode, i);
+          for (int kt = u.k0; kt < u.k1; ++kt) {
             ok = wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
                  wait_short(bars + 8 * st.slot, st.parity);
             if (!ok) {
@@ -642,6 +668,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (elect_one()) {
               const uint32_t at = st.slot * (uint32_t)(C::STAGE_BYTES >> 4);
               const uint32_t acc = tmem + buf.slot * C::TN;
+              // (both CTAs of a pair have the same k beyond their diagonal block: blocks of 256)
+              const bool pt = mode != GRAM && beyond<C>(u.tp * C::BS, kt * BK);
+              const bool qt = mode == APPLY || (mode == POLY && beyond<C>(u.tq * C::TN, kt * BK));
+              const uint32_t idesc = C::IDESC | (pt ? 1u << 15 : 0u) | (qt ? 1u << 16 : 0u);
+              const uint32_t adv_p = (pt ? 16 * 128 : 32) >> 4, adv_q = (qt ? 16 * 128 : 32) >> 4;
               const auto mma = [&](uint64_t a, uint64_t b, uint32_t more) {
                 if constexpr (PAIR)
                   mma_f16_pair(acc, a, b, idesc, more);
@@ -650,12 +681,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               };
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                mma(pl0 + at + kk * 2, qh0 + at + kk * adv_q, kk != 0);
-                mma(ph0 + at + kk * 2, ql0 + at + kk * adv_q, 1u);
+                mma(pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, kk != 0);
+                mma(ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
               }
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk)
-                mma(ph0 + at + kk * 2, qh0 + at + kk * adv_q, 1u);
+                mma(ph0 + at + kk * adv_p, qh0 + at + kk * adv_q, 1u);
               if constexpr (PAIR) {
                 mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
                 mma_commit_pair(acc_full + 8 * buf.slot);
@@ -682,26 +713,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     bool ok = true;
     for (int ph = 0; ph < 3 * p.steps; ++ph) {
       const int mode = ph % 3, step = ph / 3;
-      const int KT = (mode == GRAM ? p.np : p.mp) / BK, S = p.split[mode];
-      const int total = p.batch * p.tiles[mode] * S;
-      // pass 0: this CTA's units; pass 1, of split sums: their parts added in order, one 32 x 32
-      // block per warp at a time
+      const int S = p.split[mode], whole = p.whole[mode], total = units_of(p, mode);
+      // pass 0: this CTA's units; pass 1, where sums are split: their parts added in order, one
+      // 32 x 32 block per warp at a time
 #pragma unroll 1
       for (int pass = 0; pass < (S > 1 ? 2 : 1); ++pass) {
-        const int end = pass ? p.batch * p.tiles[mode] * C::SLOTS : total;
+        const int end = pass ? (p.batch * p.tiles[mode] - whole) * C::SLOTS : total;
         const int by = pass ? (int)gridDim.x * C::EPI_WARPS : stride;
 #pragma unroll 1
         for (int i = pass ? (int)blockIdx.x * C::EPI_WARPS + warp - 4 : first; i < end; i += by) {
           float acc[C::COLS];
 #pragma unroll
           for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
-          int mat, tp, tq, sp, row0, col0;
-          unit_at<C>(p, mode, pass ? i / C::SLOTS * S : i, mat, tp, tq, sp);
+          Unit u;
+          int row0, col0;
           if (pass == 0) {
-            row0 = tp * C::BS + cta * 128 + quad * 32;
-            col0 = tq * C::TN + grp * C::COLS;
-            const int steps = (int)((long long)KT * (sp + 1) / S) - (int)((long long)KT * sp / S);
-            for (int kt = 0; kt < steps && ok; ++kt) {
+            u = unit_at<C>(p, mode, i);
+            row0 = u.tp * C::BS + cta * 128 + quad * 32;
+            col0 = u.tq * C::TN + grp * C::COLS;
+            for (int kt = u.k0; kt < u.k1 && ok; ++kt) {
               ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
               if (!ok) {
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
@@ -728,19 +758,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             // (S is read for R: this CTA's producer has seen it written before its first copy, and
             // this makes it visible to this warp)
-            if (mode == POLY && S == 1) ok = grid_wait(p.counter, passed) && ok;
+            if (mode == POLY) ok = grid_wait(p.counter, passed) && ok;
           } else {
             const int t = i / C::SLOTS, slot = i % C::SLOTS;
-            row0 = tp * C::BS + slot / (C::TN / 32) * 32;
-            col0 = tq * C::TN + slot % (C::TN / 32) * 32;
+            tile_at<C>(p, mode, whole + t, u);
+            u.part = -1;
+            row0 = u.tp * C::BS + slot / (C::TN / 32) * 32;
+            col0 = u.tq * C::TN + slot % (C::TN / 32) * 32;
+            const float *from = p.partial + ((long long)t * S * C::SLOTS + slot) * 1024 + lane;
+#pragma unroll 2
             for (int q = 0; q < S; ++q) {
-              const float *from =
-                  p.partial + (((long long)t * S + q) * C::SLOTS + slot) * 1024 + lane;
+              float v[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) acc[j] += __ldcg(from + 32 * j);
+              for (int j = 0; j < 32; ++j) v[j] = __ldcg(from + q * (C::SLOTS * 1024) + 32 * j);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) acc[j] += v[j];
             }
           }
-          const bool mirror = mode != APPLY && tq * C::TN < tp * C::BS;
 #pragma unroll 1
           for (int j0 = 0; j0 < (pass ? 32 : C::COLS); j0 += 32) {
             float v[32];
@@ -751,11 +785,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               for (int c = 32; c < C::COLS; c += 32)
                 if (j0 == c) v[j] = acc[c + j];
             }
-            if (pass == 1 || S == 1) {
-              finish(p, mode, step, mat, row0, col0 + j0, mirror, turn, lane, v);
+            if (u.part < 0) {
+              finish(p, mode, step, u.mat, row0, col0 + j0, turn, lane, v);
             } else {
               const int slot = (cta * 4 + quad) * (C::TN / 32) + (grp * C::COLS + j0) / 32;
-              float *o = p.partial + ((long long)i * C::SLOTS + slot) * 1024 + lane;
+              float *o = p.partial + ((long long)u.part * C::SLOTS + slot) * 1024 + lane;
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[32 * j] = v[j];
             }
@@ -796,7 +830,7 @@ using Narrow = Cfg<64, false>;
 struct Plan {
   int shape;                    // 0 Pair, 1 Wide, 2 Narrow
   long long mp, np;             // short and long side, padded
-  long long tiles[3];
+  long long tiles[3], whole[3];
   int split[3];
   int parts;                    // pieces of a matrix in the norm
   long long ctas;
@@ -821,16 +855,20 @@ static double cost(const Plan &q, int shape, int batch, long long mp, long long 
   for (int mode = 0; mode < 3; ++mode) {
     const long long t = out->tiles[mode] * batch, KT = (mode == GRAM ? np : mp) / BK;
     double best = 1e300;
-    for (int S = 1; S <= 16 && S <= KT; ++S) {
-      if (S > 1 && t * S > slots) break;
-      const long long waves = (t * S + slots - 1) / slots;
-      const double busy = std::min<double>(1.0, (double)t * S / slots);
-      const double step = std::max(mma[shape], bytes[shape] / (64.0 - 14.0 * busy));
-      const double c = waves * (step * ((KT + S - 1) / S) + tile[shape]) + 2500.0 +
-                       (S > 1 ? 5000.0 : 0.0);
-      if (c < best) {
-        best = c;
-        out->split[mode] = S;
+    for (int all = 0; all < 2; ++all) {  // the last, partial round of tiles split, or all of them
+      const long long full = all ? 0 : t / slots * slots, rest = t - full;
+      for (int S = 1; S <= 16 && S <= KT; ++S) {
+        if (S > 1 && (rest == 0 || rest * S > slots)) break;
+        const long long units = full + rest * S;
+        const double step =
+            std::max(mma[shape], bytes[shape] / (64.0 - 14.0 * std::min(1.0, (double)units / slots)));
+        const double c = (S > 1 ? full / slots : (t + slots - 1) / slots) * (step * KT + tile[shape]) +
+                         2500.0 + (S > 1 ? step * ((KT + S - 1) / S) + tile[shape] + 8000.0 : 0.0);
+        if (c < best) {
+          best = c;
+          out->split[mode] = S;
+          out->whole[mode] = S > 1 ? full : t;
+        }
       }
     }
     total += best;
@@ -863,9 +901,9 @@ static Plan choose(int batch, int rows, int cols, int sms, const int *pairs) {
   size_t most = 0;
   const int area = best.shape == 0 ? 256 * 256 : best.shape == 1 ? 128 * 128 : 128 * 64;
   for (int mode = 0; mode < 3; ++mode) {
-    const long long u = best.tiles[mode] * batch * best.split[mode];
-    units = std::max(units, u);
-    if (best.split[mode] > 1) most = std::max(most, (size_t)u * area);
+    const long long parts = (best.tiles[mode] * batch - best.whole[mode]) * best.split[mode];
+    units = std::max(units, best.whole[mode] + parts);
+    most = std::max(most, (size_t)parts * area);
   }
   best.ctas = std::min(units, slots) * (best.shape == 0 ? 2 : 1);
   best.parts = (int)std::min<long long>(592, ceil_div(m * n, 8192));
@@ -977,6 +1015,7 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
   long long units = (long long)p.batch * l.parts;
   for (int mode = 0; mode < 3; ++mode) {
     p.tiles[mode] = (int)l.tiles[mode];
+    p.whole[mode] = (int)l.whole[mode];
     p.split[mode] = l.split[mode];
     units = std::max(units, p.batch * l.tiles[mode] * l.split[mode] * 64);
   }
@@ -1006,8 +1045,8 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
   const __half *const at[4] = {p.x[0], p.x[1], p.s, p.r};
   for (int i = 0; i < 4; ++i) {
     const long long ld = i < 2 ? l.np : l.mp;
-    if (!encode_map_2d_narrow(&m.p[i], at[i], 2, rows, ld, ld, 128) ||
-        (i < 3 && !encode_map_2d_narrow(&m.q[i], at[i], 2, rows, ld, ld, BOX)))
+    if (!encode_map_2d_narrow(&m.large[i], at[i], 2, rows, ld, ld, 128) ||
+        !encode_map_2d_narrow(&m.small[i], at[i], 2, rows, ld, ld, BOX))
       return cudaErrorInvalidValue;
   }
   if (l.shape == 0) return launch<Pair>(m, p, (int)l.ctas, stream);
