@@ -134,8 +134,8 @@ __device__ __forceinline__ void grid_arrive(unsigned *counter) {  // one thread,
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;\n" ::"l"(counter) : "memory");
 }
 
-// One warp; false if the count has not been reached after 8 s.
-__device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned target) {
+// One warp; false if the count has not been reached after 8 s. copies: TMA copies follow.
+__device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned target, bool copies) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) {
     unsigned v;
@@ -152,7 +152,7 @@ __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned targ
         }
       }
     }
-    proxy_fence();  // the copies that follow read what other CTAs' plain stores wrote
+    if (copies) proxy_fence();  // (they read what other CTAs' plain stores wrote)
     if (!ok) atomicCAS(&g_ns_status, 0, 4);
   }
   return __all_sync(0xffffffffu, ok);
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       bool ok = true;
       for (int ph = 0; ph < 3 * p.steps && ok; ++ph) {
         const int mode = ph % 3, step = ph / 3;
-        ok = grid_wait(p.counter, passed);
+        ok = grid_wait(p.counter, passed, true);
         if (!ok) break;
         const int x = step & 1;
         const int ip = mode == GRAM ? x : mode + 1, iq = mode == POLY ? 2 : x;  // maps of P and Q
@@ -737,6 +737,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
                 break;
               }
+              // (S will be read for R: this CTA's producer has seen it written before its first copy,
+              // and this makes it visible to this warp)
+              if (mode == POLY && kt == u.k0) ok = grid_wait(p.counter, passed, false);
               fence_after();
 #pragma unroll
               for (int j0 = 0; j0 < C::COLS; j0 += 16) {
@@ -756,23 +759,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               }
               buf.next();
             }
-            // (S is read for R: this CTA's producer has seen it written before its first copy, and
-            // this makes it visible to this warp)
-            if (mode == POLY) ok = grid_wait(p.counter, passed) && ok;
           } else {
             const int t = i / C::SLOTS, slot = i % C::SLOTS;
             tile_at<C>(p, mode, whole + t, u);
             u.part = -1;
             row0 = u.tp * C::BS + slot / (C::TN / 32) * 32;
             col0 = u.tq * C::TN + slot % (C::TN / 32) * 32;
-            const float *from = p.partial + ((long long)t * S * C::SLOTS + slot) * 1024 + lane;
-#pragma unroll 2
+            const float4 *from = reinterpret_cast<const float4 *>(
+                p.partial + ((long long)t * S * C::SLOTS + slot) * 1024) + lane;
+#pragma unroll 4
             for (int q = 0; q < S; ++q) {
-              float v[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __ldcg(from + q * (C::SLOTS * 1024) + 32 * j);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) acc[j] += v[j];
+              for (int j = 0; j < 8; ++j) {
+                const float4 v = __ldcg(from + q * (C::SLOTS * 256) + 32 * j);
+                acc[4 * j] += v.x;
+                acc[4 * j + 1] += v.y;
+                acc[4 * j + 2] += v.z;
+                acc[4 * j + 3] += v.w;
+              }
             }
           }
 #pragma unroll 1
@@ -789,9 +793,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               finish(p, mode, step, u.mat, row0, col0 + j0, turn, lane, v);
             } else {
               const int slot = (cta * 4 + quad) * (C::TN / 32) + (grp * C::COLS + j0) / 32;
-              float *o = p.partial + ((long long)u.part * C::SLOTS + slot) * 1024 + lane;
+              float4 *o = reinterpret_cast<float4 *>(
+                  p.partial + ((long long)u.part * C::SLOTS + slot) * 1024) + lane;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[32 * j] = v[j];
+              for (int j = 0; j < 8; ++j)
+                o[32 * j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
           }
         }
@@ -799,11 +805,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (warp == 4) {
           // (a CTA without work in this product must not arrive while others are still to arrive
           // for the one before)
-          if (pass == 0 && first >= total) ok = grid_wait(p.counter, passed) && ok;
+          if (pass == 0 && first >= total) ok = grid_wait(p.counter, passed, false) && ok;
           if (lane == 0) grid_arrive(p.counter);
           __syncwarp();
         }
-        if (S > 1 && pass == 0) ok = grid_wait(p.counter, passed + gridDim.x) && ok;
+        if (S > 1 && pass == 0) ok = grid_wait(p.counter, passed + gridDim.x, false) && ok;
       }
       passed += gridDim.x * (S > 1 ? 2u : 1u);
     }
@@ -863,7 +869,7 @@ static double cost(const Plan &q, int shape, int batch, long long mp, long long 
         const double step =
             std::max(mma[shape], bytes[shape] / (64.0 - 14.0 * std::min(1.0, (double)units / slots)));
         const double c = (S > 1 ? full / slots : (t + slots - 1) / slots) * (step * KT + tile[shape]) +
-                         2500.0 + (S > 1 ? step * ((KT + S - 1) / S) + tile[shape] + 8000.0 : 0.0);
+                         2500.0 + (S > 1 ? step * ((KT + S - 1) / S) + tile[shape] + 6000.0 + 500.0 * S : 0.0);
         if (c < best) {
           best = c;
           out->split[mode] = S;
