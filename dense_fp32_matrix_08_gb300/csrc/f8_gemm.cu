@@ -37,7 +37,7 @@ constexpr int BP = 128;                  // rows of P per tile
 constexpr int BK = 128;                  // k per block = per pipeline stage
 constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
-constexpr int PART_PITCH = BP + 4;       // column pitch of a cluster's partial tiles (floats)
+constexpr int PART_PITCH = BP;           // column pitch of a cluster's partial tiles (floats)
 
 // PAIR: two CTAs share a tile of 256 rows and TN columns (tcgen05 cta_group::2), each with its 128
 // rows of P and half of Q.
@@ -46,7 +46,7 @@ struct Cfg {
   static constexpr int TN = TN_;
   static constexpr bool PAIR = PAIR_;
   static constexpr int QN = PAIR ? TN / 2 : TN;     // columns of Q that this CTA holds
-  static constexpr int GROUPS = PAIR ? 4 : TN >= 128 ? 2 : 1;  // epilogue groups of four warps
+  static constexpr int GROUPS = TN >= 128 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;          // accumulator columns of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
@@ -54,10 +54,9 @@ struct Cfg {
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   // narrow tiles: about 100 KB, so that the next call's CTA fits beside this one's and is past its
   // setup when this one ends
-  static constexpr int STAGES = PAIR || TN == 16 ? 5 : TN == 128 ? 6 : 4;
-  // A pair's tile is computed in two parts of 128 columns with accumulators of their own, each read
-  // by two of the epilogue groups: the tensor core fills one while the other is read and handed
-  // back.
+  static constexpr int STAGES = TN >= 128 ? 6 : 4;
+  // A pair's tile is computed in two parts of 128 columns, one per epilogue group, with accumulators
+  // of their own: the tensor core fills one while the other is read and handed back.
   static constexpr int PARTS = PAIR ? 2 : 1;
   static constexpr int PART = TN / PARTS;           // columns of one accumulator
   static constexpr int NBUF = PAIR ? 2 : 4;         // accumulators per part
@@ -68,11 +67,14 @@ struct Cfg {
   static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
   static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
   static constexpr int TURN_BYTES = EPI_WARPS * tcx::TURN_BYTES;
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
+  static constexpr int BAR_BYTES = 8 * (3 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
   static_assert((int)F8_D_F32 == tcx::OUT_F32 && (int)F8_D_BF16 == tcx::OUT_BF16 &&
                 (int)F8_D_F16 == tcx::OUT_F16, "types of D");
+  // Two warps take turns with the k blocks of a single CTA. Each must see every use of a slot it
+  // waits on (a barrier tells only odd uses from even ones), so slots alternate as the blocks do.
+  static_assert(PAIR || (STAGES % 2 == 0 && NBUF % 2 == 0), "each slot belongs to one issuer");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
   static_assert(TN > 64 || 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -134,7 +136,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
   const uint32_t acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
   const uint32_t sc_full = acc_empty + 8 * C::PARTS * C::NBUF, sc_empty = sc_full + 8 * C::SC_DEPTH;
-  const uint32_t tmem_slot = sc_empty + 8 * C::SC_DEPTH;
+  const uint32_t order = sc_empty + 8 * C::SC_DEPTH;
+  const uint32_t tmem_slot = order + 8 * C::STAGES;
   volatile uint32_t *tmem_slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
 
@@ -162,10 +165,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       mbar_init(sc_full + 8 * d, 32);
       mbar_init(sc_empty + 8 * d, C::EPI_WARPS);
     }
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(order + 8 * s, 1);
     mbar_init_fence();
     tma_prefetch_map(&map_p);
     tma_prefetch_map(&map_q);
   }
+  __syncwarp();
   if (warp == 0) {
     if constexpr (PAIR) {
       tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
@@ -190,8 +195,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   };
 
   if (warp < 4) {
-  // a pair's 640 threads x 96 registers at launch = 128 x 64 + 512 x 104
-  if constexpr (PAIR) reg_dealloc<64>();
+  // 384 threads x 168 registers at launch = 128 x 56 + 256 x 224: a pair's epilogue thread holds 128
+  // sums
+  if constexpr (PAIR) reg_dealloc<56>();
   if (warp == 0) {
     // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
     Ring<C::STAGES> st;
@@ -242,7 +248,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   } else if (warp == 1 || warp == 3) {
     // ---- MMA issuers. What a warp does for one accumulator (two waits, four instructions, the
     // commits) takes longer than the tensor core takes for 128 columns, so two warps share it:
-    // each issues one part of every k block of a pair, else every other k block.
+    // each issues one part of every k block of a pair, else every other k block. A pair's second part
+    // goes in behind the first (`order`, a barrier per stage): side by side both would complete only
+    // after eight instructions, and their readers would wait for both.
     const int me = warp >> 1;
     const uint64_t lead_q = 128 * BK;
     const uint32_t adv_p = (p.p.mn_major ? 32 * 128 : 32) >> 4;
@@ -261,7 +269,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         if (PAIR || mine == 0) {
           const uint32_t a = acc0 + buf.slot;
           ok = wait_short(bars + 8 * st.slot, st.parity) &&
-               wait_short(acc_empty + 8 * a, buf.parity ^ 1u);
+               wait_short(acc_empty + 8 * a, buf.parity ^ 1u) &&
+               (!PAIR || me == 0 || wait_short(order + 8 * st.slot, st.parity));
           if (!ok) {
             if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
             break;
@@ -277,13 +286,15 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
               else
                 mma_f8(d, pd0 + at + kk * adv_p, qd0 + at + kk * adv_q, p.idesc, kk != 0);
             }
-            // once these have completed the accumulator is, and the stage is free of this warp
+            if (PAIR && me == 0) mbar_arrive(order + 8 * st.slot);
+            // once these have completed the stage is free of this warp, and the accumulator complete
+            // (in this order: who has seen the last accumulator knows that no arrival is to come)
             if constexpr (PAIR) {
-              mma_commit_pair(acc_full + 8 * a);
               mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
+              mma_commit_pair(acc_full + 8 * a);
             } else {
-              mma_commit(acc_full + 8 * a);
               mma_commit(bars + 8 * (C::STAGES + st.slot));
+              mma_commit(acc_full + 8 * a);
             }
           }
           __syncwarp();
@@ -336,14 +347,15 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   }
   } else {
     // ---- epilogue
-    if constexpr (PAIR) reg_alloc<104>();
+    if constexpr (PAIR) reg_alloc<224>();
     const int grp = (warp - 4) >> 2, quad = warp & 3;
-    // accumulators and columns of this group: a quarter of a pair's tile is 64 columns of the half
-    // of Q that CTA grp % 2 holds, in the accumulators of part grp / 2
-    const uint32_t acc0 = PAIR ? (grp >> 1) * C::NBUF : 0;
+    // accumulators and columns of this group: a pair's part has 64 columns of either CTA's half of Q
+    const uint32_t acc0 = PAIR ? grp * C::NBUF : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + acc0 * C::ACC_COLS +
-                               (uint32_t)((PAIR ? grp & 1 : grp) * C::COLS);
-    const int tile_col = PAIR ? 128 * (grp & 1) + 64 * (grp >> 1) : grp * C::COLS;
+                               (uint32_t)(PAIR ? 0 : grp * C::COLS);
+    const auto column = [&](int c) {  // of the tile
+      return PAIR ? 64 * grp + c + (c < 64 ? 0 : 64) : grp * C::COLS + c;
+    };
     const int p_at = p.p.shift ? 0 : quad * 32 + lane;
     Ring<C::NBUF> buf;
     Ring<C::SC_DEPTH> sl;
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_at(t, tp, tq);
-      const int row0 = tp * BP + quad * 32, col0 = tq * TN + tile_col;
+      const int row0 = tp * BP + quad * 32, col0 = tq * TN;
       unsigned long long acc[C::COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
@@ -364,11 +376,14 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         }
         fence_after();
         const float *sc = scales + sl.slot * (BP + TN);
-        const float *sqb = sc + BP + (QVEC ? tile_col : tile_col / 128);
-        const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
-        const unsigned long long s2 = pack2(s, s);
+        // (one scale of Q for each 128 columns: a pair's part has columns of two)
+        const float *sqb = sc + BP;
+        const float sp = sc[p_at];
+        const float sa = QVEC ? sp : sp * sqb[PAIR ? 0 : grp * C::COLS / 128];
+        const float sb = QVEC || !PAIR ? sa : sp * sqb[1];
+        const unsigned long long s2[2] = {pack2(sa, sa), pack2(sb, sb)};
         // the next columns are on their way from TMEM while these are scaled and added
-        constexpr int CH = PAIR || C::COLS < 32 ? 16 : 32;
+        constexpr int CH = C::COLS < 32 ? 16 : 32;
         uint32_t v[2][CH];
         const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
         tmem_ld(src, v[0]);
@@ -382,12 +397,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             unsigned long long lo = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
             unsigned long long hi = pack2(__uint_as_float(w[j + 2]), __uint_as_float(w[j + 3]));
             if constexpr (QVEC) {
-              const float4 f = *reinterpret_cast<const float4 *>(sqb + c + j);
+              const float4 f = *reinterpret_cast<const float4 *>(sqb + column(c + j));
               lo = mul2(lo, pack2(f.x, f.y));
               hi = mul2(hi, pack2(f.z, f.w));
             }
-            ffma2(acc[(c + j) / 2], lo, s2);
-            ffma2(acc[(c + j) / 2 + 1], hi, s2);
+            ffma2(acc[(c + j) / 2], lo, s2[PAIR && c >= 64]);
+            ffma2(acc[(c + j) / 2 + 1], hi, s2[PAIR && c >= 64]);
           }
         }
         fence_before();
@@ -417,15 +432,16 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             v[j] = f.x;
             v[j + 1] = f.y;
           }
-          if (row0 < p.p.extent && col0 + c < p.q.extent)
-            store_rows<CN>(out, turn, lane, row0, col0 + c, v);
+          const int col = col0 + column(c);
+          if (row0 < p.p.extent && col < p.q.extent)
+            store_rows<CN>(out, turn, lane, row0, col, v);
         }
       } else if (S == 1) {  // P of D's columns: the lanes hold neighbouring elements
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 2) {
           const float2 f = unpack2(acc[c / 2]);
-          store1(p, row0 + lane, col0 + c, f.x);
-          store1(p, row0 + lane, col0 + c + 1, f.y);
+          store1(p, row0 + lane, col0 + column(c), f.x);
+          store1(p, row0 + lane, col0 + column(c) + 1, f.y);
         }
       } else {
         // partial tile -> the ring, which every MMA of this CTA has finished reading (the
@@ -434,47 +450,66 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < C::COLS; j += 2) {
           const float2 f = unpack2(acc[j / 2]);
-          part[(tile_col + j) * PART_PITCH + quad * 32 + lane] = f.x;
-          part[(tile_col + j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
+          part[column(j) * PART_PITCH + quad * 32 + lane] = f.x;
+          part[column(j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
         }
       }
     }
   }
   __syncwarp();
   if (S > 1) {
-    // CTA `rank` finishes columns [rank * TN / S, (rank + 1) * TN / S): partials in rank order,
-    // four rows at a time. Neighbouring lanes take what D stores side by side.
+    // CTA `rank` finishes columns [rank * TN / S, (rank + 1) * TN / S): partials in rank order, a
+    // warp 32 rows (one per lane) by 8 columns at a time
     cluster_sync_all();
     if (warp >= 4) {
       int tp, tq;
-      tile_coords(first, p.tiles_p, p.tiles_q, p.group_p, tp, tq);
-      const int c0 = TN * rank / S;
-      const int cols = min(TN * (rank + 1) / S, p.q.extent - tq * TN) - c0;
-      const int quads = (min(BP, p.p.extent - tp * BP) + 3) / 4;
-#pragma unroll 2
-      for (int u = threadIdx.x - 128; u < cols * quads; u += 32 * C::EPI_WARPS) {
-        const int c = c0 + (p.d_q == 1 ? u % cols : u / quads);
-        const int r = 4 * (p.d_q == 1 ? u / cols : u % quads);
-        const uint32_t part = base + (uint32_t)(c * PART_PITCH + r) * 4;
-        float4 v[MAX_CLUSTER];
+      tile_at(first, tp, tq);
+      const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.q.extent - tq * TN);
+      const int quads = min(4, (p.p.extent - tp * BP + 31) / 32);
+      uint8_t *turn = reinterpret_cast<uint8_t *>(scales + C::SC_DEPTH * (BP + TN)) +
+                      (warp - 4) * TURN_BYTES;
+      const Out out{p.D, p.d_type, p.d_p, p.p.extent, p.q.extent, p.alpha, p.beta, p.vec};
+      const int wide = TN / S >= 16 && p.d_q == 1 ? 16 : 8;  // columns of a block
+      const int blocks = c1 > c0 ? (c1 - c0 + wide - 1) / wide * quads : 0;
+      for (int b = warp - 4; b < blocks; b += C::EPI_WARPS) {
+        const int r = b % quads * 32, c = c0 + b / quads * wide;
+        float v[16];
 #pragma unroll
-        for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
-          if (q < S) v[q] = ld_cluster4(part, (uint32_t)q);
-        float4 a = v[0];
+        for (int h = 0; h < 16; h += 8) {
+          if (h >= wide) break;
+          float w[MAX_CLUSTER][8];
 #pragma unroll
-        for (int q = 1; q < MAX_CLUSTER; ++q)
-          if (q < S) {
-            a.x += v[q].x;
-            a.y += v[q].y;
-            a.z += v[q].z;
-            a.w += v[q].w;
+          for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
+            if (q < S) {
+              // Only what is used below: a load that nothing waits for could still be under way
+              // when the other CTA leaves.
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c + h + j < c1)
+                  w[q][j] = ld_cluster1(
+                      base + (uint32_t)((c + h + j) * PART_PITCH + r + lane) * 4, (uint32_t)q);
+            }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[h + j] = 0.0f;
+            if (c + h + j < c1) {
+              v[h + j] = w[0][j];
+#pragma unroll
+              for (int q = 1; q < MAX_CLUSTER; ++q)
+                if (q < S) v[h + j] += w[q][j];
+            }
           }
-        store1(p, tp * BP + r, tq * TN + c, a.x);
-        store1(p, tp * BP + r + 1, tq * TN + c, a.y);
-        store1(p, tp * BP + r + 2, tq * TN + c, a.z);
-        store1(p, tp * BP + r + 3, tq * TN + c, a.w);
+        }
+        if (wide == 16) {
+          store_rows<16>(out, turn, lane, tp * BP + r, tq * TN + c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < c1) store1(p, tp * BP + r + lane, tq * TN + c + j, v[j]);
+        }
       }
     }
+    __syncwarp();
     cluster_sync_all();  // no CTA leaves while another may still read its partial
   }
   fence_before();

@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tma_prefetch_map(&maps.small[i]);
     }
   }
+  __syncwarp();
   if (warp == 0) {
     if constexpr (PAIR) {
       tmem_alloc_pair(tmem_slot, C::TMEM_COLS);

@@ -284,6 +284,13 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
+// One FP32 number of CTA `rank`'s shared memory at the offset of the local address `local`.
+__device__ __forceinline__ float ld_cluster1(uint32_t local, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(in_cta(local, rank)) : "memory");
+  return v;
+}
+
 // ---- Results on their way out. A warp's buffer of 2 KB holds 64 bytes of each of 32 rows as four
 // 16-byte pieces; piece j of row r lies at j ^ (r / 2 % 4), so that 8 neighbouring rows' pieces,
 // and the four pieces of 2 neighbouring rows, lie in different banks. Lanes put the rows that they

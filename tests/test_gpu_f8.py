@@ -305,6 +305,26 @@ def test_product_same_bits_every_time(shape):
         assert torch.equal(first, sg.f8_matmul(*args, transb=True, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("shape", [(1, 14336, 4096), (16, 4096, 8192)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_cold_weights_back_to_back(shape):
+    """Weights from memory, not from the cache: copies of neighbouring k blocks land in any order."""
+    M, N, K = shape
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    q, s = sg.f8_quantize(x)
+    ws = [sg.f8_quantize(torch.randn(N, K, generator=g, device="cuda"), (128, 128))
+          for _ in range(6)]
+    first = [sg.f8_matmul(q, s, *w, transb=True) for w in ws]
+    for w, f in zip(ws, first):
+        R = (q.double() * s.double().repeat_interleave(128, 1)) @ (
+            w[0].double() * w[1].double().repeat_interleave(128, 0).repeat_interleave(128, 1)).t()
+        assert (f.double() - R).norm() <= 2.0 ** -8 * R.norm()
+    for _ in range(30):
+        got = [sg.f8_matmul(q, s, *w, transb=True) for w in ws]
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
 def test_chain_on_another_stream_and_in_a_graph():
     x = rand(24, 1024, seed=1).to(torch.bfloat16).cuda()
     w = rand(512, 1024, seed=2).cuda()
