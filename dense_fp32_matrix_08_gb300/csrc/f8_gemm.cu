@@ -46,17 +46,19 @@ struct Cfg {
   static constexpr int TN = TN_;
   static constexpr bool PAIR = PAIR_;
   static constexpr int QN = PAIR ? TN / 2 : TN;     // columns of Q that this CTA holds
-  static constexpr int GROUPS = TN >= 128 ? 2 : 1;  // epilogue groups of four warps
+  static constexpr int GROUPS = PAIR ? 4 : TN >= 128 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;          // accumulator columns of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
   static constexpr int THREADS = 32 * (4 + EPI_WARPS);
   static constexpr int Q_BYTES = QN * BK;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  // narrow tiles: about 100 KB, so that the next call's CTA fits beside this one's and is past its
-  // setup when this one ends
-  static constexpr int STAGES = TN >= 128 ? 6 : 4;
-  // A pair's tile is computed in two parts of 128 columns, one per epilogue group, with accumulators
-  // of their own: the tensor core fills one while the other is read and handed back.
+  // (Half as many stages for the narrow tiles, so that the next call's CTA fits beside this one's,
+  // measured 12 to 15% slower at 1x14336x4096 and 256x4096x4096 and gained nothing on short sums.)
+  static constexpr int STAGES = PAIR ? 5 : TN >= 64 ? 6 : TN == 32 ? 8 : 10;
+  // A pair's tile is computed in two parts of 128 columns with accumulators of their own, each read
+  // by two of the epilogue groups: the tensor core fills one while the other is read and handed
+  // back. (One group of four warps per part, 128 sums per thread, was 13% slower at
+  // 8192x14336x4096: 485 against 429 us.)
   static constexpr int PARTS = PAIR ? 2 : 1;
   static constexpr int PART = TN / PARTS;           // columns of one accumulator
   static constexpr int NBUF = PAIR ? 2 : 4;         // accumulators per part
@@ -67,7 +69,7 @@ struct Cfg {
   static constexpr int SC_DEPTH = TN == 16 ? 6 : 4;
   static constexpr int SC_BYTES = SC_DEPTH * (BP + TN) * 4;
   static constexpr int TURN_BYTES = EPI_WARPS * tcx::TURN_BYTES;
-  static constexpr int BAR_BYTES = 8 * (3 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * PARTS * NBUF + 2 * SC_DEPTH) + 16;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SC_BYTES + TURN_BYTES + BAR_BYTES;
   static_assert((int)F8_D_F32 == tcx::OUT_F32 && (int)F8_D_BF16 == tcx::OUT_BF16 &&
@@ -77,7 +79,7 @@ struct Cfg {
   static_assert(PAIR || (STAGES % 2 == 0 && NBUF % 2 == 0), "each slot belongs to one issuer");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
-  static_assert(TN > 64 || 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(PAIR || TN <= 128, "an MN-major Q is one box");
   static_assert(PART_PITCH * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
 };
 
@@ -136,8 +138,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   const uint32_t acc_full = bars + 8 * (2 * C::STAGES);
   const uint32_t acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
   const uint32_t sc_full = acc_empty + 8 * C::PARTS * C::NBUF, sc_empty = sc_full + 8 * C::SC_DEPTH;
-  const uint32_t order = sc_empty + 8 * C::SC_DEPTH;
-  const uint32_t tmem_slot = order + 8 * C::STAGES;
+  const uint32_t tmem_slot = sc_empty + 8 * C::SC_DEPTH;
   volatile uint32_t *tmem_slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
 
@@ -165,7 +166,6 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       mbar_init(sc_full + 8 * d, 32);
       mbar_init(sc_empty + 8 * d, C::EPI_WARPS);
     }
-    for (int s = 0; s < C::STAGES; ++s) mbar_init(order + 8 * s, 1);
     mbar_init_fence();
     tma_prefetch_map(&map_p);
     tma_prefetch_map(&map_q);
@@ -195,9 +195,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   };
 
   if (warp < 4) {
-  // 384 threads x 168 registers at launch = 128 x 56 + 256 x 224: a pair's epilogue thread holds 128
-  // sums
-  if constexpr (PAIR) reg_dealloc<56>();
+  // a pair's 640 threads x 96 registers at launch = 128 x 64 + 512 x 104
+  if constexpr (PAIR) reg_dealloc<64>();
   if (warp == 0) {
     // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
     Ring<C::STAGES> st;
@@ -224,13 +223,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
           } else {
             mbar_expect_tx(full, C::STAGE_BYTES);
             tma_load_2d(dst, &map_p, p.p.mn_major ? p0 : k, p.p.mn_major ? k : p0, full);
-            if (p.q.mn_major) {
-#pragma unroll
-              for (int c = 0; c < TN; c += 128)
-                tma_load_2d(dst + P_BYTES + c * BK, &map_q, q0 + c, k, full);
-            } else {
-              tma_load_2d(dst + P_BYTES, &map_q, k, q0, full);
-            }
+            tma_load_2d(dst + P_BYTES, &map_q, p.q.mn_major ? q0 : k, p.q.mn_major ? k : q0, full);
           }
         }
         __syncwarp();
@@ -248,17 +241,16 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   } else if (warp == 1 || warp == 3) {
     // ---- MMA issuers. What a warp does for one accumulator (two waits, four instructions, the
     // commits) takes longer than the tensor core takes for 128 columns, so two warps share it:
-    // each issues one part of every k block of a pair, else every other k block. A pair's second part
-    // goes in behind the first (`order`, a barrier per stage): side by side both would complete only
-    // after eight instructions, and their readers would wait for both.
+    // each issues one part of every k block of a pair, else every other k block.
     const int me = warp >> 1;
-    const uint64_t lead_q = 128 * BK;
+    const uint32_t lead_q = 128 * BK;
     const uint32_t adv_p = (p.p.mn_major ? 32 * 128 : 32) >> 4;
-    const uint32_t adv_q = (p.q.mn_major ? 32 * 128 : 32) >> 4;
+    constexpr uint32_t row_q = TN < 128 ? TN : 128;  // bytes of a k of an MN-major Q
+    const uint32_t adv_q = (p.q.mn_major ? 32 * row_q : 32) >> 4;
     const uint64_t pd0 = sw128_desc(base, 16);
     // a part's 64 rows of this CTA's Q: 8 KB further, or 64 bytes into the rows of k
-    const uint64_t qd0 =
-        sw128_desc(base + P_BYTES + (PAIR ? me * (p.q.mn_major ? 64 : 64 * 128) : 0), lead_q);
+    const uint32_t q_at = base + P_BYTES + (PAIR ? me * (p.q.mn_major ? 64 : 64 * 128) : 0);
+    const uint64_t qd0 = p.q.mn_major ? mn_desc(q_at, row_q, lead_q) : sw128_desc(q_at, 16);
     const uint32_t acc0 = PAIR ? me * C::NBUF : 0;
     Ring<C::STAGES> st;
     Ring<C::NBUF> buf;
@@ -269,8 +261,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         if (PAIR || mine == 0) {
           const uint32_t a = acc0 + buf.slot;
           ok = wait_short(bars + 8 * st.slot, st.parity) &&
-               wait_short(acc_empty + 8 * a, buf.parity ^ 1u) &&
-               (!PAIR || me == 0 || wait_short(order + 8 * st.slot, st.parity));
+               wait_short(acc_empty + 8 * a, buf.parity ^ 1u);
           if (!ok) {
             if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
             break;
@@ -286,7 +277,6 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
               else
                 mma_f8(d, pd0 + at + kk * adv_p, qd0 + at + kk * adv_q, p.idesc, kk != 0);
             }
-            if (PAIR && me == 0) mbar_arrive(order + 8 * st.slot);
             // once these have completed the stage is free of this warp, and the accumulator complete
             // (in this order: who has seen the last accumulator knows that no arrival is to come)
             if constexpr (PAIR) {
@@ -347,15 +337,14 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   }
   } else {
     // ---- epilogue
-    if constexpr (PAIR) reg_alloc<224>();
+    if constexpr (PAIR) reg_alloc<104>();
     const int grp = (warp - 4) >> 2, quad = warp & 3;
-    // accumulators and columns of this group: a pair's part has 64 columns of either CTA's half of Q
-    const uint32_t acc0 = PAIR ? grp * C::NBUF : 0;
+    // accumulators and columns of this group: a quarter of a pair's tile is 64 columns of the half
+    // of Q that CTA grp % 2 holds, in the accumulators of part grp / 2
+    const uint32_t acc0 = PAIR ? (grp >> 1) * C::NBUF : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + acc0 * C::ACC_COLS +
-                               (uint32_t)(PAIR ? 0 : grp * C::COLS);
-    const auto column = [&](int c) {  // of the tile
-      return PAIR ? 64 * grp + c + (c < 64 ? 0 : 64) : grp * C::COLS + c;
-    };
+                               (uint32_t)((PAIR ? grp & 1 : grp) * C::COLS);
+    const int tile_col = PAIR ? 128 * (grp & 1) + 64 * (grp >> 1) : grp * C::COLS;
     const int p_at = p.p.shift ? 0 : quad * 32 + lane;
     Ring<C::NBUF> buf;
     Ring<C::SC_DEPTH> sl;
@@ -363,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_at(t, tp, tq);
-      const int row0 = tp * BP + quad * 32, col0 = tq * TN;
+      const int row0 = tp * BP + quad * 32, col0 = tq * TN + tile_col;
       unsigned long long acc[C::COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
@@ -376,14 +365,11 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         }
         fence_after();
         const float *sc = scales + sl.slot * (BP + TN);
-        // (one scale of Q for each 128 columns: a pair's part has columns of two)
-        const float *sqb = sc + BP;
-        const float sp = sc[p_at];
-        const float sa = QVEC ? sp : sp * sqb[PAIR ? 0 : grp * C::COLS / 128];
-        const float sb = QVEC || !PAIR ? sa : sp * sqb[1];
-        const unsigned long long s2[2] = {pack2(sa, sa), pack2(sb, sb)};
+        const float *sqb = sc + BP + (QVEC ? tile_col : tile_col / 128);
+        const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
+        const unsigned long long s2 = pack2(s, s);
         // the next columns are on their way from TMEM while these are scaled and added
-        constexpr int CH = C::COLS < 32 ? 16 : 32;
+        constexpr int CH = PAIR || C::COLS < 32 ? 16 : 32;
         uint32_t v[2][CH];
         const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
         tmem_ld(src, v[0]);
@@ -397,12 +383,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             unsigned long long lo = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
             unsigned long long hi = pack2(__uint_as_float(w[j + 2]), __uint_as_float(w[j + 3]));
             if constexpr (QVEC) {
-              const float4 f = *reinterpret_cast<const float4 *>(sqb + column(c + j));
+              const float4 f = *reinterpret_cast<const float4 *>(sqb + c + j);
               lo = mul2(lo, pack2(f.x, f.y));
               hi = mul2(hi, pack2(f.z, f.w));
             }
-            ffma2(acc[(c + j) / 2], lo, s2[PAIR && c >= 64]);
-            ffma2(acc[(c + j) / 2 + 1], hi, s2[PAIR && c >= 64]);
+            ffma2(acc[(c + j) / 2], lo, s2);
+            ffma2(acc[(c + j) / 2 + 1], hi, s2);
           }
         }
         fence_before();
@@ -432,16 +418,15 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             v[j] = f.x;
             v[j + 1] = f.y;
           }
-          const int col = col0 + column(c);
-          if (row0 < p.p.extent && col < p.q.extent)
-            store_rows<CN>(out, turn, lane, row0, col, v);
+          if (row0 < p.p.extent && col0 + c < p.q.extent)
+            store_rows<CN>(out, turn, lane, row0, col0 + c, v);
         }
       } else if (S == 1) {  // P of D's columns: the lanes hold neighbouring elements
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 2) {
           const float2 f = unpack2(acc[c / 2]);
-          store1(p, row0 + lane, col0 + column(c), f.x);
-          store1(p, row0 + lane, col0 + column(c) + 1, f.y);
+          store1(p, row0 + lane, col0 + c, f.x);
+          store1(p, row0 + lane, col0 + c + 1, f.y);
         }
       } else {
         // partial tile -> the ring, which every MMA of this CTA has finished reading (the
@@ -450,8 +435,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < C::COLS; j += 2) {
           const float2 f = unpack2(acc[j / 2]);
-          part[column(j) * PART_PITCH + quad * 32 + lane] = f.x;
-          part[column(j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
+          part[(tile_col + j) * PART_PITCH + quad * 32 + lane] = f.x;
+          part[(tile_col + j + 1) * PART_PITCH + quad * 32 + lane] = f.y;
         }
       }
     }
@@ -553,7 +538,7 @@ static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, int sms) {
     for (int tn : tns) {
       const int P = swap ? N : M, Q = swap ? M : N;
       const bool pair = tn == 256;
-      if ((swap ? a_mn : b_mn) && tn < 128) continue;  // an MN-major Q comes in 128 columns
+      if ((swap ? a_mn : b_mn) && tn < 32) continue;  // (the narrowest swizzle spans 32 bytes)
       const long long tiles = (long long)ceil_div(P, pair ? 2 * BP : BP) * ceil_div(Q, tn);
       for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
         if (S > 1 && (pair || S > KB || tiles * S > sms)) break;
@@ -615,7 +600,7 @@ static cudaError_t kernel_setup() {
 // Tensor map of one operand: `extent` rows (columns for Q) by K, k contiguous or not.
 static bool side_map(CUtensorMap *map, const void *ptr, int extent, int K, int ld, bool mn_major,
                      int box_extent) {
-  return mn_major ? encode_map_2d_narrow(map, ptr, 1, K, extent, ld, BK)
+  return mn_major ? encode_map_2d_narrow(map, ptr, 1, K, extent, ld, BK, std::min(box_extent, 128))
                   : encode_map_2d_narrow(map, ptr, 1, extent, K, ld, box_extent);
 }
 

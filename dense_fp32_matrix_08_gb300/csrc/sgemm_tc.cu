@@ -506,18 +506,21 @@ bool encode_map_2d_swizzle(CUtensorMap *map, const float *ptr, long long rows, l
 }
 
 bool encode_map_2d_narrow(CUtensorMap *map, const void *ptr, int elem_bytes, long long rows,
-                          long long cols, long long ld, int box_rows) {
+                          long long cols, long long ld, int box_rows, int span) {
   EncodeTiledFn enc = encode_fn();
-  if (!enc || (elem_bytes != 1 && elem_bytes != 2)) return false;
+  if (!enc || (elem_bytes != 1 && elem_bytes != 2) || (span != 128 && span != 64 && span != 32))
+    return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * elem_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)(span / elem_bytes), (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map,
              elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
              const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace sgemm

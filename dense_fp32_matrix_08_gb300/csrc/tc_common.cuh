@@ -284,6 +284,17 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
+// MN-major operand in boxes of `row` bytes along its rows (128, 64 or 32, which is also the span of
+// the swizzle TMA wrote it with; modes 2, 4, 6): 8-k groups are 8 rows apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr, uint32_t row, uint32_t lead) {
+  uint64_t d = (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(8 * row >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(row == 128 ? 2 : row == 64 ? 4 : 6) << 61;
+  return d;
+}
+
 // One FP32 number of CTA `rank`'s shared memory at the offset of the local address `local`.
 __device__ __forceinline__ float ld_cluster1(uint32_t local, uint32_t rank) {
   float v;
@@ -421,9 +432,9 @@ __device__ __forceinline__ void store_rows(const Out &o, uint8_t *buf, int lane,
 }  // namespace tcx
 
 // Tensor map of a rows x cols row-major matrix of 1- or 2-byte elements (row stride ld
-// elements, a multiple of 16 bytes; ptr 16-byte aligned) in boxes of 128 bytes x box_rows,
-// 128-byte swizzle; elements out of range read as zero. False if the driver rejects it.
+// elements, a multiple of 16 bytes; ptr 16-byte aligned) in boxes of span bytes x box_rows, swizzled
+// over that span (128, 64 or 32); elements out of range read as zero. False if the driver rejects it.
 bool encode_map_2d_narrow(CUtensorMap *map, const void *ptr, int elem_bytes, long long rows,
-                          long long cols, long long ld, int box_rows);
+                          long long cols, long long ld, int box_rows, int span = 128);
 
 }  // namespace sgemm
