@@ -426,3 +426,10 @@ extern "C" int f8_quantize(int rows, int cols, const void *x, int x_type, int ld
   if (x_type == F8_D_BF16) return (int)f8::launch_quantize<f8::BF16>(p, which, sms, stream);
   return (int)f8::launch_quantize<f8::F16>(p, which, sms, stream);
 }
+
+extern "C" int f8_quantize_with(const f8_quantize_args *a) {
+  if (a == nullptr) return -1;
+  return f8_quantize(a->rows, a->cols, a->x, a->x_type, a->ldx, a->block_rows, a->block_cols,
+                     a->format, a->pow2, a->q, a->ldq, a->s, a->s_row, a->s_col, a->qc, a->ldqc,
+                     a->sc, a->sc_row, a->sc_col, a->stream);
+}

@@ -13,6 +13,7 @@ For a linear layer y = x W^T:
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -21,7 +22,7 @@ from . import SgemmError, _stream, lib
 __all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
 
 # Every symbol include/f8_gemm.h declares.
-F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_gemm_status")
+F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_status")
 
 _FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -32,13 +33,19 @@ lib.f8_quantize.argtypes = ([_i, _i, _vp, _i, _i, _i, _i, _i, _i] + [_vp, _i, _v
                             [_vp])
 lib.f8_gemm.argtypes = ([_i, _i, _i, _i, _i, _f] + [_vp, _i, _i, _vp, _i, _ll, _ll] * 2 +
                         [_f, _vp, _i, _i, _vp])
+lib.f8_quantize_with.argtypes = lib.f8_gemm_with.argtypes = [ctypes.c_char_p]
 lib.f8_gemm_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
 for _name in F8_EXPORTED:
     getattr(lib, _name).restype = ctypes.c_int
 
 
+# f8_quantize_args and f8_gemm_args
+_quantize_args = struct.Struct("@iiPiiiiiiPiPqqPiPqqP").pack
+_gemm_args = struct.Struct("@iiiiifPiiPiqqPiiPiqqfPiiP").pack
+
+
 def _rows(name, t):
-    """Row stride of a 2-D CUDA tensor with unit column stride."""
+    """(rows, columns, row stride) of a 2-D CUDA tensor with unit column stride."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
@@ -47,7 +54,7 @@ def _rows(name, t):
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return max(ld, cols, 1) if rows > 1 else max(cols, 1)
+    return rows, cols, (ld if ld >= cols and rows > 1 else cols) or 1
 
 
 def _quantize(x, block, both, dtype, pow2, stream):
@@ -57,8 +64,7 @@ def _quantize(x, block, both, dtype, pow2, stream):
     xt = _TYPE.get(x.dtype)
     if xt is None:
         raise TypeError("x must be float32, bfloat16 or float16")
-    ldx = _rows("x", x)
-    rows, cols = x.shape
+    rows, cols, ldx = _rows("x", x)
     device = x.device
     br, bc = block
     ldq = (cols + 15) // 16 * 16 or 1
@@ -77,14 +83,13 @@ def _quantize(x, block, both, dtype, pow2, stream):
         qc = torch.empty_strided((rows, cols), (ldq, 1), dtype=dtype, device=device)
         sc = torch.empty_strided(((rows + 127) >> 7, cols), (cols or 1, 1), dtype=torch.float32,
                                  device=device)
-        rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, xt, ldx, br, bc, fmt, pow2,
-                             q.data_ptr() or None, ldq, s.data_ptr() or None, s_row, s_col,
-                             qc.data_ptr() or None, ldq, sc.data_ptr() or None, cols, 1,
-                             _stream(stream))
+        rc = lib.f8_quantize_with(_quantize_args(
+            rows, cols, x.data_ptr(), xt, ldx, br, bc, fmt, pow2, q.data_ptr(), ldq, s.data_ptr(),
+            s_row, s_col, qc.data_ptr(), ldq, sc.data_ptr(), cols, 1, _stream(stream) or 0))
     else:
-        rc = lib.f8_quantize(rows, cols, x.data_ptr() or None, xt, ldx, br, bc, fmt, pow2,
-                             q.data_ptr() or None, ldq, s.data_ptr() or None, s_row, s_col,
-                             None, 0, None, 0, 0, _stream(stream))
+        rc = lib.f8_quantize_with(_quantize_args(
+            rows, cols, x.data_ptr(), xt, ldx, br, bc, fmt, pow2, q.data_ptr(), ldq, s.data_ptr(),
+            s_row, s_col, 0, 0, 0, 0, 0, _stream(stream) or 0))
     if rc != 0:
         raise SgemmError(rc, "f8_quantize")
     return (q, s, qc, sc) if both else (q, s)
@@ -111,17 +116,17 @@ def _operand(name, q, scale, k_dim):
     fmt = _FORMAT.get(q.dtype)
     if fmt is None:
         raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.float8_e5m2")
-    ld = _rows(name, q)
-    if q.shape[0] <= 1:
+    rows, cols, ld = _rows(name, q)
+    if rows <= 1:
         ld = (ld + 15) // 16 * 16
     if scale.dtype is not torch.float32 or scale.dim() != 2 or not scale.is_cuda:
         raise TypeError(f"{name}'s scale must be a 2-D float32 CUDA tensor")
     if k_dim:
-        mn, k = q.shape
+        mn, k = rows, cols
         have, blocks = scale.shape
         s_mn, s_k = scale.stride()
     else:
-        k, mn = q.shape
+        k, mn = rows, cols
         blocks, have = scale.shape
         s_k, s_mn = scale.stride()
     if blocks != (k + 127) >> 7:
@@ -152,18 +157,18 @@ def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, 
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError("out has another type than out_dtype")
-        ldd = _rows("out", out)
-        if out.shape != (M, N):
+        rows, cols, ldd = _rows("out", out)
+        if rows != M or cols != N:
             raise ValueError("shape mismatch")
     dt = _TYPE.get(out.dtype)
     if dt is None:
         raise TypeError("out must be float32, bfloat16 or float16")
     if not (device == b.device == out.device == a_scale.device == b_scale.device):
         raise ValueError("operands, scales and out must be on one device")
-    rc = lib.f8_gemm(transa, transb, M, N, K, alpha, a.data_ptr() or None, fa, lda,
-                     a_scale.data_ptr() or None, ga, amn, ak, b.data_ptr() or None, fb, ldb,
-                     b_scale.data_ptr() or None, gb, bmn, bk, beta, out.data_ptr() or None, dt,
-                     ldd, _stream(stream))
+    rc = lib.f8_gemm_with(_gemm_args(
+        transa, transb, M, N, K, alpha, a.data_ptr(), fa, lda, a_scale.data_ptr(), ga, amn, ak,
+        b.data_ptr(), fb, ldb, b_scale.data_ptr(), gb, bmn, bk, beta, out.data_ptr(), dt, ldd,
+        _stream(stream) or 0))
     if rc != 0:
         raise SgemmError(rc, "f8_gemm")
     return out

@@ -70,6 +70,46 @@ int f8_gemm(int transa, int transb, int M, int N, int K, float alpha, const void
             int b_cols, long long b_scale_mn, long long b_scale_k, float beta, void *D,
             int d_type, int ldd, cudaStream_t stream);
 
+/* The arguments of f8_quantize and of f8_gemm, in their order, as structures: one pointer crosses a
+ * language binding faster than 20 to 26 values. */
+typedef struct {
+  int rows, cols;
+  const void *x;
+  int x_type, ldx, block_rows, block_cols, format, pow2;
+  void *q;
+  int ldq;
+  float *s;
+  long long s_row, s_col;
+  void *qc;
+  int ldqc;
+  float *sc;
+  long long sc_row, sc_col;
+  cudaStream_t stream;
+} f8_quantize_args;
+
+typedef struct {
+  int transa, transb, M, N, K;
+  float alpha;
+  const void *A;
+  int a_format, lda;
+  const float *a_scale;
+  int a_rows;
+  long long a_scale_mn, a_scale_k;
+  const void *B;
+  int b_format, ldb;
+  const float *b_scale;
+  int b_cols;
+  long long b_scale_mn, b_scale_k;
+  float beta;
+  void *D;
+  int d_type, ldd;
+  cudaStream_t stream;
+} f8_gemm_args;
+
+/* The calls themselves, with the same return codes. `args` is read during the call only. */
+int f8_quantize_with(const f8_quantize_args *args);
+int f8_gemm_with(const f8_gemm_args *args);
+
 /* Reads and clears the device status word of f8_gemm (synchronising): 0 = fine, 1 - 4 = a wait
  * gave up after about a second and the call's result is not to be used. Returns 0 or a
  * cudaError_t. */
