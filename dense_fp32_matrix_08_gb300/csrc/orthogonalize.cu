@@ -18,9 +18,11 @@
 // S and R are symmetric: only the tiles on or below the diagonal are computed and stored. A k step
 // to the right of the diagonal block reads the transposed tile below it, as an MN-major operand.
 // (Storing both halves made the stores of a tile 10000 of 24000 cycles longer.) The identity in R makes X' one product with no addend. The tensor core's accumulator is read out
-// after every 64 k and added up in FP32 registers: its own additions truncate (with 512 k per
-// accumulator the result at 8 x 1024 x 1024 is 1.5e-5 off, with 64 1.4e-6, and 32-bit products
-// give 2.7e-6).
+// after a chunk of 64 k and added up in FP32 registers: its own additions truncate. At 8 x 1024 x
+// 1024 the result is 1.4e-6 off with chunks of 64, 3.3e-6 with 128 and 1.5e-5 with 512 (32-bit
+// products: 2.7e-6). Results of 16 bits, whose rounding is 1e-4 and more, take chunks of 256: the
+// tensor core then works ahead while the epilogue still stores the tile before (8 x 1024 x 1024 in
+// BF16 673 -> 642 us).
 //
 // A call is two launches: norm_kernel (sums of squares) and ns_kernel, which stays resident and
 // runs all products with a grid-wide barrier between them. With a launch for each product the
@@ -89,6 +91,7 @@ struct Input {
 
 struct Params {
   int batch, steps;
+  int chunk;               // k steps per accumulator
   int mp, np;              // padded sizes of the short and the long side
   // per product: tiles of a matrix, tiles of the batch computed whole, parts of the others' sums
   int tiles[3], whole[3], split[3];
@@ -646,8 +649,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         wait_short(bars + 8 * st.slot, st.parity);
       }
     } else if (warp == 1 && (!PAIR || cta == 0)) {
-      // ---- MMA issuer: one k step per TMEM accumulator, the corrections first, so that only four
-      // additions meet a sum of full size
+      // ---- MMA issuer: one chunk per TMEM accumulator; of each k step the corrections first, so that
+      // in a chunk of one step only four additions meet a sum of full size
       const uint64_t ph0 = sw128_desc(base, BOX_BYTES), pl0 = ph0 + (C::P_TILE >> 4);
       const uint64_t qh0 = ph0 + (2 * C::P_TILE >> 4), ql0 = qh0 + (C::Q_TILE >> 4);
       Ring<C::STAGES> st;
@@ -658,8 +661,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int total = units_of(p, mode);
         for (int i = first; i < total && ok; i += stride) {
           const Unit u = unit_at<C>(p, mode, i);
+          int left = 0;  // steps left of the current chunk
           for (int kt = u.k0; kt < u.k1; ++kt) {
-            ok = wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
+            const bool fresh = left == 0;
+            if (fresh) left = min(p.chunk, u.k1 - kt);
+            --left;
+            ok = (!fresh || wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u)) &&
                  wait_short(bars + 8 * st.slot, st.parity);
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
@@ -682,7 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               };
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                mma(pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, kk != 0);
+                mma(pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, !fresh || kk != 0);
                 mma(ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
               }
 #pragma unroll
@@ -690,15 +697,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 mma(ph0 + at + kk * adv_p, qh0 + at + kk * adv_q, 1u);
               if constexpr (PAIR) {
                 mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
-                mma_commit_pair(acc_full + 8 * buf.slot);
+                if (left == 0) mma_commit_pair(acc_full + 8 * buf.slot);
               } else {
                 mma_commit(bars + 8 * (C::STAGES + st.slot));
-                mma_commit(acc_full + 8 * buf.slot);
+                if (left == 0) mma_commit(acc_full + 8 * buf.slot);
               }
             }
             __syncwarp();
             st.next();
-            buf.next();
+            if (left == 0) buf.next();
           }
         }
       }
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             u = unit_at<C>(p, mode, i);
             row0 = u.tp * C::BS + cta * 128 + quad * 32;
             col0 = u.tq * C::TN + grp * C::COLS;
-            for (int kt = u.k0; kt < u.k1 && ok; ++kt) {
+            for (int kt = u.k0; kt < u.k1 && ok; kt += p.chunk) {
               ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
               if (!ok) {
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
@@ -853,7 +860,7 @@ static double cost(const Plan &q, int shape, int batch, long long mp, long long 
   static const int rows[3] = {Pair::BS, Wide::BS, Narrow::BS}, tn[3] = {256, 128, 64};
   static const double mma[3] = {1536, 768, 384};
   static const double bytes[3] = {Pair::STAGE_BYTES, Wide::STAGE_BYTES, Narrow::STAGE_BYTES};
-  static const double tile[3] = {6000, 2500, 2000};
+  static const double tile[3] = {14000, 5000, 3000};
   *out = q;
   const long long tm = mp / rows[shape], per = rows[shape] / tn[shape];
   out->tiles[GRAM] = out->tiles[POLY] = per * tm * (tm + 1) / 2;
@@ -870,7 +877,7 @@ static double cost(const Plan &q, int shape, int batch, long long mp, long long 
         const double step =
             std::max(mma[shape], bytes[shape] / (64.0 - 14.0 * std::min(1.0, (double)units / slots)));
         const double c = (S > 1 ? full / slots : (t + slots - 1) / slots) * (step * KT + tile[shape]) +
-                         2500.0 + (S > 1 ? step * ((KT + S - 1) / S) + tile[shape] + 6000.0 + 500.0 * S : 0.0);
+                         2500.0 + (S > 1 ? step * ((KT + S - 1) / S) + tile[shape] + 8000.0 + 500.0 * S : 0.0);
         if (c < best) {
           best = c;
           out->split[mode] = S;
@@ -1127,6 +1134,7 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   ns::Params p{};
   p.batch = batch;
   p.steps = steps;
+  p.chunk = out_type == NS_F32 ? 1 : 4;
   p.in = ns::Input{G, g_type, rows, cols, ldg, g_stride,
                    (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type),
                    aligned(G, ldg, batch > 1 ? g_stride : 0, g_type)};
