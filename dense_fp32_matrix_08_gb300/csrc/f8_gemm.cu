@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are initialised
   fence_after();
-  const uint32_t tmem = *tmem_slot_ptr;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);  // (uniform)
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   // (every CTA of the grid is resident, so the next launch may take what room is left)
   griddep_launch_dependents();
@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
                                (uint32_t)((PAIR ? grp & 1 : grp) * C::COLS);
     const int tile_col = PAIR ? 128 * (grp & 1) + 64 * (grp >> 1) : grp * C::COLS;
     const int p_at = p.p.shift ? 0 : quad * 32 + lane;
+    const uint32_t full0 = acc_full + 8 * acc0;
+    const uint32_t empty0 = PAIR ? in_cta(acc_empty + 8 * acc0, 0) : acc_empty;  // (the leader's)
     Ring<C::NBUF> buf;
     Ring<C::SC_DEPTH> sl;
     bool ok = true;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_short(sc_full + 8 * sl.slot, sl.parity) &&
-                                         wait_short(acc_full + 8 * (acc0 + buf.slot), buf.parity));
+                                         wait_short(full0 + 8 * buf.slot, buf.parity));
         if (!ok) {
           if (lane == 0) atomicCAS(&g_f8_status, 0, 3);
           break;
@@ -368,16 +370,22 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         const float *sqb = sc + BP + (QVEC ? tile_col : tile_col / 128);
         const float s = QVEC ? sc[p_at] : sc[p_at] * sqb[0];
         const unsigned long long s2 = pack2(s, s);
-        // the next columns are on their way from TMEM while these are scaled and added
-        constexpr int CH = PAIR || C::COLS < 32 ? 16 : 32;
-        uint32_t v[2][CH];
+        // TMEM is read 32 columns at a time, the next while these are scaled and added. A pair's
+        // 96 registers hold one lot only (16 and 16: 431 us, not 402, at 8192x14336x4096), or
+        // two of 16 beside the scales of the columns (32 spills: 235 us, not 205, at
+        // 4096x4096x8192).
+        constexpr bool AHEAD = !PAIR || QVEC;
+        constexpr int CH = (PAIR && QVEC) || C::COLS < 32 ? 16 : 32;
+        uint32_t v[AHEAD ? 2 : 1][CH];
         const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
         tmem_ld(src, v[0]);
 #pragma unroll
         for (int c = 0; c < C::COLS; c += CH) {
-          uint32_t(&w)[CH] = v[c / CH % 2];
+          uint32_t(&w)[CH] = v[AHEAD ? c / CH % 2 : 0];
+          if (!AHEAD && c > 0) tmem_ld(src + (uint32_t)c, w);
           tmem_wait_ld(w);
-          if (c + CH < C::COLS) tmem_ld(src + (uint32_t)(c + CH), v[(c / CH + 1) % 2]);
+          if (AHEAD && c + CH < C::COLS)
+            tmem_ld(src + (uint32_t)(c + CH), v[(c / CH + 1) % 2]);
 #pragma unroll
           for (int j = 0; j < CH; j += 4) {
             unsigned long long lo = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
@@ -395,9 +403,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           if constexpr (PAIR)
-            arrive_in(in_cta(acc_empty + 8 * (acc0 + buf.slot), 0));  // the leader's
+            arrive_in(empty0 + 8 * buf.slot);
           else
-            mbar_arrive(acc_empty + 8 * buf.slot);
+            mbar_arrive(empty0 + 8 * buf.slot);
           mbar_arrive(sc_empty + 8 * sl.slot);
         }
         buf.next();

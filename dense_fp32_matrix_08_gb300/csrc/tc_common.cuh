@@ -16,19 +16,20 @@
 namespace sgemm {
 namespace tcx {
 
-// Wait for the phase of parity `parity`, with the limit of mbar_wait (sgemm_ptx.cuh). Each try
-// suspends the thread for up to 20 us, so that waiting warps leave the issue slots and the shared
-// memory port to the others; the global timer is read between tries only.
+// Wait for the phase of parity `parity`, with the limit of mbar_wait (sgemm_ptx.cuh). A try suspends
+// the thread for as long as the hardware chooses, so that waiting warps leave the issue slots and the
+// shared memory port to the others (a limit of one's own costs the 8-bit product's epilogue seven
+// instructions of 150 per block and 2% of its time); the global timer is read between tries only.
 __device__ __forceinline__ bool try_wait_suspended(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n"
       ".reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       "selp.u32 %0, 1, 0, p;\n"
       "}\n"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(20000)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -46,11 +47,14 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) {
 // Position in a ring of N slots: the slot and the parity of its use (0 for the first, 1 for the
 // second, ...). A consumer waits for the slot's "full" phase of this parity, a producer for the
 // "empty" phase of the opposite one (which a fresh mbarrier counts as complete).
-template <int N>
+template <uint32_t N>
 struct Ring {
   uint32_t slot = 0, parity = 0;
   __device__ __forceinline__ void next() {
-    if (++slot == N) {
+    if constexpr ((N & (N - 1)) == 0) {
+      parity ^= (slot + 1) / N;
+      slot = (slot + 1) % N;
+    } else if (++slot == N) {
       slot = 0;
       parity ^= 1u;
     }
