@@ -216,7 +216,10 @@ __device__ __forceinline__ Scale lanes_scale(uint32_t m, int format, int pow2) {
   return scale_of(T::top(m), format, pow2);
 }
 
-// 1 x 128 blocks: unit u = row * blocks + block; a warp takes 4 neighbouring units at a time.
+// 1 x 128 blocks: unit u = row * blocks + block; a warp takes 4 neighbouring units at a time, so that
+// it reads 1 KB (of 16 bits) at once and a block's maximum stays within 8 lanes. No shared memory, 31
+// registers: 72% of the warps resident. 8192 x 4096 BF16: 16.8 us, 6.0 TB/s
+// (89% of a copy's rate); the issue slots are then 73% busy. 1 x 4096: 1.4 us.
 template <class T, int FORMAT>
 __global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
@@ -250,7 +253,12 @@ __global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
 enum { COLS = 0, SQUARE = 1, PAIR = 2 };
 
 // One 128 x 128 tile per CTA of 8 G threads: thread (g = tid / 8, sub = tid % 8) holds columns
-// 16 sub .. + 15 of rows g, g + G, ...: 32 registers of x.
+// 16 sub .. + 15 of rows g, g + G, ...: 32 registers of x. The tile stays in registers from its one
+// read to its last use, so a CTA has no loads under way while it computes and stores: several CTAs
+// per SM overlap instead, as many as the registers allow (34 to 47% of the warps). 14336 x 4096
+// FP32 in squares: 50 us, 5.9 TB/s, 87% of a copy's rate. 8192 x 4096 BF16 by rows and by columns at
+// once: 35 us, 3.9 TB/s, with twice the arithmetic per byte read; two calls, by rows and by columns,
+// take 16.8 + 25.1 us.
 template <class T>
 constexpr int kRowGroups = T::W == 16 ? 64 : 32;
 
