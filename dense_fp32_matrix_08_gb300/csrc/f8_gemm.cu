@@ -547,9 +547,10 @@ struct Plan {
 };
 
 // Estimated time of a plan in units of 64 cycles, from times measured on GB300 with every plan
-// forced on 18 shapes: what a block of k costs a CTA (more where Q has a scale for each column),
-// the stores of a tile (three times that where the lanes hold D's rows), and a cluster's exchange.
-// The estimate's choice was within 10% of the best plan on all but the smallest of them.
+// forced on 24 shapes: what a block of k costs a CTA (more where Q has a scale for each column), the
+// stores of a tile (three times that where the lanes hold D's rows), and a cluster's exchange (twice
+// where they do: 64 x 4096 x 4096 took 9.7 us so, against 7.6 in one piece). The estimate's choice is
+// within 5% of the best plan, or within 1 us where a call takes less than 6.
 static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, bool a_vec, bool b_vec, int sms) {
   Plan best{false, false, 128, 1};
   double best_cost = 1e300;
@@ -569,7 +570,7 @@ static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, bool a_vec, bo
         const long long per_sm = (tiles * S + at_once - 1) / at_once;
         const double cost = per_sm * ((vec ? block_vec : block)[i] * ((KB + S - 1) / S) +
                                       (swap ? 3.0 : 1.0) * store[i] / S) +
-                            (S > 1 ? 25.0 + 1.1 * tn : 0.0);
+                            (S > 1 ? 25.0 + (swap ? 2.2 : 1.1) * tn : 0.0);
         if (cost < best_cost) {
           best_cost = cost;
           best = Plan{swap != 0, pair, tn, S};
@@ -683,7 +684,8 @@ extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha,
                           (long long)ldd);
   }
   p.KB = ceil_div(K, f8::BK);
-  const f8::Plan pl = f8::make_plan(M, N, p.KB, transa == 1, transb == 0, a_rows == 1, b_cols == 1, sms);
+  const f8::Plan pl =
+      f8::make_plan(M, N, p.KB, transa == 1, transb == 0, a_rows == 1, b_cols == 1, sms);
   const f8::Side sa{M, transa == 1, a_scale, a_rows == 128 ? 7 : 0, a_scale_mn, a_scale_k};
   const f8::Side sb{N, transb == 0, b_scale, b_cols == 128 ? 7 : 0, b_scale_mn, b_scale_k};
   p.p = pl.swap ? sb : sa;
