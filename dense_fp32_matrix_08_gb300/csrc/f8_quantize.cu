@@ -258,7 +258,8 @@ enum { COLS = 0, SQUARE = 1, PAIR = 2 };
 // per SM overlap instead, as many as the registers allow (34 to 47% of the warps). 14336 x 4096
 // FP32 in squares: 50 us, 5.9 TB/s, 87% of a copy's rate. 8192 x 4096 BF16 by rows and by columns at
 // once: 35 us, 3.9 TB/s, with twice the arithmetic per byte read; two calls, by rows and by columns,
-// take 16.8 + 25.1 us.
+// take 16.8 + 25.1 us. (CTAs of 512 threads with half as many elements each: 44 us for 35, 23 for 16 in
+// squares; a column's maximum then takes as many shuffles for half as many rows.)
 template <class T>
 constexpr int kRowGroups = T::W == 16 ? 64 : 32;
 

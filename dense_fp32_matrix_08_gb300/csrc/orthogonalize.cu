@@ -104,8 +104,9 @@ struct Params {
   int parts;
   double eps;
   float x_scale;
-  // per step: factors of the sums of the three products, of S in R, and R's diagonal
-  float f[MAX_STEPS][3], fs[MAX_STEPS], diag[MAX_STEPS];
+  int direct;              // a X is added to R X, R = b S + c S^2 (else R has a on its diagonal)
+  // per step: factors of the sums of the three products, of S in R, of X in R X, and R's diagonal
+  float f[MAX_STEPS][3], fs[MAX_STEPS], fx[MAX_STEPS], diag[MAX_STEPS];
   // the result
   void *user;
   int user_type, tall, m, n, vec;
@@ -223,30 +224,17 @@ __device__ __forceinline__ bool beyond(int row, int k) {
 __device__ __forceinline__ void finish(const Params &p, int mode, int step, int mat, int row0,
                                        int col0, uint8_t *buf, int lane,
                                        float (&v)[32]) {
+  const bool result = mode == APPLY && step == p.steps - 1;
+  if (result && (row0 >= p.m || col0 >= p.n)) return;
   const float f = p.f[step][mode];
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] *= f;
-  if (mode == APPLY && step == p.steps - 1) {
-    const int size = p.user_type == NS_F32 ? 4 : 2;
-    void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
-    if (row0 >= p.m || col0 >= p.n) return;
-    if (!p.tall) {
-      store_rows<32>(Out{out, p.user_type, p.ldu, p.m, p.n, p.alpha, p.beta, p.vec}, buf, lane, row0,
-                     col0, v);
-    } else if (row0 + lane < p.m) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (col0 + j < p.n)
-          finish_out(out, p.user_type, (col0 + j) * p.ldu + row0 + lane, p.alpha * v[j], p.beta);
-    }
-    return;
-  }
   const int part = lane & 3, sub = lane >> 2;  // 16-byte piece and row of 8 of coalesced accesses
   const long long ld = mode == APPLY ? p.np : p.mp, lo = p.half * ld;
   const long long row = (long long)mat * p.mp + row0;  // in the buffer
-  if (mode == POLY) {
-    const float fs = p.fs[step];
-    const __half *s = p.s + (row + sub) * ld + col0 + 8 * part;
+  if (mode == POLY || (mode == APPLY && p.direct)) {
+    const float fs = mode == POLY ? p.fs[step] : p.fx[step];
+    const __half *s = (mode == POLY ? p.s : p.x[step & 1]) + (row + sub) * ld + col0 + 8 * part;
     uint4 in[2][4];  // both halves are on their way before the first is used
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -271,11 +259,25 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
       }
       __syncwarp();
     }
-    if (row0 == col0) {
+    if (mode == POLY && row0 == col0) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (j == lane) v[j] += p.diag[step];
     }
+  }
+  if (result) {
+    const int size = p.user_type == NS_F32 ? 4 : 2;
+    void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
+    if (!p.tall) {
+      store_rows<32>(Out{out, p.user_type, p.ldu, p.m, p.n, p.alpha, p.beta, p.vec}, buf, lane, row0,
+                     col0, v);
+    } else if (row0 + lane < p.m) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j < p.n)
+          finish_out(out, p.user_type, (col0 + j) * p.ldu + row0 + lane, p.alpha * v[j], p.beta);
+    }
+    return;
   }
   // hi, then lo = what hi leaves
   __half *base = mode == GRAM ? p.s : mode == POLY ? p.r : p.x[(step + 1) & 1];
@@ -752,9 +754,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
                 break;
               }
-              // (S will be read for R: this CTA's producer has seen it written before its first copy,
-              // and this makes it visible to this warp)
-              if (mode == POLY && kt == u.k0) ok = grid_wait(p.counter, passed, false);
+              // (S will be read for R, or X for the next X: this CTA's producer has seen them written
+              // before its first copy, and this makes them visible to this warp)
+              if ((mode == POLY || (mode == APPLY && p.direct)) && kt == u.k0)
+                ok = grid_wait(p.counter, passed, false);
               fence_after();
 #pragma unroll
               for (int j0 = 0; j0 < C::COLS; j0 += 16) {
@@ -936,11 +939,11 @@ static Plan choose(int batch, int rows, int cols, int sms, const int *pairs) {
   return best;
 }
 
-// Bounds of the spectral norms: of X_t in bx[0 .. steps], of a I + b S + c S^2 in br[t], each with
+// Bounds of the spectral norms: of X_t in bx[0 .. steps], of R (see Params::direct) in br[t], each with
 // a margin of 2% for the roundings. With y = x^2 the polynomials are r(y) = a + b y + c y^2 and
 // x r(x^2); on [0, bx[t]] their extremes lie at the ends or where the derivative vanishes. False
 // where a bound leaves the range of FP32 scales.
-static bool bounds(const float *co, int steps, double *bx, double *br) {
+static bool bounds(const float *co, int steps, bool direct, double *bx, double *br) {
   const double a = co[0], b = co[1], c = co[2];
   const double disc = 9.0 * b * b - 20.0 * a * c, w = std::sqrt(std::max(disc, 0.0));
   // zeros of r'(y) = b + 2 c y and of (x r(x^2))' = a + 3 b y + 5 c y^2 (NaN or infinite where
@@ -952,9 +955,9 @@ static bool bounds(const float *co, int steps, double *bx, double *br) {
     const double top = bx[t] * bx[t];
     double mx = 0.0, mr = 0.0;
     const auto at = [&](double y) {
-      const double r = std::fabs(a + y * (b + y * c));
-      mr = std::max(mr, r);
-      mx = std::max(mx, r * std::sqrt(y));
+      const double r = y * (b + y * c);
+      mr = std::max(mr, std::fabs(direct ? r : a + r));
+      mx = std::max(mx, std::fabs(a + r) * std::sqrt(y));
     };
     at(0.0);
     at(top);
@@ -1058,8 +1061,10 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
     p.f[t][GRAM] = ss / (sx * sx);
     p.f[t][POLY] = (float)((double)co[2] * sr / ((double)ss * ss));
     p.fs[t] = (float)((double)co[1] * sr / ss);
-    p.diag[t] = co[0] * sr;
-    p.f[t][APPLY] = t + 1 < p.steps ? sn / (sr * sx) : 1.0f / (sr * sx);
+    p.diag[t] = p.direct ? 0.0f : co[0] * sr;
+    const float out = t + 1 < p.steps ? sn : 1.0f;  // scale of what the step leaves
+    p.f[t][APPLY] = out / (sr * sx);
+    p.fx[t] = (float)((double)co[0] * out / sx);
     sx = sn;
   }
   Maps m;
@@ -1119,7 +1124,7 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   double bx[65], br[64];
   if (coefficients == nullptr || !std::isfinite(coefficients[0]) ||
       !std::isfinite(coefficients[1]) || !std::isfinite(coefficients[2]) ||
-      !ns::bounds(coefficients, steps, bx, br)) return -9;
+      !ns::bounds(coefficients, steps, out_type == NS_F32, bx, br)) return -9;
   if (!(eps >= 0.0f)) return -10;
   if (any && out == nullptr) return -13;
   if (!known(out_type)) return -14;
@@ -1142,6 +1147,7 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   p.batch = batch;
   p.steps = steps;
   p.chunk = out_type == NS_F32 ? 1 : 4;
+  p.direct = out_type == NS_F32;
   p.in = ns::Input{G, g_type, rows, cols, ldg, g_stride,
                    (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type),
                    aligned(G, ldg, batch > 1 ? g_stride : 0, g_type)};
