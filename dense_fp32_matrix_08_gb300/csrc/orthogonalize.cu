@@ -13,16 +13,21 @@
 //
 // Three products per step:
 //   GRAM   S = X X^T              both operands K-major
-//   POLY   R = a I + b S + c S^2
-//   APPLY  X' = R X               X read MN-major: no transposed copy of it is ever made
+//   POLY   R = b S + c S^2 (+ a I)
+//   APPLY  X' = R X (+ a X)       X read MN-major: no transposed copy of it is ever made
 // S and R are symmetric: only the tiles on or below the diagonal are computed and stored. A k step
 // to the right of the diagonal block reads the transposed tile below it, as an MN-major operand.
-// (Storing both halves made the stores of a tile 10000 of 24000 cycles longer.) The identity in R
-// makes X' one product with no addend. The tensor core's accumulator is read out after a chunk of
-// 64 k and added up in FP32 registers: its own additions truncate. At 8 x 1024 x 1024 the result is
-// 1.4e-6 off with chunks of 64, 3.3e-6 with 128 and 1.5e-5 with 512 (32-bit products: 2.7e-6).
-// Results of 16 bits, whose rounding is 1e-4 and more, take chunks of 256: the tensor core then works
-// ahead while the epilogue still stores the tile before (8 x 1024 x 1024 in BF16 673 -> 642 us).
+// (Storing both halves made the stores of a tile 10000 of 24000 cycles longer.)
+//
+// The tensor core's own additions cut what lies below the sum that they meet. So its accumulators
+// are read out after a chunk of k and added up in FP32 registers. Results in FP32 take chunks of one
+// step (64 k) in up to four accumulators, and a X is added in the epilogue: the largest term passes
+// no tensor core. Off the exact result, five steps, plain 32-bit products in brackets: 4096 x 4096
+// 5.6e-7 (3.2e-6), 256 x 256 6.7e-7 (1.6e-6), 128 x 1000 1.3e-6 (1.7e-6), 32 x 16 1.1e-6 (0.9e-6),
+// 20 x 3000 2.0e-6 (1.3e-6). With a I in R it was 1.1, 1.4, 3.1, 1.4 and 3.2e-6 (with one accumulator
+// per step), and with chunks of 512 ten times that. Results of 16 bits, whose rounding is 1e-4 and
+// more, take chunks of 256 in one accumulator and a I in R: the tensor core then works ahead while
+// the epilogue still stores the tile before (8 x 1024 x 1024 in BF16 673 -> 642 us).
 //
 // A call is two launches: norm_kernel (sums of squares) and ns_kernel, which stays resident and
 // runs all products with a grid-wide barrier between them. With a launch for each product the
@@ -66,7 +71,9 @@ struct Cfg {
   static constexpr int GROUPS = 2;                      // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;
   static constexpr int EPI_WARPS = 4 * GROUPS, THREADS = 32 * (4 + EPI_WARPS);
-  static constexpr int TMEM_COLS = 2 * TN;
+  // accumulators of a k step (see the MMA issuer): as many as TMEM holds twice, four at most
+  static constexpr int ACCS = TN == 64 ? 4 : TN == 128 ? 2 : 1;
+  static constexpr int TMEM_COLS = 2 * ACCS * TN;
   static constexpr int SLOTS = BS / 32 * (TN / 32);     // 32 x 32 blocks of a tile
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 4) + 16;
   static constexpr int SMEM_BYTES =
@@ -521,11 +528,11 @@ __global__ void __launch_bounds__(256) copy_kernel(const Params p) {
 // epilogue, a group of four warps owns COLS columns of the tile, warp w of it TMEM lanes (rows)
 // 32 (w % 4) .. + 31. All warps together make the start values.
 //
-// What bounds it, five steps each. 4096 x 4096 FP32, pairs: 2890 us; three FP16 MMAs per product, the
+// What bounds it, five steps each. 4096 x 4096 FP32, pairs: 2900 us; three FP16 MMAs per product, the
 // instructions alone 2160 (1.9 PFLOP/s), the rest the last, partial round of tiles and their stores.
-// 8 x 1024 x 1024 BF16, 128 x 128 tiles: 551 us, 270 of them MMAs; a product is 2 to 4 rounds of
+// 8 x 1024 x 1024 BF16, 128 x 128 tiles: 542 us, 270 of them MMAs; a product is 2 to 4 rounds of
 // tiles, and the barrier, the first loads and the last stores of a product overlap nothing.
-// 4097 x 777 BF16: 322 us, the same with products of one round. 256 x 256 FP32: 110 us, 6 to 7 us for
+// 4097 x 777 BF16: 316 us, the same with products of one round. 256 x 256 FP32: 115 us, 7 to 8 us for
 // each of 15 dependent products: barrier 2, first loads 1.5, k steps 1.5, stores 1 to 2.
 
 template <class C>
@@ -658,8 +665,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         wait_short(bars + 8 * st.slot, st.parity);
       }
     } else if (warp == 1 && (!PAIR || cta == 0)) {
-      // ---- MMA issuer: one chunk per TMEM accumulator; of each k step the corrections first, so that
-      // in a chunk of one step only four additions meet a sum of full size
+      // ---- MMA issuer: one chunk per set of TMEM accumulators; of each k step the corrections first,
+      // so that in a chunk of one step only hi hi' meets a sum of full size. An instruction aligns
+      // its 16 products with the accumulator and cuts what lies below: the larger the sum it meets,
+      // the more. So hi hi' of such a chunk's four instructions go to ACCS accumulators in turn.
       const uint64_t ph0 = sw128_desc(base, BOX_BYTES), pl0 = ph0 + (C::P_TILE >> 4);
       const uint64_t qh0 = ph0 + (2 * C::P_TILE >> 4), ql0 = qh0 + (C::Q_TILE >> 4);
       Ring<C::STAGES> st;
@@ -684,26 +693,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             fence_after();
             if (elect_one()) {
               const uint32_t at = st.slot * (uint32_t)(C::STAGE_BYTES >> 4);
-              const uint32_t acc = tmem + buf.slot * C::TN;
+              const uint32_t acc = tmem + buf.slot * (C::ACCS * C::TN);
               // (both CTAs of a pair have the same k beyond their diagonal block: blocks of 256)
               const bool pt = mode != GRAM && beyond<C>(u.tp * C::BS, kt * BK);
               const bool qt = mode == APPLY || (mode == POLY && beyond<C>(u.tq * C::TN, kt * BK));
               const uint32_t idesc = C::IDESC | (pt ? 1u << 15 : 0u) | (qt ? 1u << 16 : 0u);
               const uint32_t adv_p = (pt ? 16 * 128 : 32) >> 4, adv_q = (qt ? 16 * 128 : 32) >> 4;
-              const auto mma = [&](uint64_t a, uint64_t b, uint32_t more) {
+              const auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t more) {
                 if constexpr (PAIR)
-                  mma_f16_pair(acc, a, b, idesc, more);
+                  mma_f16_pair(d, a, b, idesc, more);
                 else
-                  mma_f16(acc, a, b, idesc, more);
+                  mma_f16(d, a, b, idesc, more);
               };
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                mma(pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, !fresh || kk != 0);
-                mma(ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
+                mma(acc, pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, !fresh || kk != 0);
+                mma(acc, ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
               }
 #pragma unroll
-              for (uint32_t kk = 0; kk < BK / 16; ++kk)
-                mma(ph0 + at + kk * adv_p, qh0 + at + kk * adv_q, 1u);
+              for (uint32_t kk = 0; kk < BK / 16; ++kk) {
+                const uint32_t n = p.chunk == 1 ? kk % C::ACCS : 0;
+                mma(acc + n * C::TN, ph0 + at + kk * adv_p, qh0 + at + kk * adv_q,
+                    n == 0 || kk >= C::ACCS);
+              }
               if constexpr (PAIR) {
                 mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
                 if (left == 0) mma_commit_pair(acc_full + 8 * buf.slot);
@@ -759,13 +771,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               if ((mode == POLY || (mode == APPLY && p.direct)) && kt == u.k0)
                 ok = grid_wait(p.counter, passed, false);
               fence_after();
+#pragma unroll 1
+              for (int n = 0; n < (p.chunk == 1 ? C::ACCS : 1); ++n) {
+                const uint32_t src = src0 + (buf.slot * C::ACCS + n) * C::TN;
 #pragma unroll
-              for (int j0 = 0; j0 < C::COLS; j0 += 16) {
-                uint32_t v[16];
-                tmem_ld(src0 + buf.slot * C::TN + (uint32_t)j0, v);
-                tmem_wait_ld(v);
+                for (int j0 = 0; j0 < C::COLS; j0 += 16) {
+                  uint32_t v[16];
+                  tmem_ld(src + (uint32_t)j0, v);
+                  tmem_wait_ld(v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+                  for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+                }
               }
               fence_before();
               __syncwarp();
