@@ -13,21 +13,19 @@
 //
 // Three products per step:
 //   GRAM   S = X X^T              both operands K-major
-//   POLY   R = b S + c S^2 (+ a I)
-//   APPLY  X' = R X (+ a X)       X read MN-major: no transposed copy of it is ever made
+//   POLY   R = b S + c S^2
+//   APPLY  X' = R X + a X         X read MN-major: no transposed copy of it is ever made
 // S and R are symmetric: only the tiles on or below the diagonal are computed and stored. A k step
 // to the right of the diagonal block reads the transposed tile below it, as an MN-major operand.
 // (Storing both halves made the stores of a tile 10000 of 24000 cycles longer.)
 //
-// The tensor core's own additions cut what lies below the sum that they meet. So its accumulators
-// are read out after a chunk of k and added up in FP32 registers. Results in FP32 take chunks of one
-// step (64 k) in up to four accumulators, and a X is added in the epilogue: the largest term passes
-// no tensor core. Off the exact result, five steps, plain 32-bit products in brackets: 4096 x 4096
+// The tensor core's own additions cut what lies below the sum that they meet. So its accumulators,
+// up to four, are read out after each step of 64 k and added up in FP32 registers, and a X is added in
+// the epilogue: the largest term passes no tensor core. Results of every type are made so and rounded
+// once. Off the exact result, five steps, plain 32-bit products in brackets: 4096 x 4096
 // 5.6e-7 (3.2e-6), 256 x 256 6.7e-7 (1.6e-6), 128 x 1000 1.3e-6 (1.7e-6), 32 x 16 1.1e-6 (0.9e-6),
 // 20 x 3000 2.0e-6 (1.3e-6). With a I in R it was 1.1, 1.4, 3.1, 1.4 and 3.2e-6 (with one accumulator
-// per step), and with chunks of 512 ten times that. Results of 16 bits, whose rounding is 1e-4 and
-// more, take chunks of 256 in one accumulator and a I in R: the tensor core then works ahead while
-// the epilogue still stores the tile before (8 x 1024 x 1024 in BF16 673 -> 642 us).
+// per step), and with chunks of 512 k ten times that.
 //
 // A call is two launches: norm_kernel (sums of squares) and ns_kernel, which stays resident and
 // runs all products with a grid-wide barrier between them. With a launch for each product the
@@ -98,7 +96,6 @@ struct Input {
 
 struct Params {
   int batch, steps;
-  int chunk;               // k steps per accumulator
   int mp, np;              // padded sizes of the short and the long side
   // per product: tiles of a matrix, tiles of the batch computed whole, parts of the others' sums
   int tiles[3], whole[3], split[3];
@@ -111,9 +108,8 @@ struct Params {
   int parts;
   double eps;
   float x_scale;
-  int direct;              // a X is added to R X, R = b S + c S^2 (else R has a on its diagonal)
-  // per step: factors of the sums of the three products, of S in R, of X in R X, and R's diagonal
-  float f[MAX_STEPS][3], fs[MAX_STEPS], fx[MAX_STEPS], diag[MAX_STEPS];
+  // per step: factors of the sums of the three products, of S in R, and of X in the next X
+  float f[MAX_STEPS][3], fs[MAX_STEPS], fx[MAX_STEPS];
   // the result
   void *user;
   int user_type, tall, m, n, vec;
@@ -239,7 +235,7 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
   const int part = lane & 3, sub = lane >> 2;  // 16-byte piece and row of 8 of coalesced accesses
   const long long ld = mode == APPLY ? p.np : p.mp, lo = p.half * ld;
   const long long row = (long long)mat * p.mp + row0;  // in the buffer
-  if (mode == POLY || (mode == APPLY && p.direct)) {
+  if (mode != GRAM) {
     const float fs = mode == POLY ? p.fs[step] : p.fx[step];
     const __half *s = (mode == POLY ? p.s : p.x[step & 1]) + (row + sub) * ld + col0 + 8 * part;
     uint4 in[2][4];  // both halves are on their way before the first is used
@@ -265,11 +261,6 @@ __device__ __forceinline__ void finish(const Params &p, int mode, int step, int 
         }
       }
       __syncwarp();
-    }
-    if (mode == POLY && row0 == col0) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == lane) v[j] += p.diag[step];
     }
   }
   if (result) {
@@ -530,9 +521,10 @@ __global__ void __launch_bounds__(256) copy_kernel(const Params p) {
 //
 // What bounds it, five steps each. 4096 x 4096 FP32, pairs: 2900 us; three FP16 MMAs per product, the
 // instructions alone 2160 (1.9 PFLOP/s), the rest the last, partial round of tiles and their stores.
-// 8 x 1024 x 1024 BF16, 128 x 128 tiles: 542 us, 270 of them MMAs; a product is 2 to 4 rounds of
+// 8 x 1024 x 1024 BF16, 128 x 128 tiles: 673 us, 270 of them MMAs; a product is 2 to 4 rounds of
 // tiles, and the barrier, the first loads and the last stores of a product overlap nothing.
-// 4097 x 777 BF16: 316 us, the same with products of one round. 256 x 256 FP32: 115 us, 7 to 8 us for
+// 4097 x 777 BF16: 364 us, the same with products of one round. (16-bit results summed 256 k in one
+// accumulator, with a I in R, took 545 and 318 us, for several times the error before the rounding.) 256 x 256 FP32: 115 us, 7 to 8 us for
 // each of 15 dependent products: barrier 2, first loads 1.5, k steps 1.5, stores 1 to 2.
 
 template <class C>
@@ -665,10 +657,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         wait_short(bars + 8 * st.slot, st.parity);
       }
     } else if (warp == 1 && (!PAIR || cta == 0)) {
-      // ---- MMA issuer: one chunk per set of TMEM accumulators; of each k step the corrections first,
-      // so that in a chunk of one step only hi hi' meets a sum of full size. An instruction aligns
-      // its 16 products with the accumulator and cuts what lies below: the larger the sum it meets,
-      // the more. So hi hi' of such a chunk's four instructions go to ACCS accumulators in turn.
+      // ---- MMA issuer: one k step per set of TMEM accumulators, the corrections first, so that only
+      // hi hi' meets a sum of full size. An instruction aligns its 16 products with the accumulator
+      // and cuts what lies below: the larger the sum it meets, the more. So hi hi' of a step's four
+      // instructions go to ACCS accumulators in turn.
       const uint64_t ph0 = sw128_desc(base, BOX_BYTES), pl0 = ph0 + (C::P_TILE >> 4);
       const uint64_t qh0 = ph0 + (2 * C::P_TILE >> 4), ql0 = qh0 + (C::Q_TILE >> 4);
       Ring<C::STAGES> st;
@@ -679,12 +671,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int total = units_of(p, mode);
         for (int i = first; i < total && ok; i += stride) {
           const Unit u = unit_at<C>(p, mode, i);
-          int left = 0;  // steps left of the current chunk
           for (int kt = u.k0; kt < u.k1; ++kt) {
-            const bool fresh = left == 0;
-            if (fresh) left = min(p.chunk, u.k1 - kt);
-            --left;
-            ok = (!fresh || wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u)) &&
+            ok = wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
                  wait_short(bars + 8 * st.slot, st.parity);
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
@@ -707,26 +695,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               };
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                mma(acc, pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, !fresh || kk != 0);
+                mma(acc, pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, kk != 0);
                 mma(acc, ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
               }
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                const uint32_t n = p.chunk == 1 ? kk % C::ACCS : 0;
+                const uint32_t n = kk % C::ACCS;
                 mma(acc + n * C::TN, ph0 + at + kk * adv_p, qh0 + at + kk * adv_q,
                     n == 0 || kk >= C::ACCS);
               }
               if constexpr (PAIR) {
                 mma_commit_pair(bars + 8 * (C::STAGES + st.slot));
-                if (left == 0) mma_commit_pair(acc_full + 8 * buf.slot);
+                mma_commit_pair(acc_full + 8 * buf.slot);
               } else {
                 mma_commit(bars + 8 * (C::STAGES + st.slot));
-                if (left == 0) mma_commit(acc_full + 8 * buf.slot);
+                mma_commit(acc_full + 8 * buf.slot);
               }
             }
             __syncwarp();
             st.next();
-            if (left == 0) buf.next();
+            buf.next();
           }
         }
       }
@@ -760,7 +748,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             u = unit_at<C>(p, mode, i);
             row0 = u.tp * C::BS + cta * 128 + quad * 32;
             col0 = u.tq * C::TN + grp * C::COLS;
-            for (int kt = u.k0; kt < u.k1 && ok; kt += p.chunk) {
+            for (int kt = u.k0; kt < u.k1 && ok; ++kt) {
               ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
               if (!ok) {
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
@@ -768,11 +756,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               }
               // (S will be read for R, or X for the next X: this CTA's producer has seen them written
               // before its first copy, and this makes them visible to this warp)
-              if ((mode == POLY || (mode == APPLY && p.direct)) && kt == u.k0)
+              if (mode != GRAM && kt == u.k0)
                 ok = grid_wait(p.counter, passed, false);
               fence_after();
 #pragma unroll 1
-              for (int n = 0; n < (p.chunk == 1 ? C::ACCS : 1); ++n) {
+              for (int n = 0; n < C::ACCS; ++n) {
                 const uint32_t src = src0 + (buf.slot * C::ACCS + n) * C::TN;
 #pragma unroll
                 for (int j0 = 0; j0 < C::COLS; j0 += 16) {
@@ -955,11 +943,10 @@ static Plan choose(int batch, int rows, int cols, int sms, const int *pairs) {
   return best;
 }
 
-// Bounds of the spectral norms: of X_t in bx[0 .. steps], of R (see Params::direct) in br[t], each with
-// a margin of 2% for the roundings. With y = x^2 the polynomials are r(y) = a + b y + c y^2 and
-// x r(x^2); on [0, bx[t]] their extremes lie at the ends or where the derivative vanishes. False
+// Bounds of the spectral norms: of X_t in bx[0 .. steps], of R in br[t], each with a margin of 2% for
+// the roundings. With y = x^2 the polynomials are r(y) = b y + c y^2 and x (a + r(x^2)); on [0, bx[t]] their extremes lie at the ends or where the derivative vanishes. False
 // where a bound leaves the range of FP32 scales.
-static bool bounds(const float *co, int steps, bool direct, double *bx, double *br) {
+static bool bounds(const float *co, int steps, double *bx, double *br) {
   const double a = co[0], b = co[1], c = co[2];
   const double disc = 9.0 * b * b - 20.0 * a * c, w = std::sqrt(std::max(disc, 0.0));
   // zeros of r'(y) = b + 2 c y and of (x r(x^2))' = a + 3 b y + 5 c y^2 (NaN or infinite where
@@ -972,7 +959,7 @@ static bool bounds(const float *co, int steps, bool direct, double *bx, double *
     double mx = 0.0, mr = 0.0;
     const auto at = [&](double y) {
       const double r = y * (b + y * c);
-      mr = std::max(mr, std::fabs(direct ? r : a + r));
+      mr = std::max(mr, std::fabs(r));
       mx = std::max(mx, std::fabs(a + r) * std::sqrt(y));
     };
     at(0.0);
@@ -1077,7 +1064,6 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
     p.f[t][GRAM] = ss / (sx * sx);
     p.f[t][POLY] = (float)((double)co[2] * sr / ((double)ss * ss));
     p.fs[t] = (float)((double)co[1] * sr / ss);
-    p.diag[t] = p.direct ? 0.0f : co[0] * sr;
     const float out = t + 1 < p.steps ? sn : 1.0f;  // scale of what the step leaves
     p.f[t][APPLY] = out / (sr * sx);
     p.fx[t] = (float)((double)co[0] * out / sx);
@@ -1140,7 +1126,7 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   double bx[65], br[64];
   if (coefficients == nullptr || !std::isfinite(coefficients[0]) ||
       !std::isfinite(coefficients[1]) || !std::isfinite(coefficients[2]) ||
-      !ns::bounds(coefficients, steps, out_type == NS_F32, bx, br)) return -9;
+      !ns::bounds(coefficients, steps, bx, br)) return -9;
   if (!(eps >= 0.0f)) return -10;
   if (any && out == nullptr) return -13;
   if (!known(out_type)) return -14;
@@ -1162,8 +1148,6 @@ extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, in
   ns::Params p{};
   p.batch = batch;
   p.steps = steps;
-  p.chunk = out_type == NS_F32 ? 1 : 4;
-  p.direct = out_type == NS_F32;
   p.in = ns::Input{G, g_type, rows, cols, ldg, g_stride,
                    (ldg == cols || rows == 1) && aligned(G, 0, batch > 1 ? g_stride : 0, g_type),
                    aligned(G, ldg, batch > 1 ? g_stride : 0, g_type)};

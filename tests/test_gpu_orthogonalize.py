@@ -238,3 +238,16 @@ def test_refusals_on_the_gpu():
         with pytest.raises(sg.SgemmError) as e:
             sg.orthogonalize(g, **kw)
         assert e.value.status == code
+
+
+@pytest.mark.parametrize("otype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", [(20, 300), (256, 256), (300, 1100), (700, 520), (4, 300, 300)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_16_bit_results_are_the_fp32_ones_rounded_once(shape, otype):
+    """The type of the result changes its last rounding, and nothing that comes before it."""
+    g = rand(*shape, seed=19).to(otype).cuda()
+    wide = sg.orthogonalize(g, out_dtype=torch.float32)
+    assert torch.equal(sg.orthogonalize(g), wide.to(otype))
+    out = rand(*shape, seed=20).to(otype).cuda()
+    want = torch.addcmul(0.5 * wide, out.float(), torch.tensor(-2.0, device="cuda")).to(otype)
+    assert torch.equal(sg.orthogonalize(g, alpha=0.5, beta=-2.0, out=out), want)
