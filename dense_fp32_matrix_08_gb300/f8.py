@@ -45,7 +45,8 @@ _gemm_args = struct.Struct("@iiiiifPiiPiqqPiiPiqqfPiiP").pack
 
 
 def _rows(name, t):
-    """(rows, columns, row stride) of a 2-D CUDA tensor with unit column stride."""
+    """(rows, columns, row stride) of a 2-D CUDA tensor with unit column stride and rows that do not
+    overlap."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
@@ -54,7 +55,11 @@ def _rows(name, t):
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return rows, cols, (ld if ld >= cols and rows > 1 else cols) or 1
+    if rows <= 1:
+        return rows, cols, cols or 1
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap (an expanded tensor or a sliding window)")
+    return rows, cols, ld or 1
 
 
 def _quantize(x, block, both, dtype, pow2, stream):

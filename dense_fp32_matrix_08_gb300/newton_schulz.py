@@ -25,7 +25,8 @@ for _name in NS_EXPORTED:
 
 
 def _matrices(name, t):
-    """(type, row stride, matrix stride) of a 2-D or 3-D CUDA tensor with unit column stride."""
+    """(type, row stride, matrix stride) of a 2-D or 3-D CUDA tensor with unit column stride and rows
+    that do not overlap."""
     if t.dim() not in (2, 3):
         raise ValueError(f"{name} must be 2-D or 3-D")
     if t.dtype not in _TYPE:
@@ -35,7 +36,10 @@ def _matrices(name, t):
     rows, cols = t.shape[-2:]
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = max(t.stride(-2), cols, 1) if rows > 1 else max(cols, 1)
+    ld = t.stride(-2) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap (an expanded tensor or a sliding window)")
+    ld = ld or 1
     return _TYPE[t.dtype], ld, t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else rows * ld
 
 

@@ -409,3 +409,28 @@ def test_python_refusals_on_the_gpu():
         sg.f8_matmul(t, torch.ones(64, 1, device="cuda"), t, torch.ones(1, 1, device="cuda"),
                      transb=True)
     assert e.value.status == -9
+
+
+def test_overlapping_rows_are_refused():
+    """A gradient that autograd expanded, and a sliding window: their rows share elements, so no
+    leading dimension describes them."""
+    y = torch.zeros(8, 256, device="cuda", requires_grad=True)
+    seen = []
+    y.register_hook(seen.append)
+    (y.sum(0) * torch.arange(256, device="cuda")).sum().backward()
+    dy = seen[0]
+    assert dy.stride() == (0, 1)
+    window = torch.zeros(400, device="cuda").unfold(0, 256, 1)
+    for x in (dy, window):
+        for call in (sg.f8_quantize, sg.f8_quantize_pair):
+            with pytest.raises(ValueError, match="overlap"):
+                call(x)
+        q, s = sg.f8_quantize(x.contiguous())
+        w, ws = sg.f8_quantize(x.contiguous(), (128, 128))
+        rows = x.shape[0]
+        for out in (dy[:, :rows] if rows == 8 else window[:, :rows],
+                    torch.zeros(1, rows, device="cuda").expand(rows, rows)):
+            with pytest.raises(ValueError, match="overlap"):
+                sg.f8_matmul(q, s, w, ws, transb=True, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            sg.f8_matmul(q[:1].expand(rows, 256), s, w, ws, transb=True)

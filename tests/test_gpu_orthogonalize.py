@@ -251,3 +251,12 @@ def test_16_bit_results_are_the_fp32_ones_rounded_once(shape, otype):
     out = rand(*shape, seed=20).to(otype).cuda()
     want = torch.addcmul(0.5 * wide, out.float(), torch.tensor(-2.0, device="cuda")).to(otype)
     assert torch.equal(sg.orthogonalize(g, alpha=0.5, beta=-2.0, out=out), want)
+
+
+def test_overlapping_rows_are_refused():
+    g = torch.zeros(8, 60, device="cuda")
+    for bad in (g[:1].expand(8, 60), torch.zeros(67, device="cuda").unfold(0, 60, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            sg.orthogonalize(bad)
+        with pytest.raises(ValueError, match="overlap"):
+            sg.orthogonalize(g, out=bad)
