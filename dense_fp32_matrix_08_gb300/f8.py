@@ -26,6 +26,7 @@ F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8
 
 _FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_MOST = 0x7ffffff0  # sizes are 32-bit, rows of quantised matrices multiples of 16
 _BLOCKS = ((1, 128), (128, 1), (128, 128))
 
 _i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
@@ -56,9 +57,11 @@ def _rows(name, t):
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows <= 1:
-        return rows, cols, cols or 1
+        ld = cols
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap (an expanded tensor or a sliding window)")
+    if rows > _MOST or ld > _MOST:
+        raise ValueError(f"{name}'s sizes and row stride must be below 2^31 - 15")
     return rows, cols, ld or 1
 
 

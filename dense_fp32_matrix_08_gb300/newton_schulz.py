@@ -13,6 +13,7 @@ __all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize
 # Every symbol include/orthogonalize.h declares.
 NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status")
 
+_MOST = 0x7fffffff  # sizes are 32-bit
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
@@ -39,6 +40,8 @@ def _matrices(name, t):
     ld = t.stride(-2) if rows > 1 else cols
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap (an expanded tensor or a sliding window)")
+    if rows > _MOST or ld > _MOST or t.shape[0] > _MOST:
+        raise ValueError(f"{name}'s sizes and row stride must be below 2^31")
     ld = ld or 1
     return _TYPE[t.dtype], ld, t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else rows * ld
 
@@ -65,6 +68,7 @@ def orthogonalize(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     batch = g.shape[0] if g.dim() == 3 else 1
     rows, cols = g.shape[-2:]
     a, b, c = coefficients
+    steps = max(-1, min(steps, 65))  # (32 bits of a larger number would be another one)
     rc = lib.ns_orthogonalize(batch, rows, cols, g.data_ptr() or None, gt, ldg, gs, steps,
                               (_f * 3)(a, b, c), eps, alpha, beta, out.data_ptr() or None, ot, ldo,
                               os_, _stream(stream))

@@ -73,3 +73,33 @@ def test_one_row_or_column_needs_no_stride():
     for helper in (f8._rows, newton_schulz._matrices):
         with pytest.raises(ValueError, match="overlap"):
             helper("x", on_gpu(flat.as_strided((5, 1), (0, 1))))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float8_e4m3fn])
+def test_sizes_past_32_bits_are_refused(dtype):
+    """Sizes reach the library as 32-bit integers: one that does not fit must not become another one."""
+    from dense_fp32_matrix_08_gb300 import f8, newton_schulz
+    far = on_gpu(torch.empty((2, (1 << 32) + 16), dtype=dtype, device="meta"))
+    for t in (far, far[:, :6], far.t()[:1 << 31].t(), far.reshape(-1, 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            f8._rows("x", t)
+        if dtype is torch.float32:
+            with pytest.raises(ValueError, match="2\\^31"):
+                newton_schulz._matrices("x", t)
+    if dtype is torch.float32:
+        for call in (sg.f8_quantize, sg.f8_quantize_pair, sg.orthogonalize):
+            with pytest.raises(ValueError, match="2\\^31"):
+                call(far[:, :6])
+        with pytest.raises(ValueError, match="2\\^31"):
+            sg.orthogonalize(on_gpu(torch.empty(((1 << 32) + 1, 2, 2), device="meta")))
+
+
+def test_steps_past_32_bits_are_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    g = on_gpu(torch.empty((0, 4)))
+    assert sg.orthogonalize(g, steps=64, out=g) is g
+    for steps in (65, (1 << 32) + 5, -1, -(1 << 32)):
+        with pytest.raises(sg.SgemmError) as e:
+            sg.orthogonalize(g, steps=steps, out=g)
+        assert e.value.status == -8
