@@ -127,6 +127,28 @@ def _stream(s) -> int | None:
     return int(s.cuda_stream) or None
 
 
+def _on_stream(stream, call, used):
+    """call() with `stream` (a handle or a torch stream) as torch's current stream. What it allocates
+    belongs to that stream. Memory of `used` is not handed on while the stream may still use it, nor
+    memory of the result while the caller's stream may. Order between the two streams stays with the
+    caller."""
+    import torch
+    here = torch.cuda.current_stream()
+    if isinstance(stream, int):
+        side = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    else:
+        side = stream
+    if side.cuda_stream == here.cuda_stream:
+        return call()
+    with torch.cuda.stream(side):
+        result = call()
+    for t in used:
+        t.record_stream(side)
+    for t in result if isinstance(result, tuple) else (result,):
+        t.record_stream(here)
+    return result
+
+
 def sgemm_f32(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream=None) -> int:
     """Mirror of the C entry point; returns its status (0 = success)."""
     return lib.sgemm_f32(M, N, K, alpha, _ptr(A), lda, _ptr(B), ldb, beta, _ptr(C), ldc,

@@ -17,7 +17,7 @@ import struct
 
 import torch
 
-from . import SgemmError, _stream, lib
+from . import SgemmError, _on_stream, _stream, lib
 
 __all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
 
@@ -66,6 +66,8 @@ def _rows(name, t):
 
 
 def _quantize(x, block, both, dtype, pow2, stream):
+    if stream is not None:
+        return _on_stream(stream, lambda: _quantize(x, block, both, dtype, pow2, None), (x,))
     fmt = _FORMAT.get(dtype)
     if fmt is None:
         raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
@@ -93,11 +95,11 @@ def _quantize(x, block, both, dtype, pow2, stream):
                                  device=device)
         rc = lib.f8_quantize_with(_quantize_args(
             rows, cols, x.data_ptr(), xt, ldx, br, bc, fmt, pow2, q.data_ptr(), ldq, s.data_ptr(),
-            s_row, s_col, qc.data_ptr(), ldq, sc.data_ptr(), cols, 1, _stream(stream) or 0))
+            s_row, s_col, qc.data_ptr(), ldq, sc.data_ptr(), cols, 1, _stream(None) or 0))
     else:
         rc = lib.f8_quantize_with(_quantize_args(
             rows, cols, x.data_ptr(), xt, ldx, br, bc, fmt, pow2, q.data_ptr(), ldq, s.data_ptr(),
-            s_row, s_col, 0, 0, 0, 0, 0, _stream(stream) or 0))
+            s_row, s_col, 0, 0, 0, 0, 0, _stream(None) or 0))
     if rc != 0:
         raise SgemmError(rc, "f8_quantize")
     return (q, s, qc, sc) if both else (q, s)
@@ -106,7 +108,8 @@ def _quantize(x, block, both, dtype, pow2, stream):
 def f8_quantize(x, block=(1, 128), *, dtype=torch.float8_e4m3fn, pow2=False, stream=None):
     """Quantise a 2-D CUDA tensor (float32, bfloat16, float16) by blocks of (1, 128), (128, 1) or
     (128, 128): returns (q, scale). scale = max(amax / largest, 2^-126) of each block, with pow2
-    the least power of two not below it; q = x / scale rounded to dtype."""
+    the least power of two not below it; q = x / scale rounded to dtype. `stream`: where to run (a
+    torch stream or a handle; the current stream unless given), the results belong to it."""
     if block not in _BLOCKS:
         raise ValueError(f"block must be one of {_BLOCKS}")
     return _quantize(x, block, False, dtype, bool(pow2), stream)
@@ -151,7 +154,12 @@ def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, 
     """out = alpha * op(a) @ op(b) + beta * out on quantised operands (op: transposed if the
     flag is set). `out` is float32, bfloat16 or float16 with unit column stride; without one a
     new tensor of out_dtype (bfloat16 unless given) is returned. Each operand's scales run along
-    the contraction in blocks of 128. Raises SgemmError on a nonzero status."""
+    the contraction in blocks of 128. `stream` as in f8_quantize. Raises SgemmError on a nonzero
+    status."""
+    if stream is not None:
+        return _on_stream(stream, lambda: f8_matmul(
+            a, a_scale, b, b_scale, transa=transa, transb=transb, alpha=alpha, beta=beta, out=out,
+            out_dtype=out_dtype), [t for t in (a, a_scale, b, b_scale, out) if t is not None])
     fa, lda, ga, amn, ak, K, M = _operand("a", a, a_scale, 0 if transa else 1)
     fb, ldb, gb, bmn, bk, K2, N = _operand("b", b, b_scale, 1 if transb else 0)
     if K2 != K:
@@ -176,7 +184,7 @@ def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, 
     rc = lib.f8_gemm_with(_gemm_args(
         transa, transb, M, N, K, alpha, a.data_ptr(), fa, lda, a_scale.data_ptr(), ga, amn, ak,
         b.data_ptr(), fb, ldb, b_scale.data_ptr(), gb, bmn, bk, beta, out.data_ptr(), dt, ldd,
-        _stream(stream) or 0))
+        _stream(None) or 0))
     if rc != 0:
         raise SgemmError(rc, "f8_gemm")
     return out

@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from . import SgemmError, _stream, lib
+from . import SgemmError, _on_stream, _stream, lib
 
 __all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
            "NS_EXPORTED"]
@@ -52,7 +52,13 @@ def orthogonalize(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     X <- a X + (b S + c S^2) X, S = X X^T, from X = g / (|g|_F + eps); coefficients = (a, b, c).
     g is a matrix or a batch of them (float32, bfloat16, float16). Without `out` a new tensor of
     out_dtype (g's type unless given) is returned. With out = the weight, alpha = -rate and
-    beta = 1 - rate * decay it is the whole update. Raises SgemmError on a nonzero status."""
+    beta = 1 - rate * decay it is the whole update. `stream`: where to run (a torch stream or a handle;
+    the current stream unless given), a new result belongs to it. Raises SgemmError on a nonzero
+    status."""
+    if stream is not None:
+        return _on_stream(stream, lambda: orthogonalize(
+            g, steps=steps, coefficients=coefficients, eps=eps, alpha=alpha, beta=beta, out=out,
+            out_dtype=out_dtype), (g,) if out is None else (g, out))
     gt, ldg, gs = _matrices("g", g)
     if out is None:
         if beta != 0.0:
@@ -71,7 +77,7 @@ def orthogonalize(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     steps = max(-1, min(steps, 65))  # (32 bits of a larger number would be another one)
     rc = lib.ns_orthogonalize(batch, rows, cols, g.data_ptr() or None, gt, ldg, gs, steps,
                               (_f * 3)(a, b, c), eps, alpha, beta, out.data_ptr() or None, ot, ldo,
-                              os_, _stream(stream))
+                              os_, _stream(None))
     if rc != 0:
         raise SgemmError(rc, "ns_orthogonalize")
     return out
