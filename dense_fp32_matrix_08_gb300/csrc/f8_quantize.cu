@@ -13,7 +13,8 @@
 //    one step of Markstein's remainder iteration: exact next to a tie, where m is the tie and the
 //    remainder tiny, and within an FP32 rounding elsewhere, where nothing depends on it. So q is
 //    what the correctly rounded FP32 quotient gives, for three packed FP32 instructions per two
-//    elements and no branch.
+//    elements. m s has bits down to 2^-33 s (e4m3; 2^-40 s for e5m2), which FP32 no longer holds for
+//    s under 2^-116 (2^-109): blocks with s under 2^-100 are computed from 2^64 x and 2^64 s.
 //  * rows_kernel (1 x 128): 8 lanes hold one block, so a block's maximum is three shuffles.
 //  * tile_kernel (the other layouts): a CTA holds a 128 x 128 tile in registers, 32 of them per
 //    thread; row maxima are shuffles, column maxima and the tile's maximum meet in shared memory.
@@ -51,9 +52,12 @@ struct QuantParams {
 
 // Types of x: 16 neighbouring elements are W words. larger(): the larger magnitudes of two words
 // (with either sign; NaN over all); top(): the largest magnitude in a word, and value(): number n
-// of a word, as FP32.
+// of a word, as FP32; scaled(): a word's numbers times powers of two whose results the type holds.
+// SMALL: scales under kSmallScale occur. CTAS: of rows_kernel per SM, for the registers, where the
+// compiler alone takes too many (BF16 with 37 for 31: 18.0 us, not 17.0, for 8192 x 4096); 0: it does not.
 struct F32 {
-  static constexpr int W = 16;
+  static constexpr int W = 16, CTAS = 0;
+  static constexpr bool SMALL = true;
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     uint32_t m;
     asm("max.NaN.xorsign.abs.f32 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
@@ -61,9 +65,13 @@ struct F32 {
   }
   static __device__ __forceinline__ float top(uint32_t w) { return fabsf(__uint_as_float(w)); }
   static __device__ __forceinline__ float value(uint32_t w, int) { return __uint_as_float(w); }
+  static __device__ __forceinline__ uint32_t scaled(uint32_t w, float f, float) {
+    return __float_as_uint(__uint_as_float(w) * f);
+  }
 };
 struct BF16 {
-  static constexpr int W = 8;
+  static constexpr int W = 8, CTAS = 8;
+  static constexpr bool SMALL = true;
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     uint32_t m;
     asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
@@ -76,9 +84,14 @@ struct BF16 {
   static __device__ __forceinline__ float value(uint32_t w, int n) {
     return __uint_as_float(n ? w & 0xffff0000u : w << 16);
   }
+  static __device__ __forceinline__ uint32_t scaled(uint32_t w, float lo, float hi) {
+    return __float_as_uint(value(w, 0) * lo) >> 16 |
+           (__float_as_uint(value(w, 1) * hi) & 0xffff0000u);  // (a NaN has bits below, too)
+  }
 };
 struct F16 {
-  static constexpr int W = 8;
+  static constexpr int W = 8, CTAS = 0;
+  static constexpr bool SMALL = false;  // (its smallest number is 2^-24)
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
     uint32_t m;
     asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
@@ -139,6 +152,7 @@ __device__ __forceinline__ uint32_t max16(const Sixteen<T> &v) {
 struct Scale {
   float s, r, minus;
 };
+constexpr float kSmallScale = 0x1p-100f, kUp = 0x1p64f, kDown = 0x1p-64f;
 
 __device__ __forceinline__ Scale scale_of(float amax, int format, int pow2) {
   const uint32_t least = 0x00800000u, inf = 0x7f800000u;  // 2^-126
@@ -196,6 +210,19 @@ __device__ __forceinline__ uint4 quantize16(const Sixteen<T> &v, const Scale &s)
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A small scale's factors for 2^64 x.
+__device__ __forceinline__ void raise(Scale &s) {
+  s.r *= kDown;
+  s.minus *= kUp;
+}
+
+// v times f, a power of two (exact).
+template <class T>
+__device__ __forceinline__ void scale16(Sixteen<T> &v, float f) {
+#pragma unroll
+  for (int i = 0; i < T::W; ++i) v.w[i] = T::scaled(v.w[i], f, f);
+}
+
 // The first n of 16 bytes.
 __device__ __forceinline__ void store16(uint8_t *dst, bool vec, int n, const uint4 &w) {
   if (vec && n >= 16) {
@@ -218,10 +245,10 @@ __device__ __forceinline__ Scale lanes_scale(uint32_t m, int format, int pow2) {
 
 // 1 x 128 blocks: unit u = row * blocks + block; a warp takes 4 neighbouring units at a time, so that
 // it reads 1 KB (of 16 bits) at once and a block's maximum stays within 8 lanes. No shared memory, 31
-// registers: 72% of the warps resident. 8192 x 4096 BF16: 16.8 us, 6.0 TB/s
-// (89% of a copy's rate); the issue slots are then 73% busy. 1 x 4096: 1.4 us.
+// registers: 72% of the warps resident. 8192 x 4096 BF16: 17.0 us, 5.9 TB/s
+// (88% of a copy's rate); the issue slots are then 73% busy. 1 x 4096: 1.4 us.
 template <class T, int FORMAT>
-__global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(256, T::CTAS) rows_kernel(const QuantParams p) {
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   constexpr int size = T::W == 16 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane & 7;
@@ -237,8 +264,14 @@ __global__ void __launch_bounds__(256) rows_kernel(const QuantParams p) {
     const int n = r < p.rows ? p.cols - c : 0;
     Sixteen<T> v;
     load16<T>(reinterpret_cast<const char *>(p.x) + (r * p.ldx + c) * size, p.vec, n, v);
-    const Scale s = lanes_scale<T>(max16<T>(v), FORMAT, p.pow2);
+    Scale s = lanes_scale<T>(max16<T>(v), FORMAT, p.pow2);
     if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + b * p.a.s_col] = s.s;
+    if constexpr (T::SMALL) {
+      if (s.s < kSmallScale) {
+        raise(s);
+        scale16<T>(v, kUp);
+      }
+    }
     store16(p.a.q + r * p.a.ldq + c, p.a.vec, n, quantize16<T, FORMAT>(v, s));
     r += step_r;
     b += step_b;
@@ -256,9 +289,9 @@ enum { COLS = 0, SQUARE = 1, PAIR = 2 };
 // 16 sub .. + 15 of rows g, g + G, ...: 32 registers of x. The tile stays in registers from its one
 // read to its last use, so a CTA has no loads under way while it computes and stores: several CTAs
 // per SM overlap instead, as many as the registers allow (34 to 47% of the warps). 14336 x 4096
-// FP32 in squares: 50 us, 5.9 TB/s, 87% of a copy's rate. 8192 x 4096 BF16 by rows and by columns at
-// once: 35 us, 3.9 TB/s, with twice the arithmetic per byte read; two calls, by rows and by columns,
-// take 16.8 + 25.1 us. (CTAs of 512 threads with half as many elements each: 44 us for 35, 23 for 16 in
+// FP32 in squares: 49 us, 6.0 TB/s, 89% of a copy's rate. 8192 x 4096 BF16 by rows and by columns at
+// once: 34 us, 4.0 TB/s, with twice the arithmetic per byte read; two calls, by rows and by columns,
+// take 17.0 + 25.8 us. (CTAs of 512 threads with half as many elements each: 44 us for 35, 23 for 16 in
 // squares; a column's maximum then takes as many shuffles for half as many rows.)
 template <class T>
 constexpr int kRowGroups = T::W == 16 ? 64 : 32;
@@ -270,7 +303,7 @@ __global__ void __launch_bounds__(8 * kRowGroups<T>, T::W == 16 ? 2 : WHICH == P
   constexpr int size = T::W == 16 ? 4 : 2;
   constexpr int G = kRowGroups<T>, WARPS = G / 4, ROWS = 128 / G;
   __shared__ uint32_t top[WARPS][8 * T::W];
-  __shared__ __align__(16) float col_r[128], col_minus[128];
+  __shared__ __align__(16) float col_r[128], col_minus[128], col_up[128];
   const int tid = threadIdx.x, sub = tid & 7, g = tid >> 3, warp = tid >> 5;
   const int br = blockIdx.x / tiles_c, bc = blockIdx.x % tiles_c;
   const int r0 = br * 128 + g, c0 = bc * 128 + sub * 16;
@@ -291,8 +324,15 @@ __global__ void __launch_bounds__(8 * kRowGroups<T>, T::W == 16 ? 2 : WHICH == P
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) m = T::larger(m, top[w][0]);
-    const Scale s = scale_of(T::top(m), FORMAT, p.pow2);
+    Scale s = scale_of(T::top(m), FORMAT, p.pow2);
     if (tid == 0) p.a.s[br * p.a.s_row + bc * p.a.s_col] = s.s;
+    if constexpr (T::SMALL) {
+      if (s.s < kSmallScale) {
+        raise(s);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) scale16<T>(v[i], kUp);
+      }
+    }
     uint8_t *dst = p.a.q + r0 * p.a.ldq + c0;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
@@ -310,12 +350,19 @@ __global__ void __launch_bounds__(8 * kRowGroups<T>, T::W == 16 ? 2 : WHICH == P
       if ((tid & 31) < 8) top[warp][sub * T::W + k] = m;
     }
     __syncthreads();
+    bool small = false;
     if (tid < 128) {  // column tid of the tile
       const int word = T::W == 16 ? tid : tid / 2;
       uint32_t m = top[0][word];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) m = T::larger(m, top[w][word]);
-      const Scale s = scale_of(fabsf(T::value(m, tid & 1)), FORMAT, p.pow2);
+      const float amax = fabsf(T::value(m, tid & 1));
+      Scale s = scale_of(amax, FORMAT, p.pow2);
+      if constexpr (T::SMALL) {
+        small = s.s < kSmallScale && amax > 0.0f;  // (a column of zeros needs no correction)
+        col_up[tid] = small ? kUp : 1.0f;
+        if (small) raise(s);
+      }
       col_r[tid] = s.r;
       col_minus[tid] = s.minus;
       if (bc * 128 + tid < p.cols) o.s[br * o.s_row + (bc * 128 + tid) * o.s_col] = s.s;
@@ -325,13 +372,34 @@ __global__ void __launch_bounds__(8 * kRowGroups<T>, T::W == 16 ? 2 : WHICH == P
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         const int r = r0 + G * i;
-        const Scale s = lanes_scale<T>(max16<T>(v[i]), FORMAT, p.pow2);
+        Scale s = lanes_scale<T>(max16<T>(v[i]), FORMAT, p.pow2);
         if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + bc * p.a.s_col] = s.s;
+        if constexpr (T::SMALL) {
+          if (s.s < kSmallScale) {
+            raise(s);
+            scale16<T>(v[i], kUp);
+          }
+        }
         store16(dst + i * (G * p.a.ldq), p.a.vec, r < p.rows ? n : 0,
                 quantize16<T, FORMAT>(v[i], s));
+        if constexpr (T::SMALL) {
+          if (s.s < kSmallScale) scale16<T>(v[i], kDown);  // (the columns have their own scales)
+        }
       }
     }
-    __syncthreads();
+    if constexpr (!T::SMALL) {
+      __syncthreads();
+    } else {
+      if (__syncthreads_or(small)) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+          for (int k = 0; k < T::W; ++k) {
+            const int c = sub * 16 + k * (16 / T::W);
+            v[i].w[k] = T::scaled(v[i].w[k], col_up[c], col_up[c + (T::W == 8)]);
+          }
+      }
+    }
     uint8_t *dst = o.q + r0 * o.ldq + c0;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {

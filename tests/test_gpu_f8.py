@@ -434,3 +434,56 @@ def test_overlapping_rows_are_refused():
                 sg.f8_matmul(q, s, w, ws, transb=True, out=out)
         with pytest.raises(ValueError, match="overlap"):
             sg.f8_matmul(q[:1].expand(rows, 256), s, w, ws, transb=True)
+
+
+@pytest.mark.parametrize("power", [-126, -125, -118, -116, -112, -109, -101, -100, -99, -60])
+@pytest.mark.parametrize("dtype", [E4, E5])
+@pytest.mark.parametrize("xtype", [torch.float32, torch.bfloat16])
+def test_quantize_ties_at_small_scales(power, dtype, xtype):
+    """Numbers next to the ties of the format's smallest numbers, under scales down to the least."""
+    rows, cols = 128, 256
+    g = torch.Generator().manual_seed(200 + power)
+    least = 2.0 ** (-9 if dtype == E4 else -16)
+    top = (1.0 + torch.rand(rows, cols // 128, generator=g)) * plain.LARGEST[dtype]
+    top = torch.ldexp(top, torch.tensor(power)).to(xtype).float()
+    s = (top.double() / plain.LARGEST[dtype]).float().repeat_interleave(128, 1)
+    tie = (torch.randint(0, 16, (rows, cols), generator=g) + 0.5) * least
+    x = (tie.double() * s.double()).float()
+    near = torch.randint(-2, 3, (rows, cols), generator=g)
+    x = (x.view(torch.int32) + near).clamp_min(0).int().view(torch.float32)
+    x[:, ::128] = top
+    x = (x * (1 - 2 * torch.randint(0, 2, (rows, cols), generator=g))).to(xtype)
+    for y in (x, x.t().contiguous()):
+        for block in BLOCKS:
+            check_quantized(y.cuda(), block, dtype, False, *sg.f8_quantize(y.cuda(), block, dtype=dtype))
+        check_quantized(y.cuda(), (128, 1), dtype, True,
+                        *sg.f8_quantize(y.cuda(), (128, 1), dtype=dtype, pow2=True))
+        q, s1, qc, sc = sg.f8_quantize_pair(y.cuda(), dtype=dtype)
+        check_quantized(y.cuda(), (1, 128), dtype, False, q, s1)
+        check_quantized(y.cuda(), (128, 1), dtype, False, qc, sc)
+
+
+def test_quantize_small_beside_large_and_not_finite():
+    """Columns and rows of every magnitude in one tile: each keeps to its own scale."""
+    x = rand(256, 256, seed=31) * 2.0 ** torch.linspace(-140, 100, 256)[None, :]
+    x[:, 7] = 0.0
+    x[5, 9] = float("nan")
+    x[6, 200] = float("-inf")
+    for xtype in (torch.float32, torch.bfloat16):
+        for y in (x.to(xtype), x.to(xtype).t().contiguous()):
+            q, s, qc, sc = sg.f8_quantize_pair(y.cuda())
+            for block, got, scale in (((1, 128), q, s), ((128, 1), qc, sc)):
+                alone, salone = sg.f8_quantize(y.cuda(), block)
+                assert torch.equal(got.view(torch.uint8), alone.view(torch.uint8))
+                fine = torch.isfinite(y)
+                keep = fine.view(-1, y.shape[0] // 2, y.shape[1]) if block[0] == 128 else \
+                    fine.view(y.shape[0], -1, 128)
+                keep = keep.all(dim=1 if block[0] == 128 else 2)  # blocks of finite numbers
+                clean = torch.where(fine, y, torch.zeros_like(y))
+                eq, es = plain.quantize(clean, block, E4, False)
+                assert torch.equal(scale.cpu().double()[keep], es[keep])
+                br, bc = block
+                spread = keep[plain.block_index(256, br)][:, plain.block_index(256, bc)]
+                assert torch.equal(got.cpu().double()[spread], eq[spread])
+                assert not torch.isfinite(scale.cpu()[~keep]).any()
+                assert torch.isnan(got.cpu().float()[~fine]).all()
