@@ -11,6 +11,8 @@ torch.cuda.Stream, or None for torch's current stream on the current device.
 from __future__ import annotations
 
 import ctypes
+import importlib
+import importlib.util
 import os
 
 from ._build import LIB as LIB_PATH
@@ -40,6 +42,9 @@ EXPORTED = ("sgemm_f32", "sgemm_f32_ws", "sgemm_f32_forced", "sgemm_f32_workspac
             "sgemm_f32_host", "sgemm_f32_wait_selftest", "sgemm_f32_release_workspace",
             "sgemm_f32_fma_probe", "sgemm_f32_cluster_capacity",
             "sgemm_f32_workspace_size_min")
+# The same of include/f8_gemm.h and of include/orthogonalize.h.
+F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_status")
+NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status")
 
 
 class SgemmError(RuntimeError):
@@ -91,7 +96,16 @@ def _load() -> ctypes.CDLL:
     L.sgemm_f32_variant_info.argtypes = [i] + [pi] * 7
     L.sgemm_f32_version.argtypes = []
     L.sgemm_f32_version.restype = ctypes.c_char_p
-    for name in EXPORTED:
+    ll = ctypes.c_longlong
+    L.f8_quantize.argtypes = [i, i, vp, i, i, i, i, i, i] + [vp, i, vp, ll, ll] * 2 + [vp]
+    L.f8_gemm.argtypes = ([i, i, i, i, i, f] + [vp, i, i, vp, i, ll, ll] * 2 + [f, vp, i, i, vp])
+    L.f8_quantize_with.argtypes = L.f8_gemm_with.argtypes = [ctypes.c_char_p]
+    L.f8_gemm_status.argtypes = [pi]
+    L.ns_orthogonalize.argtypes = [i, i, i, vp, i, i, ll, i, ctypes.POINTER(f), f, f, f, vp, i, i, ll,
+                                   vp]
+    L.ns_orthogonalize_workspace_size.argtypes = [i, i, i, psz]
+    L.ns_orthogonalize_status.argtypes = [pi]
+    for name in EXPORTED + F8_EXPORTED + NS_EXPORTED:
         if name != "sgemm_f32_version":
             getattr(L, name).restype = ctypes.c_int
     return L
@@ -385,12 +399,25 @@ def sgemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 
 
 # The tensor-core operators of a linear layer's training step and of its serving: 8-bit
-# block-scaled products and the orthogonalised update (they need torch, unlike the bindings above).
-from .f8 import (F8_EXPORTED, f8_gemm_status, f8_matmul, f8_quantize,  # noqa: E402
-                 f8_quantize_pair)
-from .newton_schulz import (NS_EXPORTED, ns_orthogonalize_status,  # noqa: E402
-                            ns_orthogonalize_workspace_size, orthogonalize)
+# block-scaled products and the orthogonalised update. They need torch, which the bindings above do
+# not, so their modules are imported when one of their names is first used.
+_LATE = {"f8": ("f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status"),
+         "newton_schulz": ("orthogonalize", "ns_orthogonalize_workspace_size",
+                           "ns_orthogonalize_status")}
 
-__all__ += ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED",
-            "orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
-            "NS_EXPORTED"]
+__all__ += ["F8_EXPORTED", "NS_EXPORTED"]
+if importlib.util.find_spec("torch") is not None:
+    __all__ += [name for names in _LATE.values() for name in names]
+
+
+def __getattr__(name):
+    for module, names in _LATE.items():
+        if name == module or name in names:
+            found = importlib.import_module("." + module, __name__)
+            globals().update((n, getattr(found, n)) for n in names)
+            return globals()[name] if name in names else found
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()).union(*_LATE.values()))

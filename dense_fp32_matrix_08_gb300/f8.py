@@ -17,28 +17,14 @@ import struct
 
 import torch
 
-from . import SgemmError, _on_stream, _stream, lib
+from . import F8_EXPORTED, SgemmError, _on_stream, _stream, lib
 
 __all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
-
-# Every symbol include/f8_gemm.h declares.
-F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_status")
 
 _FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _MOST = 0x7ffffff0  # sizes are 32-bit, rows of quantised matrices multiples of 16
 _BLOCKS = ((1, 128), (128, 1), (128, 128))
-
-_i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
-lib.f8_quantize.argtypes = ([_i, _i, _vp, _i, _i, _i, _i, _i, _i] + [_vp, _i, _vp, _ll, _ll] * 2 +
-                            [_vp])
-lib.f8_gemm.argtypes = ([_i, _i, _i, _i, _i, _f] + [_vp, _i, _i, _vp, _i, _ll, _ll] * 2 +
-                        [_f, _vp, _i, _i, _vp])
-lib.f8_quantize_with.argtypes = lib.f8_gemm_with.argtypes = [ctypes.c_char_p]
-lib.f8_gemm_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
-for _name in F8_EXPORTED:
-    getattr(lib, _name).restype = ctypes.c_int
-
 
 # f8_quantize_args and f8_gemm_args
 _quantize_args = struct.Struct("@iiPiiiiiiPiPqqPiPqqP").pack

@@ -5,24 +5,13 @@ import ctypes
 
 import torch
 
-from . import SgemmError, _on_stream, _stream, lib
+from . import NS_EXPORTED, SgemmError, _on_stream, _stream, lib
 
 __all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
            "NS_EXPORTED"]
 
-# Every symbol include/orthogonalize.h declares.
-NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status")
-
 _MOST = 0x7fffffff  # sizes are 32-bit
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-
-_i, _f, _vp, _ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
-lib.ns_orthogonalize.argtypes = [_i, _i, _i, _vp, _i, _i, _ll, _i, ctypes.POINTER(_f), _f, _f, _f,
-                                 _vp, _i, _i, _ll, _vp]
-lib.ns_orthogonalize_workspace_size.argtypes = [_i, _i, _i, ctypes.POINTER(ctypes.c_size_t)]
-lib.ns_orthogonalize_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
-for _name in NS_EXPORTED:
-    getattr(lib, _name).restype = ctypes.c_int
 
 
 def _matrices(name, t):
@@ -76,7 +65,7 @@ def orthogonalize(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     a, b, c = coefficients
     steps = max(-1, min(steps, 65))  # (32 bits of a larger number would be another one)
     rc = lib.ns_orthogonalize(batch, rows, cols, g.data_ptr() or None, gt, ldg, gs, steps,
-                              (_f * 3)(a, b, c), eps, alpha, beta, out.data_ptr() or None, ot, ldo,
+                              (ctypes.c_float * 3)(a, b, c), eps, alpha, beta, out.data_ptr() or None, ot, ldo,
                               os_, _stream(None))
     if rc != 0:
         raise SgemmError(rc, "ns_orthogonalize")
