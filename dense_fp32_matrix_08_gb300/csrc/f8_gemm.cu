@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       int tp, tq;
       tile_at(t, tp, tq);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u)) {
+        ok = __all_sync(0xffffffffu, wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u));
+        if (!ok) {
           if (lane == 0) atomicCAS(&g_f8_status, 0, 1);
-          ok = false;
           break;
         }
         if (elect_one()) {
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         if (PAIR || mine == 0) {
           const uint32_t a = acc0 + buf.slot;
-          ok = wait_short(bars + 8 * st.slot, st.parity) &&
-               wait_short(acc_empty + 8 * a, buf.parity ^ 1u);
+          ok = __all_sync(0xffffffffu, wait_short(bars + 8 * st.slot, st.parity) &&
+                                           wait_short(acc_empty + 8 * a, buf.parity ^ 1u));
           if (!ok) {
             if (lane == 0) atomicCAS(&g_f8_status, 0, 2);
             break;

@@ -162,7 +162,9 @@ __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned targ
     if (copies) proxy_fence();  // (they read what other CTAs' plain stores wrote)
     if (!ok) atomicCAS(&g_ns_status, 0, 4);
   }
-  return __all_sync(0xffffffffu, ok);
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();  // (a vote orders no memory: what lane 0 has acquired is now visible to all)
+  return ok;
 }
 
 // Units of a product: the tiles computed whole, then the parts of the others.
@@ -602,7 +604,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int y0 = u.mat * p.mp, p0 = u.tp * C::BS + cta * 128;
           const int q0 = u.tq * C::TN + cta * (PAIR ? C::QN : 0);
           for (int kt = u.k0; kt < u.k1; ++kt) {
-            ok = wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u);
+            ok = __all_sync(0xffffffffu,
+                            wait_short(bars + 8 * (C::STAGES + st.slot), st.parity ^ 1u));
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 1);
               break;
@@ -672,8 +675,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = first; i < total && ok; i += stride) {
           const Unit u = unit_at<C>(p, mode, i);
           for (int kt = u.k0; kt < u.k1; ++kt) {
-            ok = wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
-                 wait_short(bars + 8 * st.slot, st.parity);
+            ok = __all_sync(0xffffffffu, wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
+                                             wait_short(bars + 8 * st.slot, st.parity));
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
               break;

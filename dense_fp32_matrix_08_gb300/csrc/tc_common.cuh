@@ -20,6 +20,9 @@ namespace tcx {
 // the thread for as long as the hardware chooses, so that waiting warps leave the issue slots and the
 // shared memory port to the others (a limit of one's own costs the 8-bit product's epilogue seven
 // instructions of 150 per block and 2% of its time); the global timer is read between tries only.
+// Lanes may answer differently when the limit runs out while the phase completes, so a warp that goes
+// on to something that needs all of its lanes (elect.sync, tcgen05.ld) takes a vote on the answer: some
+// lanes that left the loop alone would keep the others waiting for ever.
 __device__ __forceinline__ bool try_wait_suspended(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
