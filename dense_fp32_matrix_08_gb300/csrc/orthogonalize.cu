@@ -141,7 +141,13 @@ __device__ __forceinline__ void grid_arrive(unsigned *counter) {  // one thread,
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;\n" ::"l"(counter) : "memory");
 }
 
-// One warp; false if the count has not been reached after 8 s. copies: TMA copies follow.
+// Limit of a wait at the barrier, whose end other CTAs' work decides. A product's first operands, and
+// its first sums, come after the barrier and one and two waits of this CTA's own: those are waited for
+// that much longer. Every other wait is for the CTA's own (or its partner's) copies and instructions.
+constexpr unsigned long long kGridLimitNs = 8 * kWaitLimitNs;
+constexpr unsigned long long kFirstLimitNs = kGridLimitNs + kWaitLimitNs;
+
+// One warp; false if the count has not been reached after kGridLimitNs. copies: TMA copies follow.
 __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned target, bool copies) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) {
@@ -153,7 +159,7 @@ __device__ __forceinline__ bool grid_wait(const unsigned *counter, unsigned targ
       if ((i & 255u) == 255u) {
         const unsigned long long t = global_ns();
         if (t0 == 0) t0 = t;
-        if (t - t0 > 8 * kWaitLimitNs || i >= (1u << 31)) {
+        if (t - t0 > kGridLimitNs || i >= (1u << 31)) {
           ok = false;
           break;
         }
@@ -672,11 +678,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int ph = 0; ph < 3 * p.steps && ok; ++ph) {
         const int mode = ph % 3;
         const int total = units_of(p, mode);
+        unsigned long long limit = kFirstLimitNs;
         for (int i = first; i < total && ok; i += stride) {
           const Unit u = unit_at<C>(p, mode, i);
           for (int kt = u.k0; kt < u.k1; ++kt) {
             ok = __all_sync(0xffffffffu, wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u) &&
-                                             wait_short(bars + 8 * st.slot, st.parity));
+                                             wait_short(bars + 8 * st.slot, st.parity, limit));
+            limit = kWaitLimitNs;
             if (!ok) {
               if (lane == 0) atomicCAS(&g_ns_status, 0, 2);
               break;
@@ -748,11 +756,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           Unit u;
           int row0, col0;
           if (pass == 0) {
+            unsigned long long limit = kWaitLimitNs + (i == first ? kFirstLimitNs : 0);
             u = unit_at<C>(p, mode, i);
             row0 = u.tp * C::BS + cta * 128 + quad * 32;
             col0 = u.tq * C::TN + grp * C::COLS;
             for (int kt = u.k0; kt < u.k1 && ok; ++kt) {
-              ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
+              ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity, limit));
+              limit = kWaitLimitNs;
               if (!ok) {
                 if (lane == 0) atomicCAS(&g_ns_status, 0, 3);
                 break;

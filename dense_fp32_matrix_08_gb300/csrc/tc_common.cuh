@@ -16,7 +16,7 @@
 namespace sgemm {
 namespace tcx {
 
-// Wait for the phase of parity `parity`, with the limit of mbar_wait (sgemm_ptx.cuh). A try suspends
+// Wait for the phase of parity `parity`, by default with the limit of mbar_wait (sgemm_ptx.cuh). A try suspends
 // the thread for as long as the hardware chooses, so that waiting warps leave the issue slots and the
 // shared memory port to the others (a limit of one's own costs the 8-bit product's epilogue seven
 // instructions of 150 per block and 2% of its time); the global timer is read between tries only.
@@ -37,12 +37,13 @@ __device__ __forceinline__ bool try_wait_suspended(uint32_t bar, uint32_t parity
   return done != 0;
 }
 
-__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity,
+                                           unsigned long long limit = kWaitLimitNs) {
   if (try_wait_suspended(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  for (uint32_t i = 0; i < (1u << 27); ++i) {
+  for (uint32_t i = 0; i < (1u << 30); ++i) {  // (should the timer not advance)
     if (try_wait_suspended(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) return false;
+    if (global_ns() - t0 > limit) return false;
   }
   return false;
 }

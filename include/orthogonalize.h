@@ -51,8 +51,9 @@ int ns_orthogonalize(int batch, int rows, int cols, const void *G, int g_type, i
 int ns_orthogonalize_workspace_size(int batch, int rows, int cols, size_t *bytes);
 
 /* Reads and clears the device status word of ns_orthogonalize (synchronising): 0 = fine, 1 - 4 =
- * a wait gave up after about a second and the call's result is not to be used. Returns 0 or a
- * cudaError_t. */
+ * a wait gave up and the call's result is not to be used. A wait gives up after about a second where
+ * it is for a block's own copies and instructions, and after eight to ten where it depends on the
+ * other blocks. Returns 0 or a cudaError_t. */
 int ns_orthogonalize_status(int *status);
 
 #ifdef __cplusplus

@@ -20,3 +20,13 @@ def test_warps_leave_their_waits_together(name):
         s = " ".join(s.split())
         # (a wait whose answer nothing depends on: copies that must land before the warp leaves)
         assert re.search(r"__all_sync\(0xffffffffu, .*wait_short\(", s) or s.startswith("wait_short("), s
+
+
+def test_only_the_first_waits_of_a_product_depend_on_other_blocks():
+    """A block without work in a product waits for the next one's operands meanwhile: with the limit of
+    the grid-wide barrier, not with that of its own copies."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "orthogonalize.cu")).read())
+    voted = [" ".join(s.split()) for s in re.split(r"[;{}]", text) if "__all_sync(" in s]
+    first = [s for s in voted if "acc_full" in s or "acc_empty" in s]
+    assert len(first) == 2 and all(s.endswith(", limit))") for s in first), first
+    assert len(re.findall(r"limit = kWaitLimitNs;", text)) == 2
