@@ -252,20 +252,21 @@ __global__ void __launch_bounds__(256, T::CTAS) rows_kernel(const QuantParams p)
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   constexpr int size = T::W == 16 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane & 7;
-  const int blocks = (p.cols + 127) / 128;
+  const int blocks = (int)(((unsigned)p.cols + 127) / 128);
   const long long units = (long long)p.rows * blocks;
   const long long step = (long long)gridDim.x * 8 * 4;
   const int step_r = (int)(step / blocks), step_b = (int)(step % blocks);
   long long u = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
   const long long mine = u + (lane >> 3);
-  int r = (int)(mine / blocks), b = (int)(mine % blocks);
+  unsigned r = (unsigned)(mine / blocks);  // (up to rows + 2: past 31 bits where rows are most)
+  int b = (int)(mine % blocks);
   for (; u < units; u += step) {
     const int c = b * 128 + sub * 16;
-    const int n = r < p.rows ? p.cols - c : 0;
+    const int n = r < (unsigned)p.rows ? p.cols - c : 0;
     Sixteen<T> v;
     load16<T>(reinterpret_cast<const char *>(p.x) + (r * p.ldx + c) * size, p.vec, n, v);
     Scale s = lanes_scale<T>(max16<T>(v), FORMAT, p.pow2);
-    if (sub == 0 && r < p.rows) p.a.s[r * p.a.s_row + b * p.a.s_col] = s.s;
+    if (sub == 0 && r < (unsigned)p.rows) p.a.s[r * p.a.s_row + b * p.a.s_col] = s.s;
     if constexpr (T::SMALL) {
       if (s.s < kSmallScale) {
         raise(s);

@@ -487,3 +487,38 @@ def test_quantize_small_beside_large_and_not_finite():
                 assert torch.equal(got.cpu().double()[spread], eq[spread])
                 assert not torch.isfinite(scale.cpu()[~keep]).any()
                 assert torch.isnan(got.cpu().float()[~fine]).all()
+
+
+@pytest.mark.parametrize("cols", [(1 << 31) - 64, (1 << 31) - 128])
+def test_quantize_longest_row(cols):
+    """A row whose number of columns rounded up to whole blocks passes 32 bits."""
+    x = torch.full((1, cols), 2.0, dtype=torch.float16, device="cuda")
+    x[0, -64:] = torch.arange(64, device="cuda")
+    q, s = sg.f8_quantize(x)
+    assert q.shape == (1, cols) and s.shape == (1, 1 << 24 if cols % 128 else (1 << 24) - 1)
+    first = cols // 128 * 128 - (128 if cols % 128 == 0 else 0)
+    for at, n in ((0, 256), (cols // 256 * 128, 256), (first, cols - first)):
+        eq, es = plain.quantize(x[:, at:at + n].cpu(), (1, 128), E4, False)
+        assert torch.equal(q[:, at:at + n].cpu().double(), eq)
+        assert torch.equal(s[:, at // 128:(at + n + 127) // 128].cpu().double(), es)
+    sample = torch.arange(0, s.shape[1] - 1, 997, device="cuda")
+    assert (s[0, sample] == s[0, 0]).all()
+
+
+def test_quantize_most_rows():
+    """2^31 - 1 rows of one column: the last warp's lanes without a row have none to compute with."""
+    rows, guard = (1 << 31) - 1, 256
+    x = torch.full((rows,), 2.0, dtype=torch.float16, device="cuda")
+    x[-4:] = torch.tensor([1.0, -3.0, 0.0, 5.0], device="cuda")
+    q = torch.full((rows + 2 * guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows + 2 * guard,), 7.0, device="cuda")
+    rc = sg.lib.f8_quantize(rows, 1, x.data_ptr(), 2, 1, 1, 128, 0, 0, q.data_ptr() + guard, 1,
+                            s.data_ptr() + 4 * guard, 1, 1, None, 0, None, 0, 0,
+                            torch.cuda.current_stream().cuda_stream or None)
+    assert rc == 0
+    eq, es = plain.quantize(x[-6:, None].cpu(), (1, 128), E4, False)
+    assert torch.equal(q[-guard - 6:-guard].view(E4).cpu().double(), eq[:, 0])
+    assert torch.equal(s[-guard - 6:-guard].cpu().double(), es[:, 0])
+    assert (q[guard:-guard - 4].view(torch.int8) == 0x7e).all()  # 448
+    assert (q[:guard] == 0x5a).all() and (q[-guard:] == 0x5a).all()
+    assert (s[:guard] == 7.0).all() and (s[-guard:] == 7.0).all()
