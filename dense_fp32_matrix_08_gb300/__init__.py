@@ -43,8 +43,10 @@ EXPORTED = ("sgemm_f32", "sgemm_f32_ws", "sgemm_f32_forced", "sgemm_f32_workspac
             "sgemm_f32_fma_probe", "sgemm_f32_cluster_capacity",
             "sgemm_f32_workspace_size_min")
 # The same of include/f8_gemm.h and of include/orthogonalize.h.
-F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_status")
-NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status")
+F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_plan",
+               "f8_gemm_status")
+NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_plan",
+               "ns_orthogonalize_status")
 
 
 class SgemmError(RuntimeError):
@@ -100,10 +102,12 @@ def _load() -> ctypes.CDLL:
     L.f8_quantize.argtypes = [i, i, vp, i, i, i, i, i, i] + [vp, i, vp, ll, ll] * 2 + [vp]
     L.f8_gemm.argtypes = ([i, i, i, i, i, f] + [vp, i, i, vp, i, ll, ll] * 2 + [f, vp, i, i, vp])
     L.f8_quantize_with.argtypes = L.f8_gemm_with.argtypes = [ctypes.c_char_p]
+    L.f8_gemm_plan.argtypes = [i] * 8 + [pi] * 3
     L.f8_gemm_status.argtypes = [pi]
     L.ns_orthogonalize.argtypes = [i, i, i, vp, i, i, ll, i, ctypes.POINTER(f), f, f, f, vp, i, i, ll,
                                    vp]
     L.ns_orthogonalize_workspace_size.argtypes = [i, i, i, psz]
+    L.ns_orthogonalize_plan.argtypes = [i] * 4 + [pi] * 4
     L.ns_orthogonalize_status.argtypes = [pi]
     for name in EXPORTED + F8_EXPORTED + NS_EXPORTED:
         if name != "sgemm_f32_version":
@@ -401,9 +405,9 @@ def sgemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
 # The tensor-core operators of a linear layer's training step and of its serving: 8-bit
 # block-scaled products and the orthogonalised update. They need torch, which the bindings above do
 # not, so their modules are imported when one of their names is first used.
-_LATE = {"f8": ("f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status"),
+_LATE = {"f8": ("f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_plan", "f8_gemm_status"),
          "newton_schulz": ("orthogonalize", "ns_orthogonalize_workspace_size",
-                           "ns_orthogonalize_status")}
+                           "ns_orthogonalize_plan", "ns_orthogonalize_status")}
 
 __all__ += ["F8_EXPORTED", "NS_EXPORTED"]
 if importlib.util.find_spec("torch") is not None:

@@ -728,6 +728,29 @@ extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha,
   }
 }
 
+extern "C" int f8_gemm_plan(int transa, int transb, int M, int N, int K, int a_rows, int b_cols,
+                            int num_sms, int *exchanged, int *tile_cols, int *split) {
+  if (transa != 0 && transa != 1) return -1;
+  if (transb != 0 && transb != 1) return -2;
+  if (M < 1) return -3;
+  if (N < 1) return -4;
+  if (K < 1) return -5;
+  if (a_rows != 1 && a_rows != 128) return -6;
+  if (b_cols != 1 && b_cols != 128) return -7;
+  if (num_sms < 0) return -8;
+  int sms = num_sms;
+  if (sms == 0 && device_setup(&sms) != cudaSuccess) {
+    (void)cudaGetLastError();
+    sms = 152;  // no device here: the answer for a whole GB300
+  }
+  const f8::Plan pl = f8::make_plan(M, N, ceil_div(K, f8::BK), transa == 1, transb == 0,
+                                    a_rows == 1, b_cols == 1, sms);
+  if (exchanged) *exchanged = pl.swap;
+  if (tile_cols) *tile_cols = pl.tn;
+  if (split) *split = pl.split;
+  return 0;
+}
+
 extern "C" int f8_gemm_with(const f8_gemm_args *a) {
   if (a == nullptr) return -1;
   return f8_gemm(a->transa, a->transb, a->M, a->N, a->K, a->alpha, a->A, a->a_format, a->lda,

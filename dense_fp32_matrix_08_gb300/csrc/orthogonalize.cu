@@ -1118,6 +1118,34 @@ extern "C" int ns_orthogonalize_workspace_size(int batch, int rows, int cols, si
   return 0;
 }
 
+extern "C" int ns_orthogonalize_plan(int batch, int rows, int cols, int num_sms, int *tile_cols,
+                                     int tiles[3], int whole[3], int split[3]) {
+  if (batch < 1) return -1;
+  if (rows < 1) return -2;
+  if (cols < 1) return -3;
+  if (num_sms < 0) return -4;
+  int sms = num_sms, pairs = num_sms / 2;
+  const int *at_once = nullptr;
+  if (num_sms == 0) {
+    if (device_setup(&sms) == cudaSuccess && ns::kernel_setup(&at_once) == cudaSuccess) {
+      pairs = *at_once;
+    } else {
+      (void)cudaGetLastError();
+      sms = 152;  // no device here: the answer for a whole GB300
+      pairs = 76;
+    }
+  }
+  const ns::Plan l = ns::choose(batch, rows, cols, sms, &pairs);
+  if (tile_cols) *tile_cols = 256 >> l.shape;
+  for (int mode = 0; mode < 3; ++mode) {
+    if (l.tiles[mode] * batch > 0x7fffffffLL) return (int)cudaErrorInvalidConfiguration;
+    if (tiles) tiles[mode] = (int)(l.tiles[mode] * batch);
+    if (whole) whole[mode] = (int)l.whole[mode];
+    if (split) split[mode] = l.split[mode];
+  }
+  return 0;
+}
+
 extern "C" int ns_orthogonalize(int batch, int rows, int cols, const void *G, int g_type, int ldg,
                                 long long g_stride, int steps, const float *coefficients,
                                 float eps, float alpha, float beta, void *out, int out_type,

@@ -19,7 +19,8 @@ import torch
 
 from . import F8_EXPORTED, SgemmError, _on_stream, _stream, lib
 
-__all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_status", "F8_EXPORTED"]
+__all__ = ["f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_plan", "f8_gemm_status",
+           "F8_EXPORTED"]
 
 _FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -174,6 +175,17 @@ def f8_matmul(a, a_scale, b, b_scale, *, transa=False, transb=False, alpha=1.0, 
     if rc != 0:
         raise SgemmError(rc, "f8_gemm")
     return out
+
+
+def f8_gemm_plan(M, N, K, *, transa=False, transb=False, a_rows=1, b_cols=128, num_sms=0) -> dict:
+    """How f8_matmul runs a product: {"exchanged", "tile_cols", "split"} (see the header); a_rows and
+    b_cols are the rows of op(a) and the columns of op(b) that share a scale."""
+    v = [ctypes.c_int(0) for _ in range(3)]
+    rc = lib.f8_gemm_plan(int(transa), int(transb), M, N, K, a_rows, b_cols, num_sms,
+                          *[ctypes.byref(x) for x in v])
+    if rc != 0:
+        raise SgemmError(rc, "f8_gemm_plan")
+    return {"exchanged": bool(v[0].value), "tile_cols": v[1].value, "split": v[2].value}
 
 
 def f8_gemm_status() -> tuple[int, int]:

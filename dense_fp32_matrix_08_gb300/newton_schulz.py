@@ -7,8 +7,8 @@ import torch
 
 from . import NS_EXPORTED, SgemmError, _on_stream, _stream, lib
 
-__all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_status",
-           "NS_EXPORTED"]
+__all__ = ["orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_plan",
+           "ns_orthogonalize_status", "NS_EXPORTED"]
 
 _MOST = 0x7fffffff  # sizes are 32-bit
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -77,6 +77,17 @@ def ns_orthogonalize_workspace_size(batch, rows, cols) -> tuple[int, int]:
     n = ctypes.c_size_t(0)
     rc = lib.ns_orthogonalize_workspace_size(batch, rows, cols, ctypes.byref(n))
     return rc, n.value
+
+
+def ns_orthogonalize_plan(batch, rows, cols, num_sms=0) -> dict:
+    """How orthogonalize runs a problem: {"tile_cols", "tiles", "whole", "split"}, the last three for
+    each product of a step (see the header)."""
+    cols_of, three = ctypes.c_int(0), [(ctypes.c_int * 3)() for _ in range(3)]
+    rc = lib.ns_orthogonalize_plan(batch, rows, cols, num_sms, ctypes.byref(cols_of), *three)
+    if rc != 0:
+        raise SgemmError(rc, "ns_orthogonalize_plan")
+    return {"tile_cols": cols_of.value, "tiles": tuple(three[0]), "whole": tuple(three[1]),
+            "split": tuple(three[2])}
 
 
 def ns_orthogonalize_status() -> tuple[int, int]:

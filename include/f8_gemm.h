@@ -110,6 +110,15 @@ typedef struct {
 int f8_quantize_with(const f8_quantize_args *args);
 int f8_gemm_with(const f8_gemm_args *args);
 
+/* How f8_gemm runs a product on a GPU with num_sms SMs (0: the current device; without one a whole
+ * GB300). Any pointer may be NULL.
+ *   exchanged   1 if the columns of D run along the instruction's 128 rows (few rows in D)
+ *   tile_cols   16, 32, 64, 128, or 256 for tiles of 256 x 256 by pairs of blocks
+ *   split       blocks that share a tile's sum, each with its part of k
+ * Returns 0 or -i for the first illegal argument (M, N and K of 1 or more). */
+int f8_gemm_plan(int transa, int transb, int M, int N, int K, int a_rows, int b_cols, int num_sms,
+                 int *exchanged, int *tile_cols, int *split);
+
 /* Reads and clears the device status word of f8_gemm (synchronising): 0 = fine, 1 - 4 = a wait
  * gave up after about a second and the call's result is not to be used. Returns 0 or a
  * cudaError_t. */

@@ -50,6 +50,16 @@ int ns_orthogonalize(int batch, int rows, int cols, const void *G, int g_type, i
  * one: on a whole GB300). Returns 0 or -1, -2, -3 for a negative batch, rows or cols. */
 int ns_orthogonalize_workspace_size(int batch, int rows, int cols, size_t *bytes);
 
+/* How ns_orthogonalize runs a problem on a GPU with num_sms SMs (0: the current device; without one a
+ * whole GB300). Any pointer may be NULL.
+ *   tile_cols   64 or 128 (tiles of 128 rows), or 256 for tiles of 256 x 256 by pairs of blocks
+ *   tiles, whole, split   for each of the three products of a step (X X^T, S S, R X): its tiles in the
+ *               whole batch, how many of them are computed in one piece, and in how many parts along k
+ *               the others are (1 if there are none)
+ * Returns 0, -i for the first illegal argument (sizes of 1 or more), or a cudaError_t. */
+int ns_orthogonalize_plan(int batch, int rows, int cols, int num_sms, int *tile_cols, int tiles[3],
+                          int whole[3], int split[3]);
+
 /* Reads and clears the device status word of ns_orthogonalize (synchronising): 0 = fine, 1 - 4 =
  * a wait gave up and the call's result is not to be used. A wait gives up after about a second where
  * it is for a block's own copies and instructions, and after eight to ten where it depends on the
