@@ -23,9 +23,9 @@
 // up to four, are read out after each step of 64 k and added up in FP32 registers, and a X is added in
 // the epilogue: the largest term passes no tensor core. Results of every type are made so and rounded
 // once. Off the exact result, five steps, plain 32-bit products in brackets: 4096 x 4096
-// 5.6e-7 (3.2e-6), 256 x 256 6.7e-7 (1.6e-6), 128 x 1000 1.3e-6 (1.7e-6), 32 x 16 1.1e-6 (0.9e-6),
-// 20 x 3000 2.0e-6 (1.3e-6). With a I in R it was 1.1, 1.4, 3.1, 1.4 and 3.2e-6 (with one accumulator
-// per step), and with chunks of 512 k ten times that.
+// 5.6e-7 (3.2e-6), 256 x 256 6.8e-7 (1.7e-6), 128 x 1000 7.4e-7 (1.4e-6), 32 x 16 7.7e-7 (8.4e-7),
+// 20 x 3000 1.1e-6 (1.1e-6), the last three with what Cfg::FINE adds. With a I in R and one accumulator
+// per step 4096 x 4096 and 256 x 256 had 1.1 and 1.4e-6, with chunks of 512 k ten times that.
 //
 // A call is two launches: norm_kernel (sums of squares) and ns_kernel, which stays resident and
 // runs all products with a grid-wide barrier between them. With a launch for each product the
@@ -57,10 +57,15 @@ constexpr int BOX = 64;                   // rows of a small TMA box
 constexpr int BOX_BYTES = BOX * 128;
 constexpr int MAX_STEPS = 64;
 
-template <int TN_, bool PAIR_>
+// FINE, for short sides of one tile: lo lo' is added, a step's accumulators are added up before they meet
+// the longer sum, and where the registers hold it that sum runs over 8 steps first (EIGHTS). What
+// 22-bit factors and a long FP32 sum lose is then no more than plain 32-bit products lose; without it 20 x
+// 3000 was off by 1.2 times as much on average, by 2.1 times at most. It costs 1% there, 4% in large
+// batches, and would cost 7% at 512 x 512, where the error is below half of plain products' without it.
+template <int TN_, bool PAIR_, bool FINE_>
 struct Cfg {
   static constexpr int TN = TN_;                        // tile columns
-  static constexpr bool PAIR = PAIR_;
+  static constexpr bool PAIR = PAIR_, FINE = FINE_, EIGHTS = FINE && TN == 64;
   static constexpr int BS = PAIR ? 256 : 128;           // tile rows; sizes are padded to it
   static constexpr int QN = PAIR ? TN / 2 : TN;         // columns of Q that a CTA holds
   static constexpr int P_TILE = 128 * 128, Q_TILE = QN * 128;  // bytes of hi or lo
@@ -706,7 +711,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               };
 #pragma unroll
               for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                mma(acc, pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, kk != 0);
+                if (C::FINE) mma(acc, pl0 + at + kk * adv_p, ql0 + at + kk * adv_q, kk != 0);
+                mma(acc, pl0 + at + kk * adv_p, qh0 + at + kk * adv_q, C::FINE || kk != 0);
                 mma(acc, ph0 + at + kk * adv_p, ql0 + at + kk * adv_q, 1u);
               }
 #pragma unroll
@@ -750,9 +756,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int by = pass ? (int)gridDim.x * C::EPI_WARPS : stride;
 #pragma unroll 1
         for (int i = pass ? (int)blockIdx.x * C::EPI_WARPS + warp - 4 : first; i < end; i += by) {
-          float acc[C::COLS];
+          float acc[C::COLS], eights[C::EIGHTS ? C::COLS : 1];
 #pragma unroll
           for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+          if constexpr (C::EIGHTS) {
+#pragma unroll
+            for (int j = 0; j < C::COLS; ++j) eights[j] = 0.0f;
+          }
           Unit u;
           int row0, col0;
           if (pass == 0) {
@@ -772,16 +782,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               if (mode != GRAM && kt == u.k0)
                 ok = grid_wait(p.counter, passed, false);
               fence_after();
-#pragma unroll 1
-              for (int n = 0; n < C::ACCS; ++n) {
-                const uint32_t src = src0 + (buf.slot * C::ACCS + n) * C::TN;
+              if constexpr (C::FINE) {
+                const uint32_t src = src0 + buf.slot * (C::ACCS * C::TN);
 #pragma unroll
                 for (int j0 = 0; j0 < C::COLS; j0 += 16) {
-                  uint32_t v[16];
-                  tmem_ld(src + (uint32_t)j0, v);
-                  tmem_wait_ld(v);
+                  uint32_t v[C::ACCS][16];
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+                  for (int n = 0; n < C::ACCS; ++n) tmem_ld(src + (uint32_t)(n * C::TN + j0), v[n]);
+#pragma unroll
+                  for (int n = 0; n < C::ACCS; ++n) tmem_wait_ld(v[n]);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    float s = __uint_as_float(v[0][j]);
+#pragma unroll
+                    for (int n = 1; n < C::ACCS; ++n) s += __uint_as_float(v[n][j]);
+                    if constexpr (C::EIGHTS)
+                      eights[j0 + j] += s;
+                    else
+                      acc[j0 + j] += s;
+                  }
+                }
+                if constexpr (C::EIGHTS) {
+                  if (((kt - u.k0) & 7) == 7 || kt == u.k1 - 1) {
+#pragma unroll
+                    for (int j = 0; j < C::COLS; ++j) {
+                      acc[j] += eights[j];
+                      eights[j] = 0.0f;
+                    }
+                  }
+                }
+              } else {
+#pragma unroll 1
+                for (int n = 0; n < C::ACCS; ++n) {
+                  const uint32_t src = src0 + (buf.slot * C::ACCS + n) * C::TN;
+#pragma unroll
+                  for (int j0 = 0; j0 < C::COLS; j0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld(src + (uint32_t)j0, v);
+                    tmem_wait_ld(v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
+                  }
                 }
               }
               fence_before();
@@ -863,9 +904,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 // ------------------------------------------------------------------------------------
 // Host side
 
-using Pair = Cfg<256, true>;
-using Wide = Cfg<128, false>;
-using Narrow = Cfg<64, false>;
+using Pair = Cfg<256, true, false>;
+using Wide = Cfg<128, false, false>;
+using Narrow = Cfg<64, false, false>;
+using FineWide = Cfg<128, false, true>;
+using FineNarrow = Cfg<64, false, true>;
 
 // How a problem runs: tile shape and parts of the sums, with the sizes that follow.
 struct Plan {
@@ -1009,6 +1052,8 @@ static cudaError_t kernel_setup(const int **pairs) {
     d.err = set(ns_kernel<Pair>, Pair::SMEM_BYTES);
     if (d.err == cudaSuccess) d.err = set(ns_kernel<Wide>, Wide::SMEM_BYTES);
     if (d.err == cudaSuccess) d.err = set(ns_kernel<Narrow>, Narrow::SMEM_BYTES);
+    if (d.err == cudaSuccess) d.err = set(ns_kernel<FineWide>, FineWide::SMEM_BYTES);
+    if (d.err == cudaSuccess) d.err = set(ns_kernel<FineNarrow>, FineNarrow::SMEM_BYTES);
     if (d.err == cudaSuccess)
       d.pairs = cluster_ctas_of(ns_kernel<Pair>, Pair::THREADS, Pair::SMEM_BYTES, 2) / 2;
   });
@@ -1090,9 +1135,12 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
         !encode_map_2d_narrow(&m.small[i], at[i], 2, rows, ld, ld, BOX))
       return cudaErrorInvalidValue;
   }
+  const bool fine = l.mp == 128;
   if (l.shape == 0) return launch<Pair>(m, p, (int)l.ctas, stream);
-  if (l.shape == 1) return launch<Wide>(m, p, (int)l.ctas, stream);
-  return launch<Narrow>(m, p, (int)l.ctas, stream);
+  if (l.shape == 1)
+    return fine ? launch<FineWide>(m, p, (int)l.ctas, stream) : launch<Wide>(m, p, (int)l.ctas, stream);
+  return fine ? launch<FineNarrow>(m, p, (int)l.ctas, stream)
+              : launch<Narrow>(m, p, (int)l.ctas, stream);
 }
 
 }  // namespace ns
