@@ -42,6 +42,8 @@
 namespace sgemm {
 namespace tc {
 
+using namespace tcx;
+
 constexpr int BM = 128, BN = 128, BK = 32, STAGES = 3;
 constexpr int EPI_WARPS = 4, THREADS = 32 * (2 + EPI_WARPS);  // producer, MMA, epilogue
 constexpr int A_TILE = BM * BK * 4;          // one 128 x 32 FP32 operand tile of A
@@ -76,27 +78,7 @@ struct Params {
 __device__ int g_tc_status;
 
 // ------------------------------------------------------------------------------------
-// PTX wrappers
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(slot),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
+// PTX wrappers (tc_common.cuh has those that other tensor-core kernels share)
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, 128 x BN x 8, TF32 inputs, FP32 accumulation.
 __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
@@ -109,46 +91,6 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t adesc, uint64
       "}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
       : "memory");
-}
-
-// Arrive on `bar` once every tcgen05.mma this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
-      : "memory");
-}
-
-// 32 consecutive FP32 accumulator columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-      "[%32];\n"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-        "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
-        "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-}
-
-// Shared-memory matrix descriptor of a K-major operand tile laid out by TMA with the
-// 128-byte swizzle: rows of 128 bytes (32 FP32), 8-row groups 1024 bytes apart. Fields:
-// start address >> 4 (bits 0-13), leading byte offset >> 4 (bits 16-29, not used by
-// swizzled K-major layouts, set to 1), stride byte offset >> 4 (bits 32-45: 1024 B),
-// descriptor version 1 (bits 46-47), swizzle mode 2 = 128 B (bits 61-63). Advancing K by 8
-// TF32 within the 128-byte swizzle atom adds 32 bytes to the start address.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr) {
-  uint64_t d = (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
 }
 
 __device__ __forceinline__ float tf32_rna(float x) {
@@ -296,9 +238,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  tc_fence_before();
+  fence_before();
   __syncthreads();
-  tc_fence_after();
+  fence_after();
   const uint32_t tmem = *tmem_slot_ptr;
 
   if (warp == 0 && lane == 0) {
@@ -344,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         atomicCAS(&g_tc_status, 0, 2);
         break;
       }
-      tc_fence_after();
+      fence_after();
       const uint32_t acc = tmem + (uint32_t)b * ACC_COLS;
       for (int kt = 0; kt < p.KT; ++kt, ++g) {
         const int s = (int)(g % STAGES);
@@ -353,14 +295,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        tc_fence_after();
+        fence_after();
         const uint32_t st = base + s * STAGE_BYTES;
 #pragma unroll
         for (int kk = 0; kk < BK / 8; ++kk) {
-          const uint64_t ah = sw128_desc(st + kk * 32);
-          const uint64_t al = sw128_desc(st + A_TILE + kk * 32);
-          const uint64_t bh = sw128_desc(st + 2 * A_TILE + kk * 32);
-          const uint64_t bl = sw128_desc(st + 2 * A_TILE + B_TILE + kk * 32);
+          const uint64_t ah = sw128_desc(st + kk * 32, 16);
+          const uint64_t al = sw128_desc(st + A_TILE + kk * 32, 16);
+          const uint64_t bh = sw128_desc(st + 2 * A_TILE + kk * 32, 16);
+          const uint64_t bl = sw128_desc(st + 2 * A_TILE + B_TILE + kk * 32, 16);
           // small correction terms first, then the main product
           mma_tf32(acc, al, bh, (kt | kk) != 0 ? 1u : 0u);
           mma_tf32(acc, ah, bl, 1u);
@@ -383,14 +325,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) atomicCAS(&g_tc_status, 0, 3);
         break;
       }
-      tc_fence_after();
+      fence_after();
       int tm, tn;
       tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
       const int row0 = tm * BM + q * 32;
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t v[32];
-        tmem_ld32(tmem + (uint32_t)b * ACC_COLS + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tmem_ld(tmem + (uint32_t)b * ACC_COLS + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tmem_wait_ld(v);
 #pragma unroll
         for (int j = 0; j < 32; ++j) buf[lane * EPI_PITCH + j] = __uint_as_float(v[j]);
         __syncwarp();
@@ -409,13 +352,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       }
-      tc_fence_before();
+      fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + 8 * b);  // accumulator b may be reused
     }
   }
   __syncwarp();
-  tc_fence_before();
+  fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
