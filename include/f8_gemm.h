@@ -56,7 +56,9 @@ int f8_quantize(int rows, int cols, const void *x, int x_type, int ldx, int bloc
  *                    and from one block of k to the next; b_scale_mn, b_scale_k alike for the
  *                    columns of op(B)
  * A and B are 16-byte aligned with leading dimensions that are multiples of 16 (TMA reads them;
- * the padding is not read). Scales may be any numbers whose products sA * sB do not overflow.
+ * the padding is not read). Scales may be any numbers up to 2^88 whose products sA * sB are from 2^-126
+ * to 2^88, blocks of zeros with any finite scale: beyond that, scaled sums leave the range of FP32 or
+ * lose bits although D may hold them.
  *
  * Products of a block are summed by the tensor core in FP32, the blocks in FP32 registers, in an
  * order fixed by the shape: the same call gives the same bits. beta == 0 does not read D;

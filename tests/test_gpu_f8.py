@@ -522,3 +522,25 @@ def test_quantize_most_rows():
     assert (q[guard:-guard - 4].view(torch.int8) == 0x7e).all()  # 448
     assert (q[:guard] == 0x5a).all() and (q[-guard:] == 0x5a).all()
     assert (s[:guard] == 7.0).all() and (s[-guard:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [E4, E5])
+@pytest.mark.parametrize("ga,gb", [(1, 1), (1, 128), (128, 128)])
+@pytest.mark.parametrize("powers", [(88, -100), (-100, 88), (-60, -66), (40, 48), (-126, 88)])
+@pytest.mark.parametrize("shape", [(20, 300, 333), (330, 300, 260)], ids=lambda s: "x".join(map(str, s)))
+def test_product_range_of_scales(shape, powers, ga, gb, dtype):
+    """Scales at the ends of what the header allows, and a block of zeros under the least scale."""
+    M, N, K = shape
+    qa, sa = operand(M, K, (ga, 128), dtype, 1)
+    qb, sb = operand(N, K, (gb, 128), dtype, 2)
+    u = torch.rand(sa.shape, generator=torch.Generator().manual_seed(3))
+    sa, sb = torch.ldexp(1 - u / 2 if powers[0] > 0 else 1 + u, torch.tensor(powers[0])), \
+        torch.full_like(sb, 2.0 ** powers[1])
+    qa[:ga, :128], sa[0, 0] = torch.zeros(min(ga, M), 128).to(dtype), 2.0 ** -126
+    a, b = plain.values(qa, sa), plain.values(qb, sb)
+    # (alpha keeps D in FP32's range)
+    alpha = 2.0 ** -(sum(powers) // 2)
+    d = sg.f8_matmul(on_gpu(qa), sa.cuda(), on_gpu(qb), sb.cuda(), transb=True, alpha=alpha,
+                     out_dtype=torch.float32).cpu().double()
+    R, S = alpha * (a @ b.t()), abs(alpha) * (a.abs() @ b.abs().t())
+    assert ((d - R).abs() <= (K + 8) * 2.0 ** -23 * S + 2.0 ** -23 * R.abs()).all()
