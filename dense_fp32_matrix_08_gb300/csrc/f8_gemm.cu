@@ -124,13 +124,14 @@ __device__ __forceinline__ void store1(const Params &p, int row, int col, float 
 // (tile rows) 32 (w % 4) .. + 31, one row per thread.
 // QVEC: Q has a scale for each column (else one for each 128, the same for a whole group).
 //
-// What bounds it. 8192 x 14336 x 4096, BF16 result: 400 us, 2.4 PFLOP/s, the tensor core 58% busy. For
+// What bounds it. 8192 x 14336 x 4096, BF16 result: 400 us, 2.4 PFLOP/s, the tensor core 60% busy. For
 // each block of k an epilogue warp executes about 145 instructions on its 64 accumulators per lane
-// (32 of them the packed multiply-adds), which fills 68% of the issue slots; the rest is the time an
+// (32 of them the packed multiply-adds), which fills 65% of the issue slots; the rest is the time an
 // accumulator takes from the tensor core to the epilogue and back, and TMEM holds only two per part.
-// 4096 x 4096 x 8192 with a scale for each column of Q: 200 us, 1.4 PFLOP/s: twice the multiplies and
-// the reads of the scales. (The accumulators as 16 x 256-bit fragments, which need a quarter of the
-// scales per lane, took 218 us for 210 then.) 4099 x 3001 x 777: 26 us, 18 of them with rows of 3008:
+// 4096 x 4096 x 8192 with a scale for each column of Q: 203 us, 1.4 PFLOP/s, the tensor core 33% and the
+// issue slots 44% busy: 3.4 rounds of tiles take the time of four, and in them twice the multiplies and
+// the reads of the scales make that way longer. (The accumulators as 16 x 256-bit fragments, which need a
+// quarter of the scales per lane, took 218 us for 210 then.) 4099 x 3001 x 777: 27 us, 19 with rows of 3008:
 // unaligned 16-bit rows are stored element by element. (As 4-byte pairs: 33.5 us for 28.6 then, more
 // partial sectors per instruction.) 1 x 4096 x 4096 with the weight in memory: 7.0 us, 2.4 TB/s (5.5
 // from L2), most of it the start of the CTAs, the first bytes' way and the clusters' exchange.

@@ -245,8 +245,8 @@ __device__ __forceinline__ Scale lanes_scale(uint32_t m, int format, int pow2) {
 
 // 1 x 128 blocks: unit u = row * blocks + block; a warp takes 4 neighbouring units at a time, so that
 // it reads 1 KB (of 16 bits) at once and a block's maximum stays within 8 lanes. No shared memory, 31
-// registers: 72% of the warps resident. 8192 x 4096 BF16: 17.0 us, 5.9 TB/s
-// (88% of a copy's rate); the issue slots are then 73% busy. 1 x 4096: 1.4 us.
+// registers: 72% of the warps resident. 8192 x 4096 BF16: 16.8 us, 6.1 TB/s
+// (90% of a copy's rate). 1 x 4096: 1.3 us.
 template <class T, int FORMAT>
 __global__ void __launch_bounds__(256, T::CTAS) rows_kernel(const QuantParams p) {
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
@@ -292,7 +292,7 @@ enum { COLS = 0, SQUARE = 1, PAIR = 2 };
 // per SM overlap instead, as many as the registers allow (34 to 47% of the warps). 14336 x 4096
 // FP32 in squares: 49 us, 6.0 TB/s, 89% of a copy's rate. 8192 x 4096 BF16 by rows and by columns at
 // once: 34 us, 4.0 TB/s, with twice the arithmetic per byte read; two calls, by rows and by columns,
-// take 17.0 + 25.8 us. (CTAs of 512 threads with half as many elements each: 44 us for 35, 23 for 16 in
+// take 16.8 + 25.8 us. (CTAs of 512 threads with half as many elements each: 44 us for 35, 23 for 16 in
 // squares; a column's maximum then takes as many shuffles for half as many rows.)
 template <class T>
 constexpr int kRowGroups = T::W == 16 ? 64 : 32;

@@ -537,8 +537,9 @@ __global__ void __launch_bounds__(256) copy_kernel(const Params p) {
 // 8 x 1024 x 1024 BF16, 128 x 128 tiles: 673 us, 270 of them MMAs; a product is 2 to 4 rounds of
 // tiles, and the barrier, the first loads and the last stores of a product overlap nothing.
 // 4097 x 777 BF16: 364 us, the same with products of one round. (16-bit results summed 256 k in one
-// accumulator, with a I in R, took 545 and 318 us, for several times the error before the rounding.) 256 x 256 FP32: 115 us, 7 to 8 us for
-// each of 15 dependent products: barrier 2, first loads 1.5, k steps 1.5, stores 1 to 2.
+// accumulator, with a I in R, took 545 and 318 us, for several times the error before the rounding.)
+// 256 x 256 FP32: 119 us, 7 to 8 us for each of 15 dependent products: barrier 2, first loads 1.5, k steps
+// 1.5, stores 1 to 2.
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -1000,8 +1001,9 @@ static Plan choose(int batch, int rows, int cols, int sms, const int *pairs) {
 }
 
 // Bounds of the spectral norms: of X_t in bx[0 .. steps], of R in br[t], each with a margin of 2% for
-// the roundings. With y = x^2 the polynomials are r(y) = b y + c y^2 and x (a + r(x^2)); on [0, bx[t]] their extremes lie at the ends or where the derivative vanishes. False
-// where a bound leaves the range of FP32 scales.
+// the roundings. With y = x^2 the polynomials are r(y) = b y + c y^2 and x (a + r(x^2)); on [0, bx[t]]
+// their extremes lie at the ends or where the derivative vanishes. False where a bound leaves the range
+// of FP32 scales.
 static bool bounds(const float *co, int steps, double *bx, double *br) {
   const double a = co[0], b = co[1], c = co[2];
   const double disc = 9.0 * b * b - 20.0 * a * c, w = std::sqrt(std::max(disc, 0.0));
