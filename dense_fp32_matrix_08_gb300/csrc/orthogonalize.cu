@@ -515,15 +515,17 @@ __device__ __forceinline__ void start(const Params &p, float *t, float *mul) {
 __global__ void __launch_bounds__(256) copy_kernel(const Params p) {
   __shared__ float mul[2];
   const long long total = (long long)p.in.rows * p.in.cols;
-  const int mat = blockIdx.y;
-  if (threadIdx.x < 32) start_factors(p, mat, mul);
-  __syncthreads();
   const int size = p.user_type == NS_F32 ? 4 : 2;
-  void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const long long r = i / p.in.cols, c = i % p.in.cols;
-    const float x = load(p.in.g, p.in.type, mat * p.in.stride + r * p.in.ld + c) * mul[0] * mul[1];
-    finish_out(out, p.user_type, r * p.ldu + c, p.alpha * x, p.beta);
+  for (int mat = blockIdx.y; mat < p.batch; mat += gridDim.y) {
+    __syncthreads();  // (mul has been read)
+    if (threadIdx.x < 32) start_factors(p, mat, mul);
+    __syncthreads();
+    void *out = reinterpret_cast<char *>(p.user) + mat * p.user_stride * size;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+      const long long r = i / p.in.cols, c = i % p.in.cols;
+      const float x = load(p.in.g, p.in.type, mat * p.in.stride + r * p.in.ld + c) * mul[0] * mul[1];
+      finish_out(out, p.user_type, r * p.ldu + c, p.alpha * x, p.beta);
+    }
   }
 }
 
@@ -1114,8 +1116,8 @@ static cudaError_t run(const Plan &l, const float *co, const double *bx, const d
   if (e != cudaSuccess) return e;
   if (p.steps == 0) {
     const long long blocks = std::min<long long>(1024, ceil_div((long long)p.m * p.n, 1024));
-    if (p.batch > 65535) return cudaErrorInvalidConfiguration;
-    copy_kernel<<<dim3((unsigned)blocks, (unsigned)p.batch), 256, 0, stream>>>(p);
+    const unsigned mats = (unsigned)std::min(p.batch, 65535);  // (the most of a grid's y)
+    copy_kernel<<<dim3((unsigned)blocks, mats), 256, 0, stream>>>(p);
     return cudaGetLastError();
   }
   float sx = p.x_scale;

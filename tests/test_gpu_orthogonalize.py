@@ -289,3 +289,14 @@ def test_narrow_matrices_are_as_exact_as_plain_32_bit_products(shape):
             for got, errors in ((sg.orthogonalize(x), ours), (steps_in(x), products)):
                 errors += ((got.double() - w).square().sum(dim=(1, 2)).sqrt() / norm).tolist()
     assert sum(ours) <= 1.05 * sum(products), (sum(ours) / len(ours), sum(products) / len(products))
+
+
+@pytest.mark.parametrize("steps", [0, 1])
+def test_more_matrices_than_a_grid_has_rows(steps):
+    """65537 and more matrices; 6 x 2 and 2 x 6 padded to 128 x 128."""
+    for shape in ((65538, 2, 6), (65538, 6, 2)):
+        g = torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+        got = sg.orthogonalize(g, steps=steps).double()
+        want = plain(g, steps)
+        err = (got - want).square().sum(dim=(1, 2)).sqrt()
+        assert (err <= tolerance(steps, torch.float32) * want.square().sum(dim=(1, 2)).sqrt()).all()
