@@ -121,9 +121,9 @@ int f8_gemm_with(const f8_gemm_args *args);
 int f8_gemm_plan(int transa, int transb, int M, int N, int K, int a_rows, int b_cols, int num_sms,
                  int *exchanged, int *tile_cols, int *split);
 
-/* Reads and clears the device status word of f8_gemm (synchronising): 0 = fine, 1 - 4 = a wait
- * gave up after about a second and the call's result is not to be used. Returns 0 or a
- * cudaError_t. */
+/* Reads and clears the device status word of f8_gemm (synchronising copy on the legacy stream: wait
+ * first for calls on streams that do not wait for it): 0 = fine, 1 - 4 = a wait gave up after about a
+ * second and the call's result is not to be used. Returns 0 or a cudaError_t. */
 int f8_gemm_status(int *status);
 
 #ifdef __cplusplus

@@ -60,8 +60,9 @@ int ns_orthogonalize_workspace_size(int batch, int rows, int cols, size_t *bytes
 int ns_orthogonalize_plan(int batch, int rows, int cols, int num_sms, int *tile_cols, int tiles[3],
                           int whole[3], int split[3]);
 
-/* Reads and clears the device status word of ns_orthogonalize (synchronising): 0 = fine, 1 - 4 =
- * a wait gave up and the call's result is not to be used. A wait gives up after about a second where
+/* Reads and clears the device status word of ns_orthogonalize (synchronising copy on the legacy
+ * stream: wait first for calls on streams that do not wait for it): 0 = fine, 1 - 4 = a wait gave up
+ * and the call's result is not to be used. A wait gives up after about a second where
  * it is for a block's own copies and instructions, and after eight to ten where it depends on the
  * other blocks. Returns 0 or a cudaError_t. */
 int ns_orthogonalize_status(int *status);

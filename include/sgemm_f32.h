@@ -334,7 +334,8 @@ int sgemm_f32_release_workspace(size_t *released_bytes);
  * on the legacy stream): 0 = fine; 1 or 2 = a bounded mbarrier wait gave up (a consumer
  * waiting for data, or the producer waiting for a free stage), in which case the kernel
  * stopped computing and the result of that call is not valid. Every mbarrier wait in the
- * library's kernels gives up after about one second of the GPU's global timer. */
+ * library's kernels gives up after about one second of the GPU's global timer, except those of
+ * ns_orthogonalize that depend on other blocks (orthogonalize.h). */
 int sgemm_f32_status(int *status);
 
 /* Failure-path self-test of that bounded wait: one warp waits, with the kernels' own wait,
