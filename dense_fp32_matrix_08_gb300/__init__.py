@@ -42,11 +42,16 @@ EXPORTED = ("sgemm_f32", "sgemm_f32_ws", "sgemm_f32_forced", "sgemm_f32_workspac
             "sgemm_f32_host", "sgemm_f32_wait_selftest", "sgemm_f32_release_workspace",
             "sgemm_f32_fma_probe", "sgemm_f32_cluster_capacity",
             "sgemm_f32_workspace_size_min")
-# The same of include/f8_gemm.h and of include/orthogonalize.h.
+# The same of include/f8_gemm.h, orthogonalize.h, layer_norm.h, grad_clip.h and i8_linear.h.
 F8_EXPORTED = ("f8_quantize", "f8_gemm", "f8_quantize_with", "f8_gemm_with", "f8_gemm_plan",
                "f8_gemm_status")
 NS_EXPORTED = ("ns_orthogonalize", "ns_orthogonalize_workspace_size", "ns_orthogonalize_plan",
                "ns_orthogonalize_status")
+LN_EXPORTED = ("layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size",
+               "layer_norm_with", "layer_norm_backward_with")
+GC_EXPORTED = ("clip_grad_norm",)
+I8_EXPORTED = ("i8_quantize", "i8_linear", "i8_quantize_with", "i8_linear_with", "i8_linear_plan",
+               "i8_linear_status")
 
 
 class SgemmError(RuntimeError):
@@ -109,7 +114,17 @@ def _load() -> ctypes.CDLL:
     L.ns_orthogonalize_workspace_size.argtypes = [i, i, i, psz]
     L.ns_orthogonalize_plan.argtypes = [i] * 4 + [pi] * 4
     L.ns_orthogonalize_status.argtypes = [pi]
-    for name in EXPORTED + F8_EXPORTED + NS_EXPORTED:
+    L.layer_norm.argtypes = [i, i, vp, i, i, vp, vp, i, f, vp, i, vp, vp, vp]
+    L.layer_norm_backward.argtypes = [i, i, vp, i, vp, i, i, vp, vp, vp, i, vp, i, vp, vp, f, vp]
+    L.layer_norm_backward_workspace_size.argtypes = [i, i, psz]
+    L.clip_grad_norm.argtypes = [i, vp, vp, vp, f, f, vp, vp, vp, vp]
+    L.i8_quantize.argtypes = [i, i, vp, i, i, vp, i, vp, vp]
+    L.i8_linear.argtypes = [i, i, i, vp, i, vp, vp, i, vp, vp, f, vp, i, i, vp]
+    L.i8_linear_plan.argtypes = [i] * 4 + [pi] * 2
+    L.i8_linear_status.argtypes = [pi]
+    for name in ("layer_norm_with", "layer_norm_backward_with", "i8_quantize_with", "i8_linear_with"):
+        getattr(L, name).argtypes = [ctypes.c_char_p]
+    for name in EXPORTED + F8_EXPORTED + NS_EXPORTED + LN_EXPORTED + GC_EXPORTED + I8_EXPORTED:
         if name != "sgemm_f32_version":
             getattr(L, name).restype = ctypes.c_int
     return L
@@ -402,14 +417,18 @@ def sgemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     return C
 
 
-# The tensor-core operators of a linear layer's training step and of its serving: 8-bit
-# block-scaled products and the orthogonalised update. They need torch, which the bindings above do
-# not, so their modules are imported when one of their names is first used.
+# The operators of a linear layer's training step and of its serving: 8-bit block-scaled products and
+# the orthogonalised update, layer norm, clipping of gradients, and the layer on 8-bit integers. They
+# need torch, which the bindings above do not, so their modules are imported when one of their names is
+# first used.
 _LATE = {"f8": ("f8_quantize", "f8_quantize_pair", "f8_matmul", "f8_gemm_plan", "f8_gemm_status"),
          "newton_schulz": ("orthogonalize", "ns_orthogonalize_workspace_size",
-                           "ns_orthogonalize_plan", "ns_orthogonalize_status")}
+                           "ns_orthogonalize_plan", "ns_orthogonalize_status"),
+         "norm": ("layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size"),
+         "clip": ("clip_grad_norm",),
+         "i8": ("i8_quantize", "i8_linear", "i8_linear_plan", "i8_linear_status")}
 
-__all__ += ["F8_EXPORTED", "NS_EXPORTED"]
+__all__ += ["F8_EXPORTED", "NS_EXPORTED", "LN_EXPORTED", "GC_EXPORTED", "I8_EXPORTED"]
 if importlib.util.find_spec("torch") is not None:
     __all__ += [name for names in _LATE.values() for name in names]
 

@@ -1,0 +1,324 @@
+// The norm of many arrays together, and the arrays times min(1, max_norm / (norm + eps)).
+//
+// Bound by HBM: every element is read for the norm, and read again and written for the result. Two
+// launches however many arrays there are (for each 960 of them): square_kernel leaves one sum of
+// squares per CTA; every CTA of scale_kernel adds all of them up, in the same order, and scales its
+// part. The arrays are cut into pieces of kPiece elements that the CTAs take in turn. scale_kernel
+// takes them backwards, so that the last ones read for the norm come from L2.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "../../include/grad_clip.h"
+#include "sgemm_ffma.cuh"
+#include "sgemm_internal.h"
+#include "sgemm_plan.h"
+#include "tc_common.cuh"
+
+namespace sgemm {
+namespace gc {
+
+constexpr int kPiece = 16384;  // elements: 64 per thread
+constexpr int kThreads = 256;
+
+struct Array {
+  const void *in;
+  void *out;
+  long long n;
+  int first;                 // its first piece in this launch
+  uint8_t type, out_type;
+};
+
+template <int MOST>
+struct Params {
+  Array a[MOST];
+  int count, pieces;         // arrays and pieces of this launch
+  double *sums;              // of each CTA of all launches of square_kernel
+  int slot, slots;           // this launch's first one; all of them
+  float max_norm, eps;
+  float *norm;
+};
+
+// The array that piece `at` belongs to.
+template <int MOST>
+__device__ __forceinline__ const Array &array_of(const Params<MOST> &p, int at) {
+  int lo = 0, hi = p.count;  // a[lo].first <= at < a[hi].first
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (p.a[mid].first <= at) lo = mid; else hi = mid;
+  }
+  return p.a[lo];
+}
+
+// 8 neighbouring elements, or those of them that exist (the others are zero), as FP32.
+__device__ __forceinline__ void load8(const Array &a, long long i, bool vec, float (&v)[8]) {
+  const long long left = a.n - i;
+  if (vec && left >= 8) {
+    if (a.type == GC_F32) {
+      const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(a.in) + i);
+      const float4 x = s[0], y = s[1];
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.in) + i);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (a.type == GC_BF16) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+          v[2 * j] = f.x;
+          v[2 * j + 1] = f.y;
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? tcx::load_out(a.in, a.type, i + j) : 0.0f;
+}
+
+__device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Sum of squares of a thread's elements of a piece, in a scale in which FP32 holds it.
+__device__ __forceinline__ double thread_squares(const Array &a, long long at, bool vec) {
+  const long long i0 = at + threadIdx.x * 8;
+  float s = 0.0f;
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < kPiece; k += kThreads * 8) {
+    float v[8];
+    load8(a, i0 + k, vec, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s = fmaf(v[j], v[j], s);
+      any |= __float_as_uint(v[j]);
+    }
+  }
+  any &= 0x7fffffffu;
+  // 64 squares: a sum above 2^-90 has lost nothing that counts to numbers under 2^-126, and one under
+  // 2^120 is exact enough as it is. Else the elements once more, times 2^100 or 2^-70.
+  if (any == 0 || (s > 0x1p-90f && s < 0x1p120f)) return s;
+  const float up = s < 1.0f ? 0x1p100f : 0x1p-70f;
+  s = 0.0f;
+  for (int k = 0; k < kPiece; k += kThreads * 8) {
+    float v[8];
+    load8(a, i0 + k, vec, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[j] * up, v[j] * up, s);
+  }
+  return (double)s * (up > 1.0f ? 0x1p-200 : 0x1p140);
+}
+
+// Sum over the CTA, in each of its threads.
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double part[kThreads / 32];
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) v += part[w];
+  return v;
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant__ Params<MOST> p) {
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  double sum = 0.0;
+  for (int at = blockIdx.x; at < p.pieces; at += gridDim.x) {
+    const Array &a = array_of(p, at);
+    sum += thread_squares(a, (long long)(at - a.first) * kPiece, aligned16(a.in));
+  }
+  sum = cta_sum(sum);
+  if (threadIdx.x == 0) p.sums[p.slot + blockIdx.x] = sum;
+  griddep_launch_dependents();
+}
+
+// WRITE: also the scaled arrays; else the norm only (one CTA).
+template <int MOST, bool WRITE>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Params<MOST> p) {
+  griddep_wait();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < p.slots; i += kThreads) sum += p.sums[i];
+  const double norm = sqrt(cta_sum(sum));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.norm) *p.norm = (float)norm;
+  if constexpr (WRITE) {
+    const double ratio = (double)p.max_norm / (norm + (double)p.eps);
+    // (NaN stays; 0 / 0 is no reason for one)
+    const bool whole = ratio >= 1.0 || norm == 0.0;
+    // a factor near the end of FP32's range in two parts, of which neither loses bits
+    const bool tiny = ratio < 0x1p-100;
+    const float factor = whole ? 1.0f : (float)(tiny ? ratio * 0x1p64 : ratio);
+    const float shrink = !whole && tiny ? 0x1p-64f : 1.0f;
+    for (int at = p.pieces - 1 - blockIdx.x; at >= 0; at -= gridDim.x) {
+      const Array &a = array_of(p, at);
+      if (whole && a.in == a.out) continue;
+      const bool vec = aligned16(a.in), vec_out = aligned16(a.out);
+      const long long i0 = (long long)(at - a.first) * kPiece + threadIdx.x * 8;
+#pragma unroll 4
+      for (int k = 0; k < kPiece; k += kThreads * 8) {
+        const long long i = i0 + k;
+        if (i >= a.n) break;
+        float v[8];
+        load8(a, i, vec, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * shrink * factor;
+        if (vec_out && a.n - i >= 8) {
+          if (a.out_type == GC_F32) {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + i) =
+                make_uint4(tcx::pack_out(a.out_type, v[0], v[1]), tcx::pack_out(a.out_type, v[2], v[3]),
+                           tcx::pack_out(a.out_type, v[4], v[5]), tcx::pack_out(a.out_type, v[6], v[7]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < a.n - i) tcx::store_out(a.out, a.out_type, i + j, v[j]);
+        }
+      }
+    }
+  }
+  griddep_launch_dependents();
+}
+
+static int size_of(int type) { return type == GC_F32 ? 4 : 2; }
+
+// Whether a result overlaps a gradient that is not the same array, or another result.
+static bool overlapping(int count, const void *const *grads, const int *types, const long long *sizes,
+                        void *const *out, const int *out_types) {
+  struct Span {
+    uintptr_t from, to;
+    bool written;
+    int of;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * (size_t)count);
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(out[i]);
+    spans.push_back({o, o + (uintptr_t)sizes[i] * size_of(out_types[i]), true, i});
+    if (g != o || types[i] != out_types[i])
+      spans.push_back({g, g + (uintptr_t)sizes[i] * size_of(types[i]), false, i});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.from < b.from; });
+  uintptr_t read_to = 0, written_to = 0;  // ends of what began so far
+  for (const Span &s : spans) {
+    if (s.from < written_to || (s.written && s.from < read_to)) return true;
+    uintptr_t &end = s.written ? written_to : read_to;
+    end = std::max(end, s.to);
+  }
+  return false;
+}
+
+struct Call {
+  int count;
+  const void *const *grads;
+  const int *types;
+  const long long *sizes;
+  float max_norm, eps;
+  void *const *out;
+  const int *out_types;
+  float *norm;
+  cudaStream_t stream;
+};
+
+// Fills `p` with arrays from `i` on that are not empty; returns the next one.
+template <int MOST>
+static int fill(Params<MOST> &p, const Call &c, int i) {
+  p.count = p.pieces = 0;
+  for (; i < c.count && p.count < MOST; ++i) {
+    if (c.sizes[i] == 0) continue;
+    const long long pieces = ceil_div(c.sizes[i], kPiece);
+    if (p.pieces + pieces > 0x3fffffff) break;
+    p.a[p.count++] = {c.grads[i], c.out ? c.out[i] : nullptr, c.sizes[i], p.pieces, (uint8_t)c.types[i],
+                      (uint8_t)(c.out ? c.out_types[i] : 0)};
+    p.pieces += (int)pieces;
+  }
+  return i;
+}
+
+template <int MOST>
+static cudaError_t run(const Call &c, int launches, int sms) {
+  const int most = 8 * sms;  // CTAs of a launch
+  double *ws = nullptr;
+  cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
+                                          sizeof(double) * (size_t)most * launches, workspace_pool(), c.stream);
+  if (e != cudaSuccess) return e;
+  static thread_local Params<MOST> p;
+  p.sums = ws;
+  p.max_norm = c.max_norm;
+  p.eps = c.eps;
+  p.norm = c.norm;
+  p.slots = 0;
+  int i = 0;
+  do {
+    i = fill(p, c, i);
+    const int grid = std::min(p.pieces, most);
+    p.slot = p.slots;
+    p.slots += grid;
+    if (grid > 0) e = launch_1d(square_kernel<MOST>, grid, kThreads, 0, 1, c.stream, p);
+  } while (e == cudaSuccess && i < c.count);
+  if (c.out == nullptr) {
+    if (e == cudaSuccess) e = launch_1d(scale_kernel<MOST, false>, 1, kThreads, 0, 1, c.stream, p);
+  } else {
+    i = 0;
+    do {
+      i = fill(p, c, i);
+      if (e == cudaSuccess)
+        e = launch_1d(scale_kernel<MOST, true>, std::max(1, std::min(p.pieces, most)), kThreads, 0, 1,
+                      c.stream, p);
+    } while (e == cudaSuccess && i < c.count);
+  }
+  const cudaError_t ef = cudaFreeAsync(ws, c.stream);
+  return e == cudaSuccess ? ef : e;
+}
+
+}  // namespace gc
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int clip_grad_norm(int count, const void *const *grads, const int *types,
+                              const long long *sizes, float max_norm, float eps, void *const *out,
+                              const int *out_types, float *norm, cudaStream_t stream) {
+  const auto known = [](int t) { return t == GC_F32 || t == GC_BF16 || t == GC_F16; };
+  const auto misplaced = [](const void *q, int t) {
+    return reinterpret_cast<uintptr_t>(q) % gc::size_of(t) != 0;
+  };
+  if (count < 0) return -1;
+  if (count > 0 && grads == nullptr) return -2;
+  if (count > 0 && types == nullptr) return -3;
+  if (count > 0 && sizes == nullptr) return -4;
+  long long arrays = 0, pieces = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!known(types[i])) return -3;
+    if (sizes[i] < 0 || sizes[i] > (1LL << 42)) return -4;
+    if (sizes[i] > 0 && (grads[i] == nullptr || misplaced(grads[i], types[i]))) return -2;
+    arrays += sizes[i] > 0;
+    pieces += ceil_div(sizes[i], gc::kPiece);
+  }
+  if (!(max_norm >= 0.0f)) return -5;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return -6;
+  if (out != nullptr && count > 0) {
+    if (out_types == nullptr) return -8;
+    for (int i = 0; i < count; ++i) {
+      if (!known(out_types[i])) return -8;
+      if (sizes[i] > 0 && (out[i] == nullptr || misplaced(out[i], out_types[i]))) return -7;
+    }
+    if (gc::overlapping(count, grads, types, sizes, out, out_types)) return -7;
+  }
+  if (arrays == 0 && norm == nullptr) return 0;
+  int sms = 0;
+  const cudaError_t e = device_setup(&sms);
+  if (e != cudaSuccess) return (int)e;
+  const gc::Call c{count, grads, types, sizes, max_norm, eps, out, out_types, norm, stream};
+  // launches: full tables, and each time that the pieces of one would be too many
+  const auto launches = [&](int most) { return (int)(ceil_div(arrays, most) + pieces / 0x3fffffff * 2 + 1); };
+  return arrays <= 96 ? (int)gc::run<96>(c, launches(96), sms) : (int)gc::run<960>(c, launches(960), sms);
+}

@@ -1,0 +1,702 @@
+// D = x w^T on 8-bit integers with a scale for each row of x (token) and of w (channel):
+//
+//   D(i, j) = sx(i) sw(j) sum_k qx(i, k) qw(j, k) + bias(j) + beta D(i, j)
+//
+// The 8-bit integer rate of sm_103a's tensor cores is a small part of their FP16 rate, and FP16 holds
+// every int8 exactly. So the products run as FP16 ones (tcgen05, kind f16): products of two int8 are
+// at most 2^14, and a sum of 1024 of them at most 2^24, which FP32 accumulators hold without a
+// rounding. After each 1024 of k the epilogue warps take the accumulator from TMEM and add it to
+// 32-bit integers in registers. The result is the exact whole number, so that neither tiles nor splits
+// show in it.
+//
+// The weight stays int8 on its way from memory. The kernel sees the product as P = w (128 channels per
+// tile, on the instruction's 128-row side, however few tokens there are) times Q = x (TN tokens per
+// tile). A warpgroup of converters reads P's bytes from shared memory, where TMA has put them, and
+// writes them as FP16 numbers into TMEM, from where the instruction takes P: the numbers never pass
+// through shared memory, whose bandwidth (TMA's writes, the converters' and the tensor core's reads) is
+// what large tiles are short of. Q is FP16 in shared memory: converted by the same warps where it is
+// narrow, and before the kernel (unpack_kernel, into the workspace) where it is wide.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "../../include/i8_linear.h"
+#include "i8_internal.h"
+#include "sgemm_internal.h"
+#include "sgemm_plan.h"
+#include "tc_common.cuh"
+
+namespace sgemm {
+namespace i8 {
+
+constexpr int BP = 128;                  // channels per CTA and tile
+constexpr int BK = 128;                  // k per block = per pipeline stage
+constexpr int CHUNK = 8;                 // blocks of k that an accumulator holds: 1024 products
+constexpr int P_BYTES = BP * BK;
+constexpr int MAX_CLUSTER = 8;
+constexpr int LARGEST_K = 131071;        // 2^14 K < 2^31
+
+// PAIR: two CTAs share a tile of 256 channels and TN tokens (tcgen05 cta_group::2), each with its 128
+// channels and half of the tokens.
+template <int TN_, bool PAIR_ = false>
+struct Cfg {
+  static constexpr int TN = TN_;
+  static constexpr bool PAIR = PAIR_;
+  static constexpr bool CONVERT = TN <= 64;        // Q arrives as int8
+  static constexpr int QN = PAIR ? TN / 2 : TN;    // tokens that this CTA holds
+  static constexpr int GROUPS = TN >= 64 ? 2 : 1;  // epilogue groups of four warps
+  static constexpr int COLS = TN / GROUPS;         // tokens of a group
+  static constexpr int EPI_WARPS = 4 * GROUPS;
+  static constexpr int THREADS = 32 * (8 + EPI_WARPS);
+  static constexpr int Q_BYTES = QN * BK * (CONVERT ? 1 : 2);
+  static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr int STAGES = CONVERT ? (TN == 64 ? 6 : 9) : 4;
+  static constexpr int NA = 4;                     // blocks of P in TMEM (and of Q, where converted)
+  static constexpr int A_COLS = BK / 2;            // columns of one
+  static constexpr int H_BYTES = CONVERT ? QN * BK * 2 : 0;
+  // A pair's tile is computed in two parts of 128 tokens with one accumulator each: one is emptied
+  // while the tensor core works on the other's last block. Else there are two accumulators.
+  static constexpr int PARTS = PAIR ? 2 : 1;
+  static constexpr int PART = TN / PARTS;
+  static constexpr int NBUF = PAIR ? 1 : 2;
+  static constexpr int ACC_COLS = PART < 32 ? 32 : PART;
+  static constexpr int ACC_WARPS = PAIR ? 8 : EPI_WARPS;  // readers of an accumulator
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int BARS = 3 * STAGES + 2 * NA + 2 * PARTS * NBUF;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NA * H_BYTES + 8 * BARS + 16;
+  static_assert(PARTS * NBUF * ACC_COLS + NA * A_COLS <= TMEM_COLS, "TMEM columns");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && H_BYTES % 1024 == 0, "swizzled tiles");
+};
+
+struct Params {
+  int N, M, KB;        // channels, tokens, blocks of k
+  int tiles_p, tiles_q, group_p;
+  int split;           // CTAs of a cluster, each with its range of k blocks
+  uint32_t idesc;
+  const float *w_scale, *x_scale;
+  Result d;
+};
+
+// Device status word: 0 = fine; 1, 2, 3, 4 = a wait of the producer, the MMA issuer, the epilogue
+// or the converters gave up.
+__device__ int g_i8_status;
+
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// One channel's finished sums: factor and bias of the channel.
+struct Channel {
+  int at;
+  float scale, bias;
+};
+
+// Of two tokens' sums of this lane's channel: with `pairs` the even lanes store the first token's
+// numbers of their channel and the next one, the odd lanes the second token's.
+__device__ __forceinline__ void store2(const Params &p, const Channel &c, int lane, int token, int s0, int s1) {
+  const bool in = c.at < p.N;
+  const float y0 = token < p.M ? fmaf((float)s0, c.scale * p.x_scale[token], c.bias) : 0.0f;
+  const float y1 = token + 1 < p.M ? fmaf((float)s1, c.scale * p.x_scale[token + 1], c.bias) : 0.0f;
+  if (p.d.pairs) {
+    const bool odd = lane & 1;
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+    const int row = token + odd, col = c.at - odd;
+    if (row < p.M && col < p.N) {
+      const uint32_t v = odd ? tcx::pack_out(p.d.type, other, y1) : tcx::pack_out(p.d.type, y0, other);
+      uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + row * p.d.ld + col;
+      if (col + 1 < p.N)
+        *reinterpret_cast<uint32_t *>(d) = v;
+      else
+        *d = (uint16_t)v;
+    }
+    return;
+  }
+  if (in && token < p.M) tcx::finish_out(p.d.ptr, p.d.type, token * p.d.ld + c.at, y0, p.d.beta);
+  if (in && token + 1 < p.M) tcx::finish_out(p.d.ptr, p.d.type, (token + 1) * p.d.ld + c.at, y1, p.d.beta);
+}
+
+__device__ __forceinline__ Channel channel_at(const Params &p, int at) {
+  const bool in = at < p.N;
+  return {at, in ? p.w_scale[at] : 0.0f, in && p.d.bias ? p.d.bias[at] : 0.0f};
+}
+
+__device__ __forceinline__ int ld_cluster_int(uint32_t local, uint32_t rank) {
+  return __float_as_int(tcx::ld_cluster1(local, rank));
+}
+
+// Warp 0: TMA producer, warp 1: MMA issuer (one elected lane of each), warps 4 - 7: converters, one row
+// of P per thread; warps 8 ..: epilogue, a group of four warps owns COLS tokens of the tile, warp w of
+// it TMEM lanes (channels) 32 (w % 4) .. + 31, one per thread.
+template <int TN, bool PAIR>
+__global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
+    i8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+              const Params p) {
+  using C = Cfg<TN, PAIR>;
+  using namespace tcx;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = saddr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw);
+  const uint32_t halves_at = base + C::STAGES * C::STAGE_BYTES;  // Q in FP16, where it is converted
+  const uint32_t p_full = halves_at + C::NA * C::H_BYTES;
+  const uint32_t q_full = p_full + 8 * C::STAGES, empty = q_full + 8 * C::STAGES;
+  const uint32_t a_full = empty + 8 * C::STAGES, a_empty = a_full + 8 * C::NA;
+  const uint32_t acc_full = a_empty + 8 * C::NA, acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
+  const uint32_t tmem_slot = acc_empty + 8 * C::PARTS * C::NBUF;
+  volatile uint32_t *tmem_slot_ptr =
+      reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // a cluster is S CTAs with a range of k blocks each, or a pair on one tile of 256 channels
+  const int S = PAIR ? 1 : p.split, CS = PAIR ? 2 : S;
+  const int cta = CS > 1 ? (int)(blockIdx.x % (unsigned)CS) : 0;  // rank in the cluster
+  const int rank = PAIR ? 0 : cta;
+  const int first = (int)(blockIdx.x / (unsigned)CS), step = (int)(gridDim.x / (unsigned)CS);
+  const int units = PAIR ? (p.tiles_p + 1) / 2 : p.tiles_p;       // rows of tiles
+  const int tiles = units * p.tiles_q;
+  const int kb0 = (int)((long long)p.KB * rank / S);
+  const int kb1 = (int)((long long)p.KB * (rank + 1) / S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(p_full + 8 * s, 1);
+      mbar_init(q_full + 8 * s, 1);
+      mbar_init(empty + 8 * s, C::CONVERT ? 4 : 1);
+    }
+    for (int a = 0; a < C::NA; ++a) {
+      mbar_init(a_full + 8 * a, PAIR ? 8 : 4);
+      mbar_init(a_empty + 8 * a, 1);
+    }
+    for (int b = 0; b < C::PARTS * C::NBUF; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, C::ACC_WARPS);
+    }
+    mbar_init_fence();
+    tma_prefetch_map(&map_p);
+    tma_prefetch_map(&map_q);
+  }
+  __syncwarp();
+  if (warp == 0) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are initialised
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);  // (uniform)
+  const uint32_t a_tmem = tmem + C::PARTS * C::NBUF * C::ACC_COLS;
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  // (every CTA of the grid is resident, so the next launch may take what room is left)
+  griddep_launch_dependents();
+
+  const auto tile_at = [&](int t, int &tp, int &tq) {
+    tile_coords(t, units, p.tiles_q, p.group_p, tp, tq);
+    if (PAIR) tp = 2 * tp + cta;
+  };
+
+  if (warp < 4) {
+    // a pair's 512 threads x 128 registers at launch >= 128 x 56 + 128 x 96 + 256 x 168
+    if constexpr (PAIR) reg_dealloc<56>();
+    if (warp == 0) {
+      // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
+      Ring<C::STAGES> st;
+      int issued = 0;  // (up to STAGES)
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        int tp, tq;
+        tile_at(t, tp, tq);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_short(empty + 8 * st.slot, st.parity ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicCAS(&g_i8_status, 0, 1);
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t dst = base + st.slot * C::STAGE_BYTES;
+            const uint32_t pf = p_full + 8 * st.slot, qf = q_full + 8 * st.slot;
+            const int k = kb * BK, q0 = tq * TN + cta * (PAIR ? C::QN : 0);
+            mbar_expect_tx(pf, P_BYTES);
+            tma_load_2d(dst, &map_p, k, tp * BP, pf);
+            if constexpr (C::CONVERT) {
+              mbar_expect_tx(qf, C::Q_BYTES);
+              tma_load_2d(dst + P_BYTES, &map_q, k, q0, qf);
+            } else if constexpr (PAIR) {  // both CTAs' copies complete the leader's barrier
+              const uint32_t lead = in_cta(qf, 0);
+              if (cta == 0) mbar_expect_tx(qf, 2 * C::Q_BYTES);
+              tma_load_2d_pair(dst + P_BYTES, &map_q, k, q0, lead);
+              tma_load_2d_pair(dst + P_BYTES + C::QN * 128, &map_q, k + 64, q0, lead);
+            } else {
+              mbar_expect_tx(qf, C::Q_BYTES);
+              tma_load_2d(dst + P_BYTES, &map_q, k, q0, qf);
+              tma_load_2d(dst + P_BYTES + C::QN * 128, &map_q, k + 64, q0, qf);
+            }
+          }
+          __syncwarp();
+          issued = min(issued + 1, C::STAGES);
+          st.next();
+        }
+      }
+      // the last loads issued must have landed before this warp leaves (of a pair's Q: the leader
+      // waits for both, and the CTAs leave together)
+      for (; issued > 0; --issued) {
+        st.parity ^= st.slot == 0 ? 1u : 0u;
+        st.slot = st.slot == 0 ? C::STAGES - 1 : st.slot - 1;
+        wait_short(p_full + 8 * st.slot, st.parity);
+        if (!PAIR || cta == 0) wait_short(q_full + 8 * st.slot, st.parity);
+      }
+    } else if (warp == 1 && (!PAIR || cta == 0)) {
+      // ---- MMA issuer
+      const uint64_t qd0 = sw128_desc(C::CONVERT ? halves_at : base + P_BYTES, 16);
+      Ring<C::STAGES> st;
+      Ring<C::NA> ar;
+      Ring<C::NBUF> buf;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int in_chunk = (kb - kb0) % CHUNK;
+          const bool begin = in_chunk == 0, end = in_chunk == CHUNK - 1 || kb == kb1 - 1;
+          ok = __all_sync(0xffffffffu, wait_short(a_full + 8 * ar.slot, ar.parity) &&
+                                           (C::CONVERT || wait_short(q_full + 8 * st.slot, st.parity)));
+          fence_after();
+          const uint32_t a = a_tmem + ar.slot * C::A_COLS;
+          const uint64_t qd =
+              qd0 + (C::CONVERT ? ar.slot * (uint32_t)(C::H_BYTES >> 4) : st.slot * (uint32_t)(C::STAGE_BYTES >> 4));
+#pragma unroll
+          for (int part = 0; part < C::PARTS; ++part) {
+            const uint32_t which = part * C::NBUF + buf.slot;
+            if (ok && begin) {
+              ok = __all_sync(0xffffffffu, wait_short(acc_empty + 8 * which, buf.parity ^ 1u));
+              fence_after();
+            }
+            if (ok && elect_one()) {
+              const uint32_t d = tmem + which * C::ACC_COLS;
+#pragma unroll
+              for (uint32_t kk = 0; kk < BK / 16; ++kk) {
+                // 64 of k per box of 128-byte rows; a part's 64 rows of this CTA's tokens
+                const uint64_t q = qd + ((kk / 4 * C::QN * 128 + part * 64 * 128 + kk % 4 * 32) >> 4);
+                const uint32_t more = !begin || kk != 0;
+                if constexpr (PAIR)
+                  mma_f16_tmem_pair(d, a + kk * 8, q, p.idesc, more);
+                else
+                  mma_f16_tmem(d, a + kk * 8, q, p.idesc, more);
+              }
+              if (part == C::PARTS - 1) {
+                // (these before the accumulator's: who has seen the last accumulator knows that no
+                // arrival is to come)
+                if constexpr (PAIR) {
+                  mma_commit_pair(a_empty + 8 * ar.slot);
+                  mma_commit_pair(empty + 8 * st.slot);
+                } else {
+                  mma_commit(a_empty + 8 * ar.slot);
+                  if constexpr (!C::CONVERT) mma_commit(empty + 8 * st.slot);
+                }
+              }
+              if (end) {
+                if constexpr (PAIR)
+                  mma_commit_pair(acc_full + 8 * which);
+                else
+                  mma_commit(acc_full + 8 * which);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) {
+            if (lane == 0) atomicCAS(&g_i8_status, 0, 2);
+            break;
+          }
+          st.next();
+          ar.next();
+          if (end) buf.next();
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---- converters
+    if constexpr (PAIR) reg_dealloc<96>();
+    const int row = threadIdx.x - 128;  // of P
+    const uint32_t a_lane = a_tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    Ring<C::STAGES> st;
+    Ring<C::NA> ar;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_short(p_full + 8 * st.slot, st.parity) &&
+                                         (!C::CONVERT || wait_short(q_full + 8 * st.slot, st.parity)) &&
+                                         wait_short(a_empty + 8 * ar.slot, ar.parity ^ 1u));
+        if (!ok) {
+          if (lane == 0) atomicCAS(&g_i8_status, 0, 4);
+          break;
+        }
+        fence_after();
+        const uint8_t *stage = sbase + st.slot * C::STAGE_BYTES;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 64 of k: 32 columns
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 u =
+                *reinterpret_cast<const uint4 *>(stage + row * 128 + (((4 * h + c) ^ (row & 7)) << 4));
+            tcx::halves(u.x, v[8 * c], v[8 * c + 1]);
+            tcx::halves(u.y, v[8 * c + 2], v[8 * c + 3]);
+            tcx::halves(u.z, v[8 * c + 4], v[8 * c + 5]);
+            tcx::halves(u.w, v[8 * c + 6], v[8 * c + 7]);
+          }
+          tmem_st(a_lane + ar.slot * C::A_COLS + h * 32, v);
+        }
+        if constexpr (C::CONVERT) {
+          // Q: 16 of k of a token at a time, into two boxes of 64 of k with 128-byte rows
+          uint8_t *to = sbase + C::STAGES * C::STAGE_BYTES + ar.slot * C::H_BYTES;
+#pragma unroll
+          for (int i = row; i < TN * 8; i += 128) {
+            const int r = i >> 3, j = i & 7;
+            const uint4 u = *reinterpret_cast<const uint4 *>(stage + P_BYTES + r * 128 + ((j ^ (r & 7)) << 4));
+            uint4 lo, hi;
+            tcx::halves(u.x, lo.x, lo.y);
+            tcx::halves(u.y, lo.z, lo.w);
+            tcx::halves(u.z, hi.x, hi.y);
+            tcx::halves(u.w, hi.z, hi.w);
+            uint8_t *box = to + (j >> 2) * (TN * 128) + r * 128;
+            *reinterpret_cast<uint4 *>(box + (((2 * j & 7) ^ (r & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4 *>(box + (((2 * j + 1 & 7) ^ (r & 7)) << 4)) = hi;
+          }
+          async_fence();  // (the tensor core reads them)
+        }
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            arrive_in(in_cta(a_full + 8 * ar.slot, 0));
+          else
+            mbar_arrive(a_full + 8 * ar.slot);
+          if constexpr (C::CONVERT) mbar_arrive(empty + 8 * st.slot);
+        }
+        st.next();
+        ar.next();
+      }
+    }
+  } else {
+    // ---- epilogue
+    if constexpr (PAIR) reg_alloc<168>();
+    const int grp = (warp - 8) >> 2, quad = warp & 3;
+    // a group's tokens: COLS neighbouring ones, or one part of a pair's tile, 64 from each CTA's half
+    const uint32_t which0 = PAIR ? grp * C::NBUF : 0;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + which0 * C::ACC_COLS +
+                               (PAIR ? 0 : (uint32_t)(grp * C::COLS));
+    const uint32_t full0 = acc_full + 8 * which0, empty0 = acc_empty + 8 * which0;
+    Ring<C::NBUF> buf;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      int tp, tq;
+      tile_at(t, tp, tq);
+      int acc[C::COLS];
+#pragma unroll
+      for (int j = 0; j < C::COLS; ++j) acc[j] = 0;
+      for (int kb = kb0; kb < kb1; kb += CHUNK) {
+        ok = __all_sync(0xffffffffu, wait_short(full0 + 8 * buf.slot, buf.parity));
+        if (!ok) {
+          if (lane == 0) atomicCAS(&g_i8_status, 0, 3);
+          break;
+        }
+        fence_after();
+        constexpr int CH = C::COLS < 32 ? 16 : 32;
+        const uint32_t src = lane_base + buf.slot * C::ACC_COLS;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += CH) {
+          uint32_t v[CH];
+          tmem_ld(src + (uint32_t)c, v);
+          tmem_wait_ld(v);
+          if (c + CH >= C::COLS) {  // everything is in registers
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR)
+                arrive_in(in_cta(empty0 + 8 * buf.slot, 0));
+              else
+                mbar_arrive(empty0 + 8 * buf.slot);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < CH; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+        }
+        buf.next();
+      }
+      if (!ok) break;
+      if (S == 1) {
+        const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 2) {
+          const int token = tq * TN + (PAIR ? (c / 64) * 128 + grp * 64 + c % 64 : grp * C::COLS + c);
+          store2(p, ch, lane, token, acc[c], acc[c + 1]);
+        }
+      } else {
+        // partial tile -> the ring, whose every reader has finished (the last accumulator is
+        // complete): [token][channel]
+        int *part = reinterpret_cast<int *>(sbase);
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j) part[(grp * C::COLS + j) * BP + quad * 32 + lane] = acc[j];
+      }
+    }
+  }
+  __syncwarp();
+  if (S > 1) {
+    // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp two of them and 32
+    // channels at a time
+    cluster_sync_all();
+    if (warp >= 8) {
+      int tp, tq;
+      tile_at(first, tp, tq);
+      const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);  // (TN / S is even)
+      const int items = c1 > c0 ? (c1 - c0 + 1) / 2 * 4 : 0;
+      for (int i = warp - 8; i < items; i += C::EPI_WARPS) {
+        const int quad = i & 3, c = c0 + i / 4 * 2;
+        const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
+        int v[2][MAX_CLUSTER];
+#pragma unroll
+        for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
+          if (q < S) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              v[j][q] = ld_cluster_int(base + (uint32_t)((c + j) * BP + quad * 32 + lane) * 4, (uint32_t)q);
+          }
+        int s0 = v[0][0], s1 = v[1][0];
+#pragma unroll
+        for (int q = 1; q < MAX_CLUSTER; ++q)
+          if (q < S) s0 += v[0][q], s1 += v[1][q];
+        // (both are used whatever is stored: a load that nothing waits for could still be under way
+        // when the other CTA leaves)
+        asm volatile("" ::"r"(s0), "r"(s1));
+        store2(p, ch, lane, tq * TN + c, s0, s1);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while another may still read its partial
+  }
+  fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {
+    cluster_sync_all();  // no instruction, copy or arrival of the other CTA is under way
+    if (warp == 0) tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  } else {
+    if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// D = bias + beta * D (K == 0).
+__global__ void i8_bias_kernel(int M, int N, const Result d) {
+  griddep_wait();
+  const long long total = (long long)M * N;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
+       i += (long long)gridDim.x * blockDim.x) {
+    const int n = (int)(i % N);
+    tcx::finish_out(d.ptr, d.type, i / N * d.ld + n, d.bias ? d.bias[n] : 0.0f, d.beta);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Host side
+
+struct Plan {
+  int tn, split;       // tn = 0: few_kernel
+};
+
+static Plan make_plan(int M, int N, int K, int sms) {
+  if (M <= kFewRows) return {0, 1};
+  const int KB = (int)ceil_div(K, BK);
+  Plan best{128, 1};
+  double best_cost = 1e300;
+  static const int tns[5] = {256, 128, 64, 32, 16};
+  static const double block[5] = {18, 13, 9, 7, 6};
+  for (int i = 0; i < 5; ++i) {
+    const int tn = tns[i];
+    const bool pair = tn == 256;
+    const long long tiles = (long long)ceil_div(N, pair ? 2 * BP : BP) * ceil_div(M, tn);
+    for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
+      if (S > 1 && (pair || S > KB || tn / S < 2 || tiles * S > (S == 8 ? 96 : sms))) break;
+      const int at_once = pair ? sms / 2 : sms;
+      const long long per_sm = (tiles * S + at_once - 1) / at_once;
+      const double cost = per_sm * (block[i] * ((KB + S - 1) / S) + 0.25 * tn / S) +
+                          (S > 1 ? 25.0 + 0.3 * tn : 0.0) + (tn >= 128 ? 40.0 : 0.0);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {tn, S};
+      }
+    }
+  }
+  return best;
+}
+
+template <int TN, bool PAIR = false>
+static cudaError_t launch(const CUtensorMap &mp, const CUtensorMap &mq, const Params &p, int grid,
+                          cudaStream_t stream) {
+  using C = Cfg<TN, PAIR>;
+  return launch_1d(i8_kernel<TN, PAIR>, grid, C::THREADS, C::SMEM_BYTES, PAIR ? 2 : p.split, stream, mp, mq, p);
+}
+
+template <int TN, bool PAIR = false>
+static cudaError_t set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(i8_kernel<TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<TN, PAIR>::SMEM_BYTES);
+  if (e == cudaSuccess && PAIR) {
+    // the registers that the warpgroups ask for must be there: what a launch brings is what the
+    // compiler gave the kernel
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, i8_kernel<TN, PAIR>);
+    if (e == cudaSuccess && a.numRegs / 8 * 8 * Cfg<TN, PAIR>::THREADS < 128 * 56 + 128 * 96 + 256 * 168)
+      e = cudaErrorLaunchOutOfResources;
+  }
+  return e;
+}
+
+static std::once_flag g_once[64];
+static cudaError_t g_err[64];
+
+static cudaError_t kernel_setup() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(g_once[dev], [dev]() {
+    cudaError_t err = set_attributes<256, true>();
+    if (err == cudaSuccess) err = set_attributes<128>();
+    if (err == cudaSuccess) err = set_attributes<64>();
+    if (err == cudaSuccess) err = set_attributes<32>();
+    if (err == cudaSuccess) err = set_attributes<16>();
+    g_err[dev] = err;
+  });
+  return g_err[dev];
+}
+
+static cudaError_t run(const Plan &pl, int M, int N, int K, const Operand &x, const Operand &w, const Result &d,
+                       int sms, cudaStream_t stream) {
+  Params p{};
+  p.N = N;
+  p.M = M;
+  p.KB = (int)ceil_div(K, BK);
+  p.w_scale = w.scale;
+  p.x_scale = x.scale;
+  p.d = d;
+  const bool pair = pl.tn == 256;
+  const long long tiles_p = ceil_div(N, BP), tiles_q = ceil_div(M, pl.tn);
+  if (tiles_p * tiles_q > 0x7fffffffLL / MAX_CLUSTER) return cudaErrorInvalidConfiguration;
+  p.tiles_p = (int)tiles_p;
+  p.tiles_q = (int)tiles_q;
+  p.group_p = (int)std::min<long long>(pair ? 8 : 16, tiles_p);
+  p.split = pl.split;
+  // instruction descriptor: D in FP32 (bits 4-5 = 1), FP16 operands, k contiguous, N / 8 (bits 17-22),
+  // M / 16 (24-28)
+  p.idesc = (1u << 4) | ((uint32_t)((pair ? pl.tn / 2 : pl.tn) >> 3) << 17) |
+            ((uint32_t)((pair ? 2 * BP : BP) >> 4) << 24);
+  CUtensorMap mp, mq;
+  if (!encode_map_2d_narrow(&mp, w.q, 1, N, K, w.ld, BP)) return cudaErrorInvalidValue;
+  char *ws = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (pl.tn >= 128) {
+    const long long ld = ceil_div(K, 16) * 16;
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), (size_t)M * ld * 2, workspace_pool(), stream);
+    if (e != cudaSuccess) return e;
+    e = encode_map_2d_narrow(&mq, ws, 2, M, K, ld, pair ? pl.tn / 2 : pl.tn)
+            ? launch_unpack(M, K, x, ws, ld, sms, stream)
+            : cudaErrorInvalidValue;
+  } else if (!encode_map_2d_narrow(&mq, x.q, 1, M, K, x.ld, pl.tn)) {
+    return cudaErrorInvalidValue;
+  }
+  const int grid = (int)(pair ? 2 * std::min<long long>(ceil_div(tiles_p, 2) * tiles_q, sms / 2)
+                         : p.split > 1 ? tiles_p * tiles_q * p.split
+                                       : std::min<long long>(tiles_p * tiles_q, sms));
+  if (e == cudaSuccess)
+    switch (pl.tn) {
+      case 256: e = launch<256, true>(mp, mq, p, grid, stream); break;
+      case 128: e = launch<128>(mp, mq, p, grid, stream); break;
+      case 64: e = launch<64>(mp, mq, p, grid, stream); break;
+      case 32: e = launch<32>(mp, mq, p, grid, stream); break;
+      default: e = launch<16>(mp, mq, p, grid, stream);
+    }
+  if (ws != nullptr) {
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    if (e == cudaSuccess) e = ef;
+  }
+  return e;
+}
+
+}  // namespace i8
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int i8_linear(int M, int N, int K, const void *x, int ldx, const float *x_scale, const void *w,
+                         int ldw, const float *w_scale, const float *bias, float beta, void *D, int d_type,
+                         int ldd, cudaStream_t stream) {
+  const bool read = M > 0 && N > 0 && K > 0;
+  const auto bad_ptr = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
+  if (M < 0) return -1;
+  if (N < 0) return -2;
+  if (K < 0 || K > i8::LARGEST_K) return -3;
+  if (read && (x == nullptr || bad_ptr(x))) return -4;
+  if (ldx < std::max(1, K) || ldx % 16 != 0) return -5;
+  if (read && x_scale == nullptr) return -6;
+  if (read && (w == nullptr || bad_ptr(w))) return -7;
+  if (ldw < std::max(1, K) || ldw % 16 != 0) return -8;
+  if (read && w_scale == nullptr) return -9;
+  if (M > 0 && N > 0 && D == nullptr) return -12;
+  if (d_type != I8_F32 && d_type != I8_BF16 && d_type != I8_F16) return -13;
+  if (reinterpret_cast<uintptr_t>(D) % (d_type == I8_F32 ? 4 : 2) != 0) return -12;
+  if (ldd < std::max(1, N)) return -14;
+  if (M == 0 || N == 0) return 0;
+
+  int sms = 0;
+  cudaError_t e = device_setup(&sms);
+  if (e == cudaSuccess) e = i8::kernel_setup();
+  if (e != cudaSuccess) return (int)e;
+  const bool pairs = d_type != I8_F32 && beta == 0.0f && reinterpret_cast<uintptr_t>(D) % 4 == 0 &&
+                     (M == 1 || ldd % 2 == 0);
+  const i8::Result d{D, d_type, ldd, bias, beta, pairs};
+  if (K == 0) {
+    const long long blocks = std::min<long long>(ceil_div((long long)M * N, 256), 8LL * sms);
+    return (int)launch_1d(i8::i8_bias_kernel, (int)blocks, 256, 0, 1, stream, M, N, d);
+  }
+  const i8::Operand ox{static_cast<const int8_t *>(x), ldx, x_scale}, ow{static_cast<const int8_t *>(w), ldw, w_scale};
+  const i8::Plan pl = i8::make_plan(M, N, K, sms);
+  if (pl.tn == 0) return (int)i8::launch_few(M, N, K, ox, ow, d, sms, stream);
+  return (int)i8::run(pl, M, N, K, ox, ow, d, sms, stream);
+}
+
+extern "C" int i8_linear_with(const i8_linear_args *a) {
+  if (a == nullptr) return -1;
+  return i8_linear(a->M, a->N, a->K, a->x, a->ldx, a->x_scale, a->w, a->ldw, a->w_scale, a->bias, a->beta, a->D,
+                   a->d_type, a->ldd, a->stream);
+}
+
+extern "C" int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens, int *split) {
+  if (M < 1) return -1;
+  if (N < 1) return -2;
+  if (K < 1 || K > i8::LARGEST_K) return -3;
+  if (num_sms < 0) return -4;
+  int sms = num_sms;
+  if (sms == 0 && device_setup(&sms) != cudaSuccess) {
+    (void)cudaGetLastError();
+    sms = 152;  // no device here: the answer for a whole GB300
+  }
+  const i8::Plan pl = i8::make_plan(M, N, K, sms);
+  if (tile_tokens) *tile_tokens = pl.tn;
+  if (split) *split = pl.split;
+  return 0;
+}
+
+extern "C" int i8_linear_status(int *status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, i8::g_i8_status, sizeof(int));
+  if (e != cudaSuccess) return (int)e;
+  const int zero = 0;
+  e = cudaMemcpyToSymbol(i8::g_i8_status, &zero, sizeof(int));
+  if (status) *status = v;
+  return (int)e;
+}

@@ -1,0 +1,218 @@
+// Quantiser to 8-bit integers with a scale for each row:
+//   a = max(max |x|, 2^-119), scale = a / 127, q = x (127 / a) rounded to a whole number
+//
+// Bound by HBM: x is read once and a byte written for each element. A row stays packed in registers
+// between its maximum and its result. The product with 127 / a is rounded once, to a whole number, by
+// the addition of 1.5 * 2^23 in the same FMA, which leaves q in the low byte: |q| is at most 127, since
+// a (127 / a) (1 + 2^-24) is nearer to 127 than to 128.
+#include <algorithm>
+
+#include "../../include/i8_linear.h"
+#include "row_common.cuh"
+
+namespace sgemm {
+namespace i8q {
+
+using namespace rows;
+
+struct Params {
+  int rows, cols;
+  const char *x;
+  long long ldx;       // bytes
+  uint8_t *q;
+  long long ldq;
+  float *scale;
+  int vec_q;           // 8-byte stores to q are aligned
+};
+
+// The larger magnitudes of two words (with either sign; NaN over all), and the largest one in a word.
+template <class T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t m;
+  if constexpr (T::TYPE == tcx::OUT_F32)
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+  else if constexpr (T::TYPE == tcx::OUT_BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+template <class T>
+__device__ __forceinline__ uint32_t top(uint32_t w) {  // FP32 bits of a magnitude
+  if constexpr (T::TYPE == tcx::OUT_F32) return w & 0x7fffffffu;
+  w &= 0x7fff7fffu;
+  if constexpr (T::TYPE == tcx::OUT_BF16) return max(w & 0xffff0000u, w << 16);
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)max(w >> 16, w & 0xffffu))));
+}
+
+// Largest magnitude over a row's threads: FP32 bits, ordered as integers (a NaN is the largest).
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*part)[32], int turn) {
+#pragma unroll
+  for (int d = 1; d < (TPR < 32 ? TPR : 32); d *= 2) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[turn][0];
+#pragma unroll
+    for (int w = 1; w < TPR / 32; ++w) v = max(v, part[turn][w]);
+  }
+  return v;
+}
+
+struct Scale {
+  float s, r;  // scale, and what x is multiplied with
+  bool finite;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t bits) {
+  Scale o;
+  const float a = fmaxf(__uint_as_float(bits), 0x1p-119f);
+  o.finite = bits < 0x7f800000u;
+  o.s = o.finite ? __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fc00000u);
+  o.r = __fdiv_rn(127.0f, a);
+  return o;
+}
+// q in the low byte.
+__device__ __forceinline__ uint32_t rounded(float x, const Scale &s) {
+  return __float_as_uint(fmaf(x, s.r, 12582912.0f));
+}
+__device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+template <class T, int TPR, int CH, bool VEC>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) quantize_kernel(const Params p) {
+  constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
+  __shared__ uint32_t part[2][32];
+  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
+  int n[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  const long long step = (long long)gridDim.x * RPB;
+  long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
+  long long row = base + threadIdx.x / TPR;
+  Chunk<T> next[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) sh.load(p.x + row * p.ldx, c, row < p.rows ? n[c] : 0, next[c]);
+  for (int turn = 0; base < p.rows; base += step, row += step, turn ^= 1) {
+    Chunk<T> v[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) v[c] = next[c];
+    const long long ahead = row + step;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) sh.load(p.x + ahead * p.ldx, c, ahead < p.rows ? n[c] : 0, next[c]);
+    uint32_t m = v[0].w[0];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < T::W; ++i) m = larger<T>(m, v[c].w[i]);
+    const Scale s = scale_of(row_max<TPR>(top<T>(m), part, turn));
+    if (row < p.rows) {
+      if (sh.t == 0) p.scale[row] = s.s;
+      uint8_t *to = p.q + row * p.ldq;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        uint32_t q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = s.finite ? rounded(v[c][j], s) : 0;
+        if (VEC && p.vec_q && n[c] == 8) {
+          *reinterpret_cast<uint2 *>(to + sh.col(c, 0)) =
+              make_uint2(four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n[c]) to[sh.col(c, j)] = (uint8_t)q[j];
+        }
+      }
+    }
+  }
+  griddep_launch_dependents();
+}
+
+// Rows of any length: a CTA reads its row twice.
+template <class T>
+__global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
+  __shared__ uint32_t part[2][32];
+  griddep_wait();
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const char *x = p.x + row * p.ldx;
+    uint32_t m = 0;
+#pragma unroll 8
+    for (long long i = threadIdx.x; i < p.cols; i += 1024)
+      m = max(m, __float_as_uint(tcx::load_out(x, T::TYPE, i)) & 0x7fffffffu);
+    const Scale s = scale_of(row_max<1024>(m, part, turn));
+    if (threadIdx.x == 0) p.scale[row] = s.s;
+    uint8_t *to = p.q + row * p.ldq;
+#pragma unroll 8
+    for (long long i = threadIdx.x; i < p.cols; i += 1024)
+      to[i] = s.finite ? (uint8_t)rounded(tcx::load_out(x, T::TYPE, i), s) : 0;
+  }
+  griddep_launch_dependents();
+}
+
+template <class T, int TPR, int CH>
+static cudaError_t launch(const Params &p, bool vec, int sms, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
+  const long long grid =
+      std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * std::max(1, 2048 / threads));
+  return vec ? launch_1d(quantize_kernel<T, TPR, CH, true>, (int)grid, threads, 0, 1, stream, p)
+             : launch_1d(quantize_kernel<T, TPR, CH, false>, (int)grid, threads, 0, 1, stream, p);
+}
+
+template <class T>
+static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) {
+  if (p.cols <= 64) return launch<T, 8, 1>(p, vec, sms, stream);
+  if (p.cols <= 256) return launch<T, 32, 1>(p, vec, sms, stream);
+  if (p.cols <= 512) return launch<T, 32, 2>(p, vec, sms, stream);
+  if (p.cols <= 1024) return launch<T, 128, 1>(p, vec, sms, stream);
+  if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
+  if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
+  if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
+  return launch_1d(quantize_long_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+}
+
+}  // namespace i8q
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int i8_quantize(int rows, int cols, const void *x, int x_type, int ldx, void *q, int ldq,
+                           float *scale, cudaStream_t stream) {
+  const bool any = rows > 0 && cols > 0;
+  if (rows < 0) return -1;
+  if (cols < 0) return -2;
+  if (any && x == nullptr) return -3;
+  if (x_type != I8_F32 && x_type != I8_BF16 && x_type != I8_F16) return -4;
+  const int size = x_type == I8_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % size != 0) return -3;
+  if (ldx < std::max(1, cols)) return -5;
+  if (any && q == nullptr) return -6;
+  if (ldq < std::max(1, cols)) return -7;
+  if (rows > 0 && scale == nullptr) return -8;
+  if (rows == 0) return 0;
+  int sms = 0;
+  const cudaError_t e = device_setup(&sms);
+  if (e != cudaSuccess) return (int)e;
+  const auto at = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
+  i8q::Params p{};
+  p.rows = rows;
+  p.cols = cols;
+  p.x = static_cast<const char *>(x);
+  p.ldx = (long long)ldx * size;
+  p.q = static_cast<uint8_t *>(q);
+  p.ldq = ldq;
+  p.scale = scale;
+  p.vec_q = at(q) % 8 == 0 && (rows == 1 || ldq % 8 == 0);
+  const bool vec = rows::aligned(at(x), rows > 1 ? p.ldx : 0);
+  if (x_type == I8_F32) return (int)i8q::run<rows::F32>(p, vec, sms, stream);
+  if (x_type == I8_BF16) return (int)i8q::run<rows::BF16>(p, vec, sms, stream);
+  return (int)i8q::run<rows::F16>(p, vec, sms, stream);
+}
+
+extern "C" int i8_quantize_with(const i8_quantize_args *a) {
+  if (a == nullptr) return -1;
+  return i8_quantize(a->rows, a->cols, a->x, a->x_type, a->ldx, a->q, a->ldq, a->scale, a->stream);
+}

@@ -1,0 +1,235 @@
+// Layer norm over the rows of x:
+//   mean = sum x / n, var = sum (x - mean)^2 / n, rstd = 1 / sqrt(var + eps), y = (x - mean) rstd w + b
+//
+// Bound by HBM: each element is read and written once. A row stays in registers from its one read to
+// its last use, so that the variance is the mean of the squared distances themselves: no difference
+// of large sums.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/layer_norm.h"
+#include "row_common.cuh"
+
+namespace sgemm {
+namespace ln {
+
+using namespace rows;
+
+struct Params {
+  int rows, cols;
+  const char *x;
+  long long ldx;       // bytes
+  Vector weight, bias;
+  float eps, n;        // n = cols
+  char *y;
+  long long ldy;       // bytes
+  float *mean, *rstd;
+};
+
+// TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn, the next one's
+// loads under way while this one is computed. The parameters of a thread's columns stay in its
+// registers, but for the longest rows, which have too many threads for that.
+template <class T, int TPR, int CH, bool VEC>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const Params p) {
+  constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
+  constexpr bool HOLD = TPR < 1024;
+  __shared__ float2 part[2][32];
+  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
+  int n[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  const long long step = (long long)gridDim.x * RPB;
+  long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+  long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
+  Chunk<T> next[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) sh.load(p.x + row * p.ldx, c, row < p.rows ? n[c] : 0, next[c]);
+  float w[HOLD ? CH : 1][8], b[HOLD ? CH : 1][8];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[c][j] = j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
+        b[c][j] = j < n[c] ? p.bias.at(sh.col(c, j), 0.0f) : 0.0f;
+      }
+  }
+  for (; base < p.rows; base += step, row += step) {
+    Chunk<T> v[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) v[c] = next[c];
+    const long long ahead = row + step;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) sh.load(p.x + ahead * p.ldx, c, ahead < p.rows ? n[c] : 0, next[c]);
+    float sum = 0.0f, squares = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += v[c][j];
+    const float mean = row_sum<TPR>(make_float2(sum, 0.0f), part, 0).x / p.n;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = j < n[c] ? v[c][j] - mean : 0.0f;
+        squares = fmaf(d, d, squares);
+      }
+    const float var = row_sum<TPR>(make_float2(squares, 0.0f), part, 1).x / p.n;
+    const float rstd = __frsqrt_rn(var + p.eps);
+    if (row < p.rows) {
+      if (sh.t == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = HOLD ? w[HOLD ? c : 0][j] : j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
+          const float bj = HOLD ? b[HOLD ? c : 0][j] : j < n[c] ? p.bias.at(sh.col(c, j), 0.0f) : 0.0f;
+          y[j] = fmaf((v[c][j] - mean) * rstd, wj, bj);
+        }
+        Chunk<T> out;
+        pack<T>(y, out);
+        sh.store(p.y + row * p.ldy, c, n[c], out);
+      }
+    }
+  }
+  griddep_launch_dependents();
+}
+
+// Sum over the 1024 threads of a CTA, the same bits in each of them.
+__device__ __forceinline__ double cta_sum(double v, double *part) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = part[0];
+  for (int w = 1; w < 32; ++w) v += part[w];
+  return v;
+}
+
+// Rows of any length: a CTA reads its row three times (for the mean, the variance and the result).
+// 16 elements at a time are added up in FP32, the rest in 64 bits.
+template <class T>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
+  __shared__ double part[32];
+  griddep_wait();
+  const auto at = [&](const char *row, long long i) {
+    return tcx::load_out(row, T::TYPE, i);
+  };
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const char *x = p.x + row * p.ldx;
+    double total = 0.0;
+    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s += i0 + j * 1024 < p.cols ? at(x, i0 + j * 1024) : 0.0f;
+      total += s;
+    }
+    const float mean = (float)(cta_sum(total, part) / p.cols);
+    total = 0.0;
+    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float d = i0 + j * 1024 < p.cols ? at(x, i0 + j * 1024) - mean : 0.0f;
+        s = fmaf(d, d, s);
+      }
+      total += s;
+    }
+    const float rstd = __frsqrt_rn((float)(cta_sum(total, part) / p.cols) + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    char *y = p.y + row * p.ldy;
+#pragma unroll 4
+    for (long long i = threadIdx.x; i < p.cols; i += 1024)
+      tcx::store_out(y, T::TYPE, i,
+                     fmaf((at(x, i) - mean) * rstd, p.weight.at((int)i, 1.0f), p.bias.at((int)i, 0.0f)));
+  }
+  griddep_launch_dependents();
+}
+
+template <class T, int TPR, int CH>
+static cudaError_t launch(const Params &p, bool vec, int sms, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
+  // 2048 threads per SM at most, and at least one row for each CTA
+  const long long grid =
+      std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * std::max(1, 1024 / threads));
+  return vec ? launch_1d(norm_kernel<T, TPR, CH, true>, (int)grid, threads, 0, 1, stream, p)
+             : launch_1d(norm_kernel<T, TPR, CH, false>, (int)grid, threads, 0, 1, stream, p);
+}
+
+template <class T>
+static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) {
+  if (p.cols <= 64) return launch<T, 8, 1>(p, vec, sms, stream);
+  if (p.cols <= 256) return launch<T, 32, 1>(p, vec, sms, stream);
+  if (p.cols <= 512) return launch<T, 32, 2>(p, vec, sms, stream);
+  if (p.cols <= 1024) return launch<T, 128, 1>(p, vec, sms, stream);
+  if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
+  if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
+  if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
+  return launch_1d(norm_long_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+}
+
+}  // namespace ln
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const void *weight,
+                          const void *bias, int w_type, float eps, void *y, int ldy, float *mean,
+                          float *rstd, cudaStream_t stream) {
+  const auto known = [](int t) { return t == LN_F32 || t == LN_BF16 || t == LN_F16; };
+  const auto misplaced = [](const void *q, int t) {
+    return reinterpret_cast<uintptr_t>(q) % (t == LN_F32 ? 4 : 2) != 0;
+  };
+  if (rows < 0) return -1;
+  if (cols < 1) return -2;
+  if (rows > 0 && x == nullptr) return -3;
+  if (!known(x_type)) return -4;
+  if (misplaced(x, x_type)) return -3;
+  if (ldx < cols) return -5;
+  if (!known(w_type)) return -8;
+  if (misplaced(weight, w_type)) return -6;
+  if (misplaced(bias, w_type)) return -7;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return -9;
+  if (rows > 0 && y == nullptr) return -10;
+  if (misplaced(y, x_type)) return -10;
+  if (ldy < cols) return -11;
+  if (rows == 0) return 0;
+  int sms = 0;
+  const cudaError_t e = device_setup(&sms);
+  if (e != cudaSuccess) return (int)e;
+  const long long size = x_type == LN_F32 ? 4 : 2;
+  ln::Params p{};
+  p.rows = rows;
+  p.cols = cols;
+  p.x = static_cast<const char *>(x);
+  p.ldx = ldx * size;
+  p.weight = {weight, w_type};
+  p.bias = {bias, w_type};
+  p.eps = eps;
+  p.n = (float)cols;
+  p.y = static_cast<char *>(y);
+  p.ldy = ldy * size;
+  p.mean = mean;
+  p.rstd = rstd;
+  const bool vec = rows::aligned(reinterpret_cast<uintptr_t>(x), rows > 1 ? p.ldx : 0) &&
+                   rows::aligned(reinterpret_cast<uintptr_t>(y), rows > 1 ? p.ldy : 0);
+  if (x_type == LN_F32) return (int)ln::run<rows::F32>(p, vec, sms, stream);
+  if (x_type == LN_BF16) return (int)ln::run<rows::BF16>(p, vec, sms, stream);
+  return (int)ln::run<rows::F16>(p, vec, sms, stream);
+}
+
+extern "C" int layer_norm_with(const layer_norm_args *a) {
+  if (a == nullptr) return -1;
+  return layer_norm(a->rows, a->cols, a->x, a->x_type, a->ldx, a->weight, a->bias, a->w_type, a->eps,
+                    a->y, a->ldy, a->mean, a->rstd, a->stream);
+}

@@ -1,0 +1,402 @@
+// Gradients of layer norm. With h = (x - mean) rstd and g = dy w, along each row of n elements
+//   dx = rstd (g - sum g / n - h sum (g h) / n)
+// and over the rows dw = sum dy h, db = sum dy.
+//
+// Bound by HBM: dy and x are read and dx is written once. A row stays in registers between its two
+// sums and its result. dw and db are added up in the registers of the thread that holds the column,
+// over all rows of its CTA (512 at most, so that FP32 holds such a sum); the CTAs' sums meet in the
+// workspace, where reduce_kernel adds them in a fixed order.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/layer_norm.h"
+#include "row_common.cuh"
+
+namespace sgemm {
+namespace lnb {
+
+using namespace rows;
+
+constexpr int kMostRows = 512;  // rows of one FP32 sum of dw or db
+constexpr int kLongestHere = 8192;  // elements of a row that stays in registers beside the sums
+
+struct Params {
+  int rows, cols;
+  const char *dy, *x;
+  long long lddy, ldx;      // bytes
+  const float *mean, *rstd;
+  Vector weight;
+  float n;                  // cols
+  char *dx;
+  long long lddx;           // bytes
+  float *part;              // sums of dw, then of db: [2][parts][cols]; NULL: neither is wanted
+  int parts;
+  float2 *along;            // rows that do not stay in registers: sum g / n, sum (g h) / n
+};
+
+template <class T, int TPR, int CH, bool VEC>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR <= 256 ? 512 / (TPR < 128 ? 128 : TPR) : 1)
+    backward_kernel(const Params p) {
+  constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
+  __shared__ float2 part[2][32];
+  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
+  int n[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  const long long step = (long long)gridDim.x * RPB;
+  long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
+  long long row = base + threadIdx.x / TPR;
+  const long long mine = row;
+  Chunk<T> next_x[CH], next_d[CH];
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  const auto load = [&](long long r) {
+    const bool in = r < p.rows;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      sh.load(p.x + r * p.ldx, c, in ? n[c] : 0, next_x[c]);
+      sh.load(p.dy + r * p.lddy, c, in ? n[c] : 0, next_d[c]);
+    }
+    next_mean = in ? p.mean[r] : 0.0f;
+    next_rstd = in ? p.rstd[r] : 0.0f;
+  };
+  load(row);
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[c][j] = j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
+      dw[c][j] = db[c][j] = 0.0f;
+    }
+  int turn = 0;
+  for (; base < p.rows; base += step, row += step, turn ^= 1) {
+    Chunk<T> vx[CH], vd[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) vx[c] = next_x[c], vd[c] = next_d[c];
+    const float mean = next_mean, rstd = next_rstd;
+    load(row + step);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // (elements that do not exist have dy = 0, so they add nothing where rstd and mean are finite,
+        // and where those are not the row is NaN anyway; rows that do not exist have rstd = 0)
+        const float d = vd[c][j], h = (vx[c][j] - mean) * rstd, g = d * w[c][j];
+        dw[c][j] = fmaf(d, h, dw[c][j]);
+        db[c][j] += d;
+        s.x += g;
+        s.y = fmaf(g, h, s.y);
+      }
+    if (p.dx == nullptr) continue;
+    s = row_sum<TPR>(s, part, turn);
+    s.x /= p.n;
+    s.y /= p.n;
+    if (row < p.rows) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float h = (vx[c][j] - mean) * rstd;
+          y[j] = (fmaf(vd[c][j], w[c][j], -s.x) - h * s.y) * rstd;
+        }
+        Chunk<T> out;
+        pack<T>(y, out);
+        sh.store(p.dx + row * p.lddx, c, n[c], out);
+      }
+    }
+  }
+  if (p.part) {
+    float *to = p.part + mine * p.cols, *tb = to + (long long)p.parts * p.cols;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n[c]) {
+          to[sh.col(c, j)] = dw[c][j];
+          tb[sh.col(c, j)] = db[c][j];
+        }
+  }
+  griddep_launch_dependents();
+}
+
+// Rows of any length, first half: the two sums along each row, 16 elements at a time in FP32, the
+// rest in 64 bits.
+template <class T>
+__global__ void __launch_bounds__(1024) along_kernel(const Params p) {
+  __shared__ double part[2][32];
+  griddep_wait();
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const char *x = p.x + row * p.ldx, *dy = p.dy + row * p.lddy;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    double a = 0.0, b = 0.0;
+    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
+      float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const long long i = i0 + j * 1024;
+        if (i < p.cols) {
+          const float g = tcx::load_out(dy, T::TYPE, i) * p.weight.at((int)i, 1.0f);
+          sa += g;
+          sb = fmaf(g, (tcx::load_out(x, T::TYPE, i) - mean) * rstd, sb);
+        }
+      }
+      a += sa;
+      b += sb;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      a += __shfl_xor_sync(0xffffffffu, a, d);
+      b += __shfl_xor_sync(0xffffffffu, b, d);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = a, part[1][threadIdx.x >> 5] = b;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 32; ++w) a += part[0][w], b += part[1][w];
+      p.along[row] = make_float2((float)(a / p.cols), (float)(b / p.cols));
+    }
+  }
+  griddep_launch_dependents();
+}
+
+// Second half: CTA (i, j) takes 1024 columns of the j-th part of the rows.
+constexpr int kLongCols = 1024;
+template <class T>
+__global__ void __launch_bounds__(256) across_kernel(const Params p, int col_blocks, int rows_each) {
+  griddep_wait();
+  const int block = blockIdx.x % col_blocks, chunk = blockIdx.x / col_blocks;
+  const long long c0 = (long long)block * kLongCols + threadIdx.x;
+  const long long r0 = (long long)chunk * rows_each;
+  const long long r1 = r0 + rows_each < p.rows ? r0 + rows_each : p.rows;
+  float w[4], dw[4] = {}, db[4] = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = c0 + 256 * j < p.cols ? p.weight.at((int)(c0 + 256 * j), 1.0f) : 0.0f;
+#pragma unroll 2
+  for (long long row = r0; row < r1; ++row) {
+    const char *x = p.x + row * p.ldx, *dy = p.dy + row * p.lddy;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    const float2 s = p.dx ? p.along[row] : make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long i = c0 + 256 * j;
+      if (i < p.cols) {
+        const float d = tcx::load_out(dy, T::TYPE, i);
+        const float h = (tcx::load_out(x, T::TYPE, i) - mean) * rstd;
+        dw[j] = fmaf(d, h, dw[j]);
+        db[j] += d;
+        if (p.dx)
+          tcx::store_out(p.dx + row * p.lddx, T::TYPE, i, (fmaf(d, w[j], -s.x) - h * s.y) * rstd);
+      }
+    }
+  }
+  if (p.part) {
+    float *to = p.part + (long long)chunk * p.cols, *tb = to + (long long)p.parts * p.cols;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + 256 * j < p.cols) {
+        to[c0 + 256 * j] = dw[j];
+        tb[c0 + 256 * j] = db[j];
+      }
+  }
+  griddep_launch_dependents();
+}
+
+// dweight (block < blocks) or dbias: 32 columns per CTA, its 8 warps take the parts in turn, 16 of
+// them at a time in FP32 and the rest in 64 bits.
+__global__ void __launch_bounds__(256) reduce_kernel(const float *part, int parts, int cols, int blocks,
+                                                     float *dweight, float *dbias, float beta) {
+  __shared__ double sums[8][32];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool second = (int)blockIdx.x >= blocks;
+  const long long col = (long long)(blockIdx.x - (second ? blocks : 0)) * 32 + lane;
+  float *out = second ? dbias : dweight;
+  if (out == nullptr) return;
+  double total = 0.0;
+  if (col < cols) {
+    const float *from = part + (second ? (long long)parts * cols : 0) + col;
+    for (int r0 = warp; r0 < parts; r0 += 16 * 8) {
+      float v[16], s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = r0 + 8 * j < parts ? from[(long long)(r0 + 8 * j) * cols] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s += v[j];
+      total += s;
+    }
+  }
+  sums[warp][lane] = total;
+  __syncthreads();
+  if (warp == 0 && col < cols) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) total += sums[w][lane];
+    out[col] = beta != 0.0f ? (float)((double)beta * out[col] + total) : (float)total;
+  }
+  griddep_launch_dependents();
+}
+
+// ------------------------------------------------------------------------------------
+// Host side
+
+struct Plan {
+  int tpr;          // threads on a row; 0: rows do not stay in registers
+  int grid, parts;  // CTAs and sums of dw that they leave
+  int rows_each;    // (tpr == 0) rows of a sum
+};
+
+static Plan make_plan(int rows, int cols, int sms) {
+  Plan pl{};
+  pl.tpr = cols <= 64     ? 8
+           : cols <= 512  ? 32
+           : cols <= 2048 ? 128
+           : cols <= 4096 ? 256
+           : cols <= kLongestHere ? 512 : 0;
+  if (pl.tpr) {
+    const int threads = std::max(128, pl.tpr), rpb = threads / pl.tpr;
+    const long long most = ceil_div(rows, rpb);
+    const long long fill = (long long)sms * std::max(1, 512 / threads);
+    pl.grid = (int)std::min<long long>(most, std::max<long long>(fill, ceil_div(most, kMostRows)));
+    pl.parts = pl.grid * rpb;
+  } else {
+    const long long blocks = ceil_div(cols, kLongCols);
+    pl.rows_each = (int)std::max<long long>(1, std::min<long long>(kMostRows, rows * blocks / (8LL * sms)));
+    pl.parts = (int)ceil_div(rows, pl.rows_each);
+    pl.grid = 0;
+  }
+  return pl;
+}
+
+static size_t along_bytes(const Plan &pl, int rows) {
+  return pl.tpr ? 0 : ((size_t)rows * sizeof(float2) + 255) / 256 * 256;
+}
+static size_t part_bytes(const Plan &pl, int cols) { return (size_t)2 * pl.parts * cols * sizeof(float); }
+
+template <class T, int TPR, int CH>
+static cudaError_t launch(const Params &p, bool vec, int grid, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR;
+  return vec ? launch_1d(backward_kernel<T, TPR, CH, true>, grid, threads, 0, 1, stream, p)
+             : launch_1d(backward_kernel<T, TPR, CH, false>, grid, threads, 0, 1, stream, p);
+}
+
+template <class T>
+static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaStream_t stream) {
+  if (p.cols <= 64) return launch<T, 8, 1>(p, vec, pl.grid, stream);
+  if (p.cols <= 256) return launch<T, 32, 1>(p, vec, pl.grid, stream);
+  if (p.cols <= 512) return launch<T, 32, 2>(p, vec, pl.grid, stream);
+  if (p.cols <= 1024) return launch<T, 128, 1>(p, vec, pl.grid, stream);
+  if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, pl.grid, stream);
+  if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
+  if (p.cols <= kLongestHere) return launch<T, 512, 2>(p, vec, pl.grid, stream);
+  if (p.dx) {
+    const cudaError_t e = launch_1d(along_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  const long long blocks = ceil_div(p.cols, kLongCols), grid = blocks * pl.parts;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_1d(across_kernel<T>, (int)grid, 256, 0, 1, stream, p, (int)blocks, pl.rows_each);
+}
+
+}  // namespace lnb
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int layer_norm_backward_workspace_size(int rows, int cols, size_t *bytes) {
+  if (rows < 0) return -1;
+  if (cols < 1) return -2;
+  if (bytes == nullptr) return 0;
+  *bytes = 0;
+  if (rows == 0) return 0;
+  int sms = 0;
+  if (device_setup(&sms) != cudaSuccess) {
+    (void)cudaGetLastError();
+    sms = 152;  // no device here: the answer for a whole GB300
+  }
+  const lnb::Plan pl = lnb::make_plan(rows, cols, sms);
+  *bytes = lnb::along_bytes(pl, rows) + lnb::part_bytes(pl, cols);
+  return 0;
+}
+
+extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy, const void *x,
+                                   int x_type, int ldx, const float *mean, const float *rstd,
+                                   const void *weight, int w_type, void *dx, int lddx, float *dweight,
+                                   float *dbias, float beta, cudaStream_t stream) {
+  const auto known = [](int t) { return t == LN_F32 || t == LN_BF16 || t == LN_F16; };
+  const auto misplaced = [](const void *q, int t) {
+    return reinterpret_cast<uintptr_t>(q) % (t == LN_F32 ? 4 : 2) != 0;
+  };
+  if (rows < 0) return -1;
+  if (cols < 1) return -2;
+  if (rows > 0 && dy == nullptr) return -3;
+  if (lddy < cols) return -4;
+  if (rows > 0 && x == nullptr) return -5;
+  if (!known(x_type)) return -6;
+  if (misplaced(dy, x_type)) return -3;
+  if (misplaced(x, x_type)) return -5;
+  if (ldx < cols) return -7;
+  if (rows > 0 && mean == nullptr) return -8;
+  if (rows > 0 && rstd == nullptr) return -9;
+  if (!known(w_type)) return -11;
+  if (misplaced(weight, w_type)) return -10;
+  if (misplaced(dx, x_type)) return -12;
+  if (dx != nullptr && lddx < cols) return -13;
+  if (dx == nullptr && dweight == nullptr && dbias == nullptr) return 0;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  if (rows == 0 && (!sums || beta == 1.0f)) return 0;
+  int sms = 0;
+  cudaError_t e = device_setup(&sms);
+  if (e != cudaSuccess) return (int)e;
+  const int blocks = (int)ceil_div(cols, 32);
+  if (rows == 0)
+    return (int)launch_1d(lnb::reduce_kernel, 2 * blocks, 256, 0, 1, stream,
+                          static_cast<const float *>(nullptr), 0, cols, blocks, dweight, dbias, beta);
+  const lnb::Plan pl = lnb::make_plan(rows, cols, sms);
+  const long long size = x_type == LN_F32 ? 4 : 2;
+  lnb::Params p{};
+  p.rows = rows;
+  p.cols = cols;
+  p.dy = static_cast<const char *>(dy);
+  p.lddy = lddy * size;
+  p.x = static_cast<const char *>(x);
+  p.ldx = ldx * size;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.weight = {weight, w_type};
+  p.n = (float)cols;
+  p.dx = static_cast<char *>(dx);
+  p.lddx = lddx * size;
+  p.parts = pl.parts;
+  const size_t along = dx ? lnb::along_bytes(pl, rows) : 0;
+  const size_t bytes = along + (sums ? lnb::part_bytes(pl, cols) : 0);
+  char *ws = nullptr;
+  if (bytes > 0) {
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes, workspace_pool(), stream);
+    if (e != cudaSuccess) return (int)e;
+    p.along = reinterpret_cast<float2 *>(ws);
+    if (sums) p.part = reinterpret_cast<float *>(ws + along);
+  }
+  const auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
+  const bool vec = rows::aligned(at(dy), rows > 1 ? p.lddy : 0) &&
+                   rows::aligned(at(x), rows > 1 ? p.ldx : 0) &&
+                   (dx == nullptr || rows::aligned(at(dx), rows > 1 ? p.lddx : 0));
+  e = x_type == LN_F32    ? lnb::run<rows::F32>(p, pl, vec, sms, stream)
+      : x_type == LN_BF16 ? lnb::run<rows::BF16>(p, pl, vec, sms, stream)
+                          : lnb::run<rows::F16>(p, pl, vec, sms, stream);
+  if (e == cudaSuccess && sums)
+    e = launch_1d(lnb::reduce_kernel, 2 * blocks, 256, 0, 1, stream,
+                  static_cast<const float *>(p.part), pl.parts, cols, blocks, dweight, dbias, beta);
+  if (ws != nullptr) {
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    if (e == cudaSuccess) e = ef;
+  }
+  return (int)e;
+}
+
+extern "C" int layer_norm_backward_with(const layer_norm_backward_args *a) {
+  if (a == nullptr) return -1;
+  return layer_norm_backward(a->rows, a->cols, a->dy, a->lddy, a->x, a->x_type, a->ldx, a->mean, a->rstd,
+                             a->weight, a->w_type, a->dx, a->lddx, a->dweight, a->dbias, a->beta,
+                             a->stream);
+}

@@ -52,6 +52,15 @@ def _rows(name, t):
     return rows, cols, ld or 1
 
 
+def _here(name, t):
+    """The kernels run on the current device: that is where t has to be."""
+    at = t.get_device()
+    if at < 0:
+        raise TypeError(f"{name} must live on a CUDA device")
+    if at != torch.cuda.current_device():
+        raise ValueError(f"{name} is not on the current device")
+
+
 def _quantize(x, block, both, dtype, pow2, stream):
     if stream is not None:
         return _on_stream(stream, lambda: _quantize(x, block, both, dtype, pow2, None), (x,))
