@@ -20,7 +20,7 @@ struct Result {        // D(i, j) = y + beta D(i, j)
   long long ld;
   const float *bias;
   float beta;
-  int pairs;           // a 16-bit type without beta, even channels on 4-byte boundaries
+  int vec;             // no beta, and 16-byte stores to rows are aligned
 };
 
 // Few rows of x (M <= kFewRows), without tensor cores.

@@ -38,6 +38,11 @@ constexpr int P_BYTES = BP * BK;
 constexpr int MAX_CLUSTER = 8;
 constexpr int LARGEST_K = 131071;        // 2^14 K < 2^31
 
+// Results on their way out: a warp's buffer of 16 tokens' numbers of its 32 channels. (A pitch of 36: two
+// neighbouring rows' 16-byte pieces lie in different banks.)
+constexpr int OUT_PITCH = 36;
+constexpr int OUT_BYTES = 16 * OUT_PITCH * 4;
+
 // PAIR: two CTAs share a tile of 256 channels and TN tokens (tcgen05 cta_group::2), each with its 128
 // channels and half of the tokens.
 template <int TN_, bool PAIR_ = false>
@@ -52,7 +57,7 @@ struct Cfg {
   static constexpr int THREADS = 32 * (8 + EPI_WARPS);
   static constexpr int Q_BYTES = QN * BK * (CONVERT ? 1 : 2);
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = CONVERT ? (TN == 64 ? 6 : 9) : 4;
+  static constexpr int STAGES = CONVERT ? (TN == 64 ? 5 : 9) : 4;
   static constexpr int NA = 4;                     // blocks of P in TMEM (and of Q, where converted)
   static constexpr int A_COLS = BK / 2;            // columns of one
   static constexpr int H_BYTES = CONVERT ? QN * BK * 2 : 0;
@@ -65,7 +70,7 @@ struct Cfg {
   static constexpr int ACC_WARPS = PAIR ? 8 : EPI_WARPS;  // readers of an accumulator
   static constexpr int TMEM_COLS = 512;
   static constexpr int BARS = 3 * STAGES + 2 * NA + 2 * PARTS * NBUF;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NA * H_BYTES + 8 * BARS + 16;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NA * H_BYTES + EPI_WARPS * OUT_BYTES + 8 * BARS + 16;
   static_assert(PARTS * NBUF * ACC_COLS + NA * A_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
@@ -93,28 +98,54 @@ struct Channel {
   float scale, bias;
 };
 
-// Of two tokens' sums of this lane's channel: with `pairs` the even lanes store the first token's
-// numbers of their channel and the next one, the odd lanes the second token's.
-__device__ __forceinline__ void store2(const Params &p, const Channel &c, int lane, int token, int s0, int s1) {
-  const bool in = c.at < p.N;
-  const float y0 = token < p.M ? fmaf((float)s0, c.scale * p.x_scale[token], c.bias) : 0.0f;
-  const float y1 = token + 1 < p.M ? fmaf((float)s1, c.scale * p.x_scale[token + 1], c.bias) : 0.0f;
-  if (p.d.pairs) {
-    const bool odd = lane & 1;
-    const float other = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-    const int row = token + odd, col = c.at - odd;
-    if (row < p.M && col < p.N) {
-      const uint32_t v = odd ? tcx::pack_out(p.d.type, other, y1) : tcx::pack_out(p.d.type, y0, other);
-      uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + row * p.d.ld + col;
-      if (col + 1 < p.N)
-        *reinterpret_cast<uint32_t *>(d) = v;
-      else
-        *d = (uint16_t)v;
+// Sums of this lane's channel and `count` (16 or 2) neighbouring tokens, finished and stored. What is not
+// unrolled over the sums is not unrolled at all: the epilogue shares the instruction caches with the
+// converters (all inlined and unrolled it took half of their time).
+template <int COUNT>
+__device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, float *buf, int lane, int token,
+                                             const int (&sums)[COUNT]) {
+  const int rows = min(COUNT, p.M - token);
+  const float *sx = p.x_scale + token;
+#pragma unroll
+  for (int j = 0; j < COUNT; ++j)
+    buf[j * OUT_PITCH + lane] = fmaf((float)sums[j], c.scale * (j < rows ? sx[j] : 0.0f), c.bias);
+  __syncwarp();
+  const int col0 = c.at - lane;
+  if (p.d.vec && COUNT == 16 && p.d.type != tcx::OUT_F32) {
+    const int col = (lane & 3) * 8, cols = min(8, p.N - col0 - col);
+#pragma unroll 1
+    for (int r = lane >> 2; r < rows; r += 8) {
+      const float *v = buf + r * OUT_PITCH + col;
+      uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + (token + r) * p.d.ld + col0 + col;
+      if (cols == 8) {
+        const float4 x = *reinterpret_cast<const float4 *>(v), y = *reinterpret_cast<const float4 *>(v + 4);
+        *reinterpret_cast<uint4 *>(d) =
+            make_uint4(tcx::pack_out(p.d.type, x.x, x.y), tcx::pack_out(p.d.type, x.z, x.w),
+                       tcx::pack_out(p.d.type, y.x, y.y), tcx::pack_out(p.d.type, y.z, y.w));
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < cols; ++j) tcx::store_out(d, p.d.type, j, v[j]);
+      }
     }
-    return;
+  } else if (p.d.vec && COUNT == 16) {
+    const int col = (lane & 7) * 4, cols = min(4, p.N - col0 - col);
+#pragma unroll 1
+    for (int r = lane >> 3; r < rows; r += 4) {
+      const float *v = buf + r * OUT_PITCH + col;
+      float *d = static_cast<float *>(p.d.ptr) + (token + r) * p.d.ld + col0 + col;
+      if (cols == 4) {
+        *reinterpret_cast<float4 *>(d) = *reinterpret_cast<const float4 *>(v);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < cols; ++j) d[j] = v[j];
+      }
+    }
+  } else if (c.at < p.N) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+      tcx::finish_out(p.d.ptr, p.d.type, (token + r) * p.d.ld + c.at, buf[r * OUT_PITCH + lane], p.d.beta);
   }
-  if (in && token < p.M) tcx::finish_out(p.d.ptr, p.d.type, token * p.d.ld + c.at, y0, p.d.beta);
-  if (in && token + 1 < p.M) tcx::finish_out(p.d.ptr, p.d.type, (token + 1) * p.d.ld + c.at, y1, p.d.beta);
+  __syncwarp();
 }
 
 __device__ __forceinline__ Channel channel_at(const Params &p, int at) {
@@ -140,7 +171,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);
   const uint32_t halves_at = base + C::STAGES * C::STAGE_BYTES;  // Q in FP16, where it is converted
-  const uint32_t p_full = halves_at + C::NA * C::H_BYTES;
+  const uint32_t out_at = halves_at + C::NA * C::H_BYTES;        // (the epilogue's buffers)
+  const uint32_t p_full = out_at + C::EPI_WARPS * OUT_BYTES;
   const uint32_t q_full = p_full + 8 * C::STAGES, empty = q_full + 8 * C::STAGES;
   const uint32_t a_full = empty + 8 * C::STAGES, a_empty = a_full + 8 * C::NA;
   const uint32_t acc_full = a_empty + 8 * C::NA, acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
@@ -337,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         }
         fence_after();
         const uint8_t *stage = sbase + st.slot * C::STAGE_BYTES;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {  // 64 of k: 32 columns
           uint32_t v[32];
 #pragma unroll
@@ -392,6 +424,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + which0 * C::ACC_COLS +
                                (PAIR ? 0 : (uint32_t)(grp * C::COLS));
     const uint32_t full0 = acc_full + 8 * which0, empty0 = acc_empty + 8 * which0;
+    float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - 8) * OUT_BYTES);
     Ring<C::NBUF> buf;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
@@ -433,9 +466,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       if (S == 1) {
         const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 2) {
+        for (int c = 0; c < C::COLS; c += 16) {
           const int token = tq * TN + (PAIR ? (c / 64) * 128 + grp * 64 + c % 64 : grp * C::COLS + c);
-          store2(p, ch, lane, token, acc[c], acc[c + 1]);
+          int sums[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sums[j] = acc[c + j];
+          if (token < p.M) store_tokens<16>(p, ch, out, lane, token, sums);
         }
       } else {
         // partial tile -> the ring, whose every reader has finished (the last accumulator is
@@ -467,14 +503,15 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             for (int j = 0; j < 2; ++j)
               v[j][q] = ld_cluster_int(base + (uint32_t)((c + j) * BP + quad * 32 + lane) * 4, (uint32_t)q);
           }
-        int s0 = v[0][0], s1 = v[1][0];
+        int sums[2] = {v[0][0], v[1][0]};
 #pragma unroll
         for (int q = 1; q < MAX_CLUSTER; ++q)
-          if (q < S) s0 += v[0][q], s1 += v[1][q];
+          if (q < S) sums[0] += v[0][q], sums[1] += v[1][q];
         // (both are used whatever is stored: a load that nothing waits for could still be under way
         // when the other CTA leaves)
-        asm volatile("" ::"r"(s0), "r"(s1));
-        store2(p, ch, lane, tq * TN + c, s0, s1);
+        asm volatile("" ::"r"(sums[0]), "r"(sums[1]));
+        float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - 8) * OUT_BYTES);
+        store_tokens<2>(p, ch, out, lane, tq * TN + c, sums);
       }
     }
     __syncwarp();
@@ -656,9 +693,8 @@ extern "C" int i8_linear(int M, int N, int K, const void *x, int ldx, const floa
   cudaError_t e = device_setup(&sms);
   if (e == cudaSuccess) e = i8::kernel_setup();
   if (e != cudaSuccess) return (int)e;
-  const bool pairs = d_type != I8_F32 && beta == 0.0f && reinterpret_cast<uintptr_t>(D) % 4 == 0 &&
-                     (M == 1 || ldd % 2 == 0);
-  const i8::Result d{D, d_type, ldd, bias, beta, pairs};
+  const bool vec = beta == 0.0f && !bad_ptr(D) && (M == 1 || (long long)ldd * (d_type == I8_F32 ? 4 : 2) % 16 == 0);
+  const i8::Result d{D, d_type, ldd, bias, beta, vec};
   if (K == 0) {
     const long long blocks = std::min<long long>(ceil_div((long long)M * N, 256), 8LL * sms);
     return (int)launch_1d(i8::i8_bias_kernel, (int)blocks, 256, 0, 1, stream, M, N, d);
