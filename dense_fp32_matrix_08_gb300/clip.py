@@ -2,27 +2,34 @@
 from __future__ import annotations
 
 from array import array
+from operator import attrgetter
 
 import torch
 
 from . import GC_EXPORTED, SgemmError, _on_stream, _stream, lib
-from .f8 import _TYPE, _here
+from .f8 import _TYPE
 
 __all__ = ["clip_grad_norm", "GC_EXPORTED"]
 
 
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
 def _lists(name, tensors):
-    """(addresses, types, sizes) of contiguous CUDA tensors, as arrays."""
-    for t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        _here(name, t)
+    """(addresses, types, sizes) of contiguous tensors on the current device, as arrays. (There may be
+    hundreds of them: one pass of a built-in per question.)"""
+    where = set(map(_get_device, tensors))  # (a TypeError for what is no tensor)
     try:
-        types = array("i", [_TYPE[t.dtype] for t in tensors])
+        types = array("i", [_TYPE[d] for d in map(_dtype, tensors)])
     except KeyError:
         raise TypeError(f"{name} must be float32, bfloat16 or float16") from None
+    if -1 in where:
+        raise TypeError(f"{name} must live on a CUDA device")
+    if where and where != {torch.cuda.current_device()}:
+        raise ValueError(f"{name} must be on the current device")
+    if not all(map(_is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
     return (array("Q", map(torch.Tensor.data_ptr, tensors)), types,
             array("q", map(torch.Tensor.numel, tensors)))
 
@@ -44,9 +51,9 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, stream=None):
     at, types, sizes = _lists("grads", grads)
     to, to_types = at, types
     if out is not None:
-        if [t.shape for t in out] != [t.shape for t in grads]:
-            raise ValueError("shape mismatch")
         to, to_types, _ = _lists("out", out)
+        if list(map(_shape, out)) != list(map(_shape, grads)):
+            raise ValueError("shape mismatch")
     scale = out is not None or max_norm != float("inf")
     norm = torch.empty((), dtype=torch.float32, device="cuda")
     rc = lib.clip_grad_norm(

@@ -23,8 +23,9 @@ struct Result {        // D(i, j) = y + beta D(i, j)
   int vec;             // no beta, and 16-byte stores to rows are aligned
 };
 
-// Few rows of x (M <= kFewRows), without tensor cores.
-constexpr int kFewRows = 8;
+// Few rows of x (M <= kFewRows).
+constexpr int kFewRows = 32;
+cudaError_t few_setup();  // kernel attributes for the current device
 cudaError_t launch_few(int M, int N, int K, const Operand &x, const Operand &w, const Result &d, int sms,
                        cudaStream_t stream);
 

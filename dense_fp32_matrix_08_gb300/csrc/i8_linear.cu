@@ -607,6 +607,7 @@ static cudaError_t kernel_setup() {
     if (err == cudaSuccess) err = set_attributes<64>();
     if (err == cudaSuccess) err = set_attributes<32>();
     if (err == cudaSuccess) err = set_attributes<16>();
+    if (err == cudaSuccess) err = few_setup();
     g_err[dev] = err;
   });
   return g_err[dev];

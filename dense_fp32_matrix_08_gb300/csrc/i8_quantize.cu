@@ -80,28 +80,27 @@ __device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uin
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+template <class T>
+constexpr int kDepth = T::SIZE == 4 ? 3 : 4;  // rows under way: 64 to 96 KB per SM
+
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) quantize_kernel(const Params p) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / TPR) quantize_kernel(const Params p) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ uint32_t part[2][32];
-  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
-  int n[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
-  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Chunk<T> next[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) sh.load(p.x + row * p.ldx, c, row < p.rows ? n[c] : 0, next[c]);
+  Ahead<T, TPR, CH, VEC, 1, kDepth<T>> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
+  const auto &sh = ahead.sh;
+  const auto &n = ahead.n;
+  using S = Share<T, TPR, VEC>;
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  ahead.begin();
   for (int turn = 0; base < p.rows; base += step, row += step, turn ^= 1) {
-    Chunk<T> v[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) v[c] = next[c];
-    const long long ahead = row + step;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) sh.load(p.x + ahead * p.ldx, c, ahead < p.rows ? n[c] : 0, next[c]);
+    Chunk<T> in[1][CH];
+    ahead.take(in);
+    const Chunk<T>(&v)[CH] = in[0];
     uint32_t m = v[0].w[0];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -117,8 +116,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) quantize_kernel(const P
 #pragma unroll
         for (int j = 0; j < 8; ++j) q[j] = s.finite ? rounded(v[c][j], s) : 0;
         if (VEC && p.vec_q && n[c] == 8) {
-          *reinterpret_cast<uint2 *>(to + sh.col(c, 0)) =
-              make_uint2(four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7]));
+          const uint32_t lo = four(q[0], q[1], q[2], q[3]), hi = four(q[4], q[5], q[6], q[7]);
+          if constexpr (S::E == 8) {
+            *reinterpret_cast<uint2 *>(to + sh.col(c, 0)) = make_uint2(lo, hi);
+          } else {
+            *reinterpret_cast<uint32_t *>(to + sh.col(c, 0)) = lo;
+            *reinterpret_cast<uint32_t *>(to + sh.col(c, 4)) = hi;
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -152,13 +156,19 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
   griddep_launch_dependents();
 }
 
+template <class T, int TPR, int CH, bool VEC>
+static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T>>::BYTES;
+  static cudaError_t set[kDevices];
+  static std::once_flag once[kDevices];
+  const cudaError_t e = allow_bytes(quantize_kernel<T, TPR, CH, VEC>, bytes, once, set);
+  if (e != cudaSuccess) return e;
+  const long long grid = std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * (1024 / threads));
+  return launch_1d(quantize_kernel<T, TPR, CH, VEC>, (int)grid, threads, bytes, 1, stream, p);
+}
 template <class T, int TPR, int CH>
 static cudaError_t launch(const Params &p, bool vec, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
-  const long long grid =
-      std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * std::max(1, 2048 / threads));
-  return vec ? launch_1d(quantize_kernel<T, TPR, CH, true>, (int)grid, threads, 0, 1, stream, p)
-             : launch_1d(quantize_kernel<T, TPR, CH, false>, (int)grid, threads, 0, 1, stream, p);
+  return vec ? launch<T, TPR, CH, true>(p, sms, stream) : launch<T, TPR, CH, false>(p, sms, stream);
 }
 
 template <class T>

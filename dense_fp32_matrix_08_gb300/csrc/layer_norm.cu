@@ -20,80 +20,90 @@ struct Params {
   const char *x;
   long long ldx;       // bytes
   Vector weight, bias;
-  float eps, n;        // n = cols
+  float eps, n, r;     // n = cols, r = 1 / n
   char *y;
   long long ldy;       // bytes
   float *mean, *rstd;
 };
 
-// TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn, the next one's
-// loads under way while this one is computed. The parameters of a thread's columns stay in its
-// registers, but for the longest rows, which have too many threads for that.
+// CTAs of norm_kernel per SM: 768 threads with 80 registers each, or 64 registers for the longest rows.
+constexpr int per_sm(int tpr) { return tpr < 128 ? 6 : tpr <= 256 ? 768 / tpr : 1; }
+// Rows under way: about 64 KB per SM.
+template <class T, int TPR>
+constexpr int kDepth = (TPR == 512 ? 5 : 4) - (T::SIZE == 4);
+
+// TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn. The parameters of a
+// thread's columns stay in its registers, but for the longest rows, which have too many threads for that.
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel(const Params p) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kernel(const Params p) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
   constexpr bool HOLD = TPR < 1024;
-  __shared__ float2 part[2][32];
-  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
-  int n[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
-  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) RowSums<TPR, 1> sums;
   const long long step = (long long)gridDim.x * RPB;
-  long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
-  Chunk<T> next[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) sh.load(p.x + row * p.ldx, c, row < p.rows ? n[c] : 0, next[c]);
-  float w[HOLD ? CH : 1][8], b[HOLD ? CH : 1][8];
+  long long row = base + threadIdx.x / TPR;
+  Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
+  const auto &sh = ahead.sh;
+  const auto &n = ahead.n;
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  ahead.begin();
+  Two w[HOLD ? CH : 1][4], b[HOLD ? CH : 1][4];
   if constexpr (HOLD) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[c][j] = j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
-        b[c][j] = j < n[c] ? p.bias.at(sh.col(c, j), 0.0f) : 0.0f;
-      }
+    for (int c = 0; c < CH; ++c) {
+      parameters(p.weight, sh, c, n[c], 1.0f, w[c]);
+      parameters(p.bias, sh, c, n[c], 0.0f, b[c]);
+    }
   }
-  for (; base < p.rows; base += step, row += step) {
-    Chunk<T> v[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) v[c] = next[c];
-    const long long ahead = row + step;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) sh.load(p.x + ahead * p.ldx, c, ahead < p.rows ? n[c] : 0, next[c]);
-    float sum = 0.0f, squares = 0.0f;
+  char *to = p.y + row * p.ldy;
+  for (; base < p.rows; base += step, row += step, to += step * p.ldy) {
+    Chunk<T> in[1][CH];
+    ahead.take(in);
+    Two d[CH][4], total = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += v[c][j];
-    const float mean = row_sum<TPR>(make_float2(sum, 0.0f), part, 0).x / p.n;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = j < n[c] ? v[c][j] - mean : 0.0f;
-        squares = fmaf(d, d, squares);
+      for (int i = 0; i < 4; ++i) {
+        d[c][i] = pair(in[0][c], i);
+        total = add2(total, d[c][i]);
       }
-    const float var = row_sum<TPR>(make_float2(squares, 0.0f), part, 1).x / p.n;
-    const float rstd = __frsqrt_rn(var + p.eps);
+    float s[1] = {sum2(total)};
+    row_sum<TPR>(s, sums, 0);
+    const float mean = over(s[0], p.n, p.r);
+    const Two minus = both(-mean);
+    total = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[c][i] = add2(d[c][i], minus);
+        if (!ahead.whole) d[c][i] = first(d[c][i], i, n[c]);
+        total = fma2(d[c][i], d[c][i], total);
+      }
+    s[0] = sum2(total);
+    row_sum<TPR>(s, sums, 1);
+    // 1 / sqrt, with one step of Newton's iteration
+    const float v = over(s[0], p.n, p.r) + p.eps;
+    float rstd = rsqrtf(v);
+    rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
     if (row < p.rows) {
       if (sh.t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
       }
+      const Two r2 = both(rstd);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wj = HOLD ? w[HOLD ? c : 0][j] : j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
-          const float bj = HOLD ? b[HOLD ? c : 0][j] : j < n[c] ? p.bias.at(sh.col(c, j), 0.0f) : 0.0f;
-          y[j] = fmaf((v[c][j] - mean) * rstd, wj, bj);
+        if constexpr (!HOLD) {
+          parameters(p.weight, sh, c, n[c], 1.0f, w[0]);
+          parameters(p.bias, sh, c, n[c], 0.0f, b[0]);
         }
         Chunk<T> out;
-        pack<T>(y, out);
-        sh.store(p.y + row * p.ldy, c, n[c], out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          set_pair(out, i, fma2(mul2(d[c][i], r2), w[HOLD ? c : 0][i], b[HOLD ? c : 0][i]));
+        sh.store(to, c, n[c], out);
       }
     }
   }
@@ -155,14 +165,19 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
   griddep_launch_dependents();
 }
 
+template <class T, int TPR, int CH, bool VEC>
+static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>>::BYTES;
+  static cudaError_t set[kDevices];
+  static std::once_flag once[kDevices];
+  const cudaError_t e = allow_bytes(norm_kernel<T, TPR, CH, VEC>, bytes, once, set);
+  if (e != cudaSuccess) return e;
+  const long long grid = std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * per_sm(TPR));
+  return launch_1d(norm_kernel<T, TPR, CH, VEC>, (int)grid, threads, bytes, 1, stream, p);
+}
 template <class T, int TPR, int CH>
 static cudaError_t launch(const Params &p, bool vec, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
-  // 2048 threads per SM at most, and at least one row for each CTA
-  const long long grid =
-      std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * std::max(1, 1024 / threads));
-  return vec ? launch_1d(norm_kernel<T, TPR, CH, true>, (int)grid, threads, 0, 1, stream, p)
-             : launch_1d(norm_kernel<T, TPR, CH, false>, (int)grid, threads, 0, 1, stream, p);
+  return vec ? launch<T, TPR, CH, true>(p, sms, stream) : launch<T, TPR, CH, false>(p, sms, stream);
 }
 
 template <class T>
@@ -213,10 +228,11 @@ extern "C" int layer_norm(int rows, int cols, const void *x, int x_type, int ldx
   p.cols = cols;
   p.x = static_cast<const char *>(x);
   p.ldx = ldx * size;
-  p.weight = {weight, w_type};
-  p.bias = {bias, w_type};
+  p.weight = {weight, w_type, reinterpret_cast<uintptr_t>(weight) % 16 == 0};
+  p.bias = {bias, w_type, reinterpret_cast<uintptr_t>(bias) % 16 == 0};
   p.eps = eps;
   p.n = (float)cols;
+  p.r = 1.0f / p.n;
   p.y = static_cast<char *>(y);
   p.ldy = ldy * size;
   p.mean = mean;

@@ -26,7 +26,7 @@ struct Params {
   long long lddy, ldx;      // bytes
   const float *mean, *rstd;
   Vector weight;
-  float n;                  // cols
+  float n, r;               // cols, 1 / cols
   char *dx;
   long long lddx;           // bytes
   float *part;              // sums of dw, then of db: [2][parts][cols]; NULL: neither is wanted
@@ -34,90 +34,127 @@ struct Params {
   float2 *along;            // rows that do not stay in registers: sum g / n, sum (g h) / n
 };
 
+// CTAs of backward_kernel per SM: 512 threads with up to 128 registers. Rows under way: 64 to 96 KB per SM.
+constexpr int per_sm(int tpr) { return tpr < 128 ? 4 : 512 / tpr; }
+template <class T>
+constexpr int kDepth = T::SIZE == 4 ? 3 : 4;
+
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR <= 256 ? 512 / (TPR < 128 ? 128 : TPR) : 1)
-    backward_kernel(const Params p) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) backward_kernel(const Params p) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
-  __shared__ float2 part[2][32];
-  const Share<TPR, VEC> sh{p.cols, (int)(threadIdx.x % TPR)};
-  int n[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) n[c] = sh.count(c);
-  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) RowSums<TPR, 2> sums;
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  const long long mine = row;
-  Chunk<T> next_x[CH], next_d[CH];
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  const auto load = [&](long long r) {
-    const bool in = r < p.rows;
+  Ahead<T, TPR, CH, VEC, 2, kDepth<T>> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row, step);
+  const auto &sh = ahead.sh;
+  const auto &n = ahead.n;
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
+  ahead.begin();
+  float next_mean = row < p.rows ? p.mean[row] : 0.0f, next_rstd = row < p.rows ? p.rstd[row] : 0.0f;
+  Two w[CH][4], dw[CH][4], db[CH][4];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      sh.load(p.x + r * p.ldx, c, in ? n[c] : 0, next_x[c]);
-      sh.load(p.dy + r * p.lddy, c, in ? n[c] : 0, next_d[c]);
-    }
-    next_mean = in ? p.mean[r] : 0.0f;
-    next_rstd = in ? p.rstd[r] : 0.0f;
-  };
-  load(row);
-  float w[CH][8], dw[CH][8], db[CH][8];
+  for (int c = 0; c < CH; ++c) {
+    parameters(p.weight, sh, c, n[c], 1.0f, w[c]);
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[c][j] = j < n[c] ? p.weight.at(sh.col(c, j), 1.0f) : 0.0f;
-      dw[c][j] = db[c][j] = 0.0f;
-    }
+    for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = 0;
+  }
+  char *to = p.dx + row * p.lddx;
   int turn = 0;
-  for (; base < p.rows; base += step, row += step, turn ^= 1) {
-    Chunk<T> vx[CH], vd[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) vx[c] = next_x[c], vd[c] = next_d[c];
+  for (; base < p.rows; base += step, row += step, to += step * p.lddx, turn ^= 1) {
+    Chunk<T> v[2][CH];
+    ahead.take(v);
     const float mean = next_mean, rstd = next_rstd;
-    load(row + step);
-    float2 s = make_float2(0.0f, 0.0f);
+    next_mean = row + step < p.rows ? p.mean[row + step] : 0.0f;
+    next_rstd = row + step < p.rows ? p.rstd[row + step] : 0.0f;
+    const bool in = row < p.rows;
+    const Two minus = both(-mean), r2 = both(rstd);
+    float s[2] = {0.0f, 0.0f};
+    if (in) {
+      Two sg = 0, sh2 = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // (elements that do not exist have dy = 0, so they add nothing where rstd and mean are finite,
-        // and where those are not the row is NaN anyway; rows that do not exist have rstd = 0)
-        const float d = vd[c][j], h = (vx[c][j] - mean) * rstd, g = d * w[c][j];
-        dw[c][j] = fmaf(d, h, dw[c][j]);
-        db[c][j] += d;
-        s.x += g;
-        s.y = fmaf(g, h, s.y);
-      }
+        for (int i = 0; i < 4; ++i) {
+          // (elements that do not exist have dy = 0, so they add nothing where rstd and mean are finite,
+          // and where those are not the row is NaN anyway)
+          const Two d = pair(v[1][c], i), h = mul2(add2(pair(v[0][c], i), minus), r2), g = mul2(d, w[c][i]);
+          dw[c][i] = fma2(d, h, dw[c][i]);
+          db[c][i] = add2(db[c][i], d);
+          sg = add2(sg, g);
+          sh2 = fma2(g, h, sh2);
+        }
+      s[0] = sum2(sg);
+      s[1] = sum2(sh2);
+    }
     if (p.dx == nullptr) continue;
-    s = row_sum<TPR>(s, part, turn);
-    s.x /= p.n;
-    s.y /= p.n;
-    if (row < p.rows) {
+    row_sum<TPR>(s, sums, turn);
+    if (in) {
+      const Two s1 = both(-over(s[0], p.n, p.r)), s2 = both(-over(s[1], p.n, p.r));
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float h = (vx[c][j] - mean) * rstd;
-          y[j] = (fmaf(vd[c][j], w[c][j], -s.x) - h * s.y) * rstd;
-        }
         Chunk<T> out;
-        pack<T>(y, out);
-        sh.store(p.dx + row * p.lddx, c, n[c], out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const Two h = mul2(add2(pair(v[0][c], i), minus), r2);
+          set_pair(out, i, mul2(fma2(h, s2, fma2(pair(v[1][c], i), w[c][i], s1)), r2));
+        }
+        sh.store(to, c, n[c], out);
       }
     }
   }
   if (p.part) {
-    float *to = p.part + mine * p.cols, *tb = to + (long long)p.parts * p.cols;
+    // the rows of a CTA that several threads had for one column, then one sum of each column
+    float f[CH][8], g[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n[c]) {
-          to[sh.col(c, j)] = dw[c][j];
-          tb[sh.col(c, j)] = db[c][j];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = unpack2(dw[c][i]), e = unpack2(db[c][i]);
+        f[c][2 * i] = a.x, f[c][2 * i + 1] = a.y, g[c][2 * i] = e.x, g[c][2 * i + 1] = e.y;
+      }
+    if constexpr (TPR < 32) {
+#pragma unroll
+      for (int d = TPR; d < 32; d *= 2)
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            f[c][j] += __shfl_xor_sync(0xffffffffu, f[c][j], d);
+            g[c][j] += __shfl_xor_sync(0xffffffffu, g[c][j], d);
+          }
+    }
+    float *out = p.part + (long long)blockIdx.x * p.cols, *tb = out + (long long)p.parts * p.cols;
+    if constexpr (TPR < 128) {
+      constexpr int WARPS = THREADS / 32, LANES = TPR < 32 ? TPR : 32;
+      __shared__ float meet[WARPS][2][CH * 8][LANES];
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (lane < LANES) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) meet[warp][0][c * 8 + j][lane] = f[c][j], meet[warp][1][c * 8 + j][lane] = g[c][j];
+      }
+      __syncthreads();
+      if (threadIdx.x < LANES) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float a = 0.0f, e = 0.0f;
+#pragma unroll
+            for (int q = 0; q < WARPS; ++q) a += meet[q][0][c * 8 + j][lane], e += meet[q][1][c * 8 + j][lane];
+            if (j < n[c]) out[sh.col(c, j)] = a, tb[sh.col(c, j)] = e;
+          }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n[c]) out[sh.col(c, j)] = f[c][j], tb[sh.col(c, j)] = g[c][j];
+    }
   }
   griddep_launch_dependents();
 }
@@ -256,9 +293,9 @@ static Plan make_plan(int rows, int cols, int sms) {
   if (pl.tpr) {
     const int threads = std::max(128, pl.tpr), rpb = threads / pl.tpr;
     const long long most = ceil_div(rows, rpb);
-    const long long fill = (long long)sms * std::max(1, 512 / threads);
+    const long long fill = (long long)sms * per_sm(pl.tpr);
     pl.grid = (int)std::min<long long>(most, std::max<long long>(fill, ceil_div(most, kMostRows)));
-    pl.parts = pl.grid * rpb;
+    pl.parts = pl.grid;
   } else {
     const long long blocks = ceil_div(cols, kLongCols);
     pl.rows_each = (int)std::max<long long>(1, std::min<long long>(kMostRows, rows * blocks / (8LL * sms)));
@@ -273,11 +310,17 @@ static size_t along_bytes(const Plan &pl, int rows) {
 }
 static size_t part_bytes(const Plan &pl, int cols) { return (size_t)2 * pl.parts * cols * sizeof(float); }
 
+template <class T, int TPR, int CH, bool VEC>
+static cudaError_t launch(const Params &p, int grid, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR, bytes = Ahead<T, TPR, CH, VEC, 2, kDepth<T>>::BYTES;
+  static cudaError_t set[kDevices];
+  static std::once_flag once[kDevices];
+  const cudaError_t e = allow_bytes(backward_kernel<T, TPR, CH, VEC>, bytes, once, set);
+  return e != cudaSuccess ? e : launch_1d(backward_kernel<T, TPR, CH, VEC>, grid, threads, bytes, 1, stream, p);
+}
 template <class T, int TPR, int CH>
 static cudaError_t launch(const Params &p, bool vec, int grid, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR;
-  return vec ? launch_1d(backward_kernel<T, TPR, CH, true>, grid, threads, 0, 1, stream, p)
-             : launch_1d(backward_kernel<T, TPR, CH, false>, grid, threads, 0, 1, stream, p);
+  return vec ? launch<T, TPR, CH, true>(p, grid, stream) : launch<T, TPR, CH, false>(p, grid, stream);
 }
 
 template <class T>
@@ -363,8 +406,9 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   p.ldx = ldx * size;
   p.mean = mean;
   p.rstd = rstd;
-  p.weight = {weight, w_type};
+  p.weight = {weight, w_type, reinterpret_cast<uintptr_t>(weight) % 16 == 0};
   p.n = (float)cols;
+  p.r = 1.0f / p.n;
   p.dx = static_cast<char *>(dx);
   p.lddx = lddx * size;
   p.parts = pl.parts;

@@ -52,13 +52,15 @@ def _rows(name, t):
     return rows, cols, ld or 1
 
 
-def _here(name, t):
-    """The kernels run on the current device: that is where t has to be."""
+def _stream_here(name, t):
+    """(device index, handle of the current stream) for a launch on t: the kernels run on the current
+    device, and that is where t has to be."""
     at = t.get_device()
     if at < 0:
         raise TypeError(f"{name} must live on a CUDA device")
-    if at != torch.cuda.current_device():
+    if at != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is not on the current device")
+    return at, torch._C._cuda_getCurrentRawStream(at)
 
 
 def _quantize(x, block, both, dtype, pow2, stream):

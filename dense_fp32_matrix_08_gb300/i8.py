@@ -12,8 +12,8 @@ import struct
 
 import torch
 
-from . import I8_EXPORTED, SgemmError, _on_stream, _stream, lib
-from .f8 import _TYPE, _here, _rows
+from . import I8_EXPORTED, SgemmError, _on_stream, lib
+from .f8 import _TYPE, _rows, _stream_here
 
 __all__ = ["i8_quantize", "i8_linear", "i8_linear_plan", "i8_linear_status", "I8_EXPORTED"]
 
@@ -33,14 +33,14 @@ def i8_quantize(x, *, stream=None):
     if kind is None:
         raise TypeError("x must be float32, bfloat16 or float16")
     rows, cols, ldx = _rows("x", x)
-    _here("x", x)
+    _, handle = _stream_here("x", x)
     device = x.device
     # rows of a multiple of 16 bytes, as the product's copies need them
     ldq = (cols + 15) // 16 * 16 or 1
     q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.int8, device=device)
     scale = torch.empty(rows, dtype=torch.float32, device=device)
     rc = lib.i8_quantize_with(_quantize_args(rows, cols, x.data_ptr(), kind, ldx, q.data_ptr(), ldq,
-                                             scale.data_ptr(), _stream(None) or 0))
+                                             scale.data_ptr(), handle))
     if rc != 0:
         raise SgemmError(rc, "i8_quantize")
     return q, scale
@@ -53,9 +53,9 @@ def _operand(name, q, scale):
     rows, cols, ld = _rows(name, q)
     if rows <= 1 or cols == 0:  # (nothing is read from row to row)
         ld = (ld + 15) // 16 * 16
-    if scale.dtype is not torch.float32 or not scale.is_cuda:
+    if scale.dtype is not torch.float32:
         raise TypeError(f"{name}'s scale must be a float32 CUDA tensor")
-    if scale.dim() != 1 or scale.shape[0] != rows or not scale.is_contiguous():
+    if scale.shape != (rows,) or not scale.is_contiguous():
         raise ValueError(f"{name}'s scale must be a contiguous vector with one entry for each row")
     return rows, cols, ld
 
@@ -74,21 +74,20 @@ def i8_linear(x, x_scale, w, w_scale, bias=None, *, beta=0.0, out=None, out_dtyp
     N, K2, ldw = _operand("w", w, w_scale)
     if K2 != K:
         raise ValueError("shape mismatch")
-    _here("x", x)
-    device = x.device
+    at, handle = _stream_here("x", x)
     bp = 0
     if bias is not None:
         if bias.dtype is not torch.float32:
             raise TypeError("bias must be float32")
-        if bias.dim() != 1 or bias.shape[0] != N or not bias.is_contiguous():
+        if bias.shape != (N,) or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous vector of {N} elements")
-        if bias.device != device:
+        if bias.get_device() != at:
             raise ValueError("bias is on another device")
         bp = bias.data_ptr()
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs an out to scale")
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=device)
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=x.device)
         ldd = N or 1
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -99,11 +98,11 @@ def i8_linear(x, x_scale, w, w_scale, bias=None, *, beta=0.0, out=None, out_dtyp
     kind = _TYPE.get(out.dtype)
     if kind is None:
         raise TypeError("out must be float32, bfloat16 or float16")
-    if not (device == w.device == out.device == x_scale.device == w_scale.device):
+    if not (at == w.get_device() == out.get_device() == x_scale.get_device() == w_scale.get_device()):
         raise ValueError("operands, scales and out must be on one device")
     rc = lib.i8_linear_with(_linear_args(
         M, N, K, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), bp, beta,
-        out.data_ptr(), kind, ldd, _stream(None) or 0))
+        out.data_ptr(), kind, ldd, handle))
     if rc != 0:
         raise SgemmError(rc, "i8_linear")
     return out

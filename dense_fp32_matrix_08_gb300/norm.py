@@ -6,8 +6,8 @@ import struct
 
 import torch
 
-from . import LN_EXPORTED, SgemmError, _on_stream, _stream, lib
-from .f8 import _TYPE, _here, _rows
+from . import LN_EXPORTED, SgemmError, _on_stream, lib
+from .f8 import _TYPE, _rows, _stream_here
 
 __all__ = ["layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size", "LN_EXPORTED"]
 
@@ -16,27 +16,24 @@ _forward_args = struct.Struct("@iiPiiPPifPiPPP").pack
 _backward_args = struct.Struct("@iiPiPiiPPPiPiPPfP").pack
 
 
-def _vector(name, t, n, device):
-    """The address and type of a vector of n parameters; (0, 0) for None."""
-    if t is None:
-        return 0, 0
+def _vector(name, t, n, at):
+    """The address and type of a vector of n parameters on device `at`."""
     kind = _TYPE.get(t.dtype)
     if kind is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
-    if t.device != device:
+    if t.get_device() != at:
         raise ValueError(f"{name} is on another device")
     return t.data_ptr(), kind
 
 
-def _numbers(name, t, n, device):
-    """The address of n FP32 numbers; 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is not torch.float32:
+def _numbers(name, t, n, at):
+    """The address of n FP32 numbers on device `at`."""
+    address, kind = _vector(name, t, n, at)
+    if kind != 0:
         raise TypeError(f"{name} must be float32")
-    return _vector(name, t, n, device)[0]
+    return address
 
 
 def _like(name, t, x):
@@ -45,21 +42,20 @@ def _like(name, t, x):
         raise TypeError(f"{name} has another type than x")
     if t.shape != x.shape:
         raise ValueError("shape mismatch")
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError(f"{name} is on another device")
     return _rows(name, t)[2]
 
 
 def _matrix(x):
-    """(type, rows, columns, row stride) of x."""
+    """(type, rows, columns, row stride, device index, stream) of x."""
     kind = _TYPE.get(x.dtype)
     if kind is None:
         raise TypeError("x must be float32, bfloat16 or float16")
     rows, cols, ld = _rows("x", x)
     if cols < 1:
         raise ValueError("rows must have elements")
-    _here("x", x)
-    return kind, rows, cols, ld
+    return kind, rows, cols, ld, *_stream_here("x", x)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, stats=False, out=None, stream=None):
@@ -72,24 +68,26 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, stats=False, out=None, st
     if stream is not None:
         return _on_stream(stream, lambda: layer_norm(x, weight, bias, eps=eps, stats=stats, out=out),
                           [t for t in (x, weight, bias, out) if t is not None])
-    kind, rows, cols, ldx = _matrix(x)
-    device = x.device
-    wp, wt = _vector("weight", weight, cols, device)
-    bp, bt = _vector("bias", bias, cols, device)
-    if wp and bp and wt != bt:
-        raise TypeError("weight and bias must have one type")
+    kind, rows, cols, ldx, at, handle = _matrix(x)
+    wp = bp = wt = mp = rp = 0
+    if weight is not None:
+        wp, wt = _vector("weight", weight, cols, at)
+    if bias is not None:
+        bp, bt = _vector("bias", bias, cols, at)
+        if weight is not None and wt != bt:
+            raise TypeError("weight and bias must have one type")
+        wt = bt
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
         ldy = cols
     else:
         ldy = _like("out", out, x)
-    mean = rstd = None
     if stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=device)
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-    rc = lib.layer_norm_with(_forward_args(
-        rows, cols, x.data_ptr(), kind, ldx, wp, bp, wt if wp else bt, eps, out.data_ptr(), ldy,
-        mean.data_ptr() if stats else 0, rstd.data_ptr() if stats else 0, _stream(None) or 0))
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    rc = lib.layer_norm_with(_forward_args(rows, cols, x.data_ptr(), kind, ldx, wp, bp, wt, eps,
+                                           out.data_ptr(), ldy, mp, rp, handle))
     if rc != 0:
         raise SgemmError(rc, "layer_norm")
     return (out, mean, rstd) if stats else out
@@ -105,31 +103,32 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, out=None, dweight=Non
         return _on_stream(stream, lambda: layer_norm_backward(
             dy, x, mean, rstd, weight, out=out, dweight=dweight, dbias=dbias, beta=beta),
             [t for t in (dy, x, mean, rstd, weight, out, dweight, dbias) if t is not None])
-    kind, rows, cols, ldx = _matrix(x)
-    device = x.device
+    kind, rows, cols, ldx, at, handle = _matrix(x)
     lddy = _like("dy", dy, x)
     if mean is None or rstd is None:
         raise TypeError("mean and rstd are needed")
-    mp, rp = _numbers("mean", mean, rows, device), _numbers("rstd", rstd, rows, device)
-    wp, wt = _vector("weight", weight, cols, device)
+    mp, rp = _numbers("mean", mean, rows, at), _numbers("rstd", rstd, rows, at)
     if beta != 0.0 and (dweight is None or dbias is None):
         raise ValueError("beta needs dweight and dbias to scale")
+    wp = wt = dwp = dbp = 0
+    if weight is not None:
+        wp, wt = _vector("weight", weight, cols, at)
     if weight is not None or dweight is not None or dbias is not None:
         if dweight is None:
-            dweight = torch.empty(cols, dtype=torch.float32, device=device)
+            dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
         if dbias is None:
-            dbias = torch.empty(cols, dtype=torch.float32, device=device)
-    dwp, dbp = _numbers("dweight", dweight, cols, device), _numbers("dbias", dbias, cols, device)
-    if dwp and dwp == dbp:
-        raise ValueError("dweight and dbias overlap")
+            dbias = torch.empty(cols, dtype=torch.float32, device=x.device)
+        dwp, dbp = _numbers("dweight", dweight, cols, at), _numbers("dbias", dbias, cols, at)
+        if -4 * cols < dwp - dbp < 4 * cols:
+            raise ValueError("dweight and dbias overlap")
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
         lddx = cols
     else:
         lddx = _like("out", out, x)
     rc = lib.layer_norm_backward_with(_backward_args(
         rows, cols, dy.data_ptr(), lddy, x.data_ptr(), kind, ldx, mp, rp, wp, wt, out.data_ptr(), lddx,
-        dwp, dbp, beta, _stream(None) or 0))
+        dwp, dbp, beta, handle))
     if rc != 0:
         raise SgemmError(rc, "layer_norm_backward")
     return out, dweight, dbias
