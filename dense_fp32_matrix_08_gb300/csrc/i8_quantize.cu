@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / 
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 1, kDepth<T>> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
+  Ahead<T, TPR, CH, VEC, 1, kDepth<T>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
   using S = Share<T, TPR, VEC>;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
 
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T>>::BYTES;
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T>, threads>::BYTES;
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(quantize_kernel<T, TPR, CH, VEC>, bytes, once, set);

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
+  Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
         total = add2(total, d[c][i]);
       }
     float s[1] = {sum2(total)};
-    row_sum<TPR>(s, sums, 0);
+    row_sum(s, sums, 0);
     const float mean = over(s[0], p.n, p.r);
     const Two minus = both(-mean);
     total = 0;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
         total = fma2(d[c][i], d[c][i], total);
       }
     s[0] = sum2(total);
-    row_sum<TPR>(s, sums, 1);
+    row_sum(s, sums, 1);
     // 1 / sqrt, with one step of Newton's iteration
     const float v = over(s[0], p.n, p.r) + p.eps;
     float rstd = rsqrtf(v);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
 
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>>::BYTES;
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>, threads>::BYTES;
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(norm_kernel<T, TPR, CH, VEC>, bytes, once, set);

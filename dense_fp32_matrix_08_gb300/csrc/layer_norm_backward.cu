@@ -4,8 +4,8 @@
 //
 // Bound by HBM: dy and x are read and dx is written once. A row stays in registers between its two
 // sums and its result. dw and db are added up in the registers of the thread that holds the column,
-// over all rows of its CTA (512 at most, so that FP32 holds such a sum); the CTAs' sums meet in the
-// workspace, where reduce_kernel adds them in a fixed order.
+// over all rows that it gets (500 at most, so that FP32 holds such a sum); those of a CTA meet in shared
+// memory, the CTAs' sums in the workspace, where reduce_kernel adds them in a fixed order.
 #include <algorithm>
 #include <cmath>
 
@@ -17,7 +17,7 @@ namespace lnb {
 
 using namespace rows;
 
-constexpr int kMostRows = 512;  // rows of one FP32 sum of dw or db
+constexpr int kMostRows = 500;  // rows that a thread adds up in FP32
 constexpr int kLongestHere = 8192;  // elements of a row that stays in registers beside the sums
 
 struct Params {
@@ -29,25 +29,32 @@ struct Params {
   float n, r;               // cols, 1 / cols
   char *dx;
   long long lddx;           // bytes
-  float *part;              // sums of dw, then of db: [2][parts][cols]; NULL: neither is wanted
+  float *part;              // sums of dw, then of db: [2][parts][pitch]; NULL: neither is wanted
   int parts;
+  long long pitch;          // cols rounded up to a multiple of 4
   float2 *along;            // rows that do not stay in registers: sum g / n, sum (g h) / n
 };
 
-// CTAs of backward_kernel per SM: 512 threads with up to 128 registers. Rows under way: 64 to 96 KB per SM.
-constexpr int per_sm(int tpr) { return tpr < 128 ? 4 : 512 / tpr; }
+// One CTA of 512 threads per SM, with up to 128 registers each: as many rows at a time as that makes, and
+// one sum of each column per SM. Rows under way: 64 to 96 KB per SM.
+constexpr int kThreads = 512;
 template <class T>
 constexpr int kDepth = T::SIZE == 4 ? 3 : 4;
 
+// Dynamic shared memory: the ring of rows to come; at the end the sums of the CTA's rows.
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) backward_kernel(const Params p) {
-  constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
+constexpr int kBytes = std::max(Ahead<T, TPR, CH, VEC, 2, kDepth<T>, kThreads>::BYTES,
+                                TPR < kThreads ? kThreads * 2 * CH * 8 * 4 : 0);
+
+template <class T, int TPR, int CH, bool VEC>
+__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
+  constexpr int RPB = kThreads / TPR;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) RowSums<TPR, 2> sums;
+  __shared__ __align__(16) RowSums<TPR, 2, RPB> sums;
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 2, kDepth<T>> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row, step);
+  Ahead<T, TPR, CH, VEC, 2, kDepth<T>, kThreads> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
@@ -89,7 +96,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) backward_k
       s[1] = sum2(sh2);
     }
     if (p.dx == nullptr) continue;
-    row_sum<TPR>(s, sums, turn);
+    row_sum(s, sums, turn);
     if (in) {
       const Two s1 = both(-over(s[0], p.n, p.r)), s2 = both(-over(s[1], p.n, p.r));
 #pragma unroll
@@ -105,55 +112,69 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) backward_k
     }
   }
   if (p.part) {
-    // the rows of a CTA that several threads had for one column, then one sum of each column
-    float f[CH][8], g[CH][8];
+    float f[2][CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 a = unpack2(dw[c][i]), e = unpack2(db[c][i]);
-        f[c][2 * i] = a.x, f[c][2 * i + 1] = a.y, g[c][2 * i] = e.x, g[c][2 * i + 1] = e.y;
+        f[0][c][2 * i] = a.x, f[0][c][2 * i + 1] = a.y, f[1][c][2 * i] = e.x, f[1][c][2 * i + 1] = e.y;
       }
-    if constexpr (TPR < 32) {
+    // four sums of chunk c from j on, to the workspace (element by element 8192 x 4096 BF16 took 48 us
+    // for 41)
+    const auto leave = [&](int which, int c, int j, int have, const Share<T, TPR, VEC> &at, const float4 &v) {
+      float *out = p.part + ((long long)which * p.parts + blockIdx.x) * p.pitch;
+      const float u[4] = {v.x, v.y, v.z, v.w};
+      if (VEC && j + 4 <= have) {
+        *reinterpret_cast<float4 *>(out + at.col(c, j)) = v;
+      } else {
 #pragma unroll
-      for (int d = TPR; d < 32; d *= 2)
+        for (int i = 0; i < 4; ++i)
+          if (j + i < have) out[at.col(c, j + i)] = u[i];
+      }
+    };
+    if constexpr (TPR == kThreads) {
+#pragma unroll
+      for (int which = 0; which < 2; ++which)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            f[c][j] += __shfl_xor_sync(0xffffffffu, f[c][j], d);
-            g[c][j] += __shfl_xor_sync(0xffffffffu, g[c][j], d);
-          }
-    }
-    float *out = p.part + (long long)blockIdx.x * p.cols, *tb = out + (long long)p.parts * p.cols;
-    if constexpr (TPR < 128) {
-      constexpr int WARPS = THREADS / 32, LANES = TPR < 32 ? TPR : 32;
-      __shared__ float meet[WARPS][2][CH * 8][LANES];
-      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-      if (lane < LANES) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) meet[warp][0][c * 8 + j][lane] = f[c][j], meet[warp][1][c * 8 + j][lane] = g[c][j];
-      }
-      __syncthreads();
-      if (threadIdx.x < LANES) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float a = 0.0f, e = 0.0f;
-#pragma unroll
-            for (int q = 0; q < WARPS; ++q) a += meet[q][0][c * 8 + j][lane], e += meet[q][1][c * 8 + j][lane];
-            if (j < n[c]) out[sh.col(c, j)] = a, tb[sh.col(c, j)] = e;
-          }
-      }
+          for (int j = 0; j < 8; j += 4)
+            leave(which, c, j, n[c], sh, make_float4(f[which][c][j], f[which][c][j + 1], f[which][c][j + 2],
+                                                     f[which][c][j + 3]));
     } else {
+      // those of the rows that the CTA had at a time: within warps, then from all of them
+      constexpr int U = TPR < 32 ? 32 : TPR, UNITS = kThreads / U;
+      cp_async_wait<0>();
+      __syncthreads();  // (the ring is done with)
+      float4 *meet = reinterpret_cast<float4 *>(ring);  // [which][c][j / 4][unit][thread]
+      const int unit = threadIdx.x / U, t = threadIdx.x % U;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int which = 0; which < 2; ++which)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n[c]) out[sh.col(c, j)] = f[c][j], tb[sh.col(c, j)] = g[c][j];
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+          for (int d = TPR; d < 32; d *= 2)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[which][c][j] += __shfl_xor_sync(0xffffffffu, f[which][c][j], d);
+#pragma unroll
+          for (int j = 0; j < 8; j += 4)
+            meet[(((which * CH + c) * 2 + j / 4) * UNITS + unit) * U + t] =
+                make_float4(f[which][c][j], f[which][c][j + 1], f[which][c][j + 2], f[which][c][j + 3]);
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * CH * 2 * U; i += kThreads) {
+        const int t2 = i % U, k = i / U, which = k / (2 * CH), c = k / 2 % CH, j = k % 2 * 4;
+        if (t2 >= TPR) continue;  // (a narrow row's other copies)
+        float4 v = meet[k * UNITS * U + t2];
+#pragma unroll
+        for (int q = 1; q < UNITS; ++q) {
+          const float4 u = meet[(k * UNITS + q) * U + t2];
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        const Share<T, TPR, VEC> at{p.cols, t2};
+        leave(which, c, j, at.count(c), at, v);
+      }
     }
   }
   griddep_launch_dependents();
@@ -230,7 +251,7 @@ __global__ void __launch_bounds__(256) across_kernel(const Params p, int col_blo
     }
   }
   if (p.part) {
-    float *to = p.part + (long long)chunk * p.cols, *tb = to + (long long)p.parts * p.cols;
+    float *to = p.part + chunk * p.pitch, *tb = to + p.parts * p.pitch;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (c0 + 256 * j < p.cols) {
@@ -241,11 +262,14 @@ __global__ void __launch_bounds__(256) across_kernel(const Params p, int col_blo
   griddep_launch_dependents();
 }
 
-// dweight (block < blocks) or dbias: 32 columns per CTA, its 8 warps take the parts in turn, 16 of
-// them at a time in FP32 and the rest in 64 bits.
-__global__ void __launch_bounds__(256) reduce_kernel(const float *part, int parts, int cols, int blocks,
-                                                     float *dweight, float *dbias, float beta) {
-  __shared__ double sums[8][32];
+// dweight (block < blocks) or dbias: 32 columns per CTA, its 8 warps take the parts in turn, 16 of them at
+// a time in FP32 and the rest in 64 bits. About 5 us of the 41 of 8192 x 4096 BF16, of which the parts'
+// way through L2 and back is half. (CTAs of 32 warps took 7 us longer.)
+constexpr int kReduceWarps = 8;
+__global__ void __launch_bounds__(32 * kReduceWarps)
+    reduce_kernel(const float *part, int parts, int cols, long long pitch, int blocks, float *dweight,
+                  float *dbias, float beta) {
+  __shared__ double sums[kReduceWarps][32];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool second = (int)blockIdx.x >= blocks;
@@ -254,11 +278,14 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *part, int part
   if (out == nullptr) return;
   double total = 0.0;
   if (col < cols) {
-    const float *from = part + (second ? (long long)parts * cols : 0) + col;
-    for (int r0 = warp; r0 < parts; r0 += 16 * 8) {
+    const float *from = part + (second ? parts * pitch : 0) + col;
+    for (int r0 = warp; r0 < parts; r0 += 16 * kReduceWarps) {
       float v[16], s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = r0 + 8 * j < parts ? from[(long long)(r0 + 8 * j) * cols] : 0.0f;
+      for (int j = 0; j < 16; ++j) {
+        const int r = r0 + kReduceWarps * j;
+        v[j] = r < parts ? from[r * pitch] : 0.0f;
+      }
 #pragma unroll
       for (int j = 0; j < 16; ++j) s += v[j];
       total += s;
@@ -268,7 +295,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float *part, int part
   __syncthreads();
   if (warp == 0 && col < cols) {
 #pragma unroll
-    for (int w = 1; w < 8; ++w) total += sums[w][lane];
+    for (int w = 1; w < kReduceWarps; ++w) total += sums[w][lane];
     out[col] = beta != 0.0f ? (float)((double)beta * out[col] + total) : (float)total;
   }
   griddep_launch_dependents();
@@ -291,10 +318,8 @@ static Plan make_plan(int rows, int cols, int sms) {
            : cols <= 4096 ? 256
            : cols <= kLongestHere ? 512 : 0;
   if (pl.tpr) {
-    const int threads = std::max(128, pl.tpr), rpb = threads / pl.tpr;
-    const long long most = ceil_div(rows, rpb);
-    const long long fill = (long long)sms * per_sm(pl.tpr);
-    pl.grid = (int)std::min<long long>(most, std::max<long long>(fill, ceil_div(most, kMostRows)));
+    const long long most = ceil_div(rows, kThreads / pl.tpr);
+    pl.grid = (int)std::min<long long>(most, std::max<long long>(sms, ceil_div(most, kMostRows)));
     pl.parts = pl.grid;
   } else {
     const long long blocks = ceil_div(cols, kLongCols);
@@ -308,15 +333,16 @@ static Plan make_plan(int rows, int cols, int sms) {
 static size_t along_bytes(const Plan &pl, int rows) {
   return pl.tpr ? 0 : ((size_t)rows * sizeof(float2) + 255) / 256 * 256;
 }
-static size_t part_bytes(const Plan &pl, int cols) { return (size_t)2 * pl.parts * cols * sizeof(float); }
+static long long pitch_of(int cols) { return ceil_div(cols, 4) * 4; }
+static size_t part_bytes(const Plan &pl, int cols) { return (size_t)2 * pl.parts * pitch_of(cols) * sizeof(float); }
 
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int grid, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, bytes = Ahead<T, TPR, CH, VEC, 2, kDepth<T>>::BYTES;
+  constexpr int bytes = kBytes<T, TPR, CH, VEC>;
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(backward_kernel<T, TPR, CH, VEC>, bytes, once, set);
-  return e != cudaSuccess ? e : launch_1d(backward_kernel<T, TPR, CH, VEC>, grid, threads, bytes, 1, stream, p);
+  return e != cudaSuccess ? e : launch_1d(backward_kernel<T, TPR, CH, VEC>, grid, kThreads, bytes, 1, stream, p);
 }
 template <class T, int TPR, int CH>
 static cudaError_t launch(const Params &p, bool vec, int grid, cudaStream_t stream) {
@@ -393,8 +419,8 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   if (e != cudaSuccess) return (int)e;
   const int blocks = (int)ceil_div(cols, 32);
   if (rows == 0)
-    return (int)launch_1d(lnb::reduce_kernel, 2 * blocks, 256, 0, 1, stream,
-                          static_cast<const float *>(nullptr), 0, cols, blocks, dweight, dbias, beta);
+    return (int)launch_1d(lnb::reduce_kernel, 2 * blocks, 32 * lnb::kReduceWarps, 0, 1, stream,
+                          static_cast<const float *>(nullptr), 0, cols, 0LL, blocks, dweight, dbias, beta);
   const lnb::Plan pl = lnb::make_plan(rows, cols, sms);
   const long long size = x_type == LN_F32 ? 4 : 2;
   lnb::Params p{};
@@ -412,6 +438,7 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   p.dx = static_cast<char *>(dx);
   p.lddx = lddx * size;
   p.parts = pl.parts;
+  p.pitch = lnb::pitch_of(cols);
   const size_t along = dx ? lnb::along_bytes(pl, rows) : 0;
   const size_t bytes = along + (sums ? lnb::part_bytes(pl, cols) : 0);
   char *ws = nullptr;
@@ -429,8 +456,8 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
       : x_type == LN_BF16 ? lnb::run<rows::BF16>(p, pl, vec, sms, stream)
                           : lnb::run<rows::F16>(p, pl, vec, sms, stream);
   if (e == cudaSuccess && sums)
-    e = launch_1d(lnb::reduce_kernel, 2 * blocks, 256, 0, 1, stream,
-                  static_cast<const float *>(p.part), pl.parts, cols, blocks, dweight, dbias, beta);
+    e = launch_1d(lnb::reduce_kernel, 2 * blocks, 32 * lnb::kReduceWarps, 0, 1, stream,
+                  static_cast<const float *>(p.part), pl.parts, cols, p.pitch, blocks, dweight, dbias, beta);
   if (ws != nullptr) {
     const cudaError_t ef = cudaFreeAsync(ws, stream);
     if (e == cudaSuccess) e = ef;

@@ -143,10 +143,9 @@ struct Share {
 // places of a ring in shared memory, DEPTH rows ahead (what one row's registers hold under way does not
 // fill HBM's latency: layer norm of 8192 x 4096 BF16 took 37 us so), else one row ahead in registers.
 // Nobody else reads them, so there is nothing to wait for but the thread's own copies.
-template <class T, int TPR, int CH, bool VEC, int INPUTS, int DEPTH>
+template <class T, int TPR, int CH, bool VEC, int INPUTS, int DEPTH, int THREADS>
 struct Ahead {
   using S = Share<T, TPR, VEC>;
-  static constexpr int THREADS = TPR < 128 ? 128 : TPR;
   static constexpr int ROW = THREADS * CH * 8 * T::SIZE;  // bytes of the CTA's rows of one input
   static constexpr int BYTES = VEC ? DEPTH * INPUTS * ROW : 0;
   S sh;
@@ -293,27 +292,31 @@ __device__ __forceinline__ void parameters(const Vector &p, const S &sh, int c, 
   for (int i = 0; i < 4; ++i) to[i] = pack2(v[2 * i], v[2 * i + 1]);
 }
 
-// Sums of N numbers over the TPR threads of a row, the same bits in each of them. `turn` alternates between
-// calls of a kernel, so that one barrier is enough: whoever writes a buffer again has passed the barrier
-// of the call in between, before which everybody had read it.
-template <int TPR, int N>
+// Sums of N numbers over the TPR threads of a row (one of ROWS rows of a CTA), the same bits in each of
+// them. `turn` alternates between calls of a kernel, so that one barrier is enough: whoever writes a
+// buffer again has passed the barrier of the call in between, before which everybody had read it.
+template <int TPR, int N, int ROWS = 1>
 struct RowSums {
-  float part[2][N][TPR < 128 ? 4 : TPR / 32];
+  float part[TPR > 32 ? ROWS : 1][2][N][TPR < 128 ? 4 : TPR / 32];
 };
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], RowSums<TPR, N> &sums, int turn) {
+template <int TPR, int N, int ROWS>
+__device__ __forceinline__ void row_sum(float (&v)[N], RowSums<TPR, N, ROWS> &sums, int turn) {
 #pragma unroll
   for (int d = 1; d < (TPR < 32 ? TPR : 32); d *= 2)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
   if constexpr (TPR > 32) {
+    const int row = ROWS == 1 ? 0 : threadIdx.x / TPR;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) sums.part[turn][i][threadIdx.x >> 5] = v[i];
-    __syncthreads();
+      for (int i = 0; i < N; ++i) sums.part[row][turn][i][threadIdx.x % TPR >> 5] = v[i];
+    if (ROWS == 1)
+      __syncthreads();
+    else
+      tcx::named_barrier(1 + row, TPR);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float4 *from = reinterpret_cast<const float4 *>(sums.part[turn][i]);
+      const float4 *from = reinterpret_cast<const float4 *>(sums.part[row][turn][i]);
       float4 s = from[0];
 #pragma unroll
       for (int w = 1; w < TPR / 128; ++w) {

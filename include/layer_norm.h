@@ -43,9 +43,9 @@ int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const voi
  * does not read dweight and dbias; with rows == 0 they become beta times themselves. dx may be dy or
  * x itself with the same leading dimension, and must not overlap them otherwise.
  *
- * Sums along rows are FP32 (in rows of more than 8192 elements 64-bit), those over the rows FP32 for
- * up to 512 rows and 64-bit beyond, in an order fixed by the shape and the device: the same call gives
- * the same bits. The workspace (layer_norm_backward_workspace_size bytes) is a stream-ordered
+ * Sums along rows are FP32 (in rows of more than 8192 elements 64-bit), those over the rows FP32 within
+ * a block (at most 500 rows one after the other) and 64-bit beyond, in an order fixed by the shape and
+ * the device: the same call gives the same bits. The workspace (layer_norm_backward_workspace_size bytes) is a stream-ordered
  * allocation from the library's pool.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2

@@ -8,7 +8,8 @@ Bounds, with u = 2^-24, half a step of FP32, and STEPS = 64: a sum along a row p
   y      |w| (|x - mean| rstd (rel + 4 u) + em rstd) + u |y|, and one rounding to its type
   dx     with h and g off by 2 u each: rstd (8 u (|g| + |s1| + |h s2|) + STEPS u (mean|g| + |h| mean|g h|)),
          and one rounding
-  dw     sums of up to 512 rows and then of 16 parts in FP32: (min(rows, 512) + 24) u sum |dy h|; db alike
+  dw     up to 500 additions of a thread's rows, 17 more in its block and 15 of parts in FP32:
+         (min(rows, 512) + 24) u sum |dy h|; db alike
 In rows that are read more than once sums are more exact than that. A rounding to a type t is off by at
 most finfo(t).eps / 2 of the value and, in FP16, by half its smallest step, 2^-25.
 """
