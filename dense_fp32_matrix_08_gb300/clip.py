@@ -12,7 +12,7 @@ from .f8 import _TYPE
 __all__ = ["clip_grad_norm", "GC_EXPORTED"]
 
 
-_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_dtype = attrgetter("dtype")
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
@@ -38,7 +38,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, stream=None):
     """Scales gradients by min(1, max_norm / (norm + eps)), norm = sqrt(the sum of squares of all their
     elements), and returns that norm, a float32 tensor of no dimensions on the device. grads: contiguous
     CUDA tensors of float32, bfloat16 or float16, in any mixture. They are changed in place; with out, a
-    list of as many tensors of the same shapes, those are written instead, each in its own type. With
+    list of as many tensors with as many elements each, those are written instead, each in its own type. With
     max_norm = inf and no out nothing is changed: only the norm is computed. `stream`: where to run (a
     torch stream or a handle; the current stream unless given), the norm belongs to it. Raises
     SgemmError on a nonzero status (-7: results that overlap, such as one gradient given twice)."""
@@ -51,9 +51,9 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, stream=None):
     at, types, sizes = _lists("grads", grads)
     to, to_types = at, types
     if out is not None:
-        to, to_types, _ = _lists("out", out)
-        if list(map(_shape, out)) != list(map(_shape, grads)):
-            raise ValueError("shape mismatch")
+        to, to_types, have = _lists("out", out)
+        if have != sizes:
+            raise ValueError("out must have as many elements as grads, tensor by tensor")
     scale = out is not None or max_norm != float("inf")
     norm = torch.empty((), dtype=torch.float32, device="cuda")
     rc = lib.clip_grad_norm(

@@ -50,16 +50,21 @@ __device__ __forceinline__ const Array &array_of(const Params<MOST> &p, int at) 
   return p.a[lo];
 }
 
-// 8 neighbouring elements, or those of them that exist (the others are zero), as FP32.
+// What a thread takes at a time: 8 elements of 2048, as 16-byte accesses side by side: 8 neighbours, or
+// (FP32) 4 and the 4 that are 1024 further.
+__device__ __forceinline__ int place(int type, int j) {
+  return type == GC_F32 ? threadIdx.x * 4 + (j >= 4 ? kThreads * 4 - 4 : 0) + j : threadIdx.x * 8 + j;
+}
+
+// Elements place(0 .. 7) of the 2048 from i on; those that do not exist are zero.
 __device__ __forceinline__ void load8(const Array &a, long long i, bool vec, float (&v)[8]) {
-  const long long left = a.n - i;
-  if (vec && left >= 8) {
+  if (vec && i + kThreads * 8 <= a.n) {
     if (a.type == GC_F32) {
-      const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(a.in) + i);
-      const float4 x = s[0], y = s[1];
+      const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(a.in) + i) + threadIdx.x;
+      const float4 x = s[0], y = s[kThreads];
       v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
     } else {
-      const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.in) + i);
+      const uint4 u = *(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.in) + i) + threadIdx.x);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -76,20 +81,49 @@ __device__ __forceinline__ void load8(const Array &a, long long i, bool vec, flo
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < left ? tcx::load_out(a.in, a.type, i + j) : 0.0f;
+  for (int j = 0; j < 8; ++j) {
+    const long long at = i + place(a.type, j);
+    v[j] = at < a.n ? tcx::load_out(a.in, a.type, at) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8(const Array &a, long long i, bool vec, const float (&v)[8]) {
+  if (vec && i + kThreads * 8 <= a.n) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      const long long at = i + place(a.type, j);
+      if (a.out_type == GC_F32)
+        __stcs(reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+      else if (a.type == GC_F32 || j == 0) {
+        const uint32_t lo = tcx::pack_out(a.out_type, v[j], v[j + 1]), hi = tcx::pack_out(a.out_type, v[j + 2], v[j + 3]);
+        uint16_t *to = static_cast<uint16_t *>(a.out) + at;
+        if (a.type == GC_F32)
+          __stcs(reinterpret_cast<uint2 *>(to), make_uint2(lo, hi));
+        else
+          __stcs(reinterpret_cast<uint4 *>(to), make_uint4(lo, hi, tcx::pack_out(a.out_type, v[4], v[5]),
+                                                           tcx::pack_out(a.out_type, v[6], v[7])));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const long long at = i + place(a.type, j);
+    if (at < a.n) tcx::store_out(a.out, a.out_type, at, v[j]);
+  }
 }
 
 __device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Sum of squares of a thread's elements of a piece, in a scale in which FP32 holds it.
 __device__ __forceinline__ double thread_squares(const Array &a, long long at, bool vec) {
-  const long long i0 = at + threadIdx.x * 8;
   float s = 0.0f;
   uint32_t any = 0;
-#pragma unroll
-  for (int k = 0; k < kPiece; k += kThreads * 8) {
+  const int count = (int)min((long long)kPiece, a.n - at);
+#pragma unroll 4
+  for (int k = 0; k < count; k += kThreads * 8) {
     float v[8];
-    load8(a, i0 + k, vec, v);
+    load8(a, at + k, vec, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       s = fmaf(v[j], v[j], s);
@@ -102,9 +136,9 @@ __device__ __forceinline__ double thread_squares(const Array &a, long long at, b
   if (any == 0 || (s > 0x1p-90f && s < 0x1p120f)) return s;
   const float up = s < 1.0f ? 0x1p100f : 0x1p-70f;
   s = 0.0f;
-  for (int k = 0; k < kPiece; k += kThreads * 8) {
+  for (int k = 0; k < count; k += kThreads * 8) {
     float v[8];
-    load8(a, i0 + k, vec, v);
+    load8(a, at + k, vec, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = fmaf(v[j] * up, v[j] * up, s);
   }
@@ -157,30 +191,15 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
       const Array &a = array_of(p, at);
       if (whole && a.in == a.out) continue;
       const bool vec = aligned16(a.in), vec_out = aligned16(a.out);
-      const long long i0 = (long long)(at - a.first) * kPiece + threadIdx.x * 8;
+      const long long from = (long long)(at - a.first) * kPiece;
+      const int count = (int)min((long long)kPiece, a.n - from);
 #pragma unroll 4
-      for (int k = 0; k < kPiece; k += kThreads * 8) {
-        const long long i = i0 + k;
-        if (i >= a.n) break;
+      for (int k = 0; k < count; k += kThreads * 8) {
         float v[8];
-        load8(a, i, vec, v);
+        load8(a, from + k, vec, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] * shrink * factor;
-        if (vec_out && a.n - i >= 8) {
-          if (a.out_type == GC_F32) {
-            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + i) =
-                make_uint4(tcx::pack_out(a.out_type, v[0], v[1]), tcx::pack_out(a.out_type, v[2], v[3]),
-                           tcx::pack_out(a.out_type, v[4], v[5]), tcx::pack_out(a.out_type, v[6], v[7]));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < a.n - i) tcx::store_out(a.out, a.out_type, i + j, v[j]);
-        }
+        store8(a, from + k, vec_out, v);
       }
     }
   }
@@ -320,5 +339,8 @@ extern "C" int clip_grad_norm(int count, const void *const *grads, const int *ty
   const gc::Call c{count, grads, types, sizes, max_norm, eps, out, out_types, norm, stream};
   // launches: full tables, and each time that the pieces of one would be too many
   const auto launches = [&](int most) { return (int)(ceil_div(arrays, most) + pieces / 0x3fffffff * 2 + 1); };
-  return arrays <= 96 ? (int)gc::run<96>(c, launches(96), sms) : (int)gc::run<960>(c, launches(960), sms);
+  // (the table is copied for each launch: 200 arrays' in one of 960 took 15 us longer to launch)
+  return arrays <= 32    ? (int)gc::run<32>(c, launches(32), sms)
+         : arrays <= 240 ? (int)gc::run<240>(c, launches(240), sms)
+                         : (int)gc::run<960>(c, launches(960), sms);
 }

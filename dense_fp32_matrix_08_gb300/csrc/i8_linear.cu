@@ -54,10 +54,15 @@ struct Cfg {
   static constexpr int GROUPS = TN >= 64 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;         // tokens of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
-  static constexpr int THREADS = 32 * (8 + EPI_WARPS);
+  // Two converter groups take turns with the blocks of k where Q is converted, too. (Else one is enough,
+  // and the registers of 64 sums per thread are for one only: with two 128 x 14336 x 4096 took 24.9 us
+  // for 23.1.)
+  static constexpr int CONV_GROUPS = CONVERT ? 2 : 1;
+  static constexpr int FIRST_EPI = 4 + 4 * CONV_GROUPS;  // warp
+  static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
   static constexpr int Q_BYTES = QN * BK * (CONVERT ? 1 : 2);
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = CONVERT ? (TN == 64 ? 5 : 9) : 4;
+  static constexpr int STAGES = CONVERT ? (TN == 64 ? 4 : 8) : 4;
   static constexpr int NA = 4;                     // blocks of P in TMEM (and of Q, where converted)
   static constexpr int A_COLS = BK / 2;            // columns of one
   static constexpr int H_BYTES = CONVERT ? QN * BK * 2 : 0;
@@ -71,6 +76,8 @@ struct Cfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int BARS = 3 * STAGES + 2 * NA + 2 * PARTS * NBUF;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NA * H_BYTES + EPI_WARPS * OUT_BYTES + 8 * BARS + 16;
+  // (a barrier tells only odd uses of a slot from even ones: whoever waits for it must see them all)
+  static_assert(STAGES % CONV_GROUPS == 0 && NA % CONV_GROUPS == 0, "each slot belongs to one group");
   static_assert(PARTS * NBUF * ACC_COLS + NA * A_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
@@ -101,14 +108,15 @@ struct Channel {
 // Sums of this lane's channel and `count` (16 or 2) neighbouring tokens, finished and stored. What is not
 // unrolled over the sums is not unrolled at all: the epilogue shares the instruction caches with the
 // converters (all inlined and unrolled it took half of their time).
+// sx: the scale of token `token` + lane - from in each lane.
 template <int COUNT>
-__device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, float *buf, int lane, int token,
-                                             const int (&sums)[COUNT]) {
+__device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, float sx, int from, float *buf,
+                                             int lane, int token, const int (&sums)[COUNT]) {
   const int rows = min(COUNT, p.M - token);
-  const float *sx = p.x_scale + token;
 #pragma unroll
   for (int j = 0; j < COUNT; ++j)
-    buf[j * OUT_PITCH + lane] = fmaf((float)sums[j], c.scale * (j < rows ? sx[j] : 0.0f), c.bias);
+    buf[j * OUT_PITCH + lane] =
+        fmaf((float)sums[j], c.scale * __shfl_sync(0xffffffffu, sx, from + j), c.bias);
   __syncwarp();
   const int col0 = c.at - lane;
   if (p.d.vec && COUNT == 16 && p.d.type != tcx::OUT_F32) {
@@ -140,8 +148,12 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
         for (int j = 0; j < cols; ++j) d[j] = v[j];
       }
     }
+  } else if (c.at < p.N && p.d.type == tcx::OUT_F32 && p.d.beta == 0.0f) {
+    float *d = static_cast<float *>(p.d.ptr) + token * p.d.ld + c.at;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) d[r * p.d.ld] = buf[r * OUT_PITCH + lane];
   } else if (c.at < p.N) {
-#pragma unroll 1
+#pragma unroll 2
     for (int r = 0; r < rows; ++r)
       tcx::finish_out(p.d.ptr, p.d.type, (token + r) * p.d.ld + c.at, buf[r * OUT_PITCH + lane], p.d.beta);
   }
@@ -157,8 +169,8 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t local, uint32_t rank) {
   return __float_as_int(tcx::ld_cluster1(local, rank));
 }
 
-// Warp 0: TMA producer, warp 1: MMA issuer (one elected lane of each), warps 4 - 7: converters, one row
-// of P per thread; warps 8 ..: epilogue, a group of four warps owns COLS tokens of the tile, warp w of
+// Warp 0: TMA producer, warp 1: MMA issuer (one elected lane of each), then the converters, one row of P
+// per thread of a group; the last warps: epilogue, a group of four warps owns COLS tokens of the tile, warp w of
 // it TMEM lanes (channels) 32 (w % 4) .. + 31, one per thread.
 template <int TN, bool PAIR>
 __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   };
 
   if (warp < 4) {
-    // a pair's 512 threads x 128 registers at launch >= 128 x 56 + 128 x 96 + 256 x 168
+    // a pair's 512 threads x 128 registers at launch >= 128 x 56 + 128 x 96 + 256 x 176
     if constexpr (PAIR) reg_dealloc<56>();
     if (warp == 0) {
       // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
@@ -350,16 +362,23 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < C::FIRST_EPI) {
     // ---- converters
     if constexpr (PAIR) reg_dealloc<96>();
-    const int row = threadIdx.x - 128;  // of P
+    const int row = threadIdx.x % 128;  // of P
+    int turns = (warp - 4) >> 2;        // blocks until this group's next one
     const uint32_t a_lane = a_tmem + ((uint32_t)((warp & 3) * 32) << 16);
     Ring<C::STAGES> st;
     Ring<C::NA> ar;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       for (int kb = kb0; kb < kb1; ++kb) {
+        if (C::CONV_GROUPS > 1 && turns-- != 0) {
+          st.next();
+          ar.next();
+          continue;
+        }
+        turns = C::CONV_GROUPS - 1;
         ok = __all_sync(0xffffffffu, wait_short(p_full + 8 * st.slot, st.parity) &&
                                          (!C::CONVERT || wait_short(q_full + 8 * st.slot, st.parity)) &&
                                          wait_short(a_empty + 8 * ar.slot, ar.parity ^ 1u));
@@ -417,19 +436,30 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     }
   } else {
     // ---- epilogue
-    if constexpr (PAIR) reg_alloc<168>();
-    const int grp = (warp - 8) >> 2, quad = warp & 3;
+    if constexpr (PAIR) reg_alloc<176>();
+    const int grp = (warp - C::FIRST_EPI) >> 2, quad = warp & 3;
     // a group's tokens: COLS neighbouring ones, or one part of a pair's tile, 64 from each CTA's half
     const uint32_t which0 = PAIR ? grp * C::NBUF : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + which0 * C::ACC_COLS +
                                (PAIR ? 0 : (uint32_t)(grp * C::COLS));
     const uint32_t full0 = acc_full + 8 * which0, empty0 = acc_empty + 8 * which0;
-    float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - 8) * OUT_BYTES);
+    float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - C::FIRST_EPI) * OUT_BYTES);
     Ring<C::NBUF> buf;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       int tp, tq;
       tile_at(t, tp, tq);
+      // Token of column c, and what the results are multiplied with: read now, for the end.
+      const auto token_of = [&](int c) {
+        return tq * TN + (PAIR ? (c / 64) * 128 + grp * 64 + c % 64 : grp * C::COLS + c);
+      };
+      const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
+      float sx[(C::COLS + 31) / 32];
+#pragma unroll
+      for (int c = 0; c < C::COLS; c += 32) {
+        const int token = token_of(c) + lane;
+        sx[c / 32] = token < p.M ? p.x_scale[token] : 0.0f;
+      }
       int acc[C::COLS];
 #pragma unroll
       for (int j = 0; j < C::COLS; ++j) acc[j] = 0;
@@ -464,14 +494,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       }
       if (!ok) break;
       if (S == 1) {
-        const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 16) {
-          const int token = tq * TN + (PAIR ? (c / 64) * 128 + grp * 64 + c % 64 : grp * C::COLS + c);
           int sums[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) sums[j] = acc[c + j];
-          if (token < p.M) store_tokens<16>(p, ch, out, lane, token, sums);
+          if (token_of(c) < p.M) store_tokens<16>(p, ch, sx[c / 32], c % 32, out, lane, token_of(c), sums);
         }
       } else {
         // partial tile -> the ring, whose every reader has finished (the last accumulator is
@@ -487,12 +515,12 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp two of them and 32
     // channels at a time
     cluster_sync_all();
-    if (warp >= 8) {
+    if (warp >= C::FIRST_EPI) {
       int tp, tq;
       tile_at(first, tp, tq);
       const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);  // (TN / S is even)
       const int items = c1 > c0 ? (c1 - c0 + 1) / 2 * 4 : 0;
-      for (int i = warp - 8; i < items; i += C::EPI_WARPS) {
+      for (int i = warp - C::FIRST_EPI; i < items; i += C::EPI_WARPS) {
         const int quad = i & 3, c = c0 + i / 4 * 2;
         const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
         int v[2][MAX_CLUSTER];
@@ -510,8 +538,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
         // (both are used whatever is stored: a load that nothing waits for could still be under way
         // when the other CTA leaves)
         asm volatile("" ::"r"(sums[0]), "r"(sums[1]));
-        float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - 8) * OUT_BYTES);
-        store_tokens<2>(p, ch, out, lane, tq * TN + c, sums);
+        float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - C::FIRST_EPI) * OUT_BYTES);
+        const int token = tq * TN + c + lane;
+        store_tokens<2>(p, ch, lane < 2 && token < p.M ? p.x_scale[token] : 0.0f, 0, out, lane, tq * TN + c, sums);
       }
     }
     __syncwarp();
@@ -587,7 +616,7 @@ static cudaError_t set_attributes() {
     // compiler gave the kernel
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, i8_kernel<TN, PAIR>);
-    if (e == cudaSuccess && a.numRegs / 8 * 8 * Cfg<TN, PAIR>::THREADS < 128 * 56 + 128 * 96 + 256 * 168)
+    if (e == cudaSuccess && a.numRegs / 8 * 8 * Cfg<TN, PAIR>::THREADS < 128 * 56 + 128 * 96 + 256 * 176)
       e = cudaErrorLaunchOutOfResources;
   }
   return e;
@@ -607,7 +636,6 @@ static cudaError_t kernel_setup() {
     if (err == cudaSuccess) err = set_attributes<64>();
     if (err == cudaSuccess) err = set_attributes<32>();
     if (err == cudaSuccess) err = set_attributes<16>();
-    if (err == cudaSuccess) err = few_setup();
     g_err[dev] = err;
   });
   return g_err[dev];

@@ -64,7 +64,7 @@ def test_plans():
     assert sg.lib.i8_linear_plan(1, 1, 1, -1, None, None) == -4
     assert sg.i8_linear_plan(1, 4096, 4096, 152) == {"tile_tokens": 0, "split": 1}
     assert sg.i8_linear_plan(8192, 14336, 4096, 152) == {"tile_tokens": 256, "split": 1}
-    for M in (33, 40, 100, 500, 5000):
+    for M in (3, 16, 40, 100, 500, 5000):
         for N in (1, 300, 4096):
             for K in (1, 700, 131071):
                 plan = sg.i8_linear_plan(M, N, K, 152)
