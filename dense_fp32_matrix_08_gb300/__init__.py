@@ -120,7 +120,7 @@ def _load() -> ctypes.CDLL:
     L.clip_grad_norm.argtypes = [i, vp, vp, vp, f, f, vp, vp, vp, vp]
     L.i8_quantize.argtypes = [i, i, vp, i, i, vp, i, vp, vp]
     L.i8_linear.argtypes = [i, i, i, vp, i, vp, vp, i, vp, vp, f, vp, i, i, vp]
-    L.i8_linear_plan.argtypes = [i] * 4 + [pi] * 2
+    L.i8_linear_plan.argtypes = [i] * 4 + [pi] * 3
     L.i8_linear_status.argtypes = [pi]
     for name in ("layer_norm_with", "layer_norm_backward_with", "i8_quantize_with", "i8_linear_with"):
         getattr(L, name).argtypes = [ctypes.c_char_p]

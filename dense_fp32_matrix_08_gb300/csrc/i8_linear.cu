@@ -45,7 +45,7 @@ constexpr int OUT_BYTES = 16 * OUT_PITCH * 4;
 
 // PAIR: two CTAs share a tile of 256 channels and TN tokens (tcgen05 cta_group::2), each with its 128
 // channels and half of the tokens.
-template <int TN_, bool PAIR_ = false>
+template <int TN_, bool PAIR_>
 struct Cfg {
   static constexpr int TN = TN_;
   static constexpr bool PAIR = PAIR_;
@@ -54,31 +54,31 @@ struct Cfg {
   static constexpr int GROUPS = TN >= 64 ? 2 : 1;  // epilogue groups of four warps
   static constexpr int COLS = TN / GROUPS;         // tokens of a group
   static constexpr int EPI_WARPS = 4 * GROUPS;
-  // Two converter groups take turns with the blocks of k where Q is converted, too. (Else one is enough,
-  // and the registers of 64 sums per thread are for one only: with two 128 x 14336 x 4096 took 24.9 us
-  // for 23.1.)
-  static constexpr int CONV_GROUPS = CONVERT ? 2 : 1;
+  // Two converter groups take turns with the blocks of k: 384 x 14336 x 4096 takes a pair 39.5 us, with
+  // one group 43.3. (A single CTA with 64 sums per thread has no registers for the second: 24 us for 22.)
+  static constexpr int CONV_GROUPS = TN == 128 && !PAIR ? 1 : 2;
   static constexpr int FIRST_EPI = 4 + 4 * CONV_GROUPS;  // warp
   static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+  // A pair's registers per thread: control warps, converters, epilogue (where the sums are more than an
+  // even share leaves room for).
+  static constexpr int CONTROL_REGS = 56, CONV_REGS = 88, EPI_REGS = 120;
+  static constexpr int REGS = 128 * CONTROL_REGS + 128 * CONV_GROUPS * CONV_REGS + 32 * EPI_WARPS * EPI_REGS;
   static constexpr int Q_BYTES = QN * BK * (CONVERT ? 1 : 2);
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = CONVERT ? (TN == 64 ? 4 : 8) : 4;
+  static constexpr int STAGES = CONVERT ? (TN == 64 ? 4 : 8) : PAIR ? 6 : 4;
   static constexpr int NA = 4;                     // blocks of P in TMEM (and of Q, where converted)
   static constexpr int A_COLS = BK / 2;            // columns of one
   static constexpr int H_BYTES = CONVERT ? QN * BK * 2 : 0;
-  // A pair's tile is computed in two parts of 128 tokens with one accumulator each: one is emptied
-  // while the tensor core works on the other's last block. Else there are two accumulators.
-  static constexpr int PARTS = PAIR ? 2 : 1;
-  static constexpr int PART = TN / PARTS;
-  static constexpr int NBUF = PAIR ? 1 : 2;
-  static constexpr int ACC_COLS = PART < 32 ? 32 : PART;
-  static constexpr int ACC_WARPS = PAIR ? 8 : EPI_WARPS;  // readers of an accumulator
+  static constexpr int NBUF = 2;                   // accumulators
+  static constexpr int ACC_COLS = TN < 32 ? 32 : TN;
+  static constexpr int ACC_WARPS = EPI_WARPS * (PAIR ? 2 : 1);  // readers of an accumulator
   static constexpr int TMEM_COLS = 512;
-  static constexpr int BARS = 3 * STAGES + 2 * NA + 2 * PARTS * NBUF;
+  static constexpr int BARS = 3 * STAGES + 2 * NA + 2 * NBUF;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NA * H_BYTES + EPI_WARPS * OUT_BYTES + 8 * BARS + 16;
   // (a barrier tells only odd uses of a slot from even ones: whoever waits for it must see them all)
   static_assert(STAGES % CONV_GROUPS == 0 && NA % CONV_GROUPS == 0, "each slot belongs to one group");
-  static_assert(PARTS * NBUF * ACC_COLS + NA * A_COLS <= TMEM_COLS, "TMEM columns");
+  static_assert(!PAIR || REGS <= 65536 / THREADS / 8 * 8 * THREADS, "registers that a launch brings");
+  static_assert(NBUF * ACC_COLS + NA * A_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(BP * TN * 4 <= STAGES * STAGE_BYTES, "a partial tile fits in the ring");
   static_assert(STAGE_BYTES % 1024 == 0 && H_BYTES % 1024 == 0, "swizzled tiles");
@@ -105,11 +105,11 @@ struct Channel {
   float scale, bias;
 };
 
-// Sums of this lane's channel and `count` (16 or 2) neighbouring tokens, finished and stored. What is not
+// Sums of this lane's channel and COUNT neighbouring tokens, finished and stored. What is not
 // unrolled over the sums is not unrolled at all: the epilogue shares the instruction caches with the
 // converters (all inlined and unrolled it took half of their time).
 // sx: the scale of token `token` + lane - from in each lane.
-template <int COUNT>
+constexpr int COUNT = 16;
 __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, float sx, int from, float *buf,
                                              int lane, int token, const int (&sums)[COUNT]) {
   const int rows = min(COUNT, p.M - token);
@@ -119,7 +119,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
         fmaf((float)sums[j], c.scale * __shfl_sync(0xffffffffu, sx, from + j), c.bias);
   __syncwarp();
   const int col0 = c.at - lane;
-  if (p.d.vec && COUNT == 16 && p.d.type != tcx::OUT_F32) {
+  if (p.d.vec && p.d.type != tcx::OUT_F32) {
     const int col = (lane & 3) * 8, cols = min(8, p.N - col0 - col);
 #pragma unroll 1
     for (int r = lane >> 2; r < rows; r += 8) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
         for (int j = 0; j < cols; ++j) tcx::store_out(d, p.d.type, j, v[j]);
       }
     }
-  } else if (p.d.vec && COUNT == 16) {
+  } else if (p.d.vec) {
     const int col = (lane & 7) * 4, cols = min(4, p.N - col0 - col);
 #pragma unroll 1
     for (int r = lane >> 3; r < rows; r += 4) {
@@ -152,6 +152,10 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
     float *d = static_cast<float *>(p.d.ptr) + token * p.d.ld + c.at;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) d[r * p.d.ld] = buf[r * OUT_PITCH + lane];
+  } else if (c.at < p.N && p.d.beta == 0.0f) {
+    uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + token * p.d.ld + c.at;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) d[r * p.d.ld] = (uint16_t)tcx::pack_out(p.d.type, buf[r * OUT_PITCH + lane], 0.0f);
   } else if (c.at < p.N) {
 #pragma unroll 2
     for (int r = 0; r < rows; ++r)
@@ -163,10 +167,6 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
 __device__ __forceinline__ Channel channel_at(const Params &p, int at) {
   const bool in = at < p.N;
   return {at, in ? p.w_scale[at] : 0.0f, in && p.d.bias ? p.d.bias[at] : 0.0f};
-}
-
-__device__ __forceinline__ int ld_cluster_int(uint32_t local, uint32_t rank) {
-  return __float_as_int(tcx::ld_cluster1(local, rank));
 }
 
 // Warp 0: TMA producer, warp 1: MMA issuer (one elected lane of each), then the converters, one row of P
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   const uint32_t p_full = out_at + C::EPI_WARPS * OUT_BYTES;
   const uint32_t q_full = p_full + 8 * C::STAGES, empty = q_full + 8 * C::STAGES;
   const uint32_t a_full = empty + 8 * C::STAGES, a_empty = a_full + 8 * C::NA;
-  const uint32_t acc_full = a_empty + 8 * C::NA, acc_empty = acc_full + 8 * C::PARTS * C::NBUF;
-  const uint32_t tmem_slot = acc_empty + 8 * C::PARTS * C::NBUF;
+  const uint32_t acc_full = a_empty + 8 * C::NA, acc_empty = acc_full + 8 * C::NBUF;
+  const uint32_t tmem_slot = acc_empty + 8 * C::NBUF;
   volatile uint32_t *tmem_slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
 
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       mbar_init(a_full + 8 * a, PAIR ? 8 : 4);
       mbar_init(a_empty + 8 * a, 1);
     }
-    for (int b = 0; b < C::PARTS * C::NBUF; ++b) {
+    for (int b = 0; b < C::NBUF; ++b) {
       mbar_init(acc_full + 8 * b, 1);
       mbar_init(acc_empty + 8 * b, C::ACC_WARPS);
     }
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   if constexpr (PAIR) cluster_sync_all();  // the other CTA's barriers are initialised
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);  // (uniform)
-  const uint32_t a_tmem = tmem + C::PARTS * C::NBUF * C::ACC_COLS;
+  const uint32_t a_tmem = tmem + C::NBUF * C::ACC_COLS;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   // (every CTA of the grid is resident, so the next launch may take what room is left)
   griddep_launch_dependents();
@@ -247,8 +247,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   };
 
   if (warp < 4) {
-    // a pair's 512 threads x 128 registers at launch >= 128 x 56 + 128 x 96 + 256 x 176
-    if constexpr (PAIR) reg_dealloc<56>();
+    if constexpr (PAIR) reg_dealloc<C::CONTROL_REGS>();
     if (warp == 0) {
       // ---- TMA producer: the k blocks of this CTA's tiles, in order, through the ring of stages
       Ring<C::STAGES> st;
@@ -313,45 +312,34 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
           const uint32_t a = a_tmem + ar.slot * C::A_COLS;
           const uint64_t qd =
               qd0 + (C::CONVERT ? ar.slot * (uint32_t)(C::H_BYTES >> 4) : st.slot * (uint32_t)(C::STAGE_BYTES >> 4));
-#pragma unroll
-          for (int part = 0; part < C::PARTS; ++part) {
-            const uint32_t which = part * C::NBUF + buf.slot;
-            if (ok && begin) {
-              ok = __all_sync(0xffffffffu, wait_short(acc_empty + 8 * which, buf.parity ^ 1u));
-              fence_after();
-            }
-            if (ok && elect_one()) {
-              const uint32_t d = tmem + which * C::ACC_COLS;
-#pragma unroll
-              for (uint32_t kk = 0; kk < BK / 16; ++kk) {
-                // 64 of k per box of 128-byte rows; a part's 64 rows of this CTA's tokens
-                const uint64_t q = qd + ((kk / 4 * C::QN * 128 + part * 64 * 128 + kk % 4 * 32) >> 4);
-                const uint32_t more = !begin || kk != 0;
-                if constexpr (PAIR)
-                  mma_f16_tmem_pair(d, a + kk * 8, q, p.idesc, more);
-                else
-                  mma_f16_tmem(d, a + kk * 8, q, p.idesc, more);
-              }
-              if (part == C::PARTS - 1) {
-                // (these before the accumulator's: who has seen the last accumulator knows that no
-                // arrival is to come)
-                if constexpr (PAIR) {
-                  mma_commit_pair(a_empty + 8 * ar.slot);
-                  mma_commit_pair(empty + 8 * st.slot);
-                } else {
-                  mma_commit(a_empty + 8 * ar.slot);
-                  if constexpr (!C::CONVERT) mma_commit(empty + 8 * st.slot);
-                }
-              }
-              if (end) {
-                if constexpr (PAIR)
-                  mma_commit_pair(acc_full + 8 * which);
-                else
-                  mma_commit(acc_full + 8 * which);
-              }
-            }
-            __syncwarp();
+          if (ok && begin) {
+            ok = __all_sync(0xffffffffu, wait_short(acc_empty + 8 * buf.slot, buf.parity ^ 1u));
+            fence_after();
           }
+          if (ok && elect_one()) {
+            const uint32_t d = tmem + buf.slot * C::ACC_COLS;
+#pragma unroll
+            for (uint32_t kk = 0; kk < BK / 16; ++kk) {
+              // 64 of k per box of 128-byte rows
+              const uint64_t q = qd + ((kk / 4 * C::QN * 128 + kk % 4 * 32) >> 4);
+              const uint32_t more = !begin || kk != 0;
+              if constexpr (PAIR)
+                mma_f16_tmem_pair(d, a + kk * 8, q, p.idesc, more);
+              else
+                mma_f16_tmem(d, a + kk * 8, q, p.idesc, more);
+            }
+            // (the accumulator's last: who has seen the last accumulator knows that no arrival is to come)
+            if constexpr (PAIR) {
+              mma_commit_pair(a_empty + 8 * ar.slot);
+              mma_commit_pair(empty + 8 * st.slot);
+              if (end) mma_commit_pair(acc_full + 8 * buf.slot);
+            } else {
+              mma_commit(a_empty + 8 * ar.slot);
+              if constexpr (!C::CONVERT) mma_commit(empty + 8 * st.slot);
+              if (end) mma_commit(acc_full + 8 * buf.slot);
+            }
+          }
+          __syncwarp();
           if (!ok) {
             if (lane == 0) atomicCAS(&g_i8_status, 0, 2);
             break;
@@ -364,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     }
   } else if (warp < C::FIRST_EPI) {
     // ---- converters
-    if constexpr (PAIR) reg_dealloc<96>();
+    if constexpr (PAIR) reg_dealloc<C::CONV_REGS>();
     const int row = threadIdx.x % 128;  // of P
     int turns = (warp - 4) >> 2;        // blocks until this group's next one
     const uint32_t a_lane = a_tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -436,13 +424,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
     }
   } else {
     // ---- epilogue
-    if constexpr (PAIR) reg_alloc<176>();
+    if constexpr (PAIR) reg_alloc<C::EPI_REGS>();
     const int grp = (warp - C::FIRST_EPI) >> 2, quad = warp & 3;
-    // a group's tokens: COLS neighbouring ones, or one part of a pair's tile, 64 from each CTA's half
-    const uint32_t which0 = PAIR ? grp * C::NBUF : 0;
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + which0 * C::ACC_COLS +
-                               (PAIR ? 0 : (uint32_t)(grp * C::COLS));
-    const uint32_t full0 = acc_full + 8 * which0, empty0 = acc_empty + 8 * which0;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(grp * C::COLS);
     float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - C::FIRST_EPI) * OUT_BYTES);
     Ring<C::NBUF> buf;
     bool ok = true;
@@ -450,9 +434,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
       int tp, tq;
       tile_at(t, tp, tq);
       // Token of column c, and what the results are multiplied with: read now, for the end.
-      const auto token_of = [&](int c) {
-        return tq * TN + (PAIR ? (c / 64) * 128 + grp * 64 + c % 64 : grp * C::COLS + c);
-      };
+      const auto token_of = [&](int c) { return tq * TN + grp * C::COLS + c; };
       const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
       float sx[(C::COLS + 31) / 32];
 #pragma unroll
@@ -464,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
 #pragma unroll
       for (int j = 0; j < C::COLS; ++j) acc[j] = 0;
       for (int kb = kb0; kb < kb1; kb += CHUNK) {
-        ok = __all_sync(0xffffffffu, wait_short(full0 + 8 * buf.slot, buf.parity));
+        ok = __all_sync(0xffffffffu, wait_short(acc_full + 8 * buf.slot, buf.parity));
         if (!ok) {
           if (lane == 0) atomicCAS(&g_i8_status, 0, 3);
           break;
@@ -482,9 +464,9 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
             __syncwarp();
             if (lane == 0) {
               if constexpr (PAIR)
-                arrive_in(in_cta(empty0 + 8 * buf.slot, 0));
+                arrive_in(in_cta(acc_empty + 8 * buf.slot, 0));
               else
-                mbar_arrive(empty0 + 8 * buf.slot);
+                mbar_arrive(acc_empty + 8 * buf.slot);
             }
           }
 #pragma unroll
@@ -499,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
           int sums[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) sums[j] = acc[c + j];
-          if (token_of(c) < p.M) store_tokens<16>(p, ch, sx[c / 32], c % 32, out, lane, token_of(c), sums);
+          if (token_of(c) < p.M) store_tokens(p, ch, sx[c / 32], c % 32, out, lane, token_of(c), sums);
         }
       } else {
         // partial tile -> the ring, whose every reader has finished (the last accumulator is
@@ -512,35 +494,61 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   }
   __syncwarp();
   if (S > 1) {
-    // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp two of them and 32
-    // channels at a time
+    // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp AT of them at a time, a lane
+    // four neighbouring channels of each
+    constexpr int AT = TN >= 128 ? 1 : 2;  // (for the registers)
     cluster_sync_all();
     if (warp >= C::FIRST_EPI) {
       int tp, tq;
       tile_at(first, tp, tq);
-      const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);  // (TN / S is even)
-      const int items = c1 > c0 ? (c1 - c0 + 1) / 2 * 4 : 0;
-      for (int i = warp - C::FIRST_EPI; i < items; i += C::EPI_WARPS) {
-        const int quad = i & 3, c = c0 + i / 4 * 2;
-        const Channel ch = channel_at(p, tp * BP + quad * 32 + lane);
-        int v[2][MAX_CLUSTER];
+      const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);
+      const int n0 = tp * BP + lane * 4;
+      float ws[4], bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Channel ch = channel_at(p, n0 + i);
+        ws[i] = ch.scale;
+        bias[i] = ch.bias;
+      }
+      for (int c = c0 + (warp - C::FIRST_EPI) * AT; c < c1; c += C::EPI_WARPS * AT) {
+        float4 v[AT][MAX_CLUSTER];
 #pragma unroll
         for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
-          if (q < S) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              v[j][q] = ld_cluster_int(base + (uint32_t)((c + j) * BP + quad * 32 + lane) * 4, (uint32_t)q);
+          for (int j = 0; j < AT; ++j)
+            if (q < S && c + j < c1) v[j][q] = ld_cluster4(base + (uint32_t)((c + j) * BP + lane * 4) * 4, (uint32_t)q);
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+          if (c + j >= c1) break;
+          int sums[4] = {};
+#pragma unroll
+          for (int q = 0; q < MAX_CLUSTER; ++q)
+            if (q < S) {
+              sums[0] += __float_as_int(v[j][q].x);
+              sums[1] += __float_as_int(v[j][q].y);
+              sums[2] += __float_as_int(v[j][q].z);
+              sums[3] += __float_as_int(v[j][q].w);
+            }
+          // (a load that nothing waits for could still be under way when the other CTA leaves)
+          asm volatile("" ::"r"(sums[0]), "r"(sums[1]), "r"(sums[2]), "r"(sums[3]));
+          const int token = tq * TN + c + j;
+          const float sx = p.x_scale[token];
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = fmaf((float)sums[i], ws[i] * sx, bias[i]);
+          const long long at = token * p.d.ld + n0;
+          if (p.d.vec && n0 + 4 <= p.N) {
+            if (p.d.type == OUT_F32)
+              *reinterpret_cast<float4 *>(static_cast<float *>(p.d.ptr) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            else
+              *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.d.ptr) + at) =
+                  make_uint2(pack_out(p.d.type, y[0], y[1]), pack_out(p.d.type, y[2], y[3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n0 + i < p.N) finish_out(p.d.ptr, p.d.type, at + i, y[i], p.d.beta);
           }
-        int sums[2] = {v[0][0], v[1][0]};
-#pragma unroll
-        for (int q = 1; q < MAX_CLUSTER; ++q)
-          if (q < S) sums[0] += v[0][q], sums[1] += v[1][q];
-        // (both are used whatever is stored: a load that nothing waits for could still be under way
-        // when the other CTA leaves)
-        asm volatile("" ::"r"(sums[0]), "r"(sums[1]));
-        float *out = reinterpret_cast<float *>(smem_raw + (out_at - raw) + (warp - C::FIRST_EPI) * OUT_BYTES);
-        const int token = tq * TN + c + lane;
-        store_tokens<2>(p, ch, lane < 2 && token < p.M ? p.x_scale[token] : 0.0f, 0, out, lane, tq * TN + c, sums);
+        }
       }
     }
     __syncwarp();
@@ -571,29 +579,39 @@ __global__ void i8_bias_kernel(int M, int N, const Result d) {
 // Host side
 
 struct Plan {
-  int tn, split;       // tn = 0: few_kernel
+  int tn;              // tokens per tile; 0: few_kernel
+  bool pair;           // two CTAs per tile
+  int split;           // CTAs per tile, each with its part of k
 };
 
+// Estimated time of a plan in microseconds, fitted to times measured on GB300 with every plan forced on 128
+// shapes (9 to 8192 rows, N and K of 512 to 14336): a call, each block of k, each round of tiles and a
+// cluster's exchange. The estimate's choice is within 0.5% of the best plan on average, 14% at most.
+struct Cost {
+  int tn;
+  bool pair;
+  double call, block, round, exchange;
+};
+static const Cost kCosts[] = {{128, true, 5.30, 0.320, 1.87, 0.0}, {128, false, 4.89, 0.412, 1.12, 2.21},
+                              {64, false, 2.58, 0.438, 0.69, 1.73}, {32, false, 2.86, 0.325, 0.25, 1.17},
+                              {16, false, 2.28, 0.294, 0.22, 1.17}};
+
 static Plan make_plan(int M, int N, int K, int sms) {
-  if (M <= kFewRows) return {0, 1};
+  if (M <= kFewRows) return {0, false, 1};
   const int KB = (int)ceil_div(K, BK);
-  Plan best{128, 1};
+  Plan best{128, true, 1};
   double best_cost = 1e300;
-  static const int tns[5] = {256, 128, 64, 32, 16};
-  static const double block[5] = {18, 13, 9, 7, 6};
-  for (int i = 0; i < 5; ++i) {
-    const int tn = tns[i];
-    const bool pair = tn == 256;
-    const long long tiles = (long long)ceil_div(N, pair ? 2 * BP : BP) * ceil_div(M, tn);
-    for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
-      if (S > 1 && (pair || S > KB || tn / S < 2 || tiles * S > (S == 8 ? 96 : sms))) break;
-      const int at_once = pair ? sms / 2 : sms;
-      const long long per_sm = (tiles * S + at_once - 1) / at_once;
-      const double cost = per_sm * (block[i] * ((KB + S - 1) / S) + 0.25 * tn / S) +
-                          (S > 1 ? 25.0 + 0.3 * tn : 0.0) + (tn >= 128 ? 40.0 : 0.0);
+  for (const Cost &c : kCosts) {
+    const long long tiles = ceil_div(N, c.pair ? 2 * BP : BP) * ceil_div(M, c.tn);
+    const int at_once = c.pair ? sms / 2 : sms;
+    for (int S = 1; S <= (c.pair ? 1 : MAX_CLUSTER); S *= 2) {
+      // (clusters of 8 sit in one GPC each: more than about 12 of them do not run at once)
+      if (S > 1 && (S > KB || tiles * S > (S == 8 ? 96 : sms))) break;
+      const double cost = c.call + (double)ceil_div(tiles * S, at_once) * (c.block * ((KB + S - 1) / S) + c.round) +
+                          (S > 1 ? c.exchange : 0.0);
       if (cost < best_cost) {
         best_cost = cost;
-        best = {tn, S};
+        best = {c.tn, c.pair, S};
       }
     }
   }
@@ -609,14 +627,14 @@ static cudaError_t launch(const CUtensorMap &mp, const CUtensorMap &mq, const Pa
 
 template <int TN, bool PAIR = false>
 static cudaError_t set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(i8_kernel<TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<TN, PAIR>::SMEM_BYTES);
+  using C = Cfg<TN, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(i8_kernel<TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e == cudaSuccess && PAIR) {
     // the registers that the warpgroups ask for must be there: what a launch brings is what the
     // compiler gave the kernel
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, i8_kernel<TN, PAIR>);
-    if (e == cudaSuccess && a.numRegs / 8 * 8 * Cfg<TN, PAIR>::THREADS < 128 * 56 + 128 * 96 + 256 * 176)
+    if (e == cudaSuccess && a.numRegs / 8 * 8 * C::THREADS < C::REGS)
       e = cudaErrorLaunchOutOfResources;
   }
   return e;
@@ -631,7 +649,7 @@ static cudaError_t kernel_setup() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(g_once[dev], [dev]() {
-    cudaError_t err = set_attributes<256, true>();
+    cudaError_t err = set_attributes<128, true>();
     if (err == cudaSuccess) err = set_attributes<128>();
     if (err == cudaSuccess) err = set_attributes<64>();
     if (err == cudaSuccess) err = set_attributes<32>();
@@ -650,7 +668,7 @@ static cudaError_t run(const Plan &pl, int M, int N, int K, const Operand &x, co
   p.w_scale = w.scale;
   p.x_scale = x.scale;
   p.d = d;
-  const bool pair = pl.tn == 256;
+  const bool pair = pl.pair;
   const long long tiles_p = ceil_div(N, BP), tiles_q = ceil_div(M, pl.tn);
   if (tiles_p * tiles_q > 0x7fffffffLL / MAX_CLUSTER) return cudaErrorInvalidConfiguration;
   p.tiles_p = (int)tiles_p;
@@ -659,7 +677,7 @@ static cudaError_t run(const Plan &pl, int M, int N, int K, const Operand &x, co
   p.split = pl.split;
   // instruction descriptor: D in FP32 (bits 4-5 = 1), FP16 operands, k contiguous, N / 8 (bits 17-22),
   // M / 16 (24-28)
-  p.idesc = (1u << 4) | ((uint32_t)((pair ? pl.tn / 2 : pl.tn) >> 3) << 17) |
+  p.idesc = (1u << 4) | ((uint32_t)(pl.tn >> 3) << 17) |
             ((uint32_t)((pair ? 2 * BP : BP) >> 4) << 24);
   CUtensorMap mp, mq;
   if (!encode_map_2d_narrow(&mp, w.q, 1, N, K, w.ld, BP)) return cudaErrorInvalidValue;
@@ -680,8 +698,7 @@ static cudaError_t run(const Plan &pl, int M, int N, int K, const Operand &x, co
                                        : std::min<long long>(tiles_p * tiles_q, sms));
   if (e == cudaSuccess)
     switch (pl.tn) {
-      case 256: e = launch<256, true>(mp, mq, p, grid, stream); break;
-      case 128: e = launch<128>(mp, mq, p, grid, stream); break;
+      case 128: e = pair ? launch<128, true>(mp, mq, p, grid, stream) : launch<128>(mp, mq, p, grid, stream); break;
       case 64: e = launch<64>(mp, mq, p, grid, stream); break;
       case 32: e = launch<32>(mp, mq, p, grid, stream); break;
       default: e = launch<16>(mp, mq, p, grid, stream);
@@ -740,7 +757,7 @@ extern "C" int i8_linear_with(const i8_linear_args *a) {
                    a->d_type, a->ldd, a->stream);
 }
 
-extern "C" int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens, int *split) {
+extern "C" int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens, int *tile_channels, int *split) {
   if (M < 1) return -1;
   if (N < 1) return -2;
   if (K < 1 || K > i8::LARGEST_K) return -3;
@@ -752,6 +769,7 @@ extern "C" int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens
   }
   const i8::Plan pl = i8::make_plan(M, N, K, sms);
   if (tile_tokens) *tile_tokens = pl.tn;
+  if (tile_channels) *tile_channels = pl.tn == 0 ? 0 : pl.pair ? 2 * i8::BP : i8::BP;
   if (split) *split = pl.split;
   return 0;
 }

@@ -109,12 +109,12 @@ def i8_linear(x, x_scale, w, w_scale, bias=None, *, beta=0.0, out=None, out_dtyp
 
 
 def i8_linear_plan(M, N, K, num_sms=0) -> dict:
-    """How i8_linear runs a product: {"tile_tokens", "split"} (see the header)."""
-    v = [ctypes.c_int(0) for _ in range(2)]
+    """How i8_linear runs a product: {"tile_tokens", "tile_channels", "split"} (see the header)."""
+    v = [ctypes.c_int(0) for _ in range(3)]
     rc = lib.i8_linear_plan(M, N, K, num_sms, *[ctypes.byref(x) for x in v])
     if rc != 0:
         raise SgemmError(rc, "i8_linear_plan")
-    return {"tile_tokens": v[0].value, "split": v[1].value}
+    return {"tile_tokens": v[0].value, "tile_channels": v[1].value, "split": v[2].value}
 
 
 def i8_linear_status() -> tuple[int, int]:

@@ -83,11 +83,11 @@ int i8_linear_with(const i8_linear_args *args);
 
 /* How i8_linear runs a product on a GPU with num_sms SMs (0: the current device; without one a whole
  * GB300). Any pointer may be NULL.
- *   tile_tokens  rows of x per tile: 0 for the kernel of few rows without tensor cores, else 16, 32, 64,
- *                128, or 256 for tiles of 256 x 256 by pairs of blocks
- *   split        blocks that share a tile's sum, each with its part of k
+ *   tile_tokens    rows of x per tile: 16, 32, 64 or 128; 0 for the kernel of one or two rows, which has none
+ *   tile_channels  rows of w per tile: 128, or 256 where two blocks share a tile (0 as above)
+ *   split          blocks that share a tile's sum, each with its part of k
  * Returns 0 or -i for the first illegal argument (M, N and K of 1 or more). */
-int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens, int *split);
+int i8_linear_plan(int M, int N, int K, int num_sms, int *tile_tokens, int *tile_channels, int *split);
 
 /* Reads and clears the device status word of i8_linear (synchronising copy on the legacy stream: wait
  * first for calls on streams that do not wait for it): 0 = fine, 1 - 4 = a wait gave up after about a

@@ -12,6 +12,8 @@ of its type.
 import pytest
 import torch
 
+from i8_plans import SHAPES as PLANS
+
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
@@ -181,6 +183,15 @@ SHAPES = ([(m, 260, 333) for m in (1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 31, 33, 6
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
 def test_product_shapes(shape):
     check(*shape, bias=shape[0] % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("plan", PLANS, ids=lambda p: "-".join(map(str, p)))
+def test_product_every_plan(plan, dtype):
+    """Each tile and split, with a result at any alignment, one that is added to, and a bias."""
+    M, N, K = PLANS[plan]
+    check(M, N, K, dtype=dtype, bias=True)
+    check(M, N + 7, K, dtype=dtype, beta=0.5, extra=48)
 
 
 @pytest.mark.parametrize("shape", [(2600, 2700, 300), (2305, 4400, 1100), (2433, 4353, 129), (3000, 130, 3000),

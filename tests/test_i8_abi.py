@@ -2,12 +2,14 @@
 exported symbols, refusals of illegal arguments, which come before any CUDA call, plans, and the bounded
 waits of the kernel's source."""
 import os
+import random
 import re
 
 import pytest
 import torch
 
 import dense_fp32_matrix_08_gb300 as sg
+from i8_plans import SHAPES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20  # a 16-byte aligned address that is never dereferenced
@@ -60,17 +62,28 @@ def test_empty_product_needs_no_pointers():
 
 def test_plans():
     for M, N, K, code in ((0, 1, 1, -1), (1, 0, 1, -2), (1, 1, 0, -3), (1, 1, 131072, -3)):
-        assert sg.lib.i8_linear_plan(M, N, K, 152, None, None) == code
-    assert sg.lib.i8_linear_plan(1, 1, 1, -1, None, None) == -4
-    assert sg.i8_linear_plan(1, 4096, 4096, 152) == {"tile_tokens": 0, "split": 1}
-    assert sg.i8_linear_plan(8192, 14336, 4096, 152) == {"tile_tokens": 256, "split": 1}
+        assert sg.lib.i8_linear_plan(M, N, K, 152, None, None, None) == code
+    assert sg.lib.i8_linear_plan(1, 1, 1, -1, None, None, None) == -4
+    assert sg.i8_linear_plan(1, 4096, 4096, 152) == {"tile_tokens": 0, "tile_channels": 0, "split": 1}
+    assert sg.i8_linear_plan(8192, 14336, 4096, 152) == {"tile_tokens": 128, "tile_channels": 256, "split": 1}
     for M in (3, 16, 40, 100, 500, 5000):
         for N in (1, 300, 4096):
             for K in (1, 700, 131071):
                 plan = sg.i8_linear_plan(M, N, K, 152)
                 blocks = -(-K // 128)
-                assert plan["tile_tokens"] in (16, 32, 64, 128, 256) and plan["split"] in (1, 2, 4, 8)
-                assert plan["split"] <= blocks and (plan["split"] == 1 or plan["tile_tokens"] < 256)
+                assert plan["tile_tokens"] in (16, 32, 64, 128) and plan["split"] in (1, 2, 4, 8)
+                assert plan["tile_channels"] == 128 or plan["tile_tokens"] == 128
+                assert plan["split"] <= blocks and (plan["split"] == 1 or plan["tile_channels"] == 128)
+
+
+def test_every_plan_has_a_shape():
+    """The listed shapes run as they say, and a search finds no other way to run."""
+    for plan, shape in SHAPES.items():
+        assert tuple(sg.i8_linear_plan(*shape, 152).values()) == plan
+    r = random.Random(3)
+    found = {tuple(sg.i8_linear_plan(*(min(131071, int(2 ** r.uniform(0, top))) for top in (13.5, 14.5, 17)), 152)
+                   .values()) for _ in range(20000)}
+    assert found <= set(SHAPES), found - set(SHAPES)
 
 
 def test_warps_leave_their_waits_together():
