@@ -18,8 +18,8 @@
 namespace sgemm {
 namespace gc {
 
-constexpr int kPiece = 16384;  // elements: 64 per thread
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kPerSm = 4;  // CTAs per SM
+constexpr int kPiece = 64 * kThreads;       // elements
 
 struct Array {
   const void *in;
@@ -50,13 +50,13 @@ __device__ __forceinline__ const Array &array_of(const Params<MOST> &p, int at) 
   return p.a[lo];
 }
 
-// What a thread takes at a time: 8 elements of 2048, as 16-byte accesses side by side: 8 neighbours, or
-// (FP32) 4 and the 4 that are 1024 further.
+// What a thread takes at a time: 8 elements of 8 kThreads, as 16-byte accesses side by side: 8 neighbours, or
+// (FP32) 4 and the 4 that are 4 kThreads further.
 __device__ __forceinline__ int place(int type, int j) {
   return type == GC_F32 ? threadIdx.x * 4 + (j >= 4 ? kThreads * 4 - 4 : 0) + j : threadIdx.x * 8 + j;
 }
 
-// Elements place(0 .. 7) of the 2048 from i on; those that do not exist are zero.
+// Elements place(0 .. 7) from i on; those that do not exist are zero.
 __device__ __forceinline__ void load8(const Array &a, long long i, bool vec, float (&v)[8]) {
   if (vec && i + kThreads * 8 <= a.n) {
     if (a.type == GC_F32) {
@@ -145,39 +145,45 @@ __device__ __forceinline__ double thread_squares(const Array &a, long long at, b
   return (double)s * (up > 1.0f ? 0x1p-200 : 0x1p140);
 }
 
-// Sum over the CTA, in each of its threads.
-__device__ __forceinline__ double cta_sum(double v) {
-  __shared__ double part[kThreads / 32];
+// Sum of `count` numbers by a warp, in each of its lanes. (64-bit additions run at two per cycle and SM: one
+// warp of a CTA makes them.)
+__device__ __forceinline__ double warp_sum(const double *v, int count) {
+  double s = 0.0;
+  for (int i = threadIdx.x & 31; i < count; i += 32) s += v[i];
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v += part[w];
-  return v;
+  for (int d = 1; d < 32; d *= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant__ Params<MOST> p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) square_kernel(const __grid_constant__ Params<MOST> p) {
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   double sum = 0.0;
   for (int at = blockIdx.x; at < p.pieces; at += gridDim.x) {
     const Array &a = array_of(p, at);
     sum += thread_squares(a, (long long)(at - a.first) * kPiece, aligned16(a.in));
   }
-  sum = cta_sum(sum);
-  if (threadIdx.x == 0) p.sums[p.slot + blockIdx.x] = sum;
+  __shared__ double part[kThreads];
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    sum = warp_sum(part, kThreads);
+    if (threadIdx.x == 0) p.sums[p.slot + blockIdx.x] = sum;
+  }
   griddep_launch_dependents();
 }
 
 // WRITE: also the scaled arrays; else the norm only (one CTA).
 template <int MOST, bool WRITE>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Params<MOST> p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_constant__ Params<MOST> p) {
   griddep_wait();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < p.slots; i += kThreads) sum += p.sums[i];
-  const double norm = sqrt(cta_sum(sum));
+  __shared__ double total;
+  if (threadIdx.x < 32) {
+    const double sum = warp_sum(p.sums, p.slots);
+    if (threadIdx.x == 0) total = sqrt(sum);
+  }
+  __syncthreads();
+  const double norm = total;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.norm) *p.norm = (float)norm;
   if constexpr (WRITE) {
     const double ratio = (double)p.max_norm / (norm + (double)p.eps);
@@ -264,7 +270,7 @@ static int fill(Params<MOST> &p, const Call &c, int i) {
 
 template <int MOST>
 static cudaError_t run(const Call &c, int launches, int sms) {
-  const int most = 8 * sms;  // CTAs of a launch
+  const int most = kPerSm * sms;  // CTAs of a launch
   double *ws = nullptr;
   cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
                                           sizeof(double) * (size_t)most * launches, workspace_pool(), c.stream);

@@ -80,6 +80,28 @@ __device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uin
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// q of chunk c, of which n elements exist.
+template <bool VEC, class T, class S>
+__device__ __forceinline__ void put(const Params &p, const Scale &s, const S &sh, uint8_t *to, int c, int n,
+                                    const Chunk<T> &v) {
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = s.finite ? rounded(v[j], s) : 0;
+  if (VEC && p.vec_q && n == 8) {
+    const uint32_t lo = four(q[0], q[1], q[2], q[3]), hi = four(q[4], q[5], q[6], q[7]);
+    if constexpr (S::E == 8) {
+      *reinterpret_cast<uint2 *>(to + sh.col(c, 0)) = make_uint2(lo, hi);
+    } else {
+      *reinterpret_cast<uint32_t *>(to + sh.col(c, 0)) = lo;
+      *reinterpret_cast<uint32_t *>(to + sh.col(c, 4)) = hi;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) to[sh.col(c, j)] = (uint8_t)q[j];
+  }
+}
+
 template <class T>
 constexpr int kDepth = T::SIZE == 4 ? 3 : 4;  // rows under way: 64 to 96 KB per SM
 
@@ -94,7 +116,6 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / 
   Ahead<T, TPR, CH, VEC, 1, kDepth<T>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
-  using S = Share<T, TPR, VEC>;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   ahead.begin();
   for (int turn = 0; base < p.rows; base += step, row += step, turn ^= 1) {
@@ -111,31 +132,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / 
       if (sh.t == 0) p.scale[row] = s.s;
       uint8_t *to = p.q + row * p.ldq;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        uint32_t q[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = s.finite ? rounded(v[c][j], s) : 0;
-        if (VEC && p.vec_q && n[c] == 8) {
-          const uint32_t lo = four(q[0], q[1], q[2], q[3]), hi = four(q[4], q[5], q[6], q[7]);
-          if constexpr (S::E == 8) {
-            *reinterpret_cast<uint2 *>(to + sh.col(c, 0)) = make_uint2(lo, hi);
-          } else {
-            *reinterpret_cast<uint32_t *>(to + sh.col(c, 0)) = lo;
-            *reinterpret_cast<uint32_t *>(to + sh.col(c, 4)) = hi;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n[c]) to[sh.col(c, j)] = (uint8_t)q[j];
-        }
-      }
+      for (int c = 0; c < CH; ++c) put<VEC>(p, s, sh, to, c, n[c], v[c]);
     }
   }
   griddep_launch_dependents();
 }
 
 // Rows of any length: a CTA reads its row twice.
-template <class T>
+template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
   __shared__ uint32_t part[2][32];
   griddep_wait();
@@ -143,15 +147,20 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const char *x = p.x + row * p.ldx;
     uint32_t m = 0;
-#pragma unroll 8
-    for (long long i = threadIdx.x; i < p.cols; i += 1024)
-      m = max(m, __float_as_uint(tcx::load_out(x, T::TYPE, i)) & 0x7fffffffu);
-    const Scale s = scale_of(row_max<1024>(m, part, turn));
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      Chunk<T> v;
+      sh.load(x + at * T::SIZE, 0, sh.count(0), v);
+#pragma unroll
+      for (int i = 0; i < T::W; ++i) m = larger<T>(m, v.w[i]);
+    });
+    const Scale s = scale_of(row_max<1024>(top<T>(m), part, turn));
     if (threadIdx.x == 0) p.scale[row] = s.s;
-    uint8_t *to = p.q + row * p.ldq;
-#pragma unroll 8
-    for (long long i = threadIdx.x; i < p.cols; i += 1024)
-      to[i] = s.finite ? (uint8_t)rounded(tcx::load_out(x, T::TYPE, i), s) : 0;
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      const int n = sh.count(0);
+      Chunk<T> v;
+      sh.load(x + at * T::SIZE, 0, n, v);
+      put<VEC>(p, s, sh, p.q + row * p.ldq + at, 0, n, v);
+    });
   }
   griddep_launch_dependents();
 }
@@ -181,7 +190,8 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
   if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
-  return launch_1d(quantize_long_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+  return launch_1d(vec ? quantize_long_kernel<T, true> : quantize_long_kernel<T, false>, std::min(p.rows, 2 * sms),
+                   1024, 0, 1, stream, p);
 }
 
 }  // namespace i8q

@@ -110,57 +110,64 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
   griddep_launch_dependents();
 }
 
-// Sum over the 1024 threads of a CTA, the same bits in each of them.
-__device__ __forceinline__ double cta_sum(double v, double *part) {
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-  for (int w = 1; w < 32; ++w) v += part[w];
-  return v;
-}
-
-// Rows of any length: a CTA reads its row three times (for the mean, the variance and the result).
-// 16 elements at a time are added up in FP32, the rest in 64 bits.
-template <class T>
+// Rows of any length: a CTA reads its row three times (for the mean, the variance and the result; from
+// caches after the first). 8 elements at a time are added up in FP32, the rest as Long. With 64-bit sums
+// 2048 x 16392 BF16 took 450 us, most of it in the CTA-wide ones.
+template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
-  __shared__ double part[32];
+  __shared__ Long part[2][32];
+  __shared__ float told[2];
   griddep_wait();
-  const auto at = [&](const char *row, long long i) {
-    return tcx::load_out(row, T::TYPE, i);
-  };
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const char *x = p.x + row * p.ldx;
-    double total = 0.0;
-    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
-      float s = 0.0f;
+    Long total;
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      Chunk<T> v;
+      sh.load(x + at * T::SIZE, 0, sh.count(0), v);
+      Two s = pair(v, 0);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s += i0 + j * 1024 < p.cols ? at(x, i0 + j * 1024) : 0.0f;
-      total += s;
-    }
-    const float mean = (float)(cta_sum(total, part) / p.cols);
-    total = 0.0;
-    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float d = i0 + j * 1024 < p.cols ? at(x, i0 + j * 1024) - mean : 0.0f;
-        s = fmaf(d, d, s);
-      }
-      total += s;
-    }
-    const float rstd = __frsqrt_rn((float)(cta_sum(total, part) / p.cols) + p.eps);
+      for (int i = 1; i < 4; ++i) s = add2(s, pair(v, i));
+      total.add(sum2(s));
+    });
+    total = cta_sum(total, part[0]);
     if (threadIdx.x == 0) {
-      if (p.mean) p.mean[row] = mean;
-      if (p.rstd) p.rstd[row] = rstd;
+      told[0] = total.over(p.cols);
+      if (p.mean) p.mean[row] = told[0];
     }
+    __syncthreads();
+    const Two minus = both(-told[0]);
+    total = Long();
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      const int n = sh.count(0);
+      Chunk<T> v;
+      sh.load(x + at * T::SIZE, 0, n, v);
+      Two s = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Two d = first(add2(pair(v, i), minus), i, n);
+        s = fma2(d, d, s);
+      }
+      total.add(sum2(s));
+    });
+    total = cta_sum(total, part[1]);
+    if (threadIdx.x == 0) {
+      told[1] = __frsqrt_rn(total.over(p.cols) + p.eps);
+      if (p.rstd) p.rstd[row] = told[1];
+    }
+    __syncthreads();
     char *y = p.y + row * p.ldy;
-#pragma unroll 4
-    for (long long i = threadIdx.x; i < p.cols; i += 1024)
-      tcx::store_out(y, T::TYPE, i,
-                     fmaf((at(x, i) - mean) * rstd, p.weight.at((int)i, 1.0f), p.bias.at((int)i, 0.0f)));
+    const Two r2 = both(told[1]);
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      const int n = sh.count(0);
+      Chunk<T> v, out;
+      sh.load(x + at * T::SIZE, 0, n, v);
+      Two w[4], b[4];
+      parameters(from(p.weight, at), sh, 0, n, 1.0f, w);
+      parameters(from(p.bias, at), sh, 0, n, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) set_pair(out, i, fma2(mul2(add2(pair(v, i), minus), r2), w[i], b[i]));
+      sh.store(y + at * T::SIZE, 0, n, out);
+    });
   }
   griddep_launch_dependents();
 }
@@ -190,7 +197,8 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
   if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
-  return launch_1d(norm_long_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+  return launch_1d(vec ? norm_long_kernel<T, true> : norm_long_kernel<T, false>, std::min(p.rows, 2 * sms), 1024, 0,
+                   1, stream, p);
 }
 
 }  // namespace ln

@@ -180,84 +180,77 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
   griddep_launch_dependents();
 }
 
-// Rows of any length, first half: the two sums along each row, 16 elements at a time in FP32, the
-// rest in 64 bits.
-template <class T>
+// Rows of any length, first half: the two sums along each row, 8 elements at a time in FP32, the rest as
+// Long.
+template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) along_kernel(const Params p) {
-  __shared__ double part[2][32];
+  __shared__ Long part[2][2][32];
   griddep_wait();
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const char *x = p.x + row * p.ldx, *dy = p.dy + row * p.lddy;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    double a = 0.0, b = 0.0;
-    for (long long i0 = threadIdx.x; i0 < p.cols; i0 += 16 * 1024) {
-      float sa = 0.0f, sb = 0.0f;
+    const Two minus = both(-p.mean[row]), r2 = both(p.rstd[row]);
+    Long a, b;
+    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+      const int n = sh.count(0);
+      Chunk<T> vx, vd;
+      sh.load(x + at * T::SIZE, 0, n, vx);
+      sh.load(dy + at * T::SIZE, 0, n, vd);
+      Two w[4], sa = 0, sb = 0;
+      parameters(rows::from(p.weight, at), sh, 0, n, 1.0f, w);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const long long i = i0 + j * 1024;
-        if (i < p.cols) {
-          const float g = tcx::load_out(dy, T::TYPE, i) * p.weight.at((int)i, 1.0f);
-          sa += g;
-          sb = fmaf(g, (tcx::load_out(x, T::TYPE, i) - mean) * rstd, sb);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const Two g = mul2(pair(vd, i), w[i]);
+        sa = add2(sa, g);
+        sb = fma2(g, mul2(add2(pair(vx, i), minus), r2), sb);
       }
-      a += sa;
-      b += sb;
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      a += __shfl_xor_sync(0xffffffffu, a, d);
-      b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = a, part[1][threadIdx.x >> 5] = b;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < 32; ++w) a += part[0][w], b += part[1][w];
-      p.along[row] = make_float2((float)(a / p.cols), (float)(b / p.cols));
-    }
+      a.add(sum2(sa));
+      b.add(sum2(sb));
+    });
+    a = cta_sum(a, part[turn][0]);
+    b = cta_sum(b, part[turn][1]);
+    if (threadIdx.x == 0) p.along[row] = make_float2(a.over(p.cols), b.over(p.cols));
   }
   griddep_launch_dependents();
 }
 
-// Second half: CTA (i, j) takes 1024 columns of the j-th part of the rows.
-constexpr int kLongCols = 1024;
-template <class T>
+// Second half: CTA (i, j) takes 2048 columns of the j-th part of the rows.
+constexpr int kLongCols = 2048;
+template <class T, bool VEC>
 __global__ void __launch_bounds__(256) across_kernel(const Params p, int col_blocks, int rows_each) {
   griddep_wait();
   const int block = blockIdx.x % col_blocks, chunk = blockIdx.x / col_blocks;
-  const long long c0 = (long long)block * kLongCols + threadIdx.x;
+  const long long c0 = (long long)block * kLongCols;
+  const Share<T, 256, VEC> sh{(int)min(p.cols - c0, (long long)kLongCols), (int)threadIdx.x};
+  const int n = sh.count(0);
   const long long r0 = (long long)chunk * rows_each;
   const long long r1 = r0 + rows_each < p.rows ? r0 + rows_each : p.rows;
-  float w[4], dw[4] = {}, db[4] = {};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = c0 + 256 * j < p.cols ? p.weight.at((int)(c0 + 256 * j), 1.0f) : 0.0f;
+  Two w[4], dw[4] = {}, db[4] = {};
+  parameters(rows::from(p.weight, c0), sh, 0, n, 1.0f, w);
 #pragma unroll 2
   for (long long row = r0; row < r1; ++row) {
-    const char *x = p.x + row * p.ldx, *dy = p.dy + row * p.lddy;
-    const float mean = p.mean[row], rstd = p.rstd[row];
+    Chunk<T> vx, vd, out;
+    sh.load(p.x + row * p.ldx + c0 * T::SIZE, 0, n, vx);
+    sh.load(p.dy + row * p.lddy + c0 * T::SIZE, 0, n, vd);
     const float2 s = p.dx ? p.along[row] : make_float2(0.0f, 0.0f);
+    const Two minus = both(-p.mean[row]), r2 = both(p.rstd[row]), s1 = both(-s.x), s2 = both(-s.y);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long i = c0 + 256 * j;
-      if (i < p.cols) {
-        const float d = tcx::load_out(dy, T::TYPE, i);
-        const float h = (tcx::load_out(x, T::TYPE, i) - mean) * rstd;
-        dw[j] = fmaf(d, h, dw[j]);
-        db[j] += d;
-        if (p.dx)
-          tcx::store_out(p.dx + row * p.lddx, T::TYPE, i, (fmaf(d, w[j], -s.x) - h * s.y) * rstd);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const Two d = pair(vd, i), h = mul2(add2(pair(vx, i), minus), r2);
+      dw[i] = fma2(d, h, dw[i]);
+      db[i] = add2(db[i], d);
+      set_pair(out, i, mul2(fma2(h, s2, fma2(d, w[i], s1)), r2));
     }
+    if (p.dx) sh.store(p.dx + row * p.lddx + c0 * T::SIZE, 0, n, out);
   }
   if (p.part) {
-    float *to = p.part + chunk * p.pitch, *tb = to + p.parts * p.pitch;
+    float *to = p.part + chunk * p.pitch + c0, *tb = to + p.parts * p.pitch;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c0 + 256 * j < p.cols) {
-        to[c0 + 256 * j] = dw[j];
-        tb[c0 + 256 * j] = db[j];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpack2(dw[i]), e = unpack2(db[i]);
+      if (2 * i < n) to[sh.col(0, 2 * i)] = a.x, tb[sh.col(0, 2 * i)] = e.x;
+      if (2 * i + 1 < n) to[sh.col(0, 2 * i + 1)] = a.y, tb[sh.col(0, 2 * i + 1)] = e.y;
+    }
   }
   griddep_launch_dependents();
 }
@@ -359,12 +352,14 @@ static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaS
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
   if (p.cols <= kLongestHere) return launch<T, 512, 2>(p, vec, pl.grid, stream);
   if (p.dx) {
-    const cudaError_t e = launch_1d(along_kernel<T>, std::min(p.rows, 2 * sms), 1024, 0, 1, stream, p);
+    const cudaError_t e = launch_1d(vec ? along_kernel<T, true> : along_kernel<T, false>, std::min(p.rows, 2 * sms),
+                                    1024, 0, 1, stream, p);
     if (e != cudaSuccess) return e;
   }
   const long long blocks = ceil_div(p.cols, kLongCols), grid = blocks * pl.parts;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_1d(across_kernel<T>, (int)grid, 256, 0, 1, stream, p, (int)blocks, pl.rows_each);
+  return launch_1d(vec ? across_kernel<T, true> : across_kernel<T, false>, (int)grid, 256, 0, 1, stream, p, (int)blocks,
+                   pl.rows_each);
 }
 
 }  // namespace lnb

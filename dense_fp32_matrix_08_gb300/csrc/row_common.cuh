@@ -106,6 +106,14 @@ struct Share {
   // Elements that do not exist are zero.
   __device__ __forceinline__ void load(const void *row, int c, int n, Chunk<T> &v) const {
     const char *src = reinterpret_cast<const char *>(row);
+    if (VEC && n == 8) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(src + (long long)col(c, i * E) * T::SIZE);
+        v.w[4 * i] = u.x, v.w[4 * i + 1] = u.y, v.w[4 * i + 2] = u.z, v.w[4 * i + 3] = u.w;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < T::W; ++i) v.w[i] = 0;
 #pragma unroll
@@ -258,6 +266,20 @@ struct Vector {
   }
 };
 
+// The same from element `at` on.
+__device__ __forceinline__ Vector from(const Vector &p, long long at) {
+  const int size = p.type == tcx::OUT_F32 ? 4 : 2;
+  return {p.ptr ? static_cast<const char *>(p.ptr) + at * size : nullptr, p.type, p.vec};
+}
+
+// Rows that do not stay in registers are taken in blocks of 8 elements per thread of a CTA: what `each` does
+// with block after block, given the columns from its first one on and that one's number.
+template <class T, int TPR, bool VEC, class Each>
+__device__ __forceinline__ void blocks(int cols, Each &&each) {
+  for (long long at = 0; at < cols; at += 8 * TPR)
+    each(Share<T, TPR, VEC>{(int)(cols - at), (int)threadIdx.x}, at);
+}
+
 // The parameters of chunk c's columns (0 past the last one).
 template <class S>
 __device__ __forceinline__ void parameters(const Vector &p, const S &sh, int c, int n, float otherwise, Two (&to)[4]) {
@@ -326,6 +348,50 @@ __device__ __forceinline__ void row_sum(float (&v)[N], RowSums<TPR, N, ROWS> &su
       v[i] = (s.x + s.y) + (s.z + s.w);
     }
   }
+}
+
+// A sum of two FP32 numbers, hi + lo, as exact as 48 bits: for long sums, where 64-bit additions would be
+// what takes the time (two per cycle and SM). add(): the sum of hi and v without a rounding (Knuth's
+// two-sum), the rest into lo.
+struct Long {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Long &v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  // (where hi is infinite or NaN lo may be NaN: hi says it)
+  __device__ __forceinline__ float over(long long n) const {
+    return isfinite(hi) ? (float)(((double)hi + (double)lo) / (double)n) : hi;
+  }
+};
+
+// Over the 1024 threads of a CTA; the sum in the first one. Not twice without a barrier in between.
+__device__ __forceinline__ Long cta_sum(Long v, Long *part) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    Long u;
+    u.hi = __shfl_down_sync(0xffffffffu, v.hi, d);
+    u.lo = __shfl_down_sync(0xffffffffu, v.lo, d);
+    v.add(u);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    v = part[threadIdx.x];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      Long u;
+      u.hi = __shfl_down_sync(0xffffffffu, v.hi, d);
+      u.lo = __shfl_down_sync(0xffffffffu, v.lo, d);
+      v.add(u);
+    }
+  }
+  return v;
 }
 
 // s / n for the FP32 number n of elements, with r = 1 / n: the quotient corrected by its remainder.

@@ -22,7 +22,7 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  * weight and bias (cols elements of type w_type each) may be NULL: 1 and 0. mean and rstd (rows FP32
  * numbers each), which layer_norm_backward takes, may be NULL.
  *
- * Sums are FP32 (in rows of more than 16384 elements 64-bit), in an order fixed by the shape: the same
+ * Sums are FP32 (in rows of more than 16384 elements with 48 bits), in an order fixed by the shape: the same
  * call gives the same bits. Magnitudes up to 2^50 are held; with larger ones the squares leave FP32.
  * A NaN or an infinity makes its own row NaN. y may be x itself with ldy = ldx, and must not overlap
  * it otherwise.
@@ -43,7 +43,7 @@ int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const voi
  * does not read dweight and dbias; with rows == 0 they become beta times themselves. dx may be dy or
  * x itself with the same leading dimension, and must not overlap them otherwise.
  *
- * Sums along rows are FP32 (in rows of more than 8192 elements 64-bit), those over the rows FP32 within
+ * Sums along rows are FP32 (in rows of more than 8192 elements with 48 bits), those over the rows FP32 within
  * a block (at most 500 rows one after the other) and 64-bit beyond, in an order fixed by the shape and
  * the device: the same call gives the same bits. The workspace (layer_norm_backward_workspace_size bytes) is a stream-ordered
  * allocation from the library's pool.
