@@ -178,7 +178,8 @@ def _on_stream(stream, call, used):
     for t in used:
         t.record_stream(side)
     for t in result if isinstance(result, tuple) else (result,):
-        t.record_stream(here)
+        if t is not None:
+            t.record_stream(here)
     return result
 
 

@@ -21,7 +21,7 @@ def _lists(name, tensors):
     hundreds of them: one pass of a built-in per question.)"""
     where = set(map(_get_device, tensors))  # (a TypeError for what is no tensor)
     try:
-        types = array("i", [_TYPE[d] for d in map(_dtype, tensors)])
+        types = array("i", map(_TYPE.__getitem__, map(_dtype, tensors)))
     except KeyError:
         raise TypeError(f"{name} must be float32, bfloat16 or float16") from None
     if -1 in where:
