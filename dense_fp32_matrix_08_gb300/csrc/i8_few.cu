@@ -48,7 +48,7 @@ __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int c) {
 }
 
 template <int MT>
-__global__ void __launch_bounds__(32 * kWarps) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 4) few_kernel(const FewParams p) {
   __shared__ int sums[kWarps][kChannels][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = kWarps / p.parts;  // of channels per CTA
@@ -62,6 +62,15 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const FewParams p) {
 #pragma unroll
   for (int c = 0; c < kChannels; ++c) w[c] = p.w.q + min(n0 + c, (long long)p.N - 1) * p.w.ld;
   int acc[kChannels][MT] = {};
+  // The weight's first part begins its way to L2 while the kernel before this one still runs. (To L2 only,
+  // where what that kernel may yet write to it is seen.) The next launch may take what room there is.
+  // 1 x 4096 x 4096, one call after the other: 4.3 us without, 3.1 so; 1 x 14336 x 4096: 11.0 and 10.0, 10.9
+  // with twice as much.
+#pragma unroll
+  for (int c = 0; c < kChannels; ++c)
+    for (int k = k0 + 128 * lane; k < min(k1, k0 + 1024); k += 128 * 32)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(w[c] + k));
+  griddep_launch_dependents();
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
 #pragma unroll 2
   for (int k = k0 + 16 * lane; k < k1; k += 512) {
@@ -93,7 +102,6 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const FewParams p) {
       tcx::finish_out(p.d.ptr, p.d.type, m * p.d.ld + n, y, p.d.beta);
     }
   }
-  griddep_launch_dependents();
 }
 
 cudaError_t launch_few(int M, int N, int K, const Operand &x, const Operand &w, const Result &d, int sms,
@@ -111,6 +119,7 @@ cudaError_t launch_few(int M, int N, int K, const Operand &x, const Operand &w, 
 
 __global__ void __launch_bounds__(256) unpack_kernel(const int8_t *q, long long ldq, int rows, int K,
                                                      __half *out, long long ldo) {
+  griddep_launch_dependents();
   griddep_wait();
   const int chunks = (K + 15) / 16;
   const long long total = (long long)rows * chunks;
@@ -127,7 +136,6 @@ __global__ void __launch_bounds__(256) unpack_kernel(const int8_t *q, long long 
     d[0] = lo;
     d[1] = hi;
   }
-  griddep_launch_dependents();
 }
 
 cudaError_t launch_unpack(int rows, int K, const Operand &q, void *out, long long ldo, int sms,

@@ -237,14 +237,21 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot_ptr, 0);  // (uniform)
   const uint32_t a_tmem = tmem + C::NBUF * C::ACC_COLS;
-  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
-  // (every CTA of the grid is resident, so the next launch may take what room is left)
-  griddep_launch_dependents();
-
   const auto tile_at = [&](int t, int &tp, int &tq) {
     tile_coords(t, units, p.tiles_q, p.group_p, tp, tq);
     if (PAIR) tp = 2 * tp + cta;
   };
+  // The first blocks of the weight begin their way to L2 while the kernel before this one still runs. (To L2
+  // only, where what that kernel may yet write to them is seen.) Every CTA of the grid is resident, so the
+  // next launch may take what room is left.
+  if (warp == 0 && elect_one()) {
+    int tp, tq;
+    tile_at(first, tp, tq);
+    for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb) tma_prefetch_2d(&map_p, kb * BK, tp * BP);
+  }
+  __syncwarp();
+  griddep_launch_dependents();
+  griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
 
   if (warp < 4) {
     if constexpr (PAIR) reg_dealloc<C::CONTROL_REGS>();

@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / 
   Ahead<T, TPR, CH, VEC, 1, kDepth<T>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
+  griddep_launch_dependents();
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   ahead.begin();
   for (int turn = 0; base < p.rows; base += step, row += step, turn ^= 1) {
@@ -135,13 +136,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / 
       for (int c = 0; c < CH; ++c) put<VEC>(p, s, sh, to, c, n[c], v[c]);
     }
   }
-  griddep_launch_dependents();
 }
 
 // Rows of any length: a CTA reads its row twice.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
   __shared__ uint32_t part[2][32];
+  griddep_launch_dependents();
   griddep_wait();
   int turn = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
@@ -162,7 +163,6 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const Params p) {
       put<VEC>(p, s, sh, p.q + row * p.ldq + at, 0, n, v);
     });
   }
-  griddep_launch_dependents();
 }
 
 template <class T, int TPR, int CH, bool VEC>

@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
   Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
+  griddep_launch_dependents();
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   ahead.begin();
   Two w[HOLD ? CH : 1][4], b[HOLD ? CH : 1][4];
@@ -107,7 +108,6 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
       }
     }
   }
-  griddep_launch_dependents();
 }
 
 // Rows of any length: a CTA reads its row three times (for the mean, the variance and the result; from
@@ -117,6 +117,7 @@ template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
   __shared__ Long part[2][32];
   __shared__ float told[2];
+  griddep_launch_dependents();
   griddep_wait();
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const char *x = p.x + row * p.ldx;
@@ -169,7 +170,6 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
       sh.store(y + at * T::SIZE, 0, n, out);
     });
   }
-  griddep_launch_dependents();
 }
 
 template <class T, int TPR, int CH, bool VEC>

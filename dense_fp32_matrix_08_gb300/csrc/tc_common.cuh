@@ -246,6 +246,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// A tile of a copy to come, to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // 32 (16) consecutive FP32 accumulator columns of this thread's TMEM lane, readable after
 // tmem_wait_ld().
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[32]) {
