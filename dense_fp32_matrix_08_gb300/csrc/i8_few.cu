@@ -122,10 +122,16 @@ __global__ void __launch_bounds__(256) unpack_kernel(const int8_t *q, long long 
   griddep_launch_dependents();
   griddep_wait();
   const int chunks = (K + 15) / 16;
-  const long long total = (long long)rows * chunks;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
-    const long long r = i / chunks;
-    const int k = (int)(i % chunks) * 16;
+  const long long start = blockIdx.x * 256LL + threadIdx.x, step = 256LL * gridDim.x;
+  const int step_r = (int)(step / chunks), step_c = (int)(step % chunks);
+  long long r = start / chunks;
+  int c = (int)(start % chunks);
+  for (; r < rows; r += step_r, c += step_c) {
+    if (c >= chunks) {
+      c -= chunks;
+      if (++r >= rows) break;
+    }
+    const int k = c * 16;
     const uint4 v = load16(q + r * ldq, k, K, false);
     uint4 lo, hi;
     tcx::halves(v.x, lo.x, lo.y);

@@ -78,8 +78,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
     const bool in = row < p.rows;
     const Two minus = both(-mean), r2 = both(rstd);
     float s[2] = {0.0f, 0.0f};
+    // h and g stay in registers between the two passes where there is room for them
+    constexpr bool KEEP = VEC && T::SIZE == 2;
+    Two kept[KEEP ? CH : 1][4][2];
     if (in) {
-      Two sg = 0, sh2 = 0;
+      Two sg = 0, sgh = 0;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -90,10 +93,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
           dw[c][i] = fma2(d, h, dw[c][i]);
           db[c][i] = add2(db[c][i], d);
           sg = add2(sg, g);
-          sh2 = fma2(g, h, sh2);
+          sgh = fma2(g, h, sgh);
+          if constexpr (KEEP) kept[c][i][0] = h, kept[c][i][1] = g;
         }
       s[0] = sum2(sg);
-      s[1] = sum2(sh2);
+      s[1] = sum2(sgh);
     }
     if (p.dx == nullptr) continue;
     row_sum(s, sums, turn);
@@ -104,8 +108,15 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
         Chunk<T> out;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const Two h = mul2(add2(pair(v[0][c], i), minus), r2);
-          set_pair(out, i, mul2(fma2(h, s2, fma2(pair(v[1][c], i), w[c][i], s1)), r2));
+          Two h, g;
+          if constexpr (KEEP) {
+            h = kept[c][i][0];
+            g = add2(kept[c][i][1], s1);
+          } else {
+            h = mul2(add2(pair(v[0][c], i), minus), r2);
+            g = fma2(pair(v[1][c], i), w[c][i], s1);
+          }
+          set_pair(out, i, mul2(fma2(h, s2, g), r2));
         }
         sh.store(to, c, n[c], out);
       }
