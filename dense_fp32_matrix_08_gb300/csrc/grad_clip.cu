@@ -4,7 +4,9 @@
 // launches however many arrays there are (for each 960 of them): square_kernel leaves one sum of
 // squares per CTA; every CTA of scale_kernel adds all of them up, in the same order, and scales its
 // part. The arrays are cut into pieces of kPiece elements that the CTAs take in turn. scale_kernel
-// takes them backwards, so that the last ones read for the norm come from L2.
+// takes them backwards, so that the last ones read for the norm come from L2. 235 M FP32 gradients: 149 us
+// for the norm (6.3 TB/s, 93% of a copy's rate), 441 to 445 with the result in other arrays, 415 being the
+// time of the bytes at a copy's rate. 200 small arrays of two types: 19 us, two launches and little else.
 #include <algorithm>
 #include <cmath>
 #include <vector>
@@ -345,7 +347,7 @@ extern "C" int clip_grad_norm(int count, const void *const *grads, const int *ty
   const gc::Call c{count, grads, types, sizes, max_norm, eps, out, out_types, norm, stream};
   // launches: full tables, and each time that the pieces of one would be too many
   const auto launches = [&](int most) { return (int)(ceil_div(arrays, most) + pieces / 0x3fffffff * 2 + 1); };
-  // (the table is copied for each launch: 200 arrays' in one of 960 took 15 us longer to launch)
+  // (the table is copied for each launch: 6.5 us for a call of 20 arrays, 11 of 200, 30 of 900)
   return arrays <= 32    ? (int)gc::run<32>(c, launches(32), sms)
          : arrays <= 240 ? (int)gc::run<240>(c, launches(240), sms)
                          : (int)gc::run<960>(c, launches(960), sms);

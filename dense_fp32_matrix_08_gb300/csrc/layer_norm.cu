@@ -3,7 +3,11 @@
 //
 // Bound by HBM: each element is read and written once. A row stays in registers from its one read to
 // its last use, so that the variance is the mean of the squared distances themselves: no difference
-// of large sums.
+// of large sums. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
+// FP32 numbers per instruction: one by one they were 71% busy and it took 32 us). 1 x 4096: 1.7 us. Rows
+// of 1024 and less reach 66% (16-bit) to 91% (FP32): the sums' exchanges weigh more there. Rows of 16384
+// 16-bit elements take 45 us for as many bytes: 1024 threads leave no registers for the parameters, which
+// are read for each row.
 #include <algorithm>
 #include <cmath>
 
