@@ -106,7 +106,7 @@ struct Channel {
 };
 
 // Sums of this lane's channel and COUNT neighbouring tokens, finished and stored. What is not
-// unrolled over the sums is not unrolled at all: the epilogue shares the instruction caches with the
+// unrolled over the sums is unrolled little: the epilogue shares the instruction caches with the
 // converters (all inlined and unrolled it took half of their time).
 // sx: the scale of token `token` + lane - from in each lane.
 constexpr int COUNT = 16;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
   const int col0 = c.at - lane;
   if (p.d.vec && p.d.type != tcx::OUT_F32) {
     const int col = (lane & 3) * 8, cols = min(8, p.N - col0 - col);
-#pragma unroll 1
+#pragma unroll 2
     for (int r = lane >> 2; r < rows; r += 8) {
       const float *v = buf + r * OUT_PITCH + col;
       uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + (token + r) * p.d.ld + col0 + col;
@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
     }
   } else if (p.d.vec) {
     const int col = (lane & 7) * 4, cols = min(4, p.N - col0 - col);
-#pragma unroll 1
+#pragma unroll 2
     for (int r = lane >> 3; r < rows; r += 4) {
       const float *v = buf + r * OUT_PITCH + col;
       float *d = static_cast<float *>(p.d.ptr) + (token + r) * p.d.ld + col0 + col;
@@ -150,11 +150,11 @@ __device__ __forceinline__ void store_tokens(const Params &p, const Channel &c, 
     }
   } else if (c.at < p.N && p.d.type == tcx::OUT_F32 && p.d.beta == 0.0f) {
     float *d = static_cast<float *>(p.d.ptr) + token * p.d.ld + c.at;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) d[r * p.d.ld] = buf[r * OUT_PITCH + lane];
   } else if (c.at < p.N && p.d.beta == 0.0f) {
     uint16_t *d = static_cast<uint16_t *>(p.d.ptr) + token * p.d.ld + c.at;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) d[r * p.d.ld] = (uint16_t)tcx::pack_out(p.d.type, buf[r * OUT_PITCH + lane], 0.0f);
   } else if (c.at < p.N) {
 #pragma unroll 2
@@ -514,61 +514,53 @@ __global__ void __launch_bounds__(Cfg<TN, PAIR>::THREADS, 1)
   }
   __syncwarp();
   if (S > 1) {
-    // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp AT of them at a time, a lane
-    // four neighbouring channels of each
-    constexpr int AT = TN >= 128 ? 1 : 2;  // (for the registers)
+    // CTA `rank` finishes tokens [rank * TN / S, (rank + 1) * TN / S), a warp one of them at a time, a lane
+    // four neighbouring channels of it. What the results are multiplied with is read before the wait.
+    int tp, tq;
+    tile_at(first, tp, tq);
+    const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);
+    const int n0 = tp * BP + lane * 4;
+    float ws[4], bias[4], sx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Channel ch = channel_at(p, n0 + i);
+      ws[i] = ch.scale;
+      bias[i] = ch.bias;
+    }
+    if (c0 + warp < c1) sx = p.x_scale[tq * TN + c0 + warp];
     cluster_sync_all();
-    if (warp >= C::FIRST_EPI) {
-      int tp, tq;
-      tile_at(first, tp, tq);
-      const int c0 = TN * rank / S, c1 = min(TN * (rank + 1) / S, p.M - tq * TN);
-      const int n0 = tp * BP + lane * 4;
-      float ws[4], bias[4];
+    for (int c = c0 + warp; c < c1; c += C::THREADS / 32) {
+      float4 v[MAX_CLUSTER];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Channel ch = channel_at(p, n0 + i);
-        ws[i] = ch.scale;
-        bias[i] = ch.bias;
-      }
-      for (int c = c0 + (warp - C::FIRST_EPI) * AT; c < c1; c += C::EPI_WARPS * AT) {
-        float4 v[AT][MAX_CLUSTER];
+      for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
+        if (q < S) v[q] = ld_cluster4(base + (uint32_t)(c * BP + lane * 4) * 4, (uint32_t)q);
+      int sums[4] = {};
 #pragma unroll
-        for (int q = 0; q < MAX_CLUSTER; ++q)  // all loads in flight before the adds
-#pragma unroll
-          for (int j = 0; j < AT; ++j)
-            if (q < S && c + j < c1) v[j][q] = ld_cluster4(base + (uint32_t)((c + j) * BP + lane * 4) * 4, (uint32_t)q);
-#pragma unroll
-        for (int j = 0; j < AT; ++j) {
-          if (c + j >= c1) break;
-          int sums[4] = {};
-#pragma unroll
-          for (int q = 0; q < MAX_CLUSTER; ++q)
-            if (q < S) {
-              sums[0] += __float_as_int(v[j][q].x);
-              sums[1] += __float_as_int(v[j][q].y);
-              sums[2] += __float_as_int(v[j][q].z);
-              sums[3] += __float_as_int(v[j][q].w);
-            }
-          // (a load that nothing waits for could still be under way when the other CTA leaves)
-          asm volatile("" ::"r"(sums[0]), "r"(sums[1]), "r"(sums[2]), "r"(sums[3]));
-          const int token = tq * TN + c + j;
-          const float sx = p.x_scale[token];
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = fmaf((float)sums[i], ws[i] * sx, bias[i]);
-          const long long at = token * p.d.ld + n0;
-          if (p.d.vec && n0 + 4 <= p.N) {
-            if (p.d.type == OUT_F32)
-              *reinterpret_cast<float4 *>(static_cast<float *>(p.d.ptr) + at) = make_float4(y[0], y[1], y[2], y[3]);
-            else
-              *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.d.ptr) + at) =
-                  make_uint2(pack_out(p.d.type, y[0], y[1]), pack_out(p.d.type, y[2], y[3]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (n0 + i < p.N) finish_out(p.d.ptr, p.d.type, at + i, y[i], p.d.beta);
-          }
+      for (int q = 0; q < MAX_CLUSTER; ++q)
+        if (q < S) {
+          sums[0] += __float_as_int(v[q].x);
+          sums[1] += __float_as_int(v[q].y);
+          sums[2] += __float_as_int(v[q].z);
+          sums[3] += __float_as_int(v[q].w);
         }
+      // (a load that nothing waits for could still be under way when the other CTA leaves)
+      asm volatile("" ::"r"(sums[0]), "r"(sums[1]), "r"(sums[2]), "r"(sums[3]));
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = fmaf((float)sums[i], ws[i] * sx, bias[i]);
+      const int token = tq * TN + c, next = c + C::THREADS / 32;
+      if (next < c1) sx = p.x_scale[tq * TN + next];
+      const long long at = token * p.d.ld + n0;
+      if (p.d.vec && n0 + 4 <= p.N) {
+        if (p.d.type == OUT_F32)
+          *reinterpret_cast<float4 *>(static_cast<float *>(p.d.ptr) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        else
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.d.ptr) + at) =
+              make_uint2(pack_out(p.d.type, y[0], y[1]), pack_out(p.d.type, y[2], y[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + i < p.N) finish_out(p.d.ptr, p.d.type, at + i, y[i], p.d.beta);
       }
     }
     __syncwarp();
