@@ -4,10 +4,10 @@
 // Bound by HBM: each element is read and written once. A row stays in registers from its one read to
 // its last use, so that the variance is the mean of the squared distances themselves: no difference
 // of large sums. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
-// FP32 numbers per instruction: one by one they were 71% busy and it took 32 us). 1 x 4096: 1.7 us. Rows
-// of 1024 and less reach 66% (16-bit) to 91% (FP32): the sums' exchanges weigh more there. Rows of 16384
-// 16-bit elements take 45 us for as many bytes: 1024 threads leave no registers for the parameters, which
-// are read for each row.
+// FP32 numbers per instruction: one by one they were 71% busy and it took 32 us); FP32 41 us, 96%. 1 x 4096: 1.7 us.
+// 16384 x 1024 BF16 11.7 us, 84%; 16384 x 512 7.5, 66%: the sums' exchanges weigh more there. Rows of 16384 16-bit
+// elements take 45 us for as many bytes as those of 4096: 1024 threads leave no registers for the parameters,
+// which are read for each row.
 #include <algorithm>
 #include <cmath>
 
@@ -30,16 +30,23 @@ struct Params {
   float *mean, *rstd;
 };
 
-// CTAs of norm_kernel per SM: 768 threads with 80 registers each, or 64 registers for the longest rows.
-constexpr int per_sm(int tpr) { return tpr < 128 ? 6 : tpr <= 256 ? 768 / tpr : 1; }
-// Rows under way: about 64 KB per SM.
-template <class T, int TPR>
-constexpr int kDepth = (TPR == 512 ? 5 : 4) - (T::SIZE == 4);
+// CTAs of norm_kernel per SM: 768 threads with 80 registers each; 512 with 128 where a thread of a warp has
+// 32 elements; 1024 with 64 for rows of 4097 elements and more. FP32 rows of 4097 to 8192 elements and rows that are
+// not aligned: one CTA of 512 (4096 x 8192 FP32 42 us, with two of them 46 to 55; BF16 24.6, with one 27.8).
+template <class T, int TPR, int CH, bool VEC>
+constexpr int kPerSm = TPR < 128    ? (CH > 2 ? 4 : 6)
+                       : TPR <= 256 ? 768 / TPR
+                                    : (TPR == 512 && VEC && T::SIZE == 2 ? 2 : 1);
+// Rows under way. More than it takes costs time: 8192 x 4096 FP32 takes 41.0 us with two, 46.7 with three, BF16
+// 22.6 with three, 22.9 with four and 24.8 with two; where a row's bytes are few, or a CTA is alone on its SM, FP32
+// rows need three as well (16384 x 1024: 21.5 us, 24.1 with two; 4096 x 8192: 42 and 45).
+template <class T, int TPR, int CH>
+constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 && TPR != 512 ? 2 : 3;
 
 // TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn. The parameters of a
 // thread's columns stay in its registers, but for the longest rows, which have too many threads for that.
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kernel(const Params p) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>) norm_kernel(const Params p) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
   constexpr bool HOLD = TPR < 1024;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -47,10 +54,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
+  Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, THREADS> ahead(p.cols, ring, {p.x}, {p.ldx}, p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
-  griddep_launch_dependents();
+  const bool once = step >= p.rows;  // (a launch that takes a while lets the next one begin at its end)
+  if (once) griddep_launch_dependents();
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   ahead.begin();
   Two w[HOLD ? CH : 1][4], b[HOLD ? CH : 1][4];
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
     // 1 / sqrt, with one step of Newton's iteration
     const float v = over(s[0], p.n, p.r) + p.eps;
     float rstd = rsqrtf(v);
-    rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
+    if (v > 0.0f) rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
     if (row < p.rows) {
       if (sh.t == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -112,6 +120,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, per_sm(TPR)) norm_kerne
       }
     }
   }
+  if (!once) griddep_launch_dependents();
 }
 
 // Rows of any length: a CTA reads its row three times (for the mean, the variance and the result; from
@@ -178,12 +187,12 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
 
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR>, threads>::BYTES;
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, threads>::BYTES;
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(norm_kernel<T, TPR, CH, VEC>, bytes, once, set);
   if (e != cudaSuccess) return e;
-  const long long grid = std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * per_sm(TPR));
+  const long long grid = std::min<long long>(ceil_div(p.rows, rpb), (long long)sms * kPerSm<T, TPR, CH, VEC>);
   return launch_1d(norm_kernel<T, TPR, CH, VEC>, (int)grid, threads, bytes, 1, stream, p);
 }
 template <class T, int TPR, int CH>
@@ -196,7 +205,10 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 64) return launch<T, 8, 1>(p, vec, sms, stream);
   if (p.cols <= 256) return launch<T, 32, 1>(p, vec, sms, stream);
   if (p.cols <= 512) return launch<T, 32, 2>(p, vec, sms, stream);
-  if (p.cols <= 1024) return launch<T, 128, 1>(p, vec, sms, stream);
+  // (a warp per row needs no barrier, but aligned rows for its registers: 16384 x 1024 BF16 15.1 us with 128
+  // threads on a row, 12.3 so)
+  if (p.cols <= 1024 && vec) return launch<T, 32, 4, true>(p, sms, stream);
+  if (p.cols <= 1024) return launch<T, 128, 1, false>(p, sms, stream);
   if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);

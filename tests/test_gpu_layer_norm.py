@@ -244,6 +244,14 @@ def test_constant_rows_and_magnitudes():
         check(x, None, None, 0.0, sg.layer_norm(x, eps=0.0, stats=True))
 
 
+@pytest.mark.parametrize("cols", [1, 300, 5000, 20000])
+def test_constant_rows_without_eps(cols):
+    # variance 0 and eps 0: 1 / sqrt(0)
+    x = torch.full((2, cols), 3.0).cuda()
+    y, mean, rstd = sg.layer_norm(x, eps=0.0, stats=True)
+    assert (mean == 3).all() and (rstd == float("inf")).all() and torch.isnan(y).all()
+
+
 def test_no_rows():
     x = torch.empty(0, 50, device="cuda")
     y, mean, rstd = sg.layer_norm(x, stats=True)
