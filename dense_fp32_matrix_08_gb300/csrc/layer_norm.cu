@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
 
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
-  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR, bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, threads>::BYTES;
+  constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
+  constexpr int bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, threads>::BYTES;
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(norm_kernel<T, TPR, CH, VEC>, bytes, once, set);

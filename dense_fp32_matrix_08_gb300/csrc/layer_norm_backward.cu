@@ -6,8 +6,8 @@
 // sums and its result. dw and db are added up in the registers of the thread that holds the column,
 // over all rows that it gets (500 at most, so that FP32 holds such a sum); those of a CTA meet in shared
 // memory, the CTAs' sums in the workspace, where reduce_kernel adds them in a fixed order.
-// 8192 x 4096 BF16: 40.6 us, 5.0 TB/s. Without dw and db 35.7 (83% of a copy's rate): the sums' registers
-// leave 16 warps per SM, issue slots 50% busy; the rest is the sums' way. FP32: 65 us, 6.2 TB/s (91%).
+// 8192 x 4096 BF16: 39.7 us, 5.1 TB/s. Without dw and db 34.2 (87% of a copy's rate): the sums' registers
+// leave 16 warps per SM, issue slots 50% busy; the rest is the sums' way. FP32: 63 us, 6.4 TB/s (94%).
 // 4099 x 777 FP32: 12.5, of which 3.5 are for the sums; its rows are not aligned, so that they come element by
 // element. Rows of more than 8192 elements are read twice: 2048 x 16384 BF16 96 us.
 #include <algorithm>
@@ -42,8 +42,8 @@ struct Params {
 // One CTA of 512 threads per SM, with up to 128 registers each: as many rows at a time as that makes, and
 // one sum of each column per SM.
 constexpr int kThreads = 512;
-// Rows under way. More than it takes costs time: 8192 x 4096 FP32 63 us with two, 66 with three, but 16384 x 1024 FP32
-// 36.5 with three, 38.3 with two; BF16 40.0 with three, 41.0 with two.
+// Rows under way. More than it takes costs time: 8192 x 4096 FP32 63 us with two, 66 with three; FP32 rows of 1024
+// and less are short enough for three (16384 x 1024 36.5 us, 38.3 with two); BF16 40.0 with three, 41.0 with two.
 template <class T, int TPR, int CH>
 constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 ? 2 : 3;
 
@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row, step);
+  Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row,
+                                                                step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
@@ -363,7 +364,17 @@ static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaS
   if (p.cols <= 64) return launch<T, 8, 1>(p, vec, pl.grid, stream);
   if (p.cols <= 256) return launch<T, 32, 1>(p, vec, pl.grid, stream);
   if (p.cols <= 512) return launch<T, 32, 2>(p, vec, pl.grid, stream);
-  if (p.cols <= 1024) return launch<T, 128, 1>(p, vec, pl.grid, stream);
+  // (a thread with 16 elements waits as long for its row's sums as one with 8: 16384 x 1024 BF16 26.9 us with 128
+  // threads on a row, 22.5 with 64; 4099 x 777 BF16, element by element, 17.0 and 13.8. In FP32 the latter takes more
+  // registers than there are: 12.6 and 17.8. The plan, and so the workspace, is the same for both.)
+  if (p.cols <= 1024) {
+    if constexpr (T::SIZE == 4) {
+      if (!vec) return launch<T, 128, 1, false>(p, pl.grid, stream);
+      return launch<T, 64, 2, true>(p, pl.grid, stream);
+    } else {
+      return launch<T, 64, 2>(p, vec, pl.grid, stream);
+    }
+  }
   if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, pl.grid, stream);
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
   if (p.cols <= kLongestHere) return launch<T, 512, 2>(p, vec, pl.grid, stream);

@@ -317,6 +317,7 @@ __device__ __forceinline__ void parameters(const Vector &p, const S &sh, int c, 
 // Sums of N numbers over the TPR threads of a row (one of ROWS rows of a CTA), the same bits in each of
 // them. `turn` alternates between calls of a kernel, so that one barrier is enough: whoever writes a
 // buffer again has passed the barrier of the call in between, before which everybody had read it.
+// (TPR: up to 32, 64, or a multiple of 128.)
 template <int TPR, int N, int ROWS = 1>
 struct RowSums {
   float part[TPR > 32 ? ROWS : 1][2][N][TPR < 128 ? 4 : TPR / 32];
@@ -345,7 +346,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], RowSums<TPR, N, ROWS> &su
         const float4 u = from[w];
         s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
       }
-      v[i] = (s.x + s.y) + (s.z + s.w);
+      v[i] = TPR < 128 ? s.x + s.y : (s.x + s.y) + (s.z + s.w);
     }
   }
 }
