@@ -199,7 +199,9 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   }
   if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  if (p.cols <= 6144) return launch<T, 384, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
+  if (p.cols <= 12288) return launch<T, 768, 2>(p, vec, sms, stream);
   if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
   return launch_1d(vec ? quantize_long_kernel<T, true> : quantize_long_kernel<T, false>, std::min(p.rows, 2 * sms),
                    1024, 0, 1, stream, p);

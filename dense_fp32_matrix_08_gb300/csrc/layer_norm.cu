@@ -35,7 +35,7 @@ struct Params {
 // not aligned: one CTA of 512 (4096 x 8192 FP32 42 us, with two of them 46 to 55; BF16 24.6, with one 27.8).
 template <class T, int TPR, int CH, bool VEC>
 constexpr int kPerSm = TPR < 128    ? (CH > 2 ? 4 : 6)
-                       : TPR <= 256 ? 768 / TPR
+                       : TPR <= 384 ? 768 / TPR
                                     : (TPR == 512 && VEC && T::SIZE == 2 ? 2 : 1);
 // Rows under way. More than it takes costs time: 8192 x 4096 FP32 takes 41.0 us with two, 46.7 with three, BF16
 // 22.6 with three, 22.9 with four and 24.8 with two; where a row's bytes are few, or a CTA is alone on its SM, FP32
@@ -44,11 +44,17 @@ template <class T, int TPR, int CH>
 constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 && TPR != 512 ? 2 : 3;
 
 // TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn. The parameters of a
-// thread's columns stay in its registers, but for the longest rows, which have too many threads for that.
+// thread's columns stay in its registers. 1024 threads have none for that: those of 16-bit rows lie in shared memory
+// behind the ring, each thread's in places of its own (2048 x 16384 BF16 XX us, 45 where they are read from L2
+// for each row); FP32 rows need the room for the ring.
+template <class T, int TPR, bool VEC>
+constexpr bool kShared = TPR == 1024 && VEC && T::SIZE == 2;
+template <class T, int TPR, int CH, bool VEC>
+constexpr int kRing = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, TPR < 128 ? 128 : TPR>::BYTES;
 template <class T, int TPR, int CH, bool VEC>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>) norm_kernel(const Params p) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
-  constexpr bool HOLD = TPR < 1024;
+  constexpr bool HOLD = TPR < 1024, SHARED = kShared<T, TPR, VEC>;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) RowSums<TPR, 1> sums;
   const long long step = (long long)gridDim.x * RPB;
@@ -67,6 +73,19 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
     for (int c = 0; c < CH; ++c) {
       parameters(p.weight, sh, c, n[c], 1.0f, w[c]);
       parameters(p.bias, sh, c, n[c], 0.0f, b[c]);
+    }
+  }
+  ulonglong2 *mine = reinterpret_cast<ulonglong2 *>(ring + kRing<T, TPR, CH, VEC>) + threadIdx.x;
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      parameters(p.weight, sh, c, n[c], 1.0f, w[0]);
+      parameters(p.bias, sh, c, n[c], 0.0f, b[0]);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        mine[(c * 4 + i) * THREADS] = make_ulonglong2(w[0][i], w[0][i + 1]);
+        mine[(c * 4 + i + 1) * THREADS] = make_ulonglong2(b[0][i], b[0][i + 1]);
+      }
     }
   }
   char *to = p.y + row * p.ldy;
@@ -108,7 +127,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
       const Two r2 = both(rstd);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        if constexpr (!HOLD) {
+        if constexpr (SHARED) {
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const ulonglong2 wi = mine[(c * 4 + i) * THREADS], bi = mine[(c * 4 + i + 1) * THREADS];
+            w[0][i] = wi.x, w[0][i + 1] = wi.y, b[0][i] = bi.x, b[0][i + 1] = bi.y;
+          }
+        } else if constexpr (!HOLD) {
           parameters(p.weight, sh, c, n[c], 1.0f, w[0]);
           parameters(p.bias, sh, c, n[c], 0.0f, b[0]);
         }
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
 template <class T, int TPR, int CH, bool VEC>
 static cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
   constexpr int threads = TPR < 128 ? 128 : TPR, rpb = threads / TPR;
-  constexpr int bytes = Ahead<T, TPR, CH, VEC, 1, kDepth<T, TPR, CH>, threads>::BYTES;
+  constexpr int bytes = kRing<T, TPR, CH, VEC> + (kShared<T, TPR, VEC> ? 2 * CH * 8 * 4 * threads : 0);
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(norm_kernel<T, TPR, CH, VEC>, bytes, once, set);
@@ -212,7 +237,9 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 1024) return launch<T, 128, 1, false>(p, sms, stream);
   if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
   if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  if (p.cols <= 6144) return launch<T, 384, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
+  if (p.cols <= 12288) return launch<T, 768, 2>(p, vec, sms, stream);
   if (p.cols <= kLongest) return launch<T, 1024, 2>(p, vec, sms, stream);
   return launch_1d(vec ? norm_long_kernel<T, true> : norm_long_kernel<T, false>, std::min(p.rows, 2 * sms), 1024, 0,
                    1, stream, p);

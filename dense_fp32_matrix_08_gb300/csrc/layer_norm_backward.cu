@@ -363,20 +363,24 @@ template <class T>
 static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaStream_t stream) {
   if (p.cols <= 64) return launch<T, 8, 1>(p, vec, pl.grid, stream);
   if (p.cols <= 256) return launch<T, 32, 1>(p, vec, pl.grid, stream);
-  if (p.cols <= 512) return launch<T, 32, 2>(p, vec, pl.grid, stream);
-  // (a thread with 16 elements waits as long for its row's sums as one with 8: 16384 x 1024 BF16 26.9 us with 128
-  // threads on a row, 22.5 with 64; 4099 x 777 BF16, element by element, 17.0 and 13.8. In FP32 the latter takes more
-  // registers than there are: 12.6 and 17.8. The plan, and so the workspace, is the same for both.)
-  if (p.cols <= 1024) {
-    if constexpr (T::SIZE == 4) {
-      if (!vec) return launch<T, 128, 1, false>(p, pl.grid, stream);
-      return launch<T, 64, 2, true>(p, pl.grid, stream);
+  if constexpr (T::SIZE == 4) {
+    if (!vec) {
+      if (p.cols <= 512) return launch<T, 64, 1, false>(p, pl.grid, stream);
+      if (p.cols <= 1024) return launch<T, 128, 1, false>(p, pl.grid, stream);
+      if (p.cols <= 2048) return launch<T, 256, 1, false>(p, pl.grid, stream);
+      if (p.cols <= 4096) return launch<T, 512, 1, false>(p, pl.grid, stream);
     } else {
-      return launch<T, 64, 2>(p, vec, pl.grid, stream);
+      if (p.cols <= 512) return launch<T, 32, 2, true>(p, pl.grid, stream);
+      if (p.cols <= 1024) return launch<T, 64, 2, true>(p, pl.grid, stream);
+      if (p.cols <= 2048) return launch<T, 128, 2, true>(p, pl.grid, stream);
+      if (p.cols <= 4096) return launch<T, 256, 2, true>(p, pl.grid, stream);
     }
+  } else {
+    if (p.cols <= 512) return launch<T, 32, 2>(p, vec, pl.grid, stream);
+    if (p.cols <= 1024) return launch<T, 64, 2>(p, vec, pl.grid, stream);
+    if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, pl.grid, stream);
+    if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
   }
-  if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, pl.grid, stream);
-  if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
   if (p.cols <= kLongestHere) return launch<T, 512, 2>(p, vec, pl.grid, stream);
   if (p.dx) {
     const cudaError_t e = launch_1d(vec ? along_kernel<T, true> : along_kernel<T, false>, std::min(p.rows, 2 * sms),

@@ -40,7 +40,8 @@ int i8_quantize(int rows, int cols, const void *x, int x_type, int ldx, void *q,
  * numbers) may be NULL. D is M x N, row-major, of type d_type.
  *
  * The sum over k is the exact whole number (K is at most 131071, so that 32 bits hold it), whatever
- * way the product runs; scales, bias and beta are applied in FP32, with one rounding to d_type.
+ * way the product runs; scales, bias and beta are applied in FP32, with one rounding to d_type. The
+ * product of the two scales is formed first: where it leaves FP32's range, so does the result.
  * beta == 0 does not read D; K == 0 does not read x, w or their scales. D must not overlap x or w.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (M = 1, N = 2, K = 3, x = 4,
