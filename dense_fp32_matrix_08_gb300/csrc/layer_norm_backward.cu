@@ -9,7 +9,7 @@
 // 8192 x 4096 BF16: 39.7 us, 5.1 TB/s. Without dw and db 34.2 (87% of a copy's rate): the sums' registers
 // leave 16 warps per SM, issue slots 50% busy; the rest is the sums' way. FP32: 63 us, 6.4 TB/s (94%).
 // 4099 x 777 FP32: 12.5, of which 3.5 are for the sums; its rows are not aligned, so that they come element by
-// element. Rows of more than 8192 elements are read twice: 2048 x 16384 BF16 96 us.
+// element. Rows of more than 12288 elements are read twice: 2048 x 16384 BF16 96 us.
 #include <algorithm>
 #include <cmath>
 
@@ -22,7 +22,7 @@ namespace lnb {
 using namespace rows;
 
 constexpr int kMostRows = 500;  // rows that a thread adds up in FP32
-constexpr int kLongestHere = 8192;  // elements of a row that stays in registers beside the sums
+constexpr int kLongestHere = 12288;  // elements of a row that stays in registers beside the sums
 
 struct Params {
   int rows, cols;
@@ -39,41 +39,68 @@ struct Params {
   float2 *along;            // rows that do not stay in registers: sum g / n, sum (g h) / n
 };
 
-// One CTA of 512 threads per SM, with up to 128 registers each: as many rows at a time as that makes, and
-// one sum of each column per SM.
-constexpr int kThreads = 512;
+// One CTA of 512 threads per SM, with up to 128 registers each (768 with 80 for the longest rows): as many rows
+// at a time as that makes, and one sum of each column per SM.
+template <int TPR>
+constexpr int kThreads = TPR > 512 ? TPR : 512;
 // Rows under way. More than it takes costs time: 8192 x 4096 FP32 63 us with two, 66 with three; FP32 rows of 1024
 // and less are short enough for three (16384 x 1024 36.5 us, 38.3 with two); BF16 40.0 with three, 41.0 with two.
 template <class T, int TPR, int CH>
 constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 ? 2 : 3;
 
-// Dynamic shared memory: the ring of rows to come; at the end the sums of the CTA's rows.
+// Whether the weight of a thread's columns lies in shared memory, in places of the thread's own, instead of registers:
+// for rows of 8193 to 12288 elements, where it fits. (4096 x 12288 BF16 77 us, 93 with it in registers that spill, 149
+// with the rows read twice. FP32 142, with registers that spill: read again from L2 for each row 152, rows read
+// twice 208.)
+template <class T, int TPR, bool VEC>
+constexpr bool kShared = TPR > 512 && VEC && T::SIZE == 2;
+
+// Dynamic shared memory: the ring of rows to come and behind it such a weight; at the end the sums of the CTA's rows.
 template <class T, int TPR, int CH, bool VEC>
-constexpr int kBytes = std::max(Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads>::BYTES,
-                                TPR < kThreads ? kThreads * 2 * CH * 8 * 4 : 0);
+constexpr int kRing = Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads<TPR>>::BYTES;
+template <class T, int TPR, int CH, bool VEC>
+constexpr int kBytes = std::max(kRing<T, TPR, CH, VEC> + (kShared<T, TPR, VEC> ? TPR * CH * 8 * 4 : 0),
+                                TPR < kThreads<TPR> ? kThreads<TPR> * 2 * CH * 8 * 4 : 0);
 
 template <class T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
-  constexpr int RPB = kThreads / TPR;
+__global__ void __launch_bounds__(kThreads<TPR>, 1) backward_kernel(const Params p) {
+  constexpr int RPB = kThreads<TPR> / TPR;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) RowSums<TPR, 2, RPB> sums;
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
-  Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy}, p.rows, row,
-                                                                step);
+  Ahead<T, TPR, CH, VEC, 2, kDepth<T, TPR, CH>, kThreads<TPR>> ahead(p.cols, ring, {p.x, p.dy}, {p.ldx, p.lddy},
+                                                                      p.rows, row, step);
   const auto &sh = ahead.sh;
   const auto &n = ahead.n;
   griddep_wait();  // (launched with programmatic dependent launch: see launch_1d)
   ahead.begin();
   float next_mean = row < p.rows ? p.mean[row] : 0.0f, next_rstd = row < p.rows ? p.rstd[row] : 0.0f;
-  Two w[CH][4], dw[CH][4], db[CH][4];
+  constexpr bool SHARED = kShared<T, TPR, VEC>;
+  Two held[SHARED ? 1 : CH][4], dw[CH][4], db[CH][4];
+  ulonglong2 *mine = reinterpret_cast<ulonglong2 *>(ring + kRing<T, TPR, CH, VEC>) + threadIdx.x;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    parameters(p.weight, sh, c, n[c], 1.0f, w[c]);
+    Two(&w)[4] = held[SHARED ? 0 : c];
+    parameters(p.weight, sh, c, n[c], 1.0f, w);
+    if constexpr (SHARED) {
+      mine[2 * c * TPR] = make_ulonglong2(w[0], w[1]);
+      mine[(2 * c + 1) * TPR] = make_ulonglong2(w[2], w[3]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = 0;
   }
+  // The weight of chunk c: w[i] of its elements 2 i and 2 i + 1.
+  const auto weight = [&](int c, Two (&w)[4]) {
+    if constexpr (SHARED) {
+      const ulonglong2 a = mine[2 * c * TPR], b = mine[(2 * c + 1) * TPR];
+      w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = held[c][i];
+    }
+  };
   char *to = p.dx + row * p.lddx;
   int turn = 0;
   for (; base < p.rows; base += step, row += step, to += step * p.lddx, turn ^= 1) {
@@ -86,23 +113,26 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
     const Two minus = both(-mean), r2 = both(rstd);
     float s[2] = {0.0f, 0.0f};
     // h and g stay in registers between the two passes where there is room for them
-    constexpr bool KEEP = VEC && T::SIZE == 2;
+    constexpr bool KEEP = VEC && T::SIZE == 2 && TPR <= 512;
     Two kept[KEEP ? CH : 1][4][2];
     if (in) {
       Two sg = 0, sgh = 0;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c) {
+        Two w[4];
+        weight(c, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // (elements that do not exist have dy = 0, so they add nothing where rstd and mean are finite,
           // and where those are not the row is NaN anyway)
-          const Two d = pair(v[1][c], i), h = mul2(add2(pair(v[0][c], i), minus), r2), g = mul2(d, w[c][i]);
+          const Two d = pair(v[1][c], i), h = mul2(add2(pair(v[0][c], i), minus), r2), g = mul2(d, w[i]);
           dw[c][i] = fma2(d, h, dw[c][i]);
           db[c][i] = add2(db[c][i], d);
           sg = add2(sg, g);
           sgh = fma2(g, h, sgh);
           if constexpr (KEEP) kept[c][i][0] = h, kept[c][i][1] = g;
         }
+      }
       s[0] = sum2(sg);
       s[1] = sum2(sgh);
     }
@@ -113,6 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         Chunk<T> out;
+        Two w[4];
+        if constexpr (!KEEP) weight(c, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           Two h, g;
@@ -121,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
             g = add2(kept[c][i][1], s1);
           } else {
             h = mul2(add2(pair(v[0][c], i), minus), r2);
-            g = fma2(pair(v[1][c], i), w[c][i], s1);
+            g = fma2(pair(v[1][c], i), w[i], s1);
           }
           set_pair(out, i, mul2(fma2(h, s2, g), r2));
         }
@@ -150,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
           if (j + i < have) out[at.col(c, j + i)] = u[i];
       }
     };
-    if constexpr (TPR == kThreads) {
+    if constexpr (TPR == kThreads<TPR>) {
 #pragma unroll
       for (int which = 0; which < 2; ++which)
 #pragma unroll
@@ -161,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
                                                      f[which][c][j + 3]));
     } else {
       // those of the rows that the CTA had at a time: within warps, then from all of them
-      constexpr int U = TPR < 32 ? 32 : TPR, UNITS = kThreads / U;
+      constexpr int U = TPR < 32 ? 32 : TPR, UNITS = kThreads<TPR> / U;
       cp_async_wait<0>();
       __syncthreads();  // (the ring is done with)
       float4 *meet = reinterpret_cast<float4 *>(ring);  // [which][c][j / 4][unit][thread]
@@ -180,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const Params p) {
                 make_float4(f[which][c][j], f[which][c][j + 1], f[which][c][j + 2], f[which][c][j + 3]);
         }
       __syncthreads();
-      for (int i = threadIdx.x; i < 2 * CH * 2 * U; i += kThreads) {
+      for (int i = threadIdx.x; i < 2 * CH * 2 * U; i += kThreads<TPR>) {
         const int t2 = i % U, k = i / U, which = k / (2 * CH), c = k / 2 % CH, j = k % 2 * 4;
         if (t2 >= TPR) continue;  // (a narrow row's other copies)
         float4 v = meet[k * UNITS * U + t2];
@@ -320,22 +352,33 @@ struct Plan {
   int rows_each;    // (tpr == 0) rows of a sum
 };
 
-static Plan make_plan(int rows, int cols, int sms) {
-  Plan pl{};
-  pl.tpr = cols <= 64     ? 8
-           : cols <= 512  ? 32
-           : cols <= 2048 ? 128
-           : cols <= 4096 ? 256
-           : cols <= kLongestHere ? 512 : 0;
-  if (pl.tpr) {
-    const long long most = ceil_div(rows, kThreads / pl.tpr);
+// Threads on a row; 0: rows do not stay in registers. A thread with 16 elements waits as long for its row's sums as
+// one with 8: 16384 x 1024 BF16 26.9 us with 128 threads on a row, 22.5 with 64; 4099 x 777 BF16, element by element,
+// 17.0 and 13.8. `one_by_one`: FP32 rows that are not aligned, which come element by element and with 16 of them take
+// more registers than there are: 4099 x 777 12.6 us with 128 threads, 17.8 with 64; 8192 x 4095 80 with 512, 135 with
+// 256.
+static int threads_on(int cols, bool one_by_one) {
+  const int more = one_by_one ? 2 : 1;
+  return cols <= 64     ? 8
+         : cols <= 256  ? 32
+         : cols <= 512  ? 32 * more
+         : cols <= 1024 ? 64 * more
+         : cols <= 2048 ? 128 * more
+         : cols <= 4096 ? 256 * more
+         : cols <= 8192 ? 512
+         : cols <= kLongestHere ? 768 : 0;
+}
+
+static Plan make_plan(int rows, int cols, int tpr, int sms) {
+  Plan pl{tpr};
+  if (tpr) {
+    const long long most = ceil_div(rows, tpr > 512 ? 1 : 512 / tpr);
     pl.grid = (int)std::min<long long>(most, std::max<long long>(sms, ceil_div(most, kMostRows)));
     pl.parts = pl.grid;
   } else {
     const long long blocks = ceil_div(cols, kLongCols);
     pl.rows_each = (int)std::max<long long>(1, std::min<long long>(kMostRows, rows * blocks / (8LL * sms)));
     pl.parts = (int)ceil_div(rows, pl.rows_each);
-    pl.grid = 0;
   }
   return pl;
 }
@@ -352,7 +395,7 @@ static cudaError_t launch(const Params &p, int grid, cudaStream_t stream) {
   static cudaError_t set[kDevices];
   static std::once_flag once[kDevices];
   const cudaError_t e = allow_bytes(backward_kernel<T, TPR, CH, VEC>, bytes, once, set);
-  return e != cudaSuccess ? e : launch_1d(backward_kernel<T, TPR, CH, VEC>, grid, kThreads, bytes, 1, stream, p);
+  return e != cudaSuccess ? e : launch_1d(backward_kernel<T, TPR, CH, VEC>, grid, kThreads<TPR>, bytes, 1, stream, p);
 }
 template <class T, int TPR, int CH>
 static cudaError_t launch(const Params &p, bool vec, int grid, cudaStream_t stream) {
@@ -363,25 +406,31 @@ template <class T>
 static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaStream_t stream) {
   if (p.cols <= 64) return launch<T, 8, 1>(p, vec, pl.grid, stream);
   if (p.cols <= 256) return launch<T, 32, 1>(p, vec, pl.grid, stream);
-  if constexpr (T::SIZE == 4) {
-    if (!vec) {
-      if (p.cols <= 512) return launch<T, 64, 1, false>(p, pl.grid, stream);
-      if (p.cols <= 1024) return launch<T, 128, 1, false>(p, pl.grid, stream);
-      if (p.cols <= 2048) return launch<T, 256, 1, false>(p, pl.grid, stream);
-      if (p.cols <= 4096) return launch<T, 512, 1, false>(p, pl.grid, stream);
+  if (p.cols <= 4096) {
+    if constexpr (T::SIZE == 4) {
+      switch (vec ? 0 : pl.tpr) {
+        case 64: return launch<T, 64, 1, false>(p, pl.grid, stream);
+        case 128: return launch<T, 128, 1, false>(p, pl.grid, stream);
+        case 256: return launch<T, 256, 1, false>(p, pl.grid, stream);
+        case 512: return launch<T, 512, 1, false>(p, pl.grid, stream);
+      }
+      switch (pl.tpr) {
+        case 32: return launch<T, 32, 2, true>(p, pl.grid, stream);
+        case 64: return launch<T, 64, 2, true>(p, pl.grid, stream);
+        case 128: return launch<T, 128, 2, true>(p, pl.grid, stream);
+        default: return launch<T, 256, 2, true>(p, pl.grid, stream);
+      }
     } else {
-      if (p.cols <= 512) return launch<T, 32, 2, true>(p, pl.grid, stream);
-      if (p.cols <= 1024) return launch<T, 64, 2, true>(p, pl.grid, stream);
-      if (p.cols <= 2048) return launch<T, 128, 2, true>(p, pl.grid, stream);
-      if (p.cols <= 4096) return launch<T, 256, 2, true>(p, pl.grid, stream);
+      switch (pl.tpr) {
+        case 32: return launch<T, 32, 2>(p, vec, pl.grid, stream);
+        case 64: return launch<T, 64, 2>(p, vec, pl.grid, stream);
+        case 128: return launch<T, 128, 2>(p, vec, pl.grid, stream);
+        default: return launch<T, 256, 2>(p, vec, pl.grid, stream);
+      }
     }
-  } else {
-    if (p.cols <= 512) return launch<T, 32, 2>(p, vec, pl.grid, stream);
-    if (p.cols <= 1024) return launch<T, 64, 2>(p, vec, pl.grid, stream);
-    if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, pl.grid, stream);
-    if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, pl.grid, stream);
   }
-  if (p.cols <= kLongestHere) return launch<T, 512, 2>(p, vec, pl.grid, stream);
+  if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, pl.grid, stream);
+  if (p.cols <= kLongestHere) return launch<T, 768, 2>(p, vec, pl.grid, stream);
   if (p.dx) {
     const cudaError_t e = launch_1d(vec ? along_kernel<T, true> : along_kernel<T, false>, std::min(p.rows, 2 * sms),
                                     1024, 0, 1, stream, p);
@@ -409,7 +458,8 @@ extern "C" int layer_norm_backward_workspace_size(int rows, int cols, size_t *by
     (void)cudaGetLastError();
     sms = 152;  // no device here: the answer for a whole GB300
   }
-  const lnb::Plan pl = lnb::make_plan(rows, cols, sms);
+  // (the more threads on a row, the more sums)
+  const lnb::Plan pl = lnb::make_plan(rows, cols, lnb::threads_on(cols, true), sms);
   *bytes = lnb::along_bytes(pl, rows) + lnb::part_bytes(pl, cols);
   return 0;
 }
@@ -447,7 +497,6 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   if (rows == 0)
     return (int)launch_1d(lnb::reduce_kernel, 2 * blocks, 32 * lnb::kReduceWarps, 0, 1, stream,
                           static_cast<const float *>(nullptr), 0, cols, 0LL, blocks, dweight, dbias, beta);
-  const lnb::Plan pl = lnb::make_plan(rows, cols, sms);
   const long long size = x_type == LN_F32 ? 4 : 2;
   lnb::Params p{};
   p.rows = rows;
@@ -463,6 +512,11 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   p.r = 1.0f / p.n;
   p.dx = static_cast<char *>(dx);
   p.lddx = lddx * size;
+  const auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
+  const bool vec = rows::aligned(at(dy), rows > 1 ? p.lddy : 0) &&
+                   rows::aligned(at(x), rows > 1 ? p.ldx : 0) &&
+                   (dx == nullptr || rows::aligned(at(dx), rows > 1 ? p.lddx : 0));
+  const lnb::Plan pl = lnb::make_plan(rows, cols, lnb::threads_on(cols, x_type == LN_F32 && !vec), sms);
   p.parts = pl.parts;
   p.pitch = lnb::pitch_of(cols);
   const size_t along = dx ? lnb::along_bytes(pl, rows) : 0;
@@ -474,10 +528,6 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
     p.along = reinterpret_cast<float2 *>(ws);
     if (sums) p.part = reinterpret_cast<float *>(ws + along);
   }
-  const auto at = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
-  const bool vec = rows::aligned(at(dy), rows > 1 ? p.lddy : 0) &&
-                   rows::aligned(at(x), rows > 1 ? p.ldx : 0) &&
-                   (dx == nullptr || rows::aligned(at(dx), rows > 1 ? p.lddx : 0));
   e = x_type == LN_F32    ? lnb::run<rows::F32>(p, pl, vec, sms, stream)
       : x_type == LN_BF16 ? lnb::run<rows::BF16>(p, pl, vec, sms, stream)
                           : lnb::run<rows::F16>(p, pl, vec, sms, stream);

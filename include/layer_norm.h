@@ -56,8 +56,8 @@ int layer_norm_backward(int rows, int cols, const void *dy, int lddy, const void
                         int w_type, void *dx, int lddx, float *dweight, float *dbias, float beta,
                         cudaStream_t stream);
 
-/* Bytes of workspace that layer_norm_backward takes from the library's pool on the current device
- * (without one: on a whole GB300). Returns 0 or -1, -2 for an illegal rows, cols. */
+/* Bytes of workspace that layer_norm_backward takes at most from the library's pool on the current device
+ * (without one: on a whole GB300); FP32 rows that are not 16-byte aligned take the most. Returns 0 or -1, -2 for an illegal rows, cols. */
 int layer_norm_backward_workspace_size(int rows, int cols, size_t *bytes);
 
 /* The arguments of both in their order, as structures: one pointer crosses a language binding faster

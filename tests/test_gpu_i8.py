@@ -69,6 +69,14 @@ def test_quantize_many_rows(shape):
     check_quantized(x, *sg.i8_quantize(x))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(2500, 1000), (620, 4608), (620, 6144), (620, 6145), (310, 8193), (310, 12288),
+                                   (310, 12289), (160, 16384)], ids=lambda s: "x".join(map(str, s)))
+def test_quantize_layouts_of_long_rows(shape, dtype):
+    x = (rand(*shape, seed=9) * torch.exp(2 * rand(shape[0], 1, seed=1))).to(dtype).cuda()
+    check_quantized(x, *sg.i8_quantize(x))
+
+
 @pytest.mark.parametrize("cols", [33, 390, 4000, 17000])
 @pytest.mark.parametrize("offset", [0, 1, 3, 8])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

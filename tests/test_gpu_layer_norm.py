@@ -118,6 +118,24 @@ def test_parameters(shape, params):
     assert all(torch.equal(p, q) for p, q in zip(alone, full)) and alone[1] is into[0]
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(5000, 300), (3000, 700), (2500, 1501), (700, 4095), (310, 4608), (310, 6144),
+                                   (310, 6145), (310, 8193), (310, 10240), (310, 12288), (310, 12289), (310, 12296),
+                                   (160, 16384)], ids=lambda s: "x".join(map(str, s)))
+def test_layouts_of_long_rows(shape, dtype, offset):
+    """Several rows for each block in the layouts of long rows and of unaligned ones."""
+    x, w, b, dy = problem(*shape, dtype)
+    pitch = (shape[1] + offset + 7) // 8 * 8 + offset
+    x, dy = (torch.cat((t, t.new_zeros(shape[0], pitch - shape[1])), 1)[:, :shape[1]] for t in (x, dy))
+    got = sg.layer_norm(x, w, b, stats=True)
+    check(x, w, b, 1e-5, got)
+    check_backward(dy, x, *got[1:], w, sg.layer_norm_backward(dy, x, *got[1:], w))
+    alone, *none = sg.layer_norm_backward(dy, x, *got[1:])
+    assert none == [None, None]
+    check_backward(dy, x, *got[1:], None, (alone, *sg.layer_norm_backward(dy, x, *got[1:], torch.ones_like(w))[1:]))
+
+
 @pytest.mark.parametrize("shape", [(5000, 40), (3000, 130), (2500, 512), (2000, 1500), (700, 4096),
                                    (400, 8192), (70000, 16), (60, 20000)], ids=lambda s: "x".join(map(str, s)))
 def test_many_rows(shape):
