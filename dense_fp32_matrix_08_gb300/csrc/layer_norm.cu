@@ -31,10 +31,12 @@ struct Params {
 };
 
 // CTAs of norm_kernel per SM: 768 threads with 80 registers each; 512 with 128 where a thread of a warp has
-// 32 elements; 1024 with 64 for rows of 4097 elements and more. FP32 rows of 4097 to 8192 elements and rows that are
-// not aligned: one CTA of 512 (4096 x 8192 FP32 42 us, with two of them 46 to 55; BF16 24.6, with one 27.8).
+// 32 elements; 1024 with 64 where it has 8 or rows have 6145 elements and more. FP32 rows of 6145 to 8192 elements and
+// rows that are not aligned: one CTA of 512 (4096 x 8192 FP32 42 us, with two of them 46 to 55; BF16 24.6, with one
+// 27.8).
 template <class T, int TPR, int CH, bool VEC>
 constexpr int kPerSm = TPR < 128    ? (CH > 2 ? 4 : 6)
+                       : CH == 1    ? 1024 / TPR
                        : TPR <= 384 ? 768 / TPR
                                     : (TPR == 512 && VEC && T::SIZE == 2 ? 2 : 1);
 // Rows under way. More than it takes costs time: 8192 x 4096 FP32 takes 41.0 us with two, 46.7 with three, BF16
@@ -232,11 +234,19 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 256) return launch<T, 32, 1>(p, vec, sms, stream);
   if (p.cols <= 512) return launch<T, 32, 2>(p, vec, sms, stream);
   // (a warp per row needs no barrier, but aligned rows for its registers: 16384 x 1024 BF16 15.1 us with 128
-  // threads on a row, 12.3 so)
-  if (p.cols <= 1024 && vec) return launch<T, 32, 4, true>(p, sms, stream);
-  if (p.cols <= 1024) return launch<T, 128, 1, false>(p, sms, stream);
-  if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
-  if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  // threads on a row, 11.7 so. Rows that come element by element have 8 of them per thread where that is faster: 16384
+  // x 1023 BF16 17.5 us, with 768 threads per SM 22.8; 8192 x 4095 BF16 39.3, with 16 per thread 43.2, but FP32 48.6
+  // and 47.7.)
+  if (p.cols <= 1024) return vec ? launch<T, 32, 4, true>(p, sms, stream) : launch<T, 128, 1, false>(p, sms, stream);
+  if constexpr (T::SIZE == 2) {
+    if (!vec && p.cols <= 2048) return launch<T, 256, 1, false>(p, sms, stream);
+    if (!vec && p.cols <= 4096) return launch<T, 512, 1, false>(p, sms, stream);
+    if (p.cols <= 2048) return launch<T, 128, 2, true>(p, sms, stream);
+    if (p.cols <= 4096) return launch<T, 256, 2, true>(p, sms, stream);
+  } else {
+    if (p.cols <= 2048) return launch<T, 128, 2>(p, vec, sms, stream);
+    if (p.cols <= 4096) return launch<T, 256, 2>(p, vec, sms, stream);
+  }
   if (p.cols <= 6144) return launch<T, 384, 2>(p, vec, sms, stream);
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, sms, stream);
   if (p.cols <= 12288) return launch<T, 768, 2>(p, vec, sms, stream);
