@@ -5,9 +5,8 @@
 // its last use, so that the variance is the mean of the squared distances themselves: no difference
 // of large sums. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
 // FP32 numbers per instruction: one by one they were 71% busy and it took 32 us); FP32 41 us, 96%. 1 x 4096: 1.7 us.
-// 16384 x 1024 BF16 11.7 us, 84%; 16384 x 512 7.5, 66%: the sums' exchanges weigh more there. Rows of 16384 16-bit
-// elements take 45 us for as many bytes as those of 4096: 1024 threads leave no registers for the parameters,
-// which are read for each row.
+// 16384 x 1024 BF16 11.7 us, 84%; 16384 x 512 7.5, 66%: the sums' exchanges weigh more there. 2048 x 16384 BF16
+// 35.5 us, 56%: one row at a time per SM. Rows at any alignment come element by element: 8192 x 4095 BF16 39 us.
 #include <algorithm>
 #include <cmath>
 
