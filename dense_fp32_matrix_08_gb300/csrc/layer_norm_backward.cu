@@ -9,7 +9,7 @@
 // 8192 x 4096 BF16: 39.7 us, 5.1 TB/s. Without dw and db 34.2 (87% of a copy's rate): the sums' registers
 // leave 16 warps per SM, issue slots 50% busy; the rest is the sums' way. FP32: 63 us, 6.4 TB/s (94%).
 // 4099 x 777 FP32: 12.5, of which 3.5 are for the sums; its rows are not aligned, so that they come element by
-// element. Rows of more than 12288 elements are read twice: 2048 x 16384 BF16 96 us.
+// element. Longer rows than registers hold are read twice: 2048 x 16384 FP32 128 us (BF16, in registers, 72).
 #include <algorithm>
 #include <cmath>
 
@@ -22,7 +22,8 @@ namespace lnb {
 using namespace rows;
 
 constexpr int kMostRows = 500;  // rows that a thread adds up in FP32
-constexpr int kLongestHere = 12288;  // elements of a row that stays in registers beside the sums
+// Elements of a row that stays in registers beside the sums: any, and 16-bit ones that are aligned.
+constexpr int kLongestHere = 12288, kLongestPacked = kLongest;
 
 struct Params {
   int rows, cols;
@@ -39,17 +40,18 @@ struct Params {
   float2 *along;            // rows that do not stay in registers: sum g / n, sum (g h) / n
 };
 
-// One CTA of 512 threads per SM, with up to 128 registers each (768 with 80 for the longest rows): as many rows
-// at a time as that makes, and one sum of each column per SM.
+// One CTA of 512 threads per SM, with up to 128 registers each (768 with 80, 1024 with 64 for the longest rows): as
+// many rows at a time as that makes, and one sum of each column per SM.
 template <int TPR>
 constexpr int kThreads = TPR > 512 ? TPR : 512;
 // Rows under way. More than it takes costs time: 8192 x 4096 FP32 63 us with two, 66 with three; FP32 rows of 1024
 // and less are short enough for three (16384 x 1024 36.5 us, 38.3 with two); BF16 40.0 with three, 41.0 with two.
+// (Three of 16384 16-bit elements have no room.)
 template <class T, int TPR, int CH>
-constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 ? 2 : 3;
+constexpr int kDepth = (T::SIZE == 4 && TPR * CH >= 256) || TPR == 1024 ? 2 : 3;
 
 // Whether the weight of a thread's columns lies in shared memory, in places of the thread's own, instead of registers:
-// for rows of 8193 to 12288 elements, where it fits. (4096 x 12288 BF16 77 us, 93 with it in registers that spill, 149
+// for rows of 8193 elements and more, where it fits. (4096 x 12288 BF16 77 us, 93 with it in registers that spill, 149
 // with the rows read twice. FP32 142, with registers that spill: read again from L2 for each row 152, rows read
 // twice 208.)
 template <class T, int TPR, bool VEC>
@@ -356,8 +358,9 @@ struct Plan {
 // one with 8: 16384 x 1024 BF16 26.9 us with 128 threads on a row, 22.5 with 64; 4099 x 777 BF16, element by element,
 // 17.0 and 13.8. `one_by_one`: FP32 rows that are not aligned, which come element by element and with 16 of them take
 // more registers than there are: 4099 x 777 12.6 us with 128 threads, 17.8 with 64; 8192 x 4095 80 with 512, 135 with
-// 256.
-static int threads_on(int cols, bool one_by_one) {
+// 256. `packed`: 16-bit rows that are aligned, of which 1024 threads hold the longest ones, with registers that
+// spill: 2048 x 16384 72 us, read twice 96.
+static int threads_on(int cols, bool one_by_one, bool packed) {
   const int more = one_by_one ? 2 : 1;
   return cols <= 64     ? 8
          : cols <= 256  ? 32
@@ -366,7 +369,8 @@ static int threads_on(int cols, bool one_by_one) {
          : cols <= 2048 ? 128 * more
          : cols <= 4096 ? 256 * more
          : cols <= 8192 ? 512
-         : cols <= kLongestHere ? 768 : 0;
+         : cols <= kLongestHere ? 768
+         : cols <= kLongestPacked && packed ? 1024 : 0;
 }
 
 static Plan make_plan(int rows, int cols, int tpr, int sms) {
@@ -431,6 +435,9 @@ static cudaError_t run(const Params &p, const Plan &pl, bool vec, int sms, cudaS
   }
   if (p.cols <= 8192) return launch<T, 512, 2>(p, vec, pl.grid, stream);
   if (p.cols <= kLongestHere) return launch<T, 768, 2>(p, vec, pl.grid, stream);
+  if constexpr (T::SIZE == 2) {
+    if (pl.tpr == 1024) return launch<T, 1024, 2, true>(p, pl.grid, stream);
+  }
   if (p.dx) {
     const cudaError_t e = launch_1d(vec ? along_kernel<T, true> : along_kernel<T, false>, std::min(p.rows, 2 * sms),
                                     1024, 0, 1, stream, p);
@@ -458,8 +465,8 @@ extern "C" int layer_norm_backward_workspace_size(int rows, int cols, size_t *by
     (void)cudaGetLastError();
     sms = 152;  // no device here: the answer for a whole GB300
   }
-  // (the more threads on a row, the more sums)
-  const lnb::Plan pl = lnb::make_plan(rows, cols, lnb::threads_on(cols, true), sms);
+  // (the more threads on a row, the more sums; rows that are read twice leave as many as any)
+  const lnb::Plan pl = lnb::make_plan(rows, cols, lnb::threads_on(cols, true, false), sms);
   *bytes = lnb::along_bytes(pl, rows) + lnb::part_bytes(pl, cols);
   return 0;
 }
@@ -516,7 +523,8 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   const bool vec = rows::aligned(at(dy), rows > 1 ? p.lddy : 0) &&
                    rows::aligned(at(x), rows > 1 ? p.ldx : 0) &&
                    (dx == nullptr || rows::aligned(at(dx), rows > 1 ? p.lddx : 0));
-  const lnb::Plan pl = lnb::make_plan(rows, cols, lnb::threads_on(cols, x_type == LN_F32 && !vec), sms);
+  const int tpr = lnb::threads_on(cols, size == 4 && !vec, size == 2 && vec);
+  const lnb::Plan pl = lnb::make_plan(rows, cols, tpr, sms);
   p.parts = pl.parts;
   p.pitch = lnb::pitch_of(cols);
   const size_t along = dx ? lnb::along_bytes(pl, rows) : 0;
