@@ -22,9 +22,10 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  * weight and bias (cols elements of type w_type each) may be NULL: 1 and 0. mean and rstd (rows FP32
  * numbers each), which layer_norm_backward takes, may be NULL.
  *
- * Sums are FP32 (in rows of more than 16384 elements with 48 bits), in an order fixed by the shape: the same
- * call gives the same bits. Magnitudes up to 2^50 are held; with larger ones the squares leave FP32.
- * A NaN or an infinity makes its own row NaN. y may be x itself with ldy = ldx, and must not overlap
+ * Sums are FP32 (in rows of more than 16384 elements with 48 bits), in an order fixed by the shape, the type
+ * and whether rows are 16-byte aligned: the same call gives the same bits. Magnitudes up to 2^50 are held; with
+ * larger ones the squares leave FP32. A NaN or an infinity makes its own row NaN, and so does eps == 0 a
+ * constant row, whose rstd is infinite. y may be x itself with ldy = ldx, and must not overlap
  * it otherwise.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
@@ -43,9 +44,10 @@ int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const voi
  * does not read dweight and dbias; with rows == 0 they become beta times themselves. dx may be dy or
  * x itself with the same leading dimension, and must not overlap them otherwise.
  *
- * Sums along rows are FP32 (in rows of more than 8192 elements with 48 bits), those over the rows FP32 within
- * a block (at most 500 rows one after the other) and 64-bit beyond, in an order fixed by the shape and
- * the device: the same call gives the same bits. The workspace (layer_norm_backward_workspace_size bytes) is a stream-ordered
+ * Sums along rows are FP32 (with 48 bits in rows of more than 12288 elements, or of more than 16384 where they
+ * are of 16 bits and 16-byte aligned), those over the rows FP32 within a block (at most 500 rows one after the
+ * other) and 64-bit beyond, in an order fixed by the shape, the type, that alignment and the device: the same call
+ * gives the same bits. The workspace (layer_norm_backward_workspace_size bytes at most) is a stream-ordered
  * allocation from the library's pool.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
