@@ -340,6 +340,7 @@ extern "C" int clip_grad_norm(int count, const void *const *grads, const int *ty
     }
     if (gc::overlapping(count, grads, types, sizes, out, out_types)) return -7;
   }
+  if (misplaced(norm, GC_F32)) return -9;
   if (arrays == 0 && norm == nullptr) return 0;
   int sms = 0;
   const cudaError_t e = device_setup(&sms);

@@ -732,15 +732,17 @@ extern "C" int i8_linear(int M, int N, int K, const void *x, int ldx, const floa
                          int ldd, cudaStream_t stream) {
   const bool read = M > 0 && N > 0 && K > 0;
   const auto bad_ptr = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
+  const auto misplaced = [](const float *q) { return reinterpret_cast<uintptr_t>(q) % 4 != 0; };
   if (M < 0) return -1;
   if (N < 0) return -2;
   if (K < 0 || K > i8::LARGEST_K) return -3;
   if (read && (x == nullptr || bad_ptr(x))) return -4;
   if (ldx < std::max(1, K) || ldx % 16 != 0) return -5;
-  if (read && x_scale == nullptr) return -6;
+  if (read && (x_scale == nullptr || misplaced(x_scale))) return -6;
   if (read && (w == nullptr || bad_ptr(w))) return -7;
   if (ldw < std::max(1, K) || ldw % 16 != 0) return -8;
-  if (read && w_scale == nullptr) return -9;
+  if (read && (w_scale == nullptr || misplaced(w_scale))) return -9;
+  if (misplaced(bias)) return -10;
   if (M > 0 && N > 0 && D == nullptr) return -12;
   if (d_type != I8_F32 && d_type != I8_BF16 && d_type != I8_F16) return -13;
   if (reinterpret_cast<uintptr_t>(D) % (d_type == I8_F32 ? 4 : 2) != 0) return -12;

@@ -224,7 +224,7 @@ extern "C" int i8_quantize(int rows, int cols, const void *x, int x_type, int ld
   if (ldx < std::max(1, cols)) return -5;
   if (any && q == nullptr) return -6;
   if (ldq < std::max(1, cols)) return -7;
-  if (rows > 0 && scale == nullptr) return -8;
+  if ((rows > 0 && scale == nullptr) || reinterpret_cast<uintptr_t>(scale) % 4 != 0) return -8;
   if (rows == 0) return 0;
   int sms = 0;
   const cudaError_t e = device_setup(&sms);

@@ -279,6 +279,8 @@ extern "C" int layer_norm(int rows, int cols, const void *x, int x_type, int ldx
   if (rows > 0 && y == nullptr) return -10;
   if (misplaced(y, x_type)) return -10;
   if (ldy < cols) return -11;
+  if (misplaced(mean, LN_F32)) return -12;
+  if (misplaced(rstd, LN_F32)) return -13;
   if (rows == 0) return 0;
   int sms = 0;
   const cudaError_t e = device_setup(&sms);

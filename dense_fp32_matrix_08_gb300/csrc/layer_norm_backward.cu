@@ -488,12 +488,14 @@ extern "C" int layer_norm_backward(int rows, int cols, const void *dy, int lddy,
   if (misplaced(dy, x_type)) return -3;
   if (misplaced(x, x_type)) return -5;
   if (ldx < cols) return -7;
-  if (rows > 0 && mean == nullptr) return -8;
-  if (rows > 0 && rstd == nullptr) return -9;
+  if ((rows > 0 && mean == nullptr) || misplaced(mean, LN_F32)) return -8;
+  if ((rows > 0 && rstd == nullptr) || misplaced(rstd, LN_F32)) return -9;
   if (!known(w_type)) return -11;
   if (misplaced(weight, w_type)) return -10;
   if (misplaced(dx, x_type)) return -12;
   if (dx != nullptr && lddx < cols) return -13;
+  if (misplaced(dweight, LN_F32)) return -14;
+  if (misplaced(dbias, LN_F32)) return -15;
   if (dx == nullptr && dweight == nullptr && dbias == nullptr) return 0;
   const bool sums = dweight != nullptr || dbias != nullptr;
   if (rows == 0 && (!sums || beta == 1.0f)) return 0;

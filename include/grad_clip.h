@@ -35,8 +35,8 @@ enum { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 }; /* types of gradients and results 
  * The workspace is a stream-ordered allocation from the library's pool.
  *
  * Returns 0, -i for the first illegal argument (count = 1, grads = 2, types = 3, sizes = 4, max_norm =
- * 5 (>= 0), eps = 6 (>= 0, finite), out = 7 (entries, their alignment and overlaps), out_types = 8),
- * or a cudaError_t. */
+ * 5 (>= 0), eps = 6 (>= 0, finite), out = 7 (entries, their alignment and overlaps), out_types = 8,
+ * norm = 9 (aligned)), or a cudaError_t. */
 int clip_grad_norm(int count, const void *const *grads, const int *types, const long long *sizes,
                    float max_norm, float eps, void *const *out, const int *out_types, float *norm,
                    cudaStream_t stream);

@@ -29,7 +29,8 @@ enum { I8_F32 = 0, I8_BF16 = 1, I8_F16 = 2 }; /* types of x and of D */
  * between cols and ldq are not written. cols == 0 writes the scales of rows of zeros.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1, cols = 2, x = 3,
- * x_type = 4, ldx = 5, q = 6, ldq = 7, scale = 8), or a cudaError_t. */
+ * x_type = 4, ldx = 5, q = 6, ldq = 7, scale = 8), or a cudaError_t. x and scale are aligned to their
+ * elements. */
 int i8_quantize(int rows, int cols, const void *x, int x_type, int ldx, void *q, int ldq, float *scale,
                 cudaStream_t stream);
 
@@ -42,7 +43,8 @@ int i8_quantize(int rows, int cols, const void *x, int x_type, int ldx, void *q,
  * The sum over k is the exact whole number (K is at most 131071, so that 32 bits hold it), whatever
  * way the product runs; scales, bias and beta are applied in FP32, with one rounding to d_type. The
  * product of the two scales is formed first: where it leaves FP32's range, so does the result.
- * beta == 0 does not read D; K == 0 does not read x, w or their scales. D must not overlap x or w.
+ * beta == 0 does not read D; K == 0 does not read x, w or their scales. D must not overlap x or w. D, bias
+ * and the scales are aligned to their elements.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (M = 1, N = 2, K = 3, x = 4,
  * ldx = 5, x_scale = 6, w = 7, ldw = 8, w_scale = 9, bias = 10, D = 12, d_type = 13, ldd = 14), or a

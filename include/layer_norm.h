@@ -30,7 +30,7 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
  * (>= 1), x = 3, x_type = 4, ldx = 5, weight = 6, bias = 7, w_type = 8, eps = 9 (>= 0, finite),
- * y = 10, ldy = 11), or a cudaError_t. */
+ * y = 10, ldy = 11, mean = 12, rstd = 13), or a cudaError_t. Arrays are aligned to their elements. */
 int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const void *weight,
                const void *bias, int w_type, float eps, void *y, int ldy, float *mean, float *rstd,
                cudaStream_t stream);
@@ -52,7 +52,7 @@ int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const voi
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
  * (>= 1), dy = 3, lddy = 4, x = 5, x_type = 6, ldx = 7, mean = 8, rstd = 9, weight = 10, w_type = 11,
- * dx = 12, lddx = 13, dweight = 14, dbias = 15), or a cudaError_t. */
+ * dx = 12, lddx = 13, dweight = 14, dbias = 15), or a cudaError_t. Arrays are aligned to their elements. */
 int layer_norm_backward(int rows, int cols, const void *dy, int lddy, const void *x, int x_type,
                         int ldx, const float *mean, const float *rstd, const void *weight,
                         int w_type, void *dx, int lddx, float *dweight, float *dbias, float beta,
