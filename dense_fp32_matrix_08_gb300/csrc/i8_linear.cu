@@ -611,14 +611,15 @@ static const Cost kCosts[] = {{128, true, 5.30, 0.320, 1.87, 0.0}, {128, false, 
 static Plan make_plan(int M, int N, int K, int sms) {
   if (M <= kFewRows) return {0, false, 1};
   const int KB = (int)ceil_div(K, BK);
-  Plan best{128, true, 1};
+  Plan best{128, false, 1};
   double best_cost = 1e300;
   for (const Cost &c : kCosts) {
+    if (c.pair && sms < 2) continue;
     const long long tiles = ceil_div(N, c.pair ? 2 * BP : BP) * ceil_div(M, c.tn);
     const int at_once = c.pair ? sms / 2 : sms;
     for (int S = 1; S <= (c.pair ? 1 : MAX_CLUSTER); S *= 2) {
       // (clusters of 8 sit in one GPC each: more than about 12 of them do not run at once)
-      if (S > 1 && (S > KB || tiles * S > (S == 8 ? 96 : sms))) break;
+      if (S > 1 && (S > KB || tiles * S > (S == 8 ? std::min(96, sms) : sms))) break;
       const double cost = c.call + (double)ceil_div(tiles * S, at_once) * (c.block * ((KB + S - 1) / S) + c.round) +
                           (S > 1 ? c.exchange : 0.0);
       if (cost < best_cost) {
