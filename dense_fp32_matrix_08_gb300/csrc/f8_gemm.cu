@@ -563,10 +563,11 @@ static Plan make_plan(int M, int N, int KB, bool a_mn, bool b_mn, bool a_vec, bo
       const int tn = tns[i], P = swap ? N : M, Q = swap ? M : N;
       const bool pair = tn == 256, vec = swap ? a_vec : b_vec;
       if ((swap ? a_mn : b_mn) && tn < 32) continue;  // (the narrowest swizzle spans 32 bytes)
+      if (pair && sms < 2) continue;
       const long long tiles = (long long)ceil_div(P, pair ? 2 * BP : BP) * ceil_div(Q, tn);
       for (int S = 1; S <= MAX_CLUSTER; S *= 2) {
         // (clusters of 8 sit in one GPC each: more than about 12 of them do not run at once)
-        if (S > 1 && (pair || S > KB || tiles * S > (S == 8 ? 96 : sms))) break;
+        if (S > 1 && (pair || S > KB || tiles * S > (S == 8 ? std::min(96, sms) : sms))) break;
         const int at_once = pair ? sms / 2 : sms;
         const long long per_sm = (tiles * S + at_once - 1) / at_once;
         const double cost = per_sm * ((vec ? block_vec : block)[i] * ((KB + S - 1) / S) +

@@ -25,3 +25,19 @@ def test_integer_product(sms):
                 if sms == 1:
                     assert plan["tile_channels"] in (0, 128)
                 assert plan["split"] <= max(1, sms)
+
+
+def test_one_sm_does_not_end_the_process_of_the_8_bit_float_product():
+    code = "import dense_fp32_matrix_08_gb300 as sg; print(sg.f8_gemm_plan(40, 300, 2000, num_sms=1))"
+    assert subprocess.run([sys.executable, "-c", code], capture_output=True).returncode == 0
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 7, 152])
+def test_8_bit_float_product(sms):
+    for M in SIZES:
+        for N in (1, 300, 4096):
+            for K in (1, 700, 131071):
+                plan = sg.f8_gemm_plan(M, N, K, num_sms=sms)
+                if sms == 1:
+                    assert plan["tile_cols"] < 256
+                assert plan["split"] <= max(1, sms)
