@@ -643,6 +643,7 @@ extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha,
                        cudaStream_t stream) {
   const bool read = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
   const auto bad_ptr = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
+  const auto misplaced = [](const float *q) { return reinterpret_cast<uintptr_t>(q) % 4 != 0; };
   if (transa != 0 && transa != 1) return -1;
   if (transb != 0 && transb != 1) return -2;
   if (M < 0) return -3;
@@ -651,14 +652,14 @@ extern "C" int f8_gemm(int transa, int transb, int M, int N, int K, float alpha,
   if (read && (A == nullptr || bad_ptr(A))) return -7;
   if (a_format != F8_E4M3 && a_format != F8_E5M2) return -8;
   if (lda < std::max(1, transa ? M : K) || lda % 16 != 0) return -9;
-  if (read && a_scale == nullptr) return -10;
+  if (read && (a_scale == nullptr || misplaced(a_scale))) return -10;
   if (a_rows != 1 && a_rows != 128) return -11;
   if (a_scale_mn < 0) return -12;
   if (a_scale_k < 0) return -13;
   if (read && (B == nullptr || bad_ptr(B))) return -14;
   if (b_format != F8_E4M3 && b_format != F8_E5M2) return -15;
   if (ldb < std::max(1, transb ? K : N) || ldb % 16 != 0) return -16;
-  if (read && b_scale == nullptr) return -17;
+  if (read && (b_scale == nullptr || misplaced(b_scale))) return -17;
   if (b_cols != 1 && b_cols != 128) return -18;
   if (b_scale_mn < 0) return -19;
   if (b_scale_k < 0) return -20;

@@ -469,13 +469,14 @@ extern "C" int f8_quantize(int rows, int cols, const void *x, int x_type, int ld
   if (format != F8_E4M3 && format != F8_E5M2) return -8;
   if (any && q == nullptr) return -10;
   if (ldq < std::max(1, cols)) return -11;
-  if (any && s == nullptr) return -12;
+  const auto misplaced = [](const float *at) { return reinterpret_cast<uintptr_t>(at) % 4 != 0; };
+  if (any && (s == nullptr || misplaced(s))) return -12;
   if (s_row < 0) return -13;
   if (s_col < 0) return -14;
   if (qc != nullptr) {
     if (block_rows != 1) return -15;
     if (ldqc < std::max(1, cols)) return -16;
-    if (any && sc == nullptr) return -17;
+    if (any && (sc == nullptr || misplaced(sc))) return -17;
     if (sc_row < 0) return -18;
     if (sc_col < 0) return -19;
   }
