@@ -3,7 +3,9 @@
 //
 // Bound by HBM: each element is read and written once. A row stays in registers from its one read to
 // its last use, so that the variance is the mean of the squared distances themselves: no difference
-// of large sums. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
+// of large sums. The FP32 sum of a row gives its mean m to at most 53 u mean|x| (u = 2^-24). Where that is not far
+// below the spread (far_off), the distances from m, exact there, are added up for what m lacks, e = sum (x - m) / n,
+// and the variance is taken again, from (x - m) - e: a constant row has var 0 and y = b. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
 // FP32 numbers per instruction: one by one they were 71% busy and it took 32 us); FP32 41 us, 96%. 1 x 4096: 1.7 us.
 // 16384 x 1024 BF16 11.7 us, 84%; 16384 x 512 7.5, 66%: the sums' exchanges weigh more there. 2048 x 16384 BF16
 // 35.5 us, 56%: one row at a time per SM. Rows at any alignment come element by element: 8192 x 4095 BF16 39 us.
@@ -29,12 +31,13 @@ struct Params {
   float *mean, *rstd;
 };
 
-// CTAs of norm_kernel per SM: 768 threads with 80 registers each; 512 with 128 where a thread of a warp has
-// 32 elements; 1024 with 64 where it has 8 or rows have 6145 elements and more. FP32 rows of 6145 to 8192 elements and
-// rows that are not aligned: one CTA of 512 (4096 x 8192 FP32 42 us, with two of them 46 to 55; BF16 24.6, with one
-// 27.8).
+// CTAs of norm_kernel per SM: 768 threads with 80 registers each (one CTA for rows of 8193 to 12288 elements); 512 with
+// 128 where a thread of a warp has 32 elements, 384 with 160 where these are FP32 (16384 x 1024 21.3 us, 23.1 with 512,
+// whose registers spill); 1024 with 64 where it has 8, or aligned 16-bit rows have 6145 to 8192 elements, or rows more
+// than 12288. FP32 rows of 6145 to 8192 elements and rows that are not aligned: one CTA of 512 (4096 x 8192 FP32 42 us,
+// with two of them 46 to 55; BF16 24.8, with one 27.8).
 template <class T, int TPR, int CH, bool VEC>
-constexpr int kPerSm = TPR < 128    ? (CH > 2 ? 4 : 6)
+constexpr int kPerSm = TPR < 128    ? (CH > 2 ? (T::SIZE == 4 ? 3 : 4) : 6)
                        : CH == 1    ? 1024 / TPR
                        : TPR <= 384 ? 768 / TPR
                                     : (TPR == 512 && VEC && T::SIZE == 2 ? 2 : 1);
@@ -43,6 +46,11 @@ constexpr int kPerSm = TPR < 128    ? (CH > 2 ? 4 : 6)
 // rows need three as well (16384 x 1024: 21.5 us, 24.1 with two; 4096 x 8192: 42 and 45).
 template <class T, int TPR, int CH>
 constexpr int kDepth = T::SIZE == 4 && TPR * CH >= 256 && TPR != 512 ? 2 : 3;
+
+// Whether the mean `near` may be off by what counts: where it is above 4 times the root of q, the mean square of the
+// distances from it. (Below, it is off by at most 53 u (4 + 1) of the spread. Both may be 0: the squares of the
+// smallest numbers are.)
+__device__ __forceinline__ bool far_off(float near, float q) { return near * near >= 16.0f * q && q < INFINITY; }
 
 // TPR threads on a row, CTAs of TPR (at least 128) threads that take rows in turn. The parameters of a
 // thread's columns stay in its registers. 1024 threads have none for that: those of 16-bit rows lie in shared memory
@@ -57,7 +65,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
   constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
   constexpr bool HOLD = TPR < 1024, SHARED = kShared<T, TPR, VEC>;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) RowSums<TPR, 1> sums;
+  __shared__ __align__(16) RowSums<TPR, 1> sums, again;
   const long long step = (long long)gridDim.x * RPB;
   long long base = (long long)blockIdx.x * RPB;  // (the same for a whole CTA)
   long long row = base + threadIdx.x / TPR;
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
       }
     float s[1] = {sum2(total)};
     row_sum(s, sums, 0);
-    const float mean = over(s[0], p.n, p.r);
+    float mean = over(s[0], p.n, p.r);
     const Two minus = both(-mean);
     total = 0;
 #pragma unroll
@@ -116,8 +124,34 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
       }
     s[0] = sum2(total);
     row_sum(s, sums, 1);
+    float var = over(s[0], p.n, p.r);
+    const bool off = far_off(mean, var);
+    if (TPR < 32 ? __any_sync(0xffffffffu, off) : off) {  // (the same for a row's threads)
+      total = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total = add2(total, d[c][i]);
+      s[0] = sum2(total);
+      row_sum(s, again, 0);
+      const float e = TPR >= 32 || off ? over(s[0], p.n, p.r) : 0.0f;  // (a warp's other rows keep what they have)
+      mean += e;
+      const Two rest = both(-e);
+      total = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[c][i] = add2(d[c][i], rest);
+          if (!ahead.whole) d[c][i] = first(d[c][i], i, n[c]);
+          total = fma2(d[c][i], d[c][i], total);
+        }
+      s[0] = sum2(total);
+      row_sum(s, again, 1);
+      var = over(s[0], p.n, p.r);
+    }
     // 1 / sqrt, with one step of Newton's iteration
-    const float v = over(s[0], p.n, p.r) + p.eps;
+    const float v = var + p.eps;
     float rstd = rsqrtf(v);
     if (v > 0.0f) rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
     if (row < p.rows) {
@@ -155,7 +189,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
 template <class T, bool VEC>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
   __shared__ Long part[2][32];
-  __shared__ float told[2];
+  __shared__ float told[4];
   griddep_launch_dependents();
   griddep_wait();
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -170,33 +204,50 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
       total.add(sum2(s));
     });
     total = cta_sum(total, part[0]);
-    if (threadIdx.x == 0) {
-      told[0] = total.over(p.cols);
-      if (p.mean) p.mean[row] = told[0];
-    }
+    if (threadIdx.x == 0) told[0] = total.over(p.cols);
     __syncthreads();
-    const Two minus = both(-told[0]);
-    total = Long();
-    blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
-      const int n = sh.count(0);
-      Chunk<T> v;
-      sh.load(x + at * T::SIZE, 0, n, v);
-      Two s = 0;
+    const float near = told[0];
+    const Two minus = both(-near);
+    float e = 0.0f;
+    // (x - near) - e, or its square, of 8 elements at a time
+    const auto distances = [&](bool squares) {
+      Long sum;
+      const Two rest = both(-e);
+      blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
+        const int n = sh.count(0);
+        Chunk<T> v;
+        sh.load(x + at * T::SIZE, 0, n, v);
+        Two s = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Two d = first(add2(pair(v, i), minus), i, n);
-        s = fma2(d, d, s);
-      }
-      total.add(sum2(s));
-    });
-    total = cta_sum(total, part[1]);
-    if (threadIdx.x == 0) {
-      told[1] = __frsqrt_rn(total.over(p.cols) + p.eps);
-      if (p.rstd) p.rstd[row] = told[1];
-    }
+        for (int i = 0; i < 4; ++i) {
+          const Two d = first(add2(add2(pair(v, i), minus), rest), i, n);
+          s = squares ? fma2(d, d, s) : add2(d, s);
+        }
+        sum.add(sum2(s));
+      });
+      return sum;
+    };
+    total = cta_sum(distances(true), part[1]);
+    if (threadIdx.x == 0) told[1] = total.over(p.cols);
     __syncthreads();
+    float var = told[1];
+    if (far_off(near, var)) {
+      total = cta_sum(distances(false), part[0]);
+      if (threadIdx.x == 0) told[2] = total.over(p.cols);
+      __syncthreads();
+      e = told[2];
+      total = cta_sum(distances(true), part[1]);
+      if (threadIdx.x == 0) told[3] = total.over(p.cols);
+      __syncthreads();
+      var = told[3];
+    }
+    const float rstd = __frsqrt_rn(var + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = near + e;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
     char *y = p.y + row * p.ldy;
-    const Two r2 = both(told[1]);
+    const Two rest = both(-e), r2 = both(rstd);
     blocks<T, 1024, VEC>(p.cols, [&](const auto &sh, long long at) {
       const int n = sh.count(0);
       Chunk<T> v, out;
@@ -205,7 +256,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const Params p) {
       parameters(from(p.weight, at), sh, 0, n, 1.0f, w);
       parameters(from(p.bias, at), sh, 0, n, 0.0f, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) set_pair(out, i, fma2(mul2(add2(pair(v, i), minus), r2), w[i], b[i]));
+      for (int i = 0; i < 4; ++i) set_pair(out, i, fma2(mul2(add2(add2(pair(v, i), minus), rest), r2), w[i], b[i]));
       sh.store(y + at * T::SIZE, 0, n, out);
     });
   }

@@ -23,7 +23,9 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  * numbers each), which layer_norm_backward takes, may be NULL.
  *
  * Sums are FP32 (in rows of more than 16384 elements with 48 bits), in an order fixed by the shape, the type
- * and whether rows are 16-byte aligned: the same call gives the same bits. Magnitudes up to 2^50 are held; with
+ * and whether rows are 16-byte aligned: the same call gives the same bits. Where the mean is more than 4 times the
+ * spread it is corrected by the mean of the distances from it, so that a spread of a few last places counts and a
+ * constant row has its number as the mean and no variance. y takes the mean before its rounding to FP32. Magnitudes up to 2^50 are held; with
  * larger ones the squares leave FP32. A NaN or an infinity makes its own row NaN, and so does eps == 0 a
  * constant row, whose rstd is infinite. y may be x itself with ldy = ldx, and must not overlap
  * it otherwise.
