@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kPerSm<T, TPR, CH, VEC>
       row_sum(s, again, 1);
       var = over(s[0], p.n, p.r);
     }
-    // 1 / sqrt, with one step of Newton's iteration
+    // 1 / sqrt, with one step of Newton's iteration where it is neither 0 nor infinite
     const float v = var + p.eps;
     float rstd = rsqrtf(v);
-    if (v > 0.0f) rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
+    if (v > 0.0f && v < INFINITY) rstd = fmaf(0.5f * rstd, fmaf(-v * rstd, rstd, 1.0f), rstd);
     if (row < p.rows) {
       if (sh.t == 0) {
         if (p.mean) p.mean[row] = mean;

@@ -25,10 +25,11 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  * Sums are FP32 (in rows of more than 16384 elements with 48 bits), in an order fixed by the shape, the type
  * and whether rows are 16-byte aligned: the same call gives the same bits. Where the mean is more than 4 times the
  * spread it is corrected by the mean of the distances from it, so that a spread of a few last places counts and a
- * constant row has its number as the mean and no variance. y takes the mean before its rounding to FP32. Magnitudes up to 2^50 are held; with
- * larger ones the squares leave FP32. A NaN or an infinity makes its own row NaN, and so does eps == 0 a
- * constant row, whose rstd is infinite. y may be x itself with ldy = ldx, and must not overlap
- * it otherwise.
+ * constant row has its number as the mean and no variance. y takes the mean before its rounding to FP32.
+ *
+ * Magnitudes up to 2^50 are held; with larger ones the squares leave FP32: where the variance does, rstd is 0 and y
+ * the bias. A NaN or an infinity makes its own row NaN, and so does eps == 0 a constant row, whose rstd is infinite.
+ * y may be x itself with ldy = ldx, and must not overlap it otherwise.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
  * (>= 1), x = 3, x_type = 4, ldx = 5, weight = 6, bias = 7, w_type = 8, eps = 9 (>= 0, finite),
