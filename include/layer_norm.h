@@ -27,8 +27,9 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  * spread it is corrected by the mean of the distances from it, so that a spread of a few last places counts and a
  * constant row has its number as the mean and no variance. y takes the mean before its rounding to FP32.
  *
- * Magnitudes up to 2^50 are held; with larger ones the squares leave FP32: where the variance does, rstd is 0 and y
- * the bias. A NaN or an infinity makes its own row NaN, and so does eps == 0 a constant row, whose rstd is infinite.
+ * Magnitudes up to 2^62 / sqrt(cols) are held (2^50 in rows of up to 2^24 elements): their squares' sum stays in FP32.
+ * Where the variance does not, rstd is 0 and y the bias. Downwards the variance and eps together have to be 2^-120 or
+ * more, below which squares lose bits: a matter of eps == 0 alone. A NaN or an infinity makes its own row NaN, and so does eps == 0 a constant row, whose rstd is infinite.
  * y may be x itself with ldy = ldx, and must not overlap it otherwise.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
