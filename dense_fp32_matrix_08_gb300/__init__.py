@@ -117,7 +117,7 @@ def _load() -> ctypes.CDLL:
     L.layer_norm.argtypes = [i, i, vp, i, i, vp, vp, i, f, vp, i, vp, vp, vp]
     L.layer_norm_backward.argtypes = [i, i, vp, i, vp, i, i, vp, vp, vp, i, vp, i, vp, vp, f, vp]
     L.layer_norm_backward_workspace_size.argtypes = [i, i, psz]
-    L.clip_grad_norm.argtypes = [i, vp, vp, vp, f, f, vp, vp, vp, vp]
+    L.clip_grad_norm.argtypes = [i, vp, vp, vp, ctypes.c_double, ctypes.c_double, vp, vp, vp, vp]
     L.i8_quantize.argtypes = [i, i, vp, i, i, vp, i, vp, vp]
     L.i8_linear.argtypes = [i, i, i, vp, i, vp, vp, i, vp, vp, f, vp, i, i, vp]
     L.i8_linear_plan.argtypes = [i] * 4 + [pi] * 3

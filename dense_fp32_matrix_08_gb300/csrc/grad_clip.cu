@@ -37,7 +37,7 @@ struct Params {
   int count, pieces;         // arrays and pieces of this launch
   double *sums;              // of each CTA of all launches of square_kernel
   int slot, slots;           // this launch's first one; all of them
-  float max_norm, eps;
+  double max_norm, eps;
   float *norm;
 };
 
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
   const double norm = total;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.norm) *p.norm = (float)norm;
   if constexpr (WRITE) {
-    const double ratio = (double)p.max_norm / (norm + (double)p.eps);
+    const double ratio = p.max_norm / (norm + p.eps);
     // (NaN stays; 0 / 0 is no reason for one)
     const bool whole = ratio >= 1.0 || norm == 0.0;
     // a factor near the end of FP32's range in two parts, of which neither loses bits
@@ -248,7 +248,7 @@ struct Call {
   const void *const *grads;
   const int *types;
   const long long *sizes;
-  float max_norm, eps;
+  double max_norm, eps;
   void *const *out;
   const int *out_types;
   float *norm;
@@ -312,7 +312,7 @@ static cudaError_t run(const Call &c, int launches, int sms) {
 using namespace sgemm;
 
 extern "C" int clip_grad_norm(int count, const void *const *grads, const int *types,
-                              const long long *sizes, float max_norm, float eps, void *const *out,
+                              const long long *sizes, double max_norm, double eps, void *const *out,
                               const int *out_types, float *norm, cudaStream_t stream) {
   const auto known = [](int t) { return t == GC_F32 || t == GC_BF16 || t == GC_F16; };
   const auto misplaced = [](const void *q, int t) {
@@ -330,8 +330,8 @@ extern "C" int clip_grad_norm(int count, const void *const *grads, const int *ty
     arrays += sizes[i] > 0;
     pieces += ceil_div(sizes[i], gc::kPiece);
   }
-  if (!(max_norm >= 0.0f)) return -5;
-  if (!(eps >= 0.0f) || std::isinf(eps)) return -6;
+  if (!(max_norm >= 0.0)) return -5;
+  if (!(eps >= 0.0) || std::isinf(eps)) return -6;
   if (out != nullptr && count > 0) {
     if (out_types == nullptr) return -8;
     for (int i = 0; i < count; ++i) {

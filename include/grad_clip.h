@@ -18,7 +18,7 @@ enum { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 }; /* types of gradients and results 
 
 /* Of `count` arrays, the i-th of sizes[i] elements of type types[i] at grads[i]:
  *     norm   = sqrt(sum of squares of all elements)
- *     factor = min(1, max_norm / (norm + eps))
+ *     factor = min(1, max_norm / (norm + eps))               (64 bits, rounded once to FP32)
  *     out[i] = grads[i] * factor                              (FP32, rounded once to out_types[i])
  * The lists are read by the host during the call; the arrays are device memory, aligned to their
  * elements. norm (one FP32 number in device memory) may be NULL. out == NULL leaves the second part
@@ -38,7 +38,7 @@ enum { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 }; /* types of gradients and results 
  * 5 (>= 0), eps = 6 (>= 0, finite), out = 7 (entries, their alignment and overlaps), out_types = 8,
  * norm = 9 (aligned)), or a cudaError_t. */
 int clip_grad_norm(int count, const void *const *grads, const int *types, const long long *sizes,
-                   float max_norm, float eps, void *const *out, const int *out_types, float *norm,
+                   double max_norm, double eps, void *const *out, const int *out_types, float *norm,
                    cudaStream_t stream);
 
 #ifdef __cplusplus
