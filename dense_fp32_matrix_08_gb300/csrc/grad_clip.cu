@@ -191,10 +191,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
     const double ratio = p.max_norm / (norm + p.eps);
     // (NaN stays; 0 / 0 is no reason for one)
     const bool whole = ratio >= 1.0 || norm == 0.0;
-    // a factor near the end of FP32's range in two parts, of which neither loses bits
-    const bool tiny = ratio < 0x1p-100;
-    const float factor = whole ? 1.0f : (float)(tiny ? ratio * 0x1p64 : ratio);
-    const float shrink = !whole && tiny ? 0x1p-64f : 1.0f;
+    // a factor near the end of FP32's range or below it in two parts, of which neither loses bits: (x shrink) is
+    // exact wherever x ratio is not below FP32's smallest number
+    const double shrink = ratio < 0x1p-190 ? 0x1p-149 : ratio < 0x1p-100 ? 0x1p-64 : 1.0;
+    const float factor = whole ? 1.0f : (float)(ratio / shrink), less = whole ? 1.0f : (float)shrink;
     for (int at = p.pieces - 1 - blockIdx.x; at >= 0; at -= gridDim.x) {
       const Array &a = array_of(p, at);
       if (whole && a.in == a.out) continue;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
         float v[8];
         load8(a, from + k, vec, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * shrink * factor;
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * less * factor;
         store8(a, from + k, vec_out, v);
       }
     }

@@ -42,3 +42,17 @@ def test_a_limit_just_above_the_norm_changes_nothing():
     norm = math.sqrt(sum(g.double().square().sum().item() for g in grads))
     sg.clip_grad_norm(grads, norm * (1 + 1e-12) + 1e-9, eps=1e-9)
     assert all(torch.equal(g, b) for g, b in zip(grads, before))
+
+
+@pytest.mark.parametrize("limit", [2.0 ** -20, 2.0 ** -100, 3e-44, 1e-60, 1e-70, 1e-300])
+@pytest.mark.parametrize("power", [0, 60, 100, 126])
+def test_factors_below_fp32(limit, power):
+    """Large gradients and small limits, whose factor is no FP32 number although results are: off by the factor's,
+    the norm's and the product's roundings (40 u, as in test_gpu_clip), or a smallest step."""
+    g = (1 + torch.rand(5000, generator=torch.Generator().manual_seed(1))).cuda() * 2.0 ** power
+    g[1::2] *= 2.0 ** -24
+    norm = g.double().square().sum().sqrt().item()
+    out = [torch.empty_like(g)]
+    sg.clip_grad_norm([g], limit, eps=0.0, out=out)
+    want = g.double() * (limit / norm)
+    assert ((out[0].double() - want).abs() <= 40 * 2.0 ** -24 * want + 2.0 ** -149).all()
