@@ -191,10 +191,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
     const double ratio = p.max_norm / (norm + p.eps);
     // (NaN stays; 0 / 0 is no reason for one)
     const bool whole = ratio >= 1.0 || norm == 0.0;
-    // a factor near the end of FP32's range or below it in two parts, of which neither loses bits: (x shrink) is
-    // exact wherever x ratio is not below FP32's smallest number
-    const double shrink = ratio < 0x1p-190 ? 0x1p-149 : ratio < 0x1p-100 ? 0x1p-64 : 1.0;
-    const float factor = whole ? 1.0f : (float)(ratio / shrink), less = whole ? 1.0f : (float)shrink;
+    // a factor near the end of FP32's range or below it in two parts, of which neither loses bits: x less is exact
+    // wherever x ratio is not below FP32's smallest number
+    const bool low = ratio < 0x1p-100, lowest = ratio < 0x1p-190;
+    const float factor = whole ? 1.0f : (float)(ratio * (lowest ? 0x1p149 : low ? 0x1p64 : 1.0));
+    const float less = whole || !low ? 1.0f : lowest ? 0x1p-149f : 0x1p-64f;
     for (int at = p.pieces - 1 - blockIdx.x; at >= 0; at -= gridDim.x) {
       const Array &a = array_of(p, at);
       if (whole && a.in == a.out) continue;
