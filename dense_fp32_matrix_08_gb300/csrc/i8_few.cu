@@ -6,8 +6,8 @@
 // products per instruction (dp4a), and adds them up in 32-bit integers. x stays in L1. The sums are
 // whole numbers, so that any order of adding them gives the same bits. 1 x 14336 x 4096: 10.0 us, 5.9 TB/s
 // (87% of a copy's rate); 1 x 4096 x 14336: 9.1 us; 1 x 4096 x 4096: 3.1 us, in a stream of calls. Four CTAs
-// per SM, 64 registers: with five the compiler spills (1 x 4096 x 14336: 14.3 us), with three there is too
-// little under way (13.9).
+// per SM, 64 registers (of which two rows spill 24 bytes, one none): with five more spills (1 x 4096 x 14336: 14.3
+// us), with three there is too little under way (13.9).
 #include <algorithm>
 
 #include "i8_internal.h"

@@ -5,10 +5,14 @@
 // its last use, so that the variance is the mean of the squared distances themselves: no difference
 // of large sums. The FP32 sum of a row gives its mean m to at most 53 u mean|x| (u = 2^-24). Where that is not far
 // below the spread (far_off), the distances from m, exact there, are added up for what m lacks, e = sum (x - m) / n,
-// and the variance is taken again, from (x - m) - e: a constant row has var 0 and y = b. 8192 x 4096 BF16: 22.5 us, 6.0 TB/s, 88% of a copy's rate, issue slots 59% busy (pairs of
-// FP32 numbers per instruction: one by one they were 71% busy and it took 32 us); FP32 41 us, 96%. 1 x 4096: 1.7 us.
-// 16384 x 1024 BF16 11.7 us, 84%; 16384 x 512 7.5, 66%: the sums' exchanges weigh more there. 2048 x 16384 BF16
-// 35.5 us, 56%: one row at a time per SM. Rows at any alignment come element by element: 8192 x 4095 BF16 39 us.
+// and the variance is taken again, from (x - m) - e: a constant row has var 0 and y = b.
+//
+// 8192 x 4096 BF16: 22.0 us, 6.1 TB/s, 90% of a copy's rate, issue slots 59% busy (pairs of FP32 numbers per
+// instruction: one by one they were 71% busy and it took 32 us); FP32 41 us, 96%. With means of 10 times the spread
+// 32 and 41 us (corrected for every row, of whatever mean, 25.5 and 41). 1 x 4096: 1.7 us. 16384 x 1024 BF16 11.7 us,
+// 84%; 16384 x 512 7.1, 70%: the sums' exchanges weigh more there. 2048 x 16384 BF16 35.5 us, 56%: one row at a time
+// per SM. Rows at any alignment come element by element: 8192 x 4095 BF16 40 us, 4096 x 12287 83 (72 without the
+// correction's registers).
 #include <algorithm>
 #include <cmath>
 
@@ -285,7 +289,7 @@ static cudaError_t run(const Params &p, bool vec, int sms, cudaStream_t stream) 
   if (p.cols <= 512) return launch<T, 32, 2>(p, vec, sms, stream);
   // (a warp per row needs no barrier, but aligned rows for its registers: 16384 x 1024 BF16 15.1 us with 128
   // threads on a row, 11.7 so. Rows that come element by element have 8 of them per thread where that is faster: 16384
-  // x 1023 BF16 17.5 us, with 768 threads per SM 22.8; 8192 x 4095 BF16 39.3, with 16 per thread 43.2, but FP32 48.6
+  // x 1023 BF16 18.2 us, with 768 threads per SM 22.8; 8192 x 4095 BF16 40.2, with 16 per thread 43.2, but FP32 48.6
   // and 47.7.)
   if (p.cols <= 1024) return vec ? launch<T, 32, 4, true>(p, sms, stream) : launch<T, 128, 1, false>(p, sms, stream);
   if constexpr (T::SIZE == 2) {

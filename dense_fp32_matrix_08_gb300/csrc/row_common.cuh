@@ -149,7 +149,8 @@ struct Share {
 
 // A thread's chunks of the rows to come, of INPUTS matrices: with VEC as asynchronous copies into its own
 // places of a ring in shared memory, DEPTH rows ahead (what one row's registers hold under way does not
-// fill HBM's latency: layer norm of 8192 x 4096 BF16 took 37 us so, 32 with the ring), else one row ahead in registers.
+// fill HBM's latency: layer norm of 8192 x 4096 BF16 took 37 us so and 32 with the ring, when
+// numbers were still taken one by one: 22 now), else one row ahead in registers.
 // Nobody else reads them, so there is nothing to wait for but the thread's own copies.
 template <class T, int TPR, int CH, bool VEC, int INPUTS, int DEPTH, int THREADS>
 struct Ahead {

@@ -29,8 +29,9 @@ enum { LN_F32 = 0, LN_BF16 = 1, LN_F16 = 2 }; /* types of x, y, dy, dx, weight a
  *
  * Magnitudes up to 2^62 / sqrt(cols) are held (2^50 in rows of up to 2^24 elements): their squares' sum stays in FP32.
  * Where the variance does not, rstd is 0 and y the bias. Downwards the variance and eps together have to be 2^-120 or
- * more, below which squares lose bits: a matter of eps == 0 alone. A NaN or an infinity makes its own row NaN, and so does eps == 0 a constant row, whose rstd is infinite.
- * y may be x itself with ldy = ldx, and must not overlap it otherwise.
+ * more, below which squares lose bits: a matter of eps == 0 alone. A NaN or an infinity makes its own row NaN, and so
+ * does eps == 0 a constant row, whose rstd is infinite. y may be x itself with ldy = ldx, and must not overlap it
+ * otherwise.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
  * (>= 1), x = 3, x_type = 4, ldx = 5, weight = 6, bias = 7, w_type = 8, eps = 9 (>= 0, finite),
@@ -51,8 +52,9 @@ int layer_norm(int rows, int cols, const void *x, int x_type, int ldx, const voi
  * Sums along rows are FP32 (with 48 bits in rows of more than 12288 elements, or of more than 16384 where they
  * are of 16 bits and 16-byte aligned), those over the rows FP32 within a block (at most 500 rows one after the
  * other) and 64-bit beyond, in an order fixed by the shape, the type, that alignment and the device: the same call
- * gives the same bits. The workspace (layer_norm_backward_workspace_size bytes at most) is a stream-ordered
- * allocation from the library's pool.
+ * gives the same bits. The mean is the FP32 number that is given: where a spread is few of its last places, h carries
+ * its rounding. The workspace (layer_norm_backward_workspace_size bytes at most) is a stream-ordered allocation from
+ * the library's pool.
  *
  * Returns 0, -i for the first illegal argument in this signature's order (rows = 1 (>= 0), cols = 2
  * (>= 1), dy = 3, lddy = 4, x = 5, x_type = 6, ldx = 7, mean = 8, rstd = 9, weight = 10, w_type = 11,
@@ -63,7 +65,8 @@ int layer_norm_backward(int rows, int cols, const void *dy, int lddy, const void
                         cudaStream_t stream);
 
 /* Bytes of workspace that layer_norm_backward takes at most from the library's pool on the current device
- * (without one: on a whole GB300); FP32 rows that are not 16-byte aligned take the most. Returns 0 or -1, -2 for an illegal rows, cols. */
+ * (without one: on a whole GB300); FP32 rows that are not 16-byte aligned take the most. Returns 0 or -1, -2 for an
+ * illegal rows, cols. */
 int layer_norm_backward_workspace_size(int rows, int cols, size_t *bytes);
 
 /* The arguments of both in their order, as structures: one pointer crosses a language binding faster
