@@ -1,4 +1,5 @@
 """CPU-only: plans for one and for a few SMs, where there is no room for pairs of blocks."""
+import os
 import subprocess
 import sys
 
@@ -6,13 +7,14 @@ import pytest
 
 import dense_fp32_matrix_08_gb300 as sg
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SIZES = (1, 3, 40, 300, 5000)
 
 
 def test_one_sm_does_not_end_the_process():
     """In a process of its own, which a division by zero would end."""
     code = "import dense_fp32_matrix_08_gb300 as sg; print(sg.i8_linear_plan(40, 300, 2000, num_sms=1))"
-    assert subprocess.run([sys.executable, "-c", code], capture_output=True).returncode == 0
+    assert subprocess.run([sys.executable, "-c", code], capture_output=True, cwd=ROOT).returncode == 0
 
 
 @pytest.mark.parametrize("sms", [1, 2, 3, 7, 152])
@@ -29,7 +31,7 @@ def test_integer_product(sms):
 
 def test_one_sm_does_not_end_the_process_of_the_8_bit_float_product():
     code = "import dense_fp32_matrix_08_gb300 as sg; print(sg.f8_gemm_plan(40, 300, 2000, num_sms=1))"
-    assert subprocess.run([sys.executable, "-c", code], capture_output=True).returncode == 0
+    assert subprocess.run([sys.executable, "-c", code], capture_output=True, cwd=ROOT).returncode == 0
 
 
 @pytest.mark.parametrize("sms", [1, 2, 3, 7, 152])
